@@ -1,6 +1,7 @@
-"""MI355X (gfx950) Muon optimizer step, weight EMA and AdamW for the other parameters.
+"""MI355X (gfx950) Muon optimizer step, weight EMA and AdamW for the other parameters,
+with the loss of the language-model head (its gradients included) and AdamW on 8-bit states.
 
-Thin Python binding over the C ABI of libmuonstep.so (include/muonstep.h):
+Thin Python binding over the C ABI of libmuonstep.so (include/muonstep.h, include/muonstep_train.h):
 it only turns torch tensors into device pointers plus the current HIP stream.
 Every step of the computation runs in the library's HIP kernels.
 """
@@ -12,4 +13,7 @@ from ._lib import (  # noqa: F401
 from .api import (  # noqa: F401
     muon_step, muon_step_static, ema_update, ema_swap, adamw_step, workspace_size, profile_enable, profile_read, version,
     PreparedMuonStep, PreparedEma, PreparedAdamW,
+)
+from .train import (  # noqa: F401
+    AdamW8State, adamw8_step, PreparedAdamW8,
 )

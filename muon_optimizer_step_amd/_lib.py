@@ -1,4 +1,4 @@
-"""ctypes declarations of the C ABI in include/muonstep.h (no torch needed here)."""
+"""ctypes declarations of the C ABI in include/muonstep.h and include/muonstep_train.h (no torch needed here)."""
 
 from __future__ import annotations
 
@@ -22,6 +22,7 @@ MUON_NS_FP32 = 1
 MUON_NS_BF16X3 = 2
 MUON_NS_SCHEDULE_PHASES = 0
 MUON_NS_SCHEDULE_CHAIN = 1
+MUON_ADAMW8_BLOCK = 256
 
 
 class MuonTensor(ctypes.Structure):
@@ -44,6 +45,21 @@ class AdamWTensor(ctypes.Structure):
         ("exp_avg_sq", ctypes.c_void_p),
         ("ema", ctypes.c_void_p),
         ("numel", ctypes.c_int64),
+    ]
+
+
+class AdamW8Tensor(ctypes.Structure):
+    _fields_ = [
+        ("param", ctypes.c_void_p),
+        ("grad", ctypes.c_void_p),
+        ("exp_avg", ctypes.c_void_p),
+        ("exp_avg_scale", ctypes.c_void_p),
+        ("rms", ctypes.c_void_p),
+        ("rms_scale", ctypes.c_void_p),
+        ("ema", ctypes.c_void_p),
+        ("copy", ctypes.c_void_p),
+        ("numel", ctypes.c_int64),
+        ("grad_bf16", ctypes.c_int32),
     ]
 
 
@@ -107,6 +123,14 @@ def load() -> ctypes.CDLL:
     f.argtypes = [ctypes.POINTER(AdamWTensor), ctypes.c_int32, ctypes.c_float, ctypes.c_float, ctypes.c_float,
                   ctypes.c_float, ctypes.c_float, ctypes.c_int32, ctypes.c_float, ctypes.c_void_p]
     f.restype = ctypes.c_int
+    f = lib.adamw8_step
+    f.argtypes = [ctypes.POINTER(AdamW8Tensor), ctypes.c_int32, ctypes.c_float, ctypes.c_float, ctypes.c_float,
+                  ctypes.c_float, ctypes.c_float, ctypes.c_int32, ctypes.c_float, ctypes.c_int32, ctypes.c_uint64,
+                  ctypes.c_void_p]
+    f.restype = ctypes.c_int
+    for f in (lib.adamw8_encode, lib.adamw8_decode):
+        f.argtypes = [ctypes.c_void_p] * 6 + [ctypes.c_int64, ctypes.c_void_p]
+        f.restype = ctypes.c_int
     lib.muon_set_ns_schedule.argtypes = [ctypes.c_int32]
     lib.muon_set_ns_schedule.restype = ctypes.c_int
     lib.muon_plan_cache_stats.argtypes = [ctypes.POINTER(ctypes.c_int64), ctypes.POINTER(ctypes.c_int64)]
@@ -144,6 +168,15 @@ def adamw_table(entries) -> "ctypes.Array[AdamWTensor]":
     arr = (AdamWTensor * max(1, len(entries)))()
     for i, e in enumerate(entries):
         arr[i] = AdamWTensor(*e)
+    return arr
+
+
+def adamw8_table(entries) -> "ctypes.Array[AdamW8Tensor]":
+    """entries: iterable of (param, grad, exp_avg, exp_avg_scale, rms, rms_scale, ema, copy, numel, grad_bf16)."""
+    entries = list(entries)
+    arr = (AdamW8Tensor * max(1, len(entries)))()
+    for i, e in enumerate(entries):
+        arr[i] = AdamW8Tensor(*e)
     return arr
 
 

@@ -28,22 +28,13 @@
 
 #include "../../include/muonstep.h"
 #include "common.h"
+#include "host.h"
 #include "kernels.h"
 
 namespace muon {
 namespace {
 
 thread_local std::string g_last_error;
-
-int fail(int code, const char* fmt, ...) {
-    char buf[512];
-    va_list ap;
-    va_start(ap, fmt);
-    vsnprintf(buf, sizeof(buf), fmt, ap);
-    va_end(ap);
-    g_last_error = buf;
-    return code;
-}
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
@@ -73,33 +64,47 @@ hipEvent_t take_event() {
     return e;
 }
 
-// Runs `launch` (which returns the launch's hipError_t) bracketed by events
-// when profiling is on.
-template <typename F>
-hipError_t timed_launch(const char* name, hipStream_t s, F launch) {
-    bool prof;
-    {
-        std::lock_guard<std::mutex> lk(g_prof_mu);
-        prof = g_prof_enabled;
-    }
-    if (!prof) return launch();
-    hipEvent_t e0, e1;
-    {
-        std::lock_guard<std::mutex> lk(g_prof_mu);
-        e0 = take_event();
-        e1 = take_event();
-    }
-    if (!e0 || !e1) return hipErrorOutOfMemory;
-    hipError_t err = hipEventRecord(e0, s);
-    if (err != hipSuccess) return err;
-    err = launch();
-    if (err != hipSuccess) return err;
-    err = hipEventRecord(e1, s);
-    if (err != hipSuccess) return err;
-    std::lock_guard<std::mutex> lk(g_prof_mu);
-    g_pending.push_back({name, e0, e1});
-    return hipSuccess;
+}  // namespace
+
+// ------------------------------------------------------------- shared with the other host files (host.h)
+int fail(int code, const char* fmt, ...) {
+    char buf[512];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof(buf), fmt, ap);
+    va_end(ap);
+    g_last_error = buf;
+    return code;
 }
+
+int check_overlaps(std::vector<Span>& spans, const char* what) {
+    std::sort(spans.begin(), spans.end(), [](const Span& a, const Span& b) { return a.lo < b.lo; });
+    for (size_t i = 1; i < spans.size(); ++i) {
+        if (spans[i].lo < spans[i - 1].hi)
+            return fail(MUON_ERR_UNSUPPORTED, "%s: buffers of tensors %d and %d overlap", what,
+                        spans[i - 1].tensor, spans[i].tensor);
+    }
+    return MUON_OK;
+}
+
+bool profiling() {
+    std::lock_guard<std::mutex> lk(g_prof_mu);
+    return g_prof_enabled;
+}
+
+hipError_t profile_events(hipEvent_t& start, hipEvent_t& stop) {
+    std::lock_guard<std::mutex> lk(g_prof_mu);
+    start = take_event();
+    stop = take_event();
+    return start && stop ? hipSuccess : hipErrorOutOfMemory;
+}
+
+void profile_done(const char* name, hipEvent_t start, hipEvent_t stop) {
+    std::lock_guard<std::mutex> lk(g_prof_mu);
+    g_pending.push_back({name, start, stop});
+}
+
+namespace {
 
 // ------------------------------------------------------------- NS lanes
 // The matrices are independent NS problems.  Their shape groups are spread
@@ -255,21 +260,6 @@ void make_plan(const muon_tensor_t* t, int n, int mode, Plan& p) {
 }
 
 // ------------------------------------------------------------- validation
-struct Span {
-    uintptr_t lo, hi;
-    int tensor;
-};
-
-int check_overlaps(std::vector<Span>& spans, const char* what) {
-    std::sort(spans.begin(), spans.end(), [](const Span& a, const Span& b) { return a.lo < b.lo; });
-    for (size_t i = 1; i < spans.size(); ++i) {
-        if (spans[i].lo < spans[i - 1].hi)
-            return fail(MUON_ERR_UNSUPPORTED, "%s: buffers of tensors %d and %d overlap", what,
-                        spans[i - 1].tensor, spans[i].tensor);
-    }
-    return MUON_OK;
-}
-
 int validate_tensors(const muon_tensor_t* t, int32_t n, int32_t precision) {
     if (!t) return fail(MUON_ERR_INVALID_ARG, "tensors is NULL");
     if (n <= 0 || n > MUON_MAX_TENSORS) return fail(MUON_ERR_INVALID_ARG, "n = %d outside [1, %d]", n, MUON_MAX_TENSORS);
@@ -331,11 +321,6 @@ void f8_scale_exponents(const float* coeffs, int ns_steps, int* sa) {
         bound = m * 1.02;
     }
 }
-
-// Streaming tensors (EMA, AdamW): at most 2^30 workgroups per launch, so a
-// single tensor may hold at most this many elements (4 Ti elements; far above
-// any device memory).
-constexpr int64_t kMaxStreamElems = ((int64_t)1 << 30) * 1024;
 
 // ------------------------------------------------------------- schedules
 // Everything muon_step derives from the tensor list alone (validation of the
