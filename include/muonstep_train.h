@@ -84,6 +84,72 @@ int adamw8_encode(const float* exp_avg, const float* exp_avg_sq, void* exp_avg_c
 int adamw8_decode(const void* exp_avg_codes, const float* exp_avg_scale, const void* rms_codes,
                   const float* rms_scale, float* exp_avg, float* exp_avg_sq, int64_t numel, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Softmax cross entropy of the language-model head, without the logits.
+ *
+ * With z_ij = hidden_i . weight_j, l = softcap tanh(z / softcap) (softcap 0: l = z):
+ *   lse_i = log sum_j exp l_ij;   nll_i = lse_i - l_i,targets[i]
+ *   g_i = token_weights[i], or 1 / (counted tokens) where token_weights is NULL
+ *   loss = sum_i g_i nll_i
+ *   grad_hidden = d loss / d hidden;   grad_weight = d loss / d weight.
+ * A token whose target is ignore_index is not counted: its nll and lse are 0,
+ * its gradient row is 0, and whatever its hidden state holds (NaN, infinity)
+ * reaches nothing.  With no counted token loss and gradients are 0.  A
+ * target outside [0, vocab) that is not ignore_index gives a NaN nll (and
+ * loss and gradients); nothing is read out of range.
+ *
+ *   hidden       tokens x dim, weight vocab x dim: 16-bit floats of type `dtype`,
+ *                dim values contiguous, rows hidden_stride / weight_stride
+ *                elements apart (>= dim; weight rows must not overlap).
+ *   targets      int64 per token.
+ *   token_weights  NULL or float32 per token (finite).
+ *   nll          float32 per token.    lse   NULL or float32 per token.
+ *   loss         NULL or one float32.
+ *   grad_hidden, grad_weight   NULL or rows like hidden and weight, overwritten
+ *                (not added to).  Each is computed only if given; with both and
+ *                loss NULL the call only scores.
+ *   tokens >= 0, vocab >= 1, dim >= 1 (limits below); softcap finite, >= 0.
+ * Products take their 16-bit inputs as they are and sum in float32; the
+ * probabilities are rounded to 16 bits once, before they are multiplied with
+ * weight and hidden; gradients are rounded once.  dim a multiple of 8 with
+ * 16-byte aligned rows is read in place, anything else through a padded copy
+ * in the workspace.
+ * For gradients the tokens go through the workspace in pieces of at most
+ * MUON_HEAD_PIECE_BYTES of 16-bit values (vocab x piece), never all logits of a
+ * large batch at once. */
+#define MUON_HEAD_BF16 0
+#define MUON_HEAD_FP16 1
+#define MUON_HEAD_MAX_TOKENS (1 << 24)
+#define MUON_HEAD_MAX_VOCAB (1 << 22)
+#define MUON_HEAD_MAX_DIM 65536
+#define MUON_HEAD_PIECE_BYTES ((int64_t)1 << 30)
+typedef struct head_loss_t {
+    const void* hidden;
+    const void* weight;
+    const int64_t* targets;
+    const float* token_weights;
+    float* loss;
+    float* nll;
+    float* lse;
+    void* grad_hidden;
+    void* grad_weight;
+    int64_t tokens, vocab, dim;
+    int64_t hidden_stride, weight_stride, grad_hidden_stride, grad_weight_stride;
+    int64_t ignore_index;
+    float softcap;
+    int32_t dtype;
+} head_loss_t;
+
+/* Bytes of device workspace head_loss needs for this problem: its sizes,
+ * strides (<= 2^22), which outputs it has and the alignment of hidden and weight.  0 if the
+ * arguments are invalid (see muon_last_error()). */
+size_t head_loss_workspace_size(const head_loss_t* problem);
+
+/* The loss (and gradients).  workspace: a device buffer of at least
+ * head_loss_workspace_size(...) bytes, 256-byte aligned, that overlaps no
+ * tensor; its contents on entry do not matter. */
+int head_loss(const head_loss_t* problem, void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -15,5 +15,6 @@ from .api import (  # noqa: F401
     PreparedMuonStep, PreparedEma, PreparedAdamW,
 )
 from .train import (  # noqa: F401
-    AdamW8State, adamw8_step, PreparedAdamW8,
+    AdamW8State, adamw8_step, PreparedAdamW8, LinearCrossEntropy, PreparedLinearCrossEntropy, linear_cross_entropy,
+    linear_cross_entropy_grad,
 )

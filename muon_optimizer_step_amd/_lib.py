@@ -23,6 +23,12 @@ MUON_NS_BF16X3 = 2
 MUON_NS_SCHEDULE_PHASES = 0
 MUON_NS_SCHEDULE_CHAIN = 1
 MUON_ADAMW8_BLOCK = 256
+MUON_HEAD_BF16 = 0
+MUON_HEAD_FP16 = 1
+MUON_HEAD_MAX_TOKENS = 1 << 24
+MUON_HEAD_MAX_VOCAB = 1 << 22
+MUON_HEAD_MAX_DIM = 65536
+MUON_HEAD_PIECE_BYTES = 1 << 30
 
 
 class MuonTensor(ctypes.Structure):
@@ -61,6 +67,14 @@ class AdamW8Tensor(ctypes.Structure):
         ("numel", ctypes.c_int64),
         ("grad_bf16", ctypes.c_int32),
     ]
+
+
+class HeadLoss(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("hidden", "weight", "targets", "token_weights", "loss", "nll", "lse",
+                                               "grad_hidden", "grad_weight")]
+    _fields_ += [(n, ctypes.c_int64) for n in ("tokens", "vocab", "dim", "hidden_stride", "weight_stride",
+                                               "grad_hidden_stride", "grad_weight_stride", "ignore_index")]
+    _fields_ += [("softcap", ctypes.c_float), ("dtype", ctypes.c_int32)]
 
 
 class MuonError(RuntimeError):
@@ -131,6 +145,10 @@ def load() -> ctypes.CDLL:
     for f in (lib.adamw8_encode, lib.adamw8_decode):
         f.argtypes = [ctypes.c_void_p] * 6 + [ctypes.c_int64, ctypes.c_void_p]
         f.restype = ctypes.c_int
+    lib.head_loss_workspace_size.argtypes = [ctypes.POINTER(HeadLoss)]
+    lib.head_loss_workspace_size.restype = ctypes.c_size_t
+    lib.head_loss.argtypes = [ctypes.POINTER(HeadLoss), ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
+    lib.head_loss.restype = ctypes.c_int
     lib.muon_set_ns_schedule.argtypes = [ctypes.c_int32]
     lib.muon_set_ns_schedule.restype = ctypes.c_int
     lib.muon_plan_cache_stats.argtypes = [ctypes.POINTER(ctypes.c_int64), ctypes.POINTER(ctypes.c_int64)]

@@ -1,0 +1,324 @@
+// Host side of the language-model head's loss: argument checks, the layout of
+// the workspace, the pieces of the tokens and the launch sequence behind
+// head_loss in muonstep_train.h.
+//
+// One call enqueues, on the caller's stream:
+//   head_scalars (train: the mean's weight), head_pack (train: hidden with
+//   ignored rows zeroed; otherwise only what is not 16-byte aligned)
+//   for each piece of the tokens: head_logits, head_rows, and for gradients
+//   head_prob, head_grad (hidden), head_grad (weight), with head_join where K
+//   was split or the pieces' sums had to be kept in fp32
+//   head_loss (the weighted sum)
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+#include <vector>
+
+#include "../../include/muonstep_train.h"
+#include "head.h"
+#include "host.h"
+
+namespace muon {
+namespace {
+
+constexpr int kCus = 256;                 // compute units of an MI355X
+constexpr int kMinStagesPerSplit = 4;     // K stages a workgroup takes at least when K is split
+
+int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
+
+// Offsets into the workspace (-1: not there) and sizes, from the problem alone.
+struct HeadPlan {
+    bool train, small, pack_h, pack_w;
+    int64_t dim8;                 // dim rounded up to whole chunks
+    int64_t piece, pieces;        // tokens per piece
+    int64_t rows, cols;           // padded size of a piece's probabilities
+    int nsub, sub;
+    int splits_h, splits_w, stages_h, stages_w;   // K splits of the two gradients
+    bool partial_h, partial_w;
+    int64_t scalars, row_weight, row_target, ref, sum, e, hidden, weight, part_h, part_w, bytes;
+};
+
+// K of `k` elements over the workgroups that `tiles` output tiles leave idle.
+void split_k(int64_t k, int64_t tiles, int& splits, int& stages) {
+    const int total = (int)((k + kHeadK - 1) / kHeadK);
+    int want = (int)std::max<int64_t>(1, kCus / tiles);
+    want = std::min(want, std::max(1, total / kMinStagesPerSplit));
+    stages = (total + want - 1) / want;
+    splits = (total + stages - 1) / stages;
+}
+
+HeadPlan make_head_plan(const head_loss_t& p) {
+    HeadPlan q;
+    q.train = p.loss || p.grad_hidden || p.grad_weight;
+    q.dim8 = round_up(p.dim, 8);
+    auto odd = [&](const void* ptr, int64_t stride) {
+        return p.dim % 8 || stride % 8 || reinterpret_cast<uintptr_t>(ptr) % 16;
+    };
+    q.pack_h = odd(p.hidden, p.hidden_stride) || p.grad_weight;
+    q.pack_w = odd(p.weight, p.weight_stride);
+    const bool grads = p.grad_hidden || p.grad_weight;
+    q.cols = round_up(p.vocab, kHeadPad);
+    q.piece = std::max<int64_t>(p.tokens, 1);
+    // gradients: what the workspace holds of the probabilities; scoring: 2^32
+    // logits a launch, whose partial sums take 256 MB
+    const int64_t most = grads ? MUON_HEAD_PIECE_BYTES / 2 : (int64_t)1 << 32;
+    if (q.piece * q.cols > most) q.piece = std::max<int64_t>(kHeadTile, most / q.cols / kHeadTile * kHeadTile);
+    q.piece = std::min(q.piece, std::max<int64_t>(p.tokens, 1));
+    q.pieces = (p.tokens + q.piece - 1) / q.piece;
+    q.rows = round_up(q.piece, kHeadPad);
+    q.small = p.tokens <= kHeadSmall;
+    q.sub = q.small ? kHeadSmallSub : kHeadSub;
+    q.nsub = q.small ? (int)(q.cols / kHeadSmallSub) : (int)((p.vocab + kHeadTile - 1) / kHeadTile) * (kHeadTile / kHeadSub);
+    const int64_t tiles_d = (p.dim + kHeadTile - 1) / kHeadTile;
+    split_k(q.cols, (q.piece + kHeadTile - 1) / kHeadTile * tiles_d, q.splits_h, q.stages_h);
+    split_k(q.rows, (p.vocab + kHeadTile - 1) / kHeadTile * tiles_d, q.splits_w, q.stages_w);
+    q.partial_h = p.grad_hidden && q.splits_h > 1;
+    q.partial_w = p.grad_weight && (q.splits_w > 1 || q.pieces > 1);
+    int64_t off = 0;
+    auto take = [&](bool there, int64_t bytes) {
+        const int64_t at = there ? off : -1;
+        if (there) off = round_up(off + bytes, 256);
+        return at;
+    };
+    q.scalars = take(true, 16);
+    q.row_weight = take(q.train, 4 * (p.tokens + kHeadPad));
+    q.row_target = take(q.train, 4 * (p.tokens + kHeadPad));
+    q.ref = take(true, 4 * (int64_t)q.nsub * q.rows);
+    q.sum = take(true, 4 * (int64_t)q.nsub * q.rows);
+    q.e = take(grads, 2 * q.rows * q.cols);
+    q.hidden = take(q.pack_h, 2 * round_up(p.tokens, kHeadPad) * q.dim8);
+    q.weight = take(q.pack_w, 2 * p.vocab * q.dim8);
+    q.part_h = take(q.partial_h, 4 * (int64_t)q.splits_h * q.piece * q.dim8);
+    q.part_w = take(q.partial_w, 4 * (int64_t)q.splits_w * p.vocab * q.dim8);
+    q.bytes = std::max<int64_t>(off, 256);
+    return q;
+}
+
+int validate_sizes(const head_loss_t* p) {
+    if (!p) return fail(MUON_ERR_INVALID_ARG, "problem is NULL");
+    if (p->tokens < 0 || p->vocab < 1 || p->dim < 1)
+        return fail(MUON_ERR_INVALID_ARG, "tokens = %lld, vocab = %lld, dim = %lld: tokens >= 0, vocab and dim >= 1",
+                    (long long)p->tokens, (long long)p->vocab, (long long)p->dim);
+    if (p->tokens > MUON_HEAD_MAX_TOKENS || p->vocab > MUON_HEAD_MAX_VOCAB || p->dim > MUON_HEAD_MAX_DIM)
+        return fail(MUON_ERR_UNSUPPORTED, "tokens = %lld, vocab = %lld, dim = %lld beyond the limits", (long long)p->tokens,
+                    (long long)p->vocab, (long long)p->dim);
+    if (p->dtype != MUON_HEAD_BF16 && p->dtype != MUON_HEAD_FP16)
+        return fail(MUON_ERR_INVALID_ARG, "dtype = %d is not MUON_HEAD_BF16 or MUON_HEAD_FP16", p->dtype);
+    if (!std::isfinite(p->softcap) || p->softcap < 0.f) return fail(MUON_ERR_INVALID_ARG, "softcap must be finite and >= 0");
+    if (p->hidden_stride < p->dim || p->weight_stride < p->dim || (p->grad_hidden && p->grad_hidden_stride < p->dim) ||
+        (p->grad_weight && p->grad_weight_stride < p->dim))
+        return fail(MUON_ERR_INVALID_ARG, "a row stride is smaller than dim = %lld", (long long)p->dim);
+    const int64_t far = (int64_t)1 << 22;   // 256 rows apart fits 32 bits of bytes
+    if (p->hidden_stride > far || p->weight_stride > far || (p->grad_hidden && p->grad_hidden_stride > far) ||
+        (p->grad_weight && p->grad_weight_stride > far))
+        return fail(MUON_ERR_UNSUPPORTED, "a row stride is beyond 2^22");
+    return MUON_OK;
+}
+
+int validate_buffers(const head_loss_t& p, const void* workspace, size_t bytes) {
+    const int64_t n = p.tokens;
+    if (!p.weight || (n > 0 && (!p.hidden || !p.targets || !p.nll)))
+        return fail(MUON_ERR_INVALID_ARG, "hidden, weight, targets and nll must be non-NULL");
+    auto rows = [](int64_t r, int64_t stride, int64_t dim) { return r > 0 ? 2 * ((r - 1) * stride + dim) : 0; };
+    // inputs may share memory with each other; what is written may not
+    const struct { const void* p; int64_t bytes; int align; bool written; } buf[10] = {
+        {p.hidden, rows(n, p.hidden_stride, p.dim), 2, false},
+        {p.weight, rows(p.vocab, p.weight_stride, p.dim), 2, false},
+        {p.targets, 8 * n, 8, false},
+        {p.token_weights, 4 * n, 4, false},
+        {p.loss, 4, 4, true},
+        {p.nll, 4 * n, 4, true},
+        {p.lse, 4 * n, 4, true},
+        {p.grad_hidden, rows(n, p.grad_hidden_stride, p.dim), 2, true},
+        {p.grad_weight, rows(p.vocab, p.grad_weight_stride, p.dim), 2, true},
+        {workspace, (int64_t)bytes, 256, true}};
+    for (int i = 0; i < 10; ++i) {
+        if (!buf[i].p || buf[i].bytes == 0) continue;
+        const uintptr_t lo = reinterpret_cast<uintptr_t>(buf[i].p);
+        if (lo % buf[i].align) return fail(MUON_ERR_INVALID_ARG, "buffer %d is not %d-byte aligned", i, buf[i].align);
+        for (int j = 0; j < i; ++j) {
+            if (!buf[j].p || !(buf[i].written || buf[j].written)) continue;
+            const uintptr_t lj = reinterpret_cast<uintptr_t>(buf[j].p);
+            if (lo < lj + buf[j].bytes && lj < lo + buf[i].bytes)
+                return fail(MUON_ERR_UNSUPPORTED, "head_loss: buffers %d and %d overlap", j, i);
+        }
+    }
+    return MUON_OK;
+}
+
+#define HEAD_TRY(name, call)                                                                                    \
+    do {                                                                                                        \
+        const hipError_t err_ = timed_launch(name, s, [&] { return call; });                                    \
+        if (err_ != hipSuccess) return fail(MUON_ERR_HIP, "%s launch failed: %s", name, hipGetErrorString(err_)); \
+    } while (0)
+
+int enqueue_head(const head_loss_t& p, const HeadPlan& q, uint8_t* ws, hipStream_t s) {
+    float* scalars = reinterpret_cast<float*>(ws + q.scalars);
+    float* row_weight = q.train ? reinterpret_cast<float*>(ws + q.row_weight) : nullptr;
+    int* row_target = q.train ? reinterpret_cast<int*>(ws + q.row_target) : nullptr;
+    const int dim = (int)p.dim, vocab = (int)p.vocab;
+    if (q.train) {
+        const HeadScalars a = {p.targets, p.token_weights, scalars, p.ignore_index, p.tokens, p.dtype};
+        HEAD_TRY("head_scalars", launch_head_scalars(a, s));
+    }
+    const uint8_t* h = static_cast<const uint8_t*>(p.hidden);
+    const void* w = p.weight;
+    int64_t h_pitch = p.hidden_stride, w_pitch = p.weight_stride;
+    if (q.pack_h && p.tokens) {
+        const HeadPack a = {p.hidden, p.hidden_stride, ws + q.hidden, q.dim8, (int)round_up(p.tokens, kHeadPad), (int)p.tokens,
+                            dim, p.targets, p.ignore_index};
+        HEAD_TRY("head_pack", launch_head_pack(a, s));
+        h = ws + q.hidden;
+        h_pitch = q.dim8;
+    }
+    if (q.pack_w) {
+        const HeadPack a = {p.weight, p.weight_stride, ws + q.weight, q.dim8, vocab, vocab, dim, nullptr, 0};
+        HEAD_TRY("head_pack", launch_head_pack(a, s));
+        w = ws + q.weight;
+        w_pitch = q.dim8;
+    }
+    float* ref = reinterpret_cast<float*>(ws + q.ref);
+    float* sum = reinterpret_cast<float*>(ws + q.sum);
+    const float inv_cap = p.softcap > 0.f ? 1.0f / p.softcap : 0.f;
+    auto vec = [&](const void* ptr, int64_t stride) {
+        return dim % 8 == 0 && stride % 8 == 0 && reinterpret_cast<uintptr_t>(ptr) % 16 == 0;
+    };
+    const int tiles_d = (dim + kHeadTile - 1) / kHeadTile;
+    for (int64_t at = 0; at < p.tokens; at += q.piece) {
+        const int tokens = (int)std::min(q.piece, p.tokens - at), rows = (int)round_up(tokens, kHeadPad);
+        const uint8_t* hp = h + at * h_pitch * 2;
+        HeadLogits a;
+        memset(&a, 0, sizeof(a));
+        a.h = hp;
+        a.w = w;
+        a.h_pitch = h_pitch;
+        a.w_pitch = w_pitch;
+        a.e = q.e >= 0 ? ws + q.e : nullptr;
+        a.e_pitch = q.cols;
+        a.e_rows = rows;
+        a.ref = ref;
+        a.sum = sum;
+        a.stat_pitch = rows;
+        a.tokens = tokens;
+        a.vocab = vocab;
+        a.dim = (int)(q.pack_h && q.pack_w ? q.dim8 : p.dim);
+        a.cap = p.softcap;
+        a.inv_cap = inv_cap;
+        a.tiles_v = (vocab + kHeadTile - 1) / kHeadTile;
+        a.tiles_t = (tokens + kHeadTile - 1) / kHeadTile;
+        HEAD_TRY(q.small ? "head_logits_small" : "head_logits", launch_head_logits(a, p.dtype, q.small, s));
+        HeadRows r;
+        memset(&r, 0, sizeof(r));
+        r.ref = ref;
+        r.sum = sum;
+        r.stat_pitch = rows;
+        r.nsub = q.nsub;
+        r.h = hp;
+        r.w = w;
+        r.h_pitch = h_pitch;
+        r.w_pitch = w_pitch;
+        r.targets = p.targets + at;
+        r.weights = p.token_weights ? p.token_weights + at : nullptr;
+        r.scalars = scalars;
+        r.nll = p.nll + at;
+        r.lse = p.lse ? p.lse + at : nullptr;
+        r.row_weight = q.train ? row_weight + at : nullptr;
+        r.row_target = q.train ? row_target + at : nullptr;
+        r.ignore_index = p.ignore_index;
+        r.tokens = tokens;
+        r.rows = q.train ? rows : tokens;
+        r.vocab = vocab;
+        r.dim = a.dim;
+        r.cap = p.softcap;
+        r.inv_cap = inv_cap;
+        r.train = q.train;
+        HEAD_TRY("head_rows", launch_head_rows(r, p.dtype, s));
+        if (q.e < 0) continue;
+        const HeadProb b = {ws + q.e, q.cols, rows, (int)q.cols, ref, sum, rows, q.sub, row_weight + at, row_target + at, inv_cap};
+        HEAD_TRY("head_prob", launch_head_prob(b, p.dtype, s));
+        HeadGrad g;
+        memset(&g, 0, sizeof(g));
+        g.p = ws + q.e;
+        g.p_pitch = q.cols;
+        g.p_rows = rows;
+        g.p_cols = (int)q.cols;
+        g.dim = dim;
+        g.tiles_d = tiles_d;
+        g.scalars = scalars;
+        if (p.grad_hidden) {
+            uint8_t* out = static_cast<uint8_t*>(p.grad_hidden) + at * p.grad_hidden_stride * 2;
+            g.a = w;
+            g.a_pitch = w_pitch;
+            g.a_rows = vocab;
+            g.cols = tokens;
+            g.k = (int)q.cols;
+            g.splits = q.splits_h;
+            g.stages_per_split = q.stages_h;
+            g.tiles_c = (tokens + kHeadTile - 1) / kHeadTile;
+            g.out = out;
+            g.out_pitch = p.grad_hidden_stride;
+            g.out_vec = vec(out, p.grad_hidden_stride);
+            g.partial = q.partial_h ? reinterpret_cast<float*>(ws + q.part_h) : nullptr;
+            g.partial_pitch = q.dim8;
+            HEAD_TRY("head_grad_hidden", launch_head_grad(g, p.dtype, false, s));
+            if (q.partial_h) {
+                const HeadJoin j = {g.partial, q.dim8, q.splits_h, tokens, dim, out, p.grad_hidden_stride, scalars};
+                HEAD_TRY("head_join", launch_head_join(j, p.dtype, s));
+            }
+        }
+        if (p.grad_weight) {
+            g.a = hp;
+            g.a_pitch = h_pitch;
+            g.a_rows = rows;
+            g.cols = vocab;
+            g.k = rows;
+            g.splits = q.splits_w;
+            g.stages_per_split = q.stages_w;
+            g.tiles_c = (vocab + kHeadTile - 1) / kHeadTile;
+            g.out = p.grad_weight;
+            g.out_pitch = p.grad_weight_stride;
+            g.out_vec = vec(p.grad_weight, p.grad_weight_stride);
+            g.partial = q.partial_w ? reinterpret_cast<float*>(ws + q.part_w) : nullptr;
+            g.partial_pitch = q.dim8;
+            g.accumulate = at > 0;
+            HEAD_TRY("head_grad_weight", launch_head_grad(g, p.dtype, true, s));
+        }
+    }
+    if (p.grad_weight && (q.partial_w || p.tokens == 0)) {
+        // no tokens: no splits to add, the gradient is zero
+        const HeadJoin j = {q.part_w >= 0 ? reinterpret_cast<const float*>(ws + q.part_w) : nullptr, q.dim8,
+                            p.tokens ? q.splits_w : 0, vocab, dim, p.grad_weight, p.grad_weight_stride, scalars};
+        HEAD_TRY("head_join", launch_head_join(j, p.dtype, s));
+    }
+    if (p.loss) {
+        const HeadLoss a = {p.nll, row_weight, scalars, p.loss, p.tokens};
+        HEAD_TRY("head_loss", launch_head_loss(a, s));
+    }
+    return MUON_OK;
+}
+
+}  // namespace
+}  // namespace muon
+
+using namespace muon;
+
+extern "C" {
+
+size_t head_loss_workspace_size(const head_loss_t* problem) {
+    if (validate_sizes(problem) != MUON_OK) return 0;
+    return (size_t)make_head_plan(*problem).bytes;
+}
+
+int head_loss(const head_loss_t* problem, void* workspace, size_t workspace_bytes, void* stream) {
+    int rc = validate_sizes(problem);
+    if (rc) return rc;
+    const head_loss_t& p = *problem;
+    const HeadPlan q = make_head_plan(p);
+    if (!workspace || workspace_bytes < (size_t)q.bytes)
+        return fail(MUON_ERR_WORKSPACE, "workspace of %zu bytes given, %lld needed", workspace ? workspace_bytes : (size_t)0,
+                    (long long)q.bytes);
+    if ((rc = validate_buffers(p, workspace, (size_t)q.bytes))) return rc;
+    return enqueue_head(p, q, static_cast<uint8_t*>(workspace), static_cast<hipStream_t>(stream));
+}
+
+}  // extern "C"

@@ -3,10 +3,10 @@
 from __future__ import annotations
 
 import ctypes
-from typing import Optional
+from typing import NamedTuple, Optional
 
 from . import _lib
-from .api import _stream_handle, _torch
+from .api import _stream_handle, _torch, _workspace_for
 
 
 def _check(t, name: str, dtypes, numel: Optional[int] = None):
@@ -162,3 +162,126 @@ def adamw8_step(params, grads, states, *, lr: float, betas=(0.9, 0.999), eps: fl
     PreparedAdamW8(params, grads, states, emas=emas, copies=copies)(
         lr=lr, betas=betas, eps=eps, weight_decay=weight_decay, step=step, seed=seed, ema_decay=ema_decay,
         stream=stream)
+
+
+# ------------------------------------------------------------- loss of the language-model head
+
+class LinearCrossEntropy(NamedTuple):
+    """What the head's loss returns: per-token nll and lse; with gradients also the loss and both gradients."""
+    nll: object
+    lse: object
+    loss: object = None
+    grad_hidden: object = None
+    grad_weight: object = None
+
+
+def _check_rows(t, name: str, dtype=None, shape=None):
+    """A 2-D HIP tensor of a 16-bit float type with contiguous rows."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in (torch.bfloat16, torch.float16) or (dtype is not None and t.dtype != dtype):
+        raise TypeError(f"{name} must be {dtype if dtype is not None else 'bfloat16 or float16'}, got {t.dtype}")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be on a HIP device, got {t.device}")
+    if t.dim() != 2 or (shape is not None and tuple(t.shape) != tuple(shape)):
+        raise ValueError(f"{name} must be 2-D{f' of shape {tuple(shape)}' if shape is not None else ''}, got {tuple(t.shape)}")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows, strides {t.stride()}")
+    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+        raise ValueError(f"{name}'s rows overlap, strides {t.stride()}")
+
+
+class PreparedLinearCrossEntropy:
+    """The head's loss with the tensors marshalled once (same tensors and result buffers every call).
+
+    hidden [tokens, dim] and weight [vocab, dim] (bfloat16 or float16, rows may be strided), targets [tokens] int64.
+    grads: compute the loss and the gradients, not only nll and lse (grad_hidden=False or grad_weight=False leaves
+    that one out; a tensor given there receives it).  token_weights: float32 [tokens], or None for the mean over the
+    tokens whose target is not ignore_index.  softcap: logits are softcap * tanh(z / softcap), 0 for none.
+    Each call returns the same LinearCrossEntropy of result tensors, overwritten.
+    """
+
+    def __init__(self, hidden, weight, targets, *, token_weights=None, ignore_index: int = -100, softcap: float = 0.0,
+                 grads: bool = False, grad_hidden=None, grad_weight=None, workspace=None, stream=None):
+        torch = _torch()
+        _check_rows(hidden, "hidden")
+        _check_rows(weight, "weight", hidden.dtype)
+        tokens, dim = hidden.shape
+        vocab = weight.shape[0]
+        if weight.shape[1] != dim:
+            raise ValueError(f"weight has {weight.shape[1]} columns, hidden {dim}")
+        _check(targets, "targets", (torch.int64,), tokens)
+        if token_weights is not None:
+            _check(token_weights, "token_weights", (torch.float32,), tokens)
+        if not grads and (token_weights is not None or grad_hidden is not None or grad_weight is not None):
+            raise ValueError("token_weights, grad_hidden and grad_weight are for grads=True")
+        device = _same_device((hidden, weight, targets, token_weights), "linear_cross_entropy")
+        s = stream if stream is not None else torch.cuda.current_stream(device)
+        with torch.cuda.stream(s):
+            nll, lse = (torch.empty(tokens, dtype=torch.float32, device=device) for _ in "nl")
+            loss = torch.empty((), dtype=torch.float32, device=device) if grads else None
+            if grads and grad_hidden is None:
+                grad_hidden = torch.empty(tokens, dim, dtype=hidden.dtype, device=device)
+            if grads and grad_weight is None:
+                grad_weight = torch.empty(vocab, dim, dtype=hidden.dtype, device=device)
+        grad_hidden = grad_hidden if grad_hidden is not False else None
+        grad_weight = grad_weight if grad_weight is not False else None
+        if grad_hidden is not None:
+            _check_rows(grad_hidden, "grad_hidden", hidden.dtype, (tokens, dim))
+        if grad_weight is not None:
+            _check_rows(grad_weight, "grad_weight", hidden.dtype, (vocab, dim))
+        _same_device((hidden, grad_hidden, grad_weight), "linear_cross_entropy")
+        self.result = LinearCrossEntropy(nll, lse, loss, grad_hidden, grad_weight)
+        self._keep = (hidden, weight, targets, token_weights)
+        ptr = lambda t: t.data_ptr() if t is not None else 0  # noqa: E731
+        pitch = lambda t: max(t.stride(0), dim) if t is not None else dim  # noqa: E731
+        self.problem = _lib.HeadLoss(
+            ptr(hidden), ptr(weight), ptr(targets), ptr(token_weights), ptr(loss), ptr(nll), ptr(lse), ptr(grad_hidden),
+            ptr(grad_weight), tokens, vocab, dim, pitch(hidden), pitch(weight), pitch(grad_hidden), pitch(grad_weight),
+            int(ignore_index), float(softcap),
+            _lib.MUON_HEAD_BF16 if hidden.dtype == torch.bfloat16 else _lib.MUON_HEAD_FP16)
+        self._lib = _lib.load()
+        need = self._lib.head_loss_workspace_size(self.problem)
+        if need == 0:
+            raise _lib.MuonError(_lib.MUON_ERR_INVALID_ARG, self._lib.muon_last_error().decode())
+        if workspace is None:
+            # allocated on the stream the calls run on, so that its memory is reused only in that stream's order
+            with torch.cuda.stream(s):
+                workspace = torch.empty(int(need), dtype=torch.uint8, device=device)
+        self.workspace = workspace
+        self._ws = (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+        self.device = device
+
+    def __call__(self, stream=None) -> LinearCrossEntropy:
+        _lib.check(self._lib.head_loss(self.problem, *self._ws, _stream_handle(stream, self.device)))
+        return self.result
+
+
+def _one_call(hidden, weight, targets, workspace, stream, **kw):
+    """A prepared loss run once on the stream's cached workspace."""
+    torch = _torch()
+    if workspace is None and isinstance(hidden, torch.Tensor) and hidden.device.type == "cuda":
+        s = stream if stream is not None else torch.cuda.current_stream(hidden.device)
+        probe = PreparedLinearCrossEntropy(hidden, weight, targets, workspace=torch.empty(0, dtype=torch.uint8,
+                                           device=hidden.device), stream=s, **kw)
+        need = int(probe._lib.head_loss_workspace_size(probe.problem))
+        ws = _workspace_for(need, hidden.device, s)
+        probe.workspace, probe._ws = ws, (ws.data_ptr(), ws.numel())
+        return probe(stream=s)
+    return PreparedLinearCrossEntropy(hidden, weight, targets, workspace=workspace, stream=stream, **kw)(stream=stream)
+
+
+def linear_cross_entropy(hidden, weight, targets, *, ignore_index: int = -100, softcap: float = 0.0, workspace=None,
+                         stream=None) -> LinearCrossEntropy:
+    """Scores tokens: nll and log-sum-exp of each under softmax(hidden @ weight.T), float32, without the logits."""
+    return _one_call(hidden, weight, targets, workspace, stream, ignore_index=ignore_index, softcap=softcap)
+
+
+def linear_cross_entropy_grad(hidden, weight, targets, *, token_weights=None, ignore_index: int = -100,
+                              softcap: float = 0.0, grad_hidden=None, grad_weight=None, workspace=None,
+                              stream=None) -> LinearCrossEntropy:
+    """The loss of a training step with the gradients of hidden and weight (see PreparedLinearCrossEntropy)."""
+    return _one_call(hidden, weight, targets, workspace, stream, token_weights=token_weights,
+                     ignore_index=ignore_index, softcap=softcap, grads=True, grad_hidden=grad_hidden,
+                     grad_weight=grad_weight)
