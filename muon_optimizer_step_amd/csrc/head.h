@@ -8,12 +8,23 @@ namespace muon {
 
 enum HeadType { kHeadBf16 = 0, kHeadFp16 = 1 };
 
-constexpr int kHeadK = 64;         // K elements per LDS stage: 128 bytes of a row
+constexpr int kHeadK = 64;         // K elements per LDS stage
 constexpr int kHeadPad = 64;       // rows and columns of the probability piece are padded to it
 constexpr int kHeadTile = 256;     // output tile edge of the products
 constexpr int kHeadSmall = 64;     // tokens up to which the vocabulary is streamed past all of them at once
 constexpr int kHeadSub = 128;      // vocabulary entries per partial maximum and sum, tiled kernel
 constexpr int kHeadSmallSub = 32;  // the same, streaming kernel
+
+// What the weights in P and the sums over P are scaled by, over all tokens of
+// the call; computed by one more workgroup of the first head_logits launch.
+struct HeadScalars {
+    const int64_t* targets;
+    const float* weights;    // nullable
+    float* scalars;          // NULL: nothing to do in this launch
+    int64_t ignore_index;
+    int tokens;
+    int type;
+};
 
 // Logits of a piece of the tokens against the whole vocabulary, reduced to a
 // reference exponent and a sum per token and `sub` vocabulary entries, and (e
@@ -31,6 +42,7 @@ struct HeadLogits {
     int tokens, vocab, dim;
     float cap, inv_cap;      // 0: no cap
     int tiles_v, tiles_t;
+    HeadScalars scalars;
 };
 
 // Per token: log-sum-exp, loss, and the factors of the gradient.
@@ -43,15 +55,27 @@ struct HeadRows {
     int64_t h_pitch, w_pitch;
     const int64_t* targets;
     const float* weights;    // nullable
-    const float* scalars;    // [0] mean weight, [1] probability scale, [2] its inverse
+    const float* scalars;    // [0] what weights are multiplied by in P, [1] what sums over P are multiplied by
     float* nll;
     float* lse;              // nullable
-    float* row_weight;       // train: weight of the token (times the probability scale)
+    float* row_weight;       // train: weight of the token in P
     int* row_target;         // train: its target, -1 for none
+    void* copy;              // nullable: rows x copy_pitch, hidden with zeros for tokens that do not count
+    int64_t copy_pitch;
     int64_t ignore_index;
     int tokens, rows, vocab, dim;   // rows: tokens padded
     float cap, inv_cap;
     int train;
+};
+
+// sum of weight x nll over all tokens of the call; by one more workgroup of the
+// last head_prob launch, or on its own.
+struct HeadLoss {
+    const float* nll;
+    const float* row_weight;
+    const float* scalars;
+    float* loss;             // NULL: nothing to do in this launch
+    int tokens;
 };
 
 struct HeadProb {
@@ -64,6 +88,7 @@ struct HeadProb {
     const float* row_weight;
     const int* row_target;
     float inv_cap;           // 0: no cap
+    HeadLoss loss;
 };
 
 // out[col][d] = sum over k of P(k, col) A[k][d].
@@ -85,13 +110,22 @@ struct HeadGrad {
     int accumulate;          // add to what partial holds
     const float* scalars;
 };
+// Both gradients of a piece; one without an output has tiles_c == 0.
+struct HeadGrads {
+    HeadGrad hidden, weight;
+};
 
+// out[col][d] = sum over the splits' partials, for up to two gradients.
 struct HeadJoin {
-    const float* partial;
-    int64_t partial_pitch;
-    int splits, cols, dim;
-    void* out;
-    int64_t out_pitch;
+    struct Part {
+        const float* partial;
+        int64_t partial_pitch;
+        int splits, cols;    // cols == 0: nothing to do
+        void* out;
+        int64_t out_pitch;
+        int out_vec;
+    } part[2];
+    int dim;
     const float* scalars;
 };
 
@@ -105,30 +139,12 @@ struct HeadPack {
     int64_t ignore_index;
 };
 
-struct HeadScalars {
-    const int64_t* targets;
-    const float* weights;
-    float* scalars;
-    int64_t ignore_index;
-    int64_t tokens;
-    int type;
-};
-
-struct HeadLoss {
-    const float* nll;
-    const float* row_weight;
-    const float* scalars;
-    float* loss;
-    int64_t tokens;
-};
-
 hipError_t launch_head_logits(const HeadLogits& a, int type, bool small, hipStream_t s);
 hipError_t launch_head_rows(const HeadRows& a, int type, hipStream_t s);
 hipError_t launch_head_prob(const HeadProb& a, int type, hipStream_t s);
-hipError_t launch_head_grad(const HeadGrad& a, int type, bool k_is_token, hipStream_t s);
+hipError_t launch_head_grads(const HeadGrads& a, int type, hipStream_t s);
 hipError_t launch_head_join(const HeadJoin& a, int type, hipStream_t s);
 hipError_t launch_head_pack(const HeadPack& a, hipStream_t s);
-hipError_t launch_head_scalars(const HeadScalars& a, hipStream_t s);
 hipError_t launch_head_loss(const HeadLoss& a, hipStream_t s);
 
 }  // namespace muon

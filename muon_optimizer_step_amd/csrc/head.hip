@@ -60,8 +60,12 @@ template <> __device__ inline void unpack8<f16>(const u32x4& w, float* v) {
     for (int k = 0; k < 8; ++k) v[k] = (float)h[k];
 }
 
-template <int N> __device__ inline void wait_loads() { asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory"); }
-__device__ inline void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+// Waits as builtins, which the compiler's own count of outstanding LDS reads
+// takes into account (an opaque wait would be followed by another).
+template <int N> __device__ inline void wait_loads() {
+    __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | (15 << 8) | ((N >> 4) << 14));
+}
+__device__ inline void wait_lds() { __builtin_amdgcn_s_waitcnt(15 | (7 << 4) | (0 << 8) | (3 << 14)); }
 __device__ inline void bare_barrier() {
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_barrier();
@@ -71,54 +75,57 @@ __device__ inline void bare_barrier() {
 // cap tanh(z / cap); exact to a few ulp of cap, which is the scale that counts.
 __device__ inline float capped(float z, float cap, float inv_cap) {
     const float t = __builtin_amdgcn_exp2f(z * inv_cap * (2.0f * kLog2e));
-    return cap - 2.0f * cap / (t + 1.0f);
+    return fmaf(-2.0f * cap, __builtin_amdgcn_rcpf(t + 1.0f), cap);
 }
 
-// 16 bytes per lane straight into LDS, at dst + 16 x lane (dst the wave's).
-__device__ inline void direct_load(const uint8_t* src, uint8_t* dst) {
-    __builtin_amdgcn_global_load_lds(src, (lds_ptr)dst, 16, 0, 0);
+// 16 bytes per lane, from base + off, straight into LDS at address dst + 16 x
+// lane (base and dst the wave's).  As assembly because the compiler makes every
+// transposing LDS read wait for all direct loads that it knows of, those of
+// later stages too; there is no result register, and the K loop waits for its
+// loads itself.
+__device__ inline void direct_load(const uint8_t* base, uint32_t off, uint32_t dst) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(dst), "v"(off), "s"(base)
+                 : "memory");
 }
+__device__ inline uint32_t lds_address(const uint8_t* p) { return (uint32_t)(uintptr_t)(lds_ptr)p; }
 
 // ---------------------------------------------------------------- operand staging
-// A row operand (K contiguous): ROWS rows x 128 bytes of K per stage, the
-// 16-byte chunk c of row r in slot c ^ ((r / 2) % 8), which keeps the 16-byte
-// fragment reads of 32 rows free of bank conflicts.  Direct loads: one wave
-// instruction fills 8 rows.
-template <int ROWS, int WAVES>
+// A stage is 64 K of both operands of a 256 x 256 tile, 32 KB each.
+//
+// A row operand (K contiguous): 256 rows x 128 bytes of K per stage (a whole
+// cache line: 64-byte pieces cost the vector L1 twice the fills), the 16-byte
+// chunk c of row r in slot c ^ ((r / 2) % 8), which keeps the 16-byte fragment
+// reads of 32 rows free of bank conflicts.  Direct loads: one wave instruction
+// fills 8 rows.
+constexpr int kOperand = kHeadTile * kHeadK * 2;     // bytes of one operand of a stage
+template <int WAVES>
 struct RowOperand {
-    static constexpr int kBytes = ROWS * 128;
-    static constexpr int kLoads = ROWS / 8 / WAVES;
-    static_assert(ROWS % (8 * WAVES) == 0, "whole instructions per wave");
+    static constexpr int kLoads = kHeadTile / 8 / WAVES;
+    static_assert(kHeadTile % (8 * WAVES) == 0 && WAVES % 2 == 0, "whole instructions per wave");
     const uint8_t* base;
     uint32_t off[kLoads];
     int chunk;      // source chunk of this lane within a stage
 
-    // rows row0 .. row0 + ROWS of a matrix with `rows` rows; rows beyond its end repeat the last one
+    // rows row0 .. row0 + 255 of a matrix with `rows` rows; rows beyond its end repeat the last one
     __device__ inline void init(const void* m, int64_t pitch_bytes, int64_t row0, int64_t rows, int wave, int lane) {
         base = static_cast<const uint8_t*>(m) + row0 * pitch_bytes;
-        const int last = (int)min<int64_t>(rows - 1 - row0, ROWS - 1);
+        const int last = (int)min<int64_t>(rows - 1 - row0, kHeadTile - 1);
         chunk = 0;
 #pragma unroll
         for (int j = 0; j < kLoads; ++j) {
             const int r = 8 * (j * WAVES + wave) + lane / 8;
-            chunk = (lane % 8) ^ ((r >> 1) & 7);
+            chunk = (lane % 8) ^ ((r >> 1) & 7);      // the same for every j
             off[j] = (uint32_t)(min(r, last) * pitch_bytes) + chunk * 16;
-            static_assert(WAVES % 2 == 0, "the chunk is the same for every j");
         }
     }
-    __device__ inline void load(uint8_t* lds, int64_t kbyte, int wave) const {
-#pragma unroll
-        for (int j = 0; j < kLoads; ++j)
-            direct_load(base + kbyte + off[j], lds + (j * WAVES + wave) * 1024);
+    __device__ inline void load(uint32_t lds, int j, int64_t kbyte, int wave) const {
+        direct_load(base + kbyte, off[j], lds + (j * WAVES + wave) * 1024);
     }
     // the last stage where K ends inside it: `chunks` of 8, zeros behind them
-    __device__ inline void load_tail(uint8_t* lds, int64_t kbyte, int chunks, int wave, int lane) const {
-#pragma unroll
-        for (int j = 0; j < kLoads; ++j) {
-            u32x4 v = {0u, 0u, 0u, 0u};
-            if (chunk < chunks) v = *reinterpret_cast<const u32x4*>(base + kbyte + off[j]);
-            *reinterpret_cast<u32x4*>(lds + (j * WAVES + wave) * 1024 + lane * 16) = v;
-        }
+    __device__ inline void load_tail(uint8_t* lds, int j, int64_t kbyte, int chunks, int wave, int lane) const {
+        u32x4 v = {0u, 0u, 0u, 0u};
+        if (chunk < chunks) v = *reinterpret_cast<const u32x4*>(base + kbyte + off[j]);
+        *reinterpret_cast<u32x4*>(lds + (j * WAVES + wave) * 1024 + lane * 16) = v;
     }
     // fragment of 32 rows from `row`: lane l holds row perm(l % 32), K 16 kc + 8 (l / 32) .. + 7
     static __device__ inline u32x4 frag(const uint8_t* lds, int row, int kc, int lane) {
@@ -138,11 +145,11 @@ __device__ inline int swap23(int r) { return (r & 0x13) | ((r & 4) << 1) | ((r &
 // read, and the 4 rows x 64 bytes of 32 lanes, lie in different banks.
 template <int WAVES>
 struct ColOperand {
-    static constexpr int kBytes = kHeadK * 512;
     static constexpr int kLoads = kHeadK / 2 / WAVES;
     const uint8_t* base;
     int64_t pitch;
     uint32_t off[kLoads];
+    int chunk[kLoads], row[kLoads];
     static __device__ inline int slot_xor(int k) { return 2 * ((0x7520 >> (4 * (k & 3))) & 7); }
     // columns col0 .. of a matrix with cols_pad columns (a multiple of 8); chunks beyond repeat the last
     __device__ inline void init(const void* m, int64_t pitch_bytes, int col0, int cols_pad, int wave, int lane) {
@@ -151,16 +158,20 @@ struct ColOperand {
         const int last = (cols_pad - col0) / 8 - 1;
 #pragma unroll
         for (int j = 0; j < kLoads; ++j) {
-            const int r = 2 * (j * WAVES + wave) + lane / 32;
-            off[j] = (uint32_t)(min((lane % 32) ^ slot_xor(r), last) * 16);
+            row[j] = 2 * (j * WAVES + wave) + lane / 32;
+            chunk[j] = min((lane % 32) ^ slot_xor(row[j]), last) * 16;
+            off[j] = (uint32_t)(row[j] * pitch) + chunk[j];
         }
     }
     // K rows k0 .. k0 + 63 of `rows` rows; rows beyond repeat the last
-    __device__ inline void load(uint8_t* lds, int64_t k0, int64_t rows, int wave, int lane) const {
-#pragma unroll
-        for (int j = 0; j < kLoads; ++j) {
-            const int64_t r = min(k0 + 2 * (j * WAVES + wave) + lane / 32, rows - 1);
-            direct_load(base + r * pitch + off[j], lds + (j * WAVES + wave) * 1024);
+    __device__ inline void load(uint32_t lds, int j, int64_t k0, int64_t rows, int wave) const {
+        const uint32_t at = lds + (j * WAVES + wave) * 1024;
+        if (k0 + kHeadK <= rows) {
+            direct_load(base + k0 * pitch, off[j], at);
+        } else {
+            const int64_t first = min(k0, rows - 1);
+            const int last = (int)(rows - 1 - first);
+            direct_load(base + first * pitch, (uint32_t)(min(row[j], last) * pitch) + chunk[j], at);
         }
     }
     // fragment of 32 columns from `col`: lane l holds column (perm of) l % 32, K 16 kc + 8 (l / 32) .. + 7.
@@ -181,6 +192,82 @@ struct ColOperand {
     }
 };
 
+// ---------------------------------------------------------------- K loop
+// acc += A B over `stages` stages of 64 K; the first `whole` stages consist of
+// direct loads only.  load_a(kt, slot, u), load_b issue load u of 4 of this
+// wave for stage kt; a(slot, i, kc), b(slot, j, kc) read fragments of 16 K.
+//
+// LDS is a ring of five operand slots (all 160 KB): A of stage k is in slot
+// 2 k mod 5, B in 2 k + 1 mod 5.  The barrier at the end of stage k - 1 sits before
+// the MFMAs of its last 16 K, whose fragments are in registers by then.  It
+// frees that stage's two slots, which the loads of B of stage k + 1 and A of
+// stage k + 2 fill, one load after every four MFMAs so that their issue does
+// not hold the MFMAs up; and it publishes stage k, whose first fragments
+// are read while the last MFMAs run.  At its end only B of stage k + 1, issued
+// in the first half of the window, has to have arrived; A of k + 2 may be under way.
+constexpr int kSlots = 5;
+constexpr size_t kRingBytes = (size_t)kSlots * kOperand;
+template <typename T, int TA, int TB, typename LoadA, typename LoadB, typename FragA, typename FragB>
+__device__ inline void k_loop(floatx16 (&acc)[TA][TB], int stages, int whole, LoadA load_a, LoadB load_b, FragA a, FragB b) {
+    static_assert(kHeadK == 64, "four steps of 16 K per stage");
+    u32x4 fa[2][TA], fb[2][TB];
+    auto slot = [](int n) { return n >= kSlots ? n - kSlots : n; };
+    auto read = [&](int set, int slot_a, int slot_b, int kc) {
+#pragma unroll
+        for (int i = 0; i < TA; ++i) fa[set][i] = a(slot_a, i, kc);
+#pragma unroll
+        for (int j = 0; j < TB; ++j) fb[set][j] = b(slot_b, j, kc);
+    };
+    // the MFMAs of one step with two loads between them
+    auto multiply = [&](int set, auto load) {
+#pragma unroll
+        for (int n = 0; n < TA * TB; ++n) {
+            acc[n / TB][n % TB] = mfma<T>(fa[set][n / TB], fb[set][n % TB], acc[n / TB][n % TB]);
+            if (n == TA * TB / 4 || n == TA * TB * 3 / 4) {
+                __builtin_amdgcn_sched_barrier(0);
+                load(n == TA * TB / 4 ? 0 : 1);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+    };
+    if (stages <= 0) return;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) load_a(0, 0, u);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) load_b(0, 1, u);
+    if (stages > 1)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) load_a(1, 2, u);
+    if (whole > 1) wait_loads<4>();
+    else wait_loads<0>();
+    wait_lds();
+    bare_barrier();
+    read(0, 0, 1, 0);
+    if (stages > 1) {
+        load_b(1, 3, 0);
+        load_b(1, 3, 1);
+    }
+    int at = 0;      // slot of A of stage kt
+    for (int kt = 0; kt < stages; ++kt) {
+        const int sa = at, sb = slot(at + 1), sa1 = slot(at + 2), sb1 = slot(at + 3), sa2 = slot(at + 4);
+        read(1, sa, sb, 1);
+        multiply(0, [&](int u) { if (kt + 1 < stages) load_b(kt + 1, sb1, 2 + u); });
+        read(0, sa, sb, 2);
+        multiply(1, [&](int u) { if (kt + 2 < stages) load_a(kt + 2, sa2, u); });
+        read(1, sa, sb, 3);
+        multiply(0, [&](int u) { if (kt + 2 < stages) load_a(kt + 2, sa2, 2 + u); });
+        wait_lds();              // this wave's last fragments of stage kt, or its part of a tail
+        if (kt + 1 < stages) {
+            if (kt + 2 < whole) wait_loads<4>();
+            else wait_loads<0>();
+            bare_barrier();
+            read(0, sa1, sb1, 0);
+        }
+        multiply(1, [&](int u) { if (kt + 2 < stages) load_b(kt + 2, sa, u); });    // slot 2 (k + 2) + 1 = 2 k mod 5
+        at = sa1;
+    }
+}
+
 // Work item of this workgroup: workgroups go round-robin over the XCDs, and
 // each XCD takes a contiguous range of items, whose operands its L2 shares.
 __device__ inline int xcd_item(int items) {
@@ -190,6 +277,46 @@ __device__ inline int xcd_item(int items) {
     return at < per && i < items ? i : -1;
 }
 inline int xcd_grid(int items) { return (items + kXcds - 1) / kXcds * kXcds; }
+
+// What a token's weight is multiplied by in P, and what the sums over P are
+// multiplied by.  The mean's weight 1 / count comes in only after the sums, in
+// fp32: in P its own rounding to 16 bits would be one error common to all
+// tokens.  fp16 probabilities are scaled by a power of two (the largest weight
+// becomes 2^13 .. 2^14, so a probability of 1e-9 is still a normal number; bf16
+// has fp32's range).
+template <int THREADS>
+__device__ inline void head_scalars(const HeadScalars& a, void* lds) {
+    constexpr int kWaves = THREADS / kWave;
+    int* count = static_cast<int*>(lds);
+    float* top = static_cast<float*>(lds) + kWaves;
+    int n = 0;
+    float m = 0.f;
+    for (int i = threadIdx.x; i < a.tokens; i += THREADS) {
+        const bool counted = a.targets[i] != a.ignore_index;
+        n += counted;
+        if (a.weights && counted) m = fmaxf(m, fabsf(a.weights[i]));
+    }
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) {
+        n += __shfl_xor(n, off, kWave);
+        m = fmaxf(m, __shfl_xor(m, off, kWave));
+    }
+    if (threadIdx.x % kWave == 0) {
+        count[threadIdx.x / kWave] = n;
+        top[threadIdx.x / kWave] = m;
+    }
+    __syncthreads();
+    if (threadIdx.x != 0) return;
+    for (int w = 1; w < kWaves; ++w) {
+        n += count[w];
+        m = fmaxf(m, top[w]);
+    }
+    if (!a.weights) m = 1.f;
+    float scale = 1.f;
+    if (a.type == kHeadFp16 && m > 1e-30f && m < 1e30f) scale = ldexpf(1.0f, 14 - __builtin_amdgcn_frexp_expf(m));
+    a.scalars[0] = scale;
+    a.scalars[1] = (a.weights ? 1.0f : 1.0f / (float)max(n, 1)) / scale;
+}
 
 // ---------------------------------------------------------------- logits
 // What one wave does with its logits: acc[tv][tt] holds 32 vocabulary entries
@@ -201,6 +328,8 @@ __device__ inline void logits_epilogue(const HeadLogits& a, floatx16 (&acc)[TV][
 #pragma unroll
     for (int tt = 0; tt < TT; ++tt) {
         const int token = t0 + 32 * tt + lane % 32;
+        int end = a.vocab - v0 - 8 * half;
+        asm volatile("" : "+v"(end));     // compared with anew for each tt: the masks of all registers do not fit in scalars
         float top = -INFINITY;
 #pragma unroll
         for (int tv = 0; tv < TV; ++tv)
@@ -208,7 +337,7 @@ __device__ inline void logits_epilogue(const HeadLogits& a, floatx16 (&acc)[TV][
             for (int r = 0; r < 16; ++r) {
                 float z = acc[tv][tt][r];
                 if (CAP) z = capped(z, a.cap, a.inv_cap);
-                if (!whole && v0 + 32 * tv + 16 * (r / 8) + 8 * half + r % 8 >= a.vocab) z = -INFINITY;
+                if (!whole && 32 * tv + 16 * (r / 8) + r % 8 >= end) z = -INFINITY;
                 acc[tv][tt][r] = z;
                 top = fmaxf(top, z);
             }
@@ -242,12 +371,16 @@ __device__ inline void logits_epilogue(const HeadLogits& a, floatx16 (&acc)[TV][
 }
 
 // Tile of 256 vocabulary entries x 256 tokens: 8 waves of 128 x 64, 32x32x16
-// MFMAs, two LDS buffers of 64 K each filled by direct loads.
+// MFMAs.
 template <typename T, bool STORE, bool CAP>
 __global__ __launch_bounds__(512, 2) void head_logits_kernel(const HeadLogits a) {
     constexpr int WV = 2, WT = 4, TV = 4, TT = 2, BV = WV * TV * 32, BT = WT * TT * 32, NW = WV * WT;
     static_assert(TV * 32 == kHeadSub, "one partial per wave");
     extern __shared__ __align__(16) uint8_t lds[];
+    if (blockIdx.x == gridDim.x - 1) {
+        if (a.scalars.scalars) head_scalars<512>(a.scalars, lds);
+        return;
+    }
     const int item = xcd_item(a.tiles_v * a.tiles_t);
     if (item < 0) return;
     // token tiles in groups of 8, vocabulary tiles within: the tiles that an XCD
@@ -255,25 +388,17 @@ __global__ __launch_bounds__(512, 2) void head_logits_kernel(const HeadLogits a)
     const int group = item / (8 * a.tiles_v), in_group = item - group * 8 * a.tiles_v;
     const int width = min(8, a.tiles_t - 8 * group);
     const int tile_v = in_group / width, tile_t = 8 * group + in_group % width;
-    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave, wv = wave / WT, wt = wave % WT;
+    const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), wv = wave / WT, wt = wave % WT;
 
-    typedef RowOperand<BV, NW> WOp;
-    typedef RowOperand<BT, NW> HOp;
-    WOp W;
-    HOp H;
+    typedef RowOperand<NW> Op;
+    Op W, H;
     W.init(a.w, a.w_pitch * 2, (int64_t)tile_v * BV, a.vocab, wave, lane);
     H.init(a.h, a.h_pitch * 2, (int64_t)tile_t * BT, a.tokens, wave, lane);
-    constexpr int kStage = WOp::kBytes + HOp::kBytes;
     const int stages = (a.dim + kHeadK - 1) / kHeadK, whole = a.dim / kHeadK;
-    auto load = [&](int kt, int b) {
-        uint8_t* dst = lds + b * kStage;
-        if (kt < whole) {
-            W.load(dst, (int64_t)kt * 128, wave);
-            H.load(dst + WOp::kBytes, (int64_t)kt * 128, wave);
-        } else {
-            W.load_tail(dst, (int64_t)kt * 128, a.dim % kHeadK / 8, wave, lane);
-            H.load_tail(dst + WOp::kBytes, (int64_t)kt * 128, a.dim % kHeadK / 8, wave, lane);
-        }
+    auto load = [&](const Op& op, int kt, int slot, int u) {
+        const int64_t k = (int64_t)kt * kHeadK * 2;
+        if (kt < whole) op.load(lds_address(lds) + slot * kOperand, u, k, wave);
+        else op.load_tail(lds + slot * kOperand, u, k, a.dim % kHeadK / 8, wave, lane);
     };
     floatx16 acc[TV][TT];
 #pragma unroll
@@ -281,27 +406,11 @@ __global__ __launch_bounds__(512, 2) void head_logits_kernel(const HeadLogits a)
 #pragma unroll
         for (int j = 0; j < TT; ++j) acc[i][j] = floatx16(0.f);
     const int arow = wv * TV * 32 + swap23(lane % 32), brow = wt * TT * 32 + lane % 32;
-    load(0, 0);
-    for (int kt = 0; kt < stages; ++kt) {
-        wait_loads<0>();
-        wait_lds();
-        bare_barrier();      // stage kt is in LDS, and every wave is done with stage kt - 1
-        if (kt + 1 < stages) load(kt + 1, (kt + 1) & 1);
-        const uint8_t* tw = lds + (kt & 1) * kStage;
-        const uint8_t* th = tw + WOp::kBytes;
-#pragma unroll
-        for (int kc = 0; kc < kHeadK / 16; ++kc) {
-            u32x4 fa[TV], fb[TT];
-#pragma unroll
-            for (int i = 0; i < TV; ++i) fa[i] = WOp::frag(tw, arow + 32 * i, kc, lane);
-#pragma unroll
-            for (int j = 0; j < TT; ++j) fb[j] = HOp::frag(th, brow + 32 * j, kc, lane);
-#pragma unroll
-            for (int i = 0; i < TV; ++i)
-#pragma unroll
-                for (int j = 0; j < TT; ++j) acc[i][j] = mfma<T>(fa[i], fb[j], acc[i][j]);
-        }
-    }
+    k_loop<T, TV, TT>(
+        acc, stages, whole, [&](int kt, int slot, int u) { load(W, kt, slot, u); },
+        [&](int kt, int slot, int u) { load(H, kt, slot, u); },
+        [&](int slot, int i, int kc) { return Op::frag(lds + slot * kOperand, arow + 32 * i, kc, lane); },
+        [&](int slot, int j, int kc) { return Op::frag(lds + slot * kOperand, brow + 32 * j, kc, lane); });
     logits_epilogue<TV, TT, STORE, CAP>(a, acc, tile_v * BV + wv * TV * 32, tile_t * BT + wt * TT * 32, tile_v * WV + wv, lane);
 }
 
@@ -311,6 +420,10 @@ __global__ __launch_bounds__(512, 2) void head_logits_kernel(const HeadLogits a)
 template <typename T, int TT, bool STORE, bool CAP>
 __global__ __launch_bounds__(256) void head_logits_small_kernel(const HeadLogits a) {
     __shared__ __align__(16) float part[4][TT][16][kWave];
+    if (blockIdx.x == gridDim.x - 1) {
+        if (a.scalars.scalars) head_scalars<256>(a.scalars, part);
+        return;
+    }
     const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
     const int v0 = blockIdx.x * 32;
     const T* w = static_cast<const T*>(a.w) + (int64_t)min(v0 + swap23(lane % 32), a.vocab - 1) * a.w_pitch + 8 * (lane / 32);
@@ -401,8 +514,14 @@ __global__ __launch_bounds__(256) void head_rows_kernel(const HeadRows a) {
     }
     dot = all(dot, [](float x, float y) { return x + y; });
     if (a.cap > 0.f) dot = capped(dot, a.cap, a.inv_cap);
+    if (a.copy && held)
+        for (int d = 8 * s; d < a.dim; d += 8 * S) {
+            u32x4 v = {0u, 0u, 0u, 0u};
+            if (counted) v = *reinterpret_cast<const u32x4*>(static_cast<const T*>(a.h) + (int64_t)row * a.h_pitch + d);
+            *reinterpret_cast<u32x4*>(static_cast<T*>(a.copy) + (int64_t)row * a.copy_pitch + d) = v;
+        }
     float weight = 0.f;
-    if (counted) weight = valid ? (a.train ? (a.weights ? a.weights[row] : a.scalars[0]) * a.scalars[1] : 1.f) : __builtin_nanf("");
+    if (counted) weight = valid ? (a.train ? (a.weights ? a.weights[row] : 1.f) * a.scalars[0] : 1.f) : __builtin_nanf("");
     if (s == 0 && live) {
         const float lse = lse2 * kLn2;
         float nll = valid ? lse - dot : __builtin_nanf("");
@@ -421,10 +540,29 @@ __global__ __launch_bounds__(256) void head_rows_kernel(const HeadRows a) {
     }
 }
 
+// sum of weight x nll, in an order that depends on nothing but THREADS.
+template <int THREADS>
+__device__ inline void head_loss_sum(const HeadLoss& a) {
+    __shared__ float red[THREADS / kWave];
+    float sum = 0.f;
+#pragma unroll 4
+    for (int i = threadIdx.x; i < a.tokens; i += THREADS) sum = fmaf(a.row_weight[i], a.nll[i], sum);
+    sum = wave_sum(sum);
+    if (threadIdx.x % kWave == 0) red[threadIdx.x / kWave] = sum;
+    __syncthreads();
+    if (threadIdx.x != 0) return;
+    for (int w = 1; w < THREADS / kWave; ++w) sum += red[w];
+    *a.loss = sum * a.scalars[1];
+}
+
 // ---------------------------------------------------------------- probabilities
 // 8 rows x 2048 columns of the piece per workgroup, 8 columns of a row per thread.
 template <typename T, bool CAP>
 __global__ __launch_bounds__(256) void head_prob_kernel(const HeadProb a) {
+    if (blockIdx.x == gridDim.x - 1) {
+        if (a.loss.loss) head_loss_sum<256>(a.loss);
+        return;
+    }
     const int across = (a.cols + 2047) / 2048, row0 = blockIdx.x / across * 8;
     const int col = (blockIdx.x % across * 256 + threadIdx.x) * 8;
     if (col >= a.cols) return;
@@ -460,62 +598,45 @@ __global__ __launch_bounds__(256) void head_prob_kernel(const HeadProb a) {
 // tiles alone would leave compute units idle.  A = W or H with K strided; P with K
 // contiguous (dH, K the vocabulary) or strided (dW, K the tokens).
 template <typename T, bool KTOKEN>
-__global__ __launch_bounds__(512, 2) void head_grad_kernel(const HeadGrad a) {
+__device__ inline void head_grad_tile(const HeadGrad& a, int item, uint8_t* lds) {
     constexpr int WD = 2, WC = 4, TD = 4, TC = 2, NW = WD * WC;
-    extern __shared__ __align__(16) uint8_t lds[];
-    const int item = xcd_item(a.tiles_c * a.tiles_d * a.splits);
-    if (item < 0) return;
     const int split = item / (a.tiles_c * a.tiles_d), tile = item - split * a.tiles_c * a.tiles_d;
     const int tile_c = tile / a.tiles_d, tile_d = tile % a.tiles_d;
-    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave, wd = wave / WC, wc = wave % WC;
+    const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), wd = wave / WC, wc = wave % WC;
     const int d0 = tile_d * kHeadTile, c0 = tile_c * kHeadTile;
     const int s0 = split * a.stages_per_split, s1 = min(a.k / kHeadK, s0 + a.stages_per_split);
 
     typedef ColOperand<NW> COp;
-    typedef RowOperand<kHeadTile, NW> ROp;
+    typedef RowOperand<NW> ROp;
     COp A, Q;
     ROp P;
     A.init(a.a, a.a_pitch * 2, d0, (a.dim + 7) / 8 * 8, wave, lane);
     if constexpr (KTOKEN) Q.init(a.p, a.p_pitch * 2, c0, a.p_cols, wave, lane);
     else P.init(a.p, a.p_pitch * 2, c0, a.p_rows, wave, lane);
-    constexpr int kStage = 2 * COp::kBytes;
-    auto load = [&](int kt, int b) {
-        uint8_t* dst = lds + b * kStage;
-        A.load(dst, (int64_t)kt * kHeadK, a.a_rows, wave, lane);
-        if constexpr (KTOKEN) Q.load(dst + COp::kBytes, (int64_t)kt * kHeadK, a.p_rows, wave, lane);
-        else P.load(dst + COp::kBytes, (int64_t)kt * 128, wave);
-    };
     floatx16 acc[TD][TC];
 #pragma unroll
     for (int i = 0; i < TD; ++i)
 #pragma unroll
         for (int j = 0; j < TC; ++j) acc[i][j] = floatx16(0.f);
-    if (s0 < s1) load(s0, 0);
-    for (int kt = s0; kt < s1; ++kt) {
-        wait_loads<0>();
-        wait_lds();
-        bare_barrier();      // stage kt is in LDS, and every wave is done with stage kt - 1
-        if (kt + 1 < s1) load(kt + 1, (kt + 1 - s0) & 1);
-        const uint8_t* ta = lds + ((kt - s0) & 1) * kStage;
-        const uint8_t* tp = ta + COp::kBytes;
-#pragma unroll
-        for (int kc = 0; kc < kHeadK / 16; ++kc) {
-            u32x4 fa[TD], fb[TC];
-#pragma unroll
-            for (int i = 0; i < TD; ++i) fa[i] = COp::template frag<true>(ta, wd * TD * 32 + 32 * i, kc, lane);
-#pragma unroll
-            for (int j = 0; j < TC; ++j) {
-                const int c = wc * TC * 32 + 32 * j;
-                if constexpr (KTOKEN) fb[j] = COp::template frag<false>(tp, c, kc, lane);
-                else fb[j] = ROp::frag(tp, c + lane % 32, kc, lane);
-            }
-#pragma unroll
-            for (int i = 0; i < TD; ++i)
-#pragma unroll
-                for (int j = 0; j < TC; ++j) acc[i][j] = mfma<T>(fa[i], fb[j], acc[i][j]);
-        }
-    }
-    const float unscale = a.scalars[2];
+    k_loop<T, TD, TC>(
+        acc, s1 - s0, s1 - s0,
+        [&](int kt, int slot, int u) {
+            A.load(lds_address(lds) + slot * kOperand, u, (int64_t)(s0 + kt) * kHeadK, a.a_rows, wave);
+        },
+        [&](int kt, int slot, int u) {
+            const int64_t k = (int64_t)(s0 + kt) * kHeadK;
+            if constexpr (KTOKEN) Q.load(lds_address(lds) + slot * kOperand, u, k, a.p_rows, wave);
+            else P.load(lds_address(lds) + slot * kOperand, u, k * 2, wave);
+        },
+        [&](int slot, int i, int kc) {
+            return COp::template frag<true>(lds + slot * kOperand, wd * TD * 32 + 32 * i, kc, lane);
+        },
+        [&](int slot, int j, int kc) {
+            const int c = wc * TC * 32 + 32 * j;
+            if constexpr (KTOKEN) return COp::template frag<false>(lds + slot * kOperand, c, kc, lane);
+            else return ROp::frag(lds + slot * kOperand, c + lane % 32, kc, lane);
+        });
+    const float unscale = a.scalars[1];
 #pragma unroll
     for (int j = 0; j < TC; ++j) {
         const int c = c0 + wc * TC * 32 + 32 * j + lane % 32;
@@ -549,20 +670,49 @@ __global__ __launch_bounds__(512, 2) void head_grad_kernel(const HeadGrad a) {
     }
 }
 
+// Both gradients of a piece in one launch, so that their tiles fill the
+// compute units together.
+template <typename T>
+__global__ __launch_bounds__(512, 2) void head_grads_kernel(const HeadGrads a) {
+    extern __shared__ __align__(16) uint8_t lds[];
+    // each XCD an equal number of items and its share of both kinds, those with K
+    // the vocabulary (the longer ones) first
+    const int items_h = a.hidden.tiles_c * a.hidden.tiles_d * a.hidden.splits;
+    const int items_w = a.weight.tiles_c * a.weight.tiles_d * a.weight.splits;
+    const int per = gridDim.x / kXcds, xcd = blockIdx.x % kXcds, at = blockIdx.x / kXcds;
+    const int begin = (int)((int64_t)xcd * items_h / kXcds), end = (int)((int64_t)(xcd + 1) * items_h / kXcds);
+    if (at < end - begin) {
+        head_grad_tile<T, false>(a.hidden, begin + at, lds);
+    } else {
+        const int i = xcd * per - begin + at - (end - begin);
+        if (i < items_w) head_grad_tile<T, true>(a.weight, i, lds);
+    }
+}
+
 // The splits' sums in order, rounded once.
 template <typename T>
 __global__ __launch_bounds__(256) void head_join_kernel(const HeadJoin a) {
-    const int64_t quads = (a.dim + 3) / 4, items = quads * a.cols;
-    const float unscale = a.scalars[2];
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < items; i += (int64_t)gridDim.x * 256) {
-        const int64_t c = i / quads, d = (i - c * quads) * 4;
-        floatx4 sum = {0.f, 0.f, 0.f, 0.f};
-        for (int s = 0; s < a.splits; ++s)
-            sum += *reinterpret_cast<const floatx4*>(a.partial + (s * (int64_t)a.cols + c) * a.partial_pitch + d);
-        T* dst = static_cast<T*>(a.out) + c * a.out_pitch + d;
+    const int64_t octs = (a.dim + 7) / 8, first = octs * a.part[0].cols, items = first + octs * a.part[1].cols;
+    const float unscale = a.scalars[1];
+    for (int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x; n < items; n += (int64_t)gridDim.x * 256) {
+        const bool second = n >= first;
+        const HeadJoin::Part& p = a.part[second];
+        const int64_t i = second ? n - first : n, c = i / octs, d = (i - c * octs) * 8;
+        floatx4 lo = {0.f, 0.f, 0.f, 0.f}, hi = lo;
+        const float* src = p.partial + c * p.partial_pitch + d;
+        for (int s = 0; s < p.splits; ++s, src += (int64_t)p.cols * p.partial_pitch) {
+            lo += reinterpret_cast<const floatx4*>(src)[0];
+            hi += reinterpret_cast<const floatx4*>(src)[1];
+        }
+        float v[8];
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (d + e < a.dim) dst[e] = (T)(sum[e] * unscale);
+        for (int e = 0; e < 4; ++e) { v[e] = lo[e] * unscale; v[4 + e] = hi[e] * unscale; }
+        T* dst = static_cast<T*>(p.out) + c * p.out_pitch + d;
+        if (p.out_vec) *reinterpret_cast<u32x4*>(dst) = pack8<T>(v);
+        else
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (d + e < a.dim) dst[e] = (T)v[e];
     }
 }
 
@@ -587,58 +737,7 @@ __global__ __launch_bounds__(256) void head_pack_kernel(const HeadPack a) {
     }
 }
 
-// The weight of a token in the mean, and the power of two that fp16
-// probabilities are scaled by (the largest weight becomes 2^13 .. 2^14, so a
-// probability of 1e-9 is still a normal number; bf16 has fp32's range).
-__global__ __launch_bounds__(1024) void head_scalars_kernel(const HeadScalars a) {
-    __shared__ int count[16];
-    __shared__ float top[16];
-    int n = 0;
-    float m = 0.f;
-    for (int64_t i = threadIdx.x; i < a.tokens; i += 1024) {
-        const bool counted = a.targets[i] != a.ignore_index;
-        n += counted;
-        if (a.weights && counted) m = fmaxf(m, fabsf(a.weights[i]));
-    }
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) {
-        n += __shfl_xor(n, off, kWave);
-        m = fmaxf(m, __shfl_xor(m, off, kWave));
-    }
-    if (threadIdx.x % kWave == 0) {
-        count[threadIdx.x / kWave] = n;
-        top[threadIdx.x / kWave] = m;
-    }
-    __syncthreads();
-    if (threadIdx.x != 0) return;
-    for (int w = 1; w < 16; ++w) {
-        n += count[w];
-        m = fmaxf(m, top[w]);
-    }
-    const float mean = 1.0f / (float)max(n, 1);
-    if (!a.weights) m = mean;
-    a.scalars[0] = mean;
-    float scale = 1.f;
-    if (a.type == kHeadFp16 && m > 1e-30f && m < 1e30f) scale = ldexpf(1.0f, 14 - __builtin_amdgcn_frexp_expf(m));
-    a.scalars[1] = scale;
-    a.scalars[2] = 1.0f / scale;
-}
-
-// sum of weight x nll, in a fixed order.
-__global__ __launch_bounds__(1024) void head_loss_kernel(const HeadLoss a) {
-    __shared__ float red[16];
-    float sum = 0.f;
-    for (int64_t i = threadIdx.x; i < a.tokens; i += 1024) {
-        const float w = a.row_weight[i];
-        if (w != 0.f) sum = fmaf(w, a.nll[i], sum);
-    }
-    sum = wave_sum(sum);
-    if (threadIdx.x % kWave == 0) red[threadIdx.x / kWave] = sum;
-    __syncthreads();
-    if (threadIdx.x != 0) return;
-    for (int w = 1; w < 16; ++w) sum += red[w];
-    *a.loss = sum * a.scalars[2];
-}
+__global__ __launch_bounds__(1024) void head_loss_kernel(const HeadLoss a) { head_loss_sum<1024>(a); }
 
 template <typename K>
 hipError_t allow_lds(K kernel, size_t bytes) {
@@ -649,14 +748,13 @@ template <typename T, bool STORE, bool CAP>
 hipError_t logits_launch(const HeadLogits& a, bool small, hipStream_t s) {
     if (small) {
         const int groups = (int)(a.e_pitch / kHeadSmallSub);   // the padded columns too: they become zeros
-        if (a.tokens <= 32) head_logits_small_kernel<T, 1, STORE, CAP><<<groups, 256, 0, s>>>(a);
-        else head_logits_small_kernel<T, 2, STORE, CAP><<<groups, 256, 0, s>>>(a);
+        if (a.tokens <= 32) head_logits_small_kernel<T, 1, STORE, CAP><<<groups + 1, 256, 0, s>>>(a);
+        else head_logits_small_kernel<T, 2, STORE, CAP><<<groups + 1, 256, 0, s>>>(a);
         return hipGetLastError();
     }
-    constexpr size_t bytes = 2 * 2 * kHeadTile * 128;
-    const hipError_t allowed = allow_lds(&head_logits_kernel<T, STORE, CAP>, bytes);
+    const hipError_t allowed = allow_lds(&head_logits_kernel<T, STORE, CAP>, kRingBytes);
     if (allowed != hipSuccess) return allowed;
-    head_logits_kernel<T, STORE, CAP><<<xcd_grid(a.tiles_v * a.tiles_t), 512, bytes, s>>>(a);
+    head_logits_kernel<T, STORE, CAP><<<xcd_grid(a.tiles_v * a.tiles_t) + 1, 512, kRingBytes, s>>>(a);
     return hipGetLastError();
 }
 
@@ -676,18 +774,19 @@ hipError_t rows_typed(const HeadRows& a, hipStream_t s) {
 
 template <typename T>
 hipError_t prob_typed(const HeadProb& a, hipStream_t s) {
-    const int grid = (a.cols + 2047) / 2048 * ((a.rows + 7) / 8);
+    const int grid = (a.cols + 2047) / 2048 * ((a.rows + 7) / 8) + 1;
     if (a.inv_cap > 0.f) head_prob_kernel<T, true><<<grid, 256, 0, s>>>(a);
     else head_prob_kernel<T, false><<<grid, 256, 0, s>>>(a);
     return hipGetLastError();
 }
 
-template <typename T, bool KTOKEN>
-hipError_t grad_launch(const HeadGrad& a, hipStream_t s) {
-    constexpr size_t bytes = 2 * 2 * kHeadK * 512;
-    const hipError_t allowed = allow_lds(&head_grad_kernel<T, KTOKEN>, bytes);
+template <typename T>
+hipError_t grads_launch(const HeadGrads& a, hipStream_t s) {
+    const hipError_t allowed = allow_lds(&head_grads_kernel<T>, kRingBytes);
     if (allowed != hipSuccess) return allowed;
-    head_grad_kernel<T, KTOKEN><<<xcd_grid(a.tiles_c * a.tiles_d * a.splits), 512, bytes, s>>>(a);
+    const int grid = xcd_grid(a.hidden.tiles_c * a.hidden.tiles_d * a.hidden.splits +
+                              a.weight.tiles_c * a.weight.tiles_d * a.weight.splits);
+    head_grads_kernel<T><<<grid, 512, kRingBytes, s>>>(a);
     return hipGetLastError();
 }
 
@@ -702,23 +801,19 @@ hipError_t launch_head_rows(const HeadRows& a, int type, hipStream_t s) {
 hipError_t launch_head_prob(const HeadProb& a, int type, hipStream_t s) {
     return type == kHeadBf16 ? prob_typed<bf16>(a, s) : prob_typed<f16>(a, s);
 }
-hipError_t launch_head_grad(const HeadGrad& a, int type, bool k_is_token, hipStream_t s) {
-    if (type == kHeadBf16) return k_is_token ? grad_launch<bf16, true>(a, s) : grad_launch<bf16, false>(a, s);
-    return k_is_token ? grad_launch<f16, true>(a, s) : grad_launch<f16, false>(a, s);
+hipError_t launch_head_grads(const HeadGrads& a, int type, hipStream_t s) {
+    return type == kHeadBf16 ? grads_launch<bf16>(a, s) : grads_launch<f16>(a, s);
 }
 hipError_t launch_head_join(const HeadJoin& a, int type, hipStream_t s) {
-    const int64_t groups = std::min<int64_t>(4096, ((int64_t)a.cols * ((a.dim + 3) / 4) + 255) / 256);
-    if (type == kHeadBf16) head_join_kernel<bf16><<<(int)groups, 256, 0, s>>>(a);
-    else head_join_kernel<f16><<<(int)groups, 256, 0, s>>>(a);
+    const int64_t items = ((int64_t)a.part[0].cols + a.part[1].cols) * ((a.dim + 7) / 8);
+    const int groups = (int)std::min<int64_t>(4096, (items + 255) / 256);
+    if (type == kHeadBf16) head_join_kernel<bf16><<<groups, 256, 0, s>>>(a);
+    else head_join_kernel<f16><<<groups, 256, 0, s>>>(a);
     return hipGetLastError();
 }
 hipError_t launch_head_pack(const HeadPack& a, hipStream_t s) {
     const int64_t groups = std::min<int64_t>(4096, (a.dst_pitch / 8 * a.rows + 255) / 256);
     head_pack_kernel<<<(int)groups, 256, 0, s>>>(a);
-    return hipGetLastError();
-}
-hipError_t launch_head_scalars(const HeadScalars& a, hipStream_t s) {
-    head_scalars_kernel<<<1, 1024, 0, s>>>(a);
     return hipGetLastError();
 }
 hipError_t launch_head_loss(const HeadLoss& a, hipStream_t s) {

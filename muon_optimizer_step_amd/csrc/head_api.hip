@@ -3,12 +3,12 @@
 // head_loss in muonstep_train.h.
 //
 // One call enqueues, on the caller's stream:
-//   head_scalars (train: the mean's weight), head_pack (train: hidden with
-//   ignored rows zeroed; otherwise only what is not 16-byte aligned)
-//   for each piece of the tokens: head_logits, head_rows, and for gradients
-//   head_prob, head_grad (hidden), head_grad (weight), with head_join where K
-//   was split or the pieces' sums had to be kept in fp32
-//   head_loss (the weighted sum)
+//   head_pack   only for inputs that are not 16-byte aligned
+//   for each piece of the tokens: head_logits (and the scale of the weights, one
+//   workgroup), head_rows (with a copy of hidden for the gradient of weight),
+//   and for gradients head_prob (and the loss, one workgroup), head_grads, with
+//   head_join where K was split or the pieces' sums had to be kept in fp32
+//   head_loss   only where the loss is wanted without gradients
 #include <algorithm>
 #include <cmath>
 #include <cstring>
@@ -28,7 +28,7 @@ int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 
 // Offsets into the workspace (-1: not there) and sizes, from the problem alone.
 struct HeadPlan {
-    bool train, small, pack_h, pack_w;
+    bool train, small, pack_h, pack_w, copy_h;
     int64_t dim8;                 // dim rounded up to whole chunks
     int64_t piece, pieces;        // tokens per piece
     int64_t rows, cols;           // padded size of a piece's probabilities
@@ -38,13 +38,34 @@ struct HeadPlan {
     int64_t scalars, row_weight, row_target, ref, sum, e, hidden, weight, part_h, part_w, bytes;
 };
 
-// K of `k` elements over the workgroups that `tiles` output tiles leave idle.
-void split_k(int64_t k, int64_t tiles, int& splits, int& stages) {
-    const int total = (int)((k + kHeadK - 1) / kHeadK);
-    int want = (int)std::max<int64_t>(1, kCus / tiles);
-    want = std::min(want, std::max(1, total / kMinStagesPerSplit));
-    stages = (total + want - 1) / want;
-    splits = (total + stages - 1) / stages;
+// Splits of K for the two gradients, of n and m tiles of `a` and `b` stages:
+// the pair that takes least by this estimate, in stages.  256 workgroups run
+// at a time; a tile costs kTileStages more for its prologue and epilogue; a
+// split's partial sums are written and read again, kPartStages per tile.
+// (Measured: a stage takes 1.8 us, prologue and epilogue 5 us, a partial
+// sum 13 us with head_join's share.)
+void split_k(int64_t n, int a, int64_t m, int b, int& splits_a, int& splits_b) {
+    constexpr double kTileStages = 3.0, kPartStages = 8.0;
+    static const int tried[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32};
+    double best = 1e300;
+    splits_a = splits_b = 1;
+    for (int i : tried) {
+        if (i > 1 && (n == 0 || a / i < kMinStagesPerSplit)) break;
+        for (int j : tried) {
+            if (j > 1 && (m == 0 || b / j < kMinStagesPerSplit)) break;
+            const double la = n ? (a + i - 1) / i + kTileStages + (i > 1 ? kPartStages : 0.0) : 0.0;
+            const double lb = m ? (b + j - 1) / j + kTileStages + (j > 1 ? kPartStages : 0.0) : 0.0;
+            const int64_t items = n * i + m * j;
+            const double longest = std::max(la, lb), even = (n * i * la + m * j * lb) / kCus;
+            // the last items to start are gradient tiles of weight; their round is on average half full
+            const double cost = items <= kCus ? longest : std::max(longest, even + 0.5 * (m ? lb : la));
+            if (cost < best) {
+                best = cost;
+                splits_a = i;
+                splits_b = j;
+            }
+        }
+    }
 }
 
 HeadPlan make_head_plan(const head_loss_t& p) {
@@ -54,7 +75,8 @@ HeadPlan make_head_plan(const head_loss_t& p) {
     auto odd = [&](const void* ptr, int64_t stride) {
         return p.dim % 8 || stride % 8 || reinterpret_cast<uintptr_t>(ptr) % 16;
     };
-    q.pack_h = odd(p.hidden, p.hidden_stride) || p.grad_weight;
+    q.pack_h = odd(p.hidden, p.hidden_stride);
+    q.copy_h = !q.pack_h && p.grad_weight;
     q.pack_w = odd(p.weight, p.weight_stride);
     const bool grads = p.grad_hidden || p.grad_weight;
     q.cols = round_up(p.vocab, kHeadPad);
@@ -70,8 +92,11 @@ HeadPlan make_head_plan(const head_loss_t& p) {
     q.sub = q.small ? kHeadSmallSub : kHeadSub;
     q.nsub = q.small ? (int)(q.cols / kHeadSmallSub) : (int)((p.vocab + kHeadTile - 1) / kHeadTile) * (kHeadTile / kHeadSub);
     const int64_t tiles_d = (p.dim + kHeadTile - 1) / kHeadTile;
-    split_k(q.cols, (q.piece + kHeadTile - 1) / kHeadTile * tiles_d, q.splits_h, q.stages_h);
-    split_k(q.rows, (p.vocab + kHeadTile - 1) / kHeadTile * tiles_d, q.splits_w, q.stages_w);
+    const int all_h = (int)(q.cols / kHeadK), all_w = (int)(q.rows / kHeadK);
+    split_k(p.grad_hidden ? (q.piece + kHeadTile - 1) / kHeadTile * tiles_d : 0, all_h,
+            p.grad_weight ? (p.vocab + kHeadTile - 1) / kHeadTile * tiles_d : 0, all_w, q.splits_h, q.splits_w);
+    q.stages_h = (all_h + q.splits_h - 1) / q.splits_h;
+    q.stages_w = (all_w + q.splits_w - 1) / q.splits_w;
     q.partial_h = p.grad_hidden && q.splits_h > 1;
     q.partial_w = p.grad_weight && (q.splits_w > 1 || q.pieces > 1);
     int64_t off = 0;
@@ -86,7 +111,7 @@ HeadPlan make_head_plan(const head_loss_t& p) {
     q.ref = take(true, 4 * (int64_t)q.nsub * q.rows);
     q.sum = take(true, 4 * (int64_t)q.nsub * q.rows);
     q.e = take(grads, 2 * q.rows * q.cols);
-    q.hidden = take(q.pack_h, 2 * round_up(p.tokens, kHeadPad) * q.dim8);
+    q.hidden = take(q.pack_h || q.copy_h, 2 * (q.pack_h ? round_up(p.tokens, kHeadPad) : q.rows) * q.dim8);
     q.weight = take(q.pack_w, 2 * p.vocab * q.dim8);
     q.part_h = take(q.partial_h, 4 * (int64_t)q.splits_h * q.piece * q.dim8);
     q.part_w = take(q.partial_w, 4 * (int64_t)q.splits_w * p.vocab * q.dim8);
@@ -157,10 +182,6 @@ int enqueue_head(const head_loss_t& p, const HeadPlan& q, uint8_t* ws, hipStream
     float* row_weight = q.train ? reinterpret_cast<float*>(ws + q.row_weight) : nullptr;
     int* row_target = q.train ? reinterpret_cast<int*>(ws + q.row_target) : nullptr;
     const int dim = (int)p.dim, vocab = (int)p.vocab;
-    if (q.train) {
-        const HeadScalars a = {p.targets, p.token_weights, scalars, p.ignore_index, p.tokens, p.dtype};
-        HEAD_TRY("head_scalars", launch_head_scalars(a, s));
-    }
     const uint8_t* h = static_cast<const uint8_t*>(p.hidden);
     const void* w = p.weight;
     int64_t h_pitch = p.hidden_stride, w_pitch = p.weight_stride;
@@ -206,6 +227,7 @@ int enqueue_head(const head_loss_t& p, const HeadPlan& q, uint8_t* ws, hipStream
         a.inv_cap = inv_cap;
         a.tiles_v = (vocab + kHeadTile - 1) / kHeadTile;
         a.tiles_t = (tokens + kHeadTile - 1) / kHeadTile;
+        if (q.train && at == 0) a.scalars = {p.targets, p.token_weights, scalars, p.ignore_index, (int)p.tokens, p.dtype};
         HEAD_TRY(q.small ? "head_logits_small" : "head_logits", launch_head_logits(a, p.dtype, q.small, s));
         HeadRows r;
         memset(&r, 0, sizeof(r));
@@ -224,6 +246,8 @@ int enqueue_head(const head_loss_t& p, const HeadPlan& q, uint8_t* ws, hipStream
         r.lse = p.lse ? p.lse + at : nullptr;
         r.row_weight = q.train ? row_weight + at : nullptr;
         r.row_target = q.train ? row_target + at : nullptr;
+        r.copy = q.copy_h ? ws + q.hidden : nullptr;
+        r.copy_pitch = q.dim8;
         r.ignore_index = p.ignore_index;
         r.tokens = tokens;
         r.rows = q.train ? rows : tokens;
@@ -234,64 +258,77 @@ int enqueue_head(const head_loss_t& p, const HeadPlan& q, uint8_t* ws, hipStream
         r.train = q.train;
         HEAD_TRY("head_rows", launch_head_rows(r, p.dtype, s));
         if (q.e < 0) continue;
-        const HeadProb b = {ws + q.e, q.cols, rows, (int)q.cols, ref, sum, rows, q.sub, row_weight + at, row_target + at, inv_cap};
+        const bool last = at + q.piece >= p.tokens;
+        HeadProb b = {ws + q.e, q.cols, rows, (int)q.cols, ref, sum, rows, q.sub, row_weight + at, row_target + at, inv_cap, {}};
+        if (last && p.loss) b.loss = {p.nll, row_weight, scalars, p.loss, (int)p.tokens};
         HEAD_TRY("head_prob", launch_head_prob(b, p.dtype, s));
-        HeadGrad g;
+        HeadGrads g;
         memset(&g, 0, sizeof(g));
-        g.p = ws + q.e;
-        g.p_pitch = q.cols;
-        g.p_rows = rows;
-        g.p_cols = (int)q.cols;
-        g.dim = dim;
-        g.tiles_d = tiles_d;
-        g.scalars = scalars;
+        auto common = [&](HeadGrad& x, int64_t cols) {
+            x.p = ws + q.e;
+            x.p_pitch = q.cols;
+            x.p_rows = rows;
+            x.p_cols = (int)q.cols;
+            x.dim = dim;
+            x.cols = (int)cols;
+            x.tiles_c = (int)((cols + kHeadTile - 1) / kHeadTile);
+            x.tiles_d = tiles_d;
+            x.partial_pitch = q.dim8;
+            x.scalars = scalars;
+        };
+        HeadJoin j;
+        memset(&j, 0, sizeof(j));
+        j.dim = dim;
+        j.scalars = scalars;
         if (p.grad_hidden) {
-            uint8_t* out = static_cast<uint8_t*>(p.grad_hidden) + at * p.grad_hidden_stride * 2;
-            g.a = w;
-            g.a_pitch = w_pitch;
-            g.a_rows = vocab;
-            g.cols = tokens;
-            g.k = (int)q.cols;
-            g.splits = q.splits_h;
-            g.stages_per_split = q.stages_h;
-            g.tiles_c = (tokens + kHeadTile - 1) / kHeadTile;
-            g.out = out;
-            g.out_pitch = p.grad_hidden_stride;
-            g.out_vec = vec(out, p.grad_hidden_stride);
-            g.partial = q.partial_h ? reinterpret_cast<float*>(ws + q.part_h) : nullptr;
-            g.partial_pitch = q.dim8;
-            HEAD_TRY("head_grad_hidden", launch_head_grad(g, p.dtype, false, s));
-            if (q.partial_h) {
-                const HeadJoin j = {g.partial, q.dim8, q.splits_h, tokens, dim, out, p.grad_hidden_stride, scalars};
-                HEAD_TRY("head_join", launch_head_join(j, p.dtype, s));
-            }
+            HeadGrad& x = g.hidden;
+            common(x, tokens);
+            x.a = w;
+            x.a_pitch = w_pitch;
+            x.a_rows = vocab;
+            x.k = (int)q.cols;
+            x.splits = q.splits_h;
+            x.stages_per_split = q.stages_h;
+            x.out = static_cast<uint8_t*>(p.grad_hidden) + at * p.grad_hidden_stride * 2;
+            x.out_pitch = p.grad_hidden_stride;
+            x.out_vec = vec(x.out, x.out_pitch);
+            x.partial = q.partial_h ? reinterpret_cast<float*>(ws + q.part_h) : nullptr;
+            if (q.partial_h) j.part[0] = {x.partial, q.dim8, q.splits_h, tokens, x.out, x.out_pitch, x.out_vec};
         }
         if (p.grad_weight) {
-            g.a = hp;
-            g.a_pitch = h_pitch;
-            g.a_rows = rows;
-            g.cols = vocab;
-            g.k = rows;
-            g.splits = q.splits_w;
-            g.stages_per_split = q.stages_w;
-            g.tiles_c = (vocab + kHeadTile - 1) / kHeadTile;
-            g.out = p.grad_weight;
-            g.out_pitch = p.grad_weight_stride;
-            g.out_vec = vec(p.grad_weight, p.grad_weight_stride);
-            g.partial = q.partial_w ? reinterpret_cast<float*>(ws + q.part_w) : nullptr;
-            g.partial_pitch = q.dim8;
-            g.accumulate = at > 0;
-            HEAD_TRY("head_grad_weight", launch_head_grad(g, p.dtype, true, s));
+            HeadGrad& x = g.weight;
+            common(x, vocab);
+            x.a = q.copy_h ? ws + q.hidden : hp;     // ignored rows are zero in either
+            x.a_pitch = q.dim8;
+            x.a_rows = rows;
+            x.k = rows;
+            x.splits = q.splits_w;
+            x.stages_per_split = q.stages_w;
+            x.out = p.grad_weight;
+            x.out_pitch = p.grad_weight_stride;
+            x.out_vec = vec(x.out, x.out_pitch);
+            x.partial = q.partial_w ? reinterpret_cast<float*>(ws + q.part_w) : nullptr;
+            x.accumulate = at > 0;
+            if (q.partial_w && last) j.part[1] = {x.partial, q.dim8, q.splits_w, vocab, x.out, x.out_pitch, x.out_vec};
+        }
+        HEAD_TRY("head_grads", launch_head_grads(g, p.dtype, s));
+        if (j.part[0].cols || j.part[1].cols) HEAD_TRY("head_join", launch_head_join(j, p.dtype, s));
+    }
+    if (p.tokens == 0 && (p.grad_weight || p.loss)) {
+        // no tokens: the sums are empty
+        HeadJoin j;
+        memset(&j, 0, sizeof(j));
+        j.dim = dim;
+        j.scalars = scalars;
+        const HeadPack a = {nullptr, 0, scalars, 8, 1, 0, 8, nullptr, 0};
+        HEAD_TRY("head_pack", launch_head_pack(a, s));
+        if (p.grad_weight) {
+            j.part[1] = {nullptr, q.dim8, 0, vocab, p.grad_weight, p.grad_weight_stride, vec(p.grad_weight, p.grad_weight_stride)};
+            HEAD_TRY("head_join", launch_head_join(j, p.dtype, s));
         }
     }
-    if (p.grad_weight && (q.partial_w || p.tokens == 0)) {
-        // no tokens: no splits to add, the gradient is zero
-        const HeadJoin j = {q.part_w >= 0 ? reinterpret_cast<const float*>(ws + q.part_w) : nullptr, q.dim8,
-                            p.tokens ? q.splits_w : 0, vocab, dim, p.grad_weight, p.grad_weight_stride, scalars};
-        HEAD_TRY("head_join", launch_head_join(j, p.dtype, s));
-    }
-    if (p.loss) {
-        const HeadLoss a = {p.nll, row_weight, scalars, p.loss, p.tokens};
+    if (p.loss && (q.e < 0 || p.tokens == 0)) {
+        const HeadLoss a = {p.nll, row_weight, scalars, p.loss, (int)p.tokens};
         HEAD_TRY("head_loss", launch_head_loss(a, s));
     }
     return MUON_OK;
