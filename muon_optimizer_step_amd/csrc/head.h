@@ -11,9 +11,14 @@ enum HeadType { kHeadBf16 = 0, kHeadFp16 = 1 };
 constexpr int kHeadK = 64;         // K elements per LDS stage
 constexpr int kHeadPad = 64;       // rows and columns of the probability piece are padded to it
 constexpr int kHeadTile = 256;     // output tile edge of the products
-constexpr int kHeadSmall = 64;     // tokens up to which the vocabulary is streamed past all of them at once
-constexpr int kHeadSub = 128;      // vocabulary entries per partial maximum and sum, tiled kernel
-constexpr int kHeadSmallSub = 32;  // the same, streaming kernel
+constexpr int kHeadMidVocab = 128; // vocabulary entries of a tile of the kernels for few tokens or small problems
+constexpr int kHeadStream = 32;    // tokens that the streaming kernel takes at most
+constexpr int kHeadStreamSub = 32; // vocabulary entries of its workgroups
+
+// Kernels for the logits, and the vocabulary entries of their partial maxima
+// and sums (what one wave holds).
+enum LogitsVariant { kLogitsStream = 0, kLogitsMid32, kLogitsMid64, kLogitsMid128, kLogitsTile };
+constexpr int logits_sub(int variant) { return variant == kLogitsTile ? 128 : variant == kLogitsMid128 ? 64 : 32; }
 
 // What the weights in P and the sums over P are scaled by, over all tokens of
 // the call; computed by one more workgroup of the first head_logits launch.
@@ -139,7 +144,7 @@ struct HeadPack {
     int64_t ignore_index;
 };
 
-hipError_t launch_head_logits(const HeadLogits& a, int type, bool small, hipStream_t s);
+hipError_t launch_head_logits(const HeadLogits& a, int type, int variant, hipStream_t s);
 hipError_t launch_head_rows(const HeadRows& a, int type, hipStream_t s);
 hipError_t launch_head_prob(const HeadProb& a, int type, hipStream_t s);
 hipError_t launch_head_grads(const HeadGrads& a, int type, hipStream_t s);

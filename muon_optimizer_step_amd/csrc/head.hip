@@ -87,29 +87,35 @@ __device__ inline void direct_load(const uint8_t* base, uint32_t off, uint32_t d
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(dst), "v"(off), "s"(base)
                  : "memory");
 }
+// The same from an address of each lane's own.
+__device__ inline void direct_load_from(const uint8_t* src, uint32_t dst) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(dst), "v"(src) : "memory");
+}
+__device__ __align__(16) const uint8_t kZeros[16] = {};   // what K beyond its end is loaded from
 __device__ inline uint32_t lds_address(const uint8_t* p) { return (uint32_t)(uintptr_t)(lds_ptr)p; }
 
 // ---------------------------------------------------------------- operand staging
 // A stage is 64 K of both operands of a 256 x 256 tile, 32 KB each.
 //
-// A row operand (K contiguous): 256 rows x 128 bytes of K per stage (a whole
+// A row operand (K contiguous): ROWS rows x 128 bytes of K per stage (a whole
 // cache line: 64-byte pieces cost the vector L1 twice the fills), the 16-byte
 // chunk c of row r in slot c ^ ((r / 2) % 8), which keeps the 16-byte fragment
 // reads of 32 rows free of bank conflicts.  Direct loads: one wave instruction
 // fills 8 rows.
 constexpr int kOperand = kHeadTile * kHeadK * 2;     // bytes of one operand of a stage
-template <int WAVES>
+template <int ROWS, int WAVES>
 struct RowOperand {
-    static constexpr int kLoads = kHeadTile / 8 / WAVES;
-    static_assert(kHeadTile % (8 * WAVES) == 0 && WAVES % 2 == 0, "whole instructions per wave");
+    static constexpr int kBytes = ROWS * kHeadK * 2;
+    static constexpr int kLoads = ROWS / 8 / WAVES;
+    static_assert(ROWS % (8 * WAVES) == 0 && WAVES % 2 == 0, "whole instructions per wave");
     const uint8_t* base;
     uint32_t off[kLoads];
     int chunk;      // source chunk of this lane within a stage
 
-    // rows row0 .. row0 + 255 of a matrix with `rows` rows; rows beyond its end repeat the last one
+    // rows row0 .. row0 + ROWS - 1 of a matrix with `rows` rows; rows beyond its end repeat the last one
     __device__ inline void init(const void* m, int64_t pitch_bytes, int64_t row0, int64_t rows, int wave, int lane) {
         base = static_cast<const uint8_t*>(m) + row0 * pitch_bytes;
-        const int last = (int)min<int64_t>(rows - 1 - row0, kHeadTile - 1);
+        const int last = (int)min<int64_t>(rows - 1 - row0, ROWS - 1);
         chunk = 0;
 #pragma unroll
         for (int j = 0; j < kLoads; ++j) {
@@ -118,14 +124,12 @@ struct RowOperand {
             off[j] = (uint32_t)(min(r, last) * pitch_bytes) + chunk * 16;
         }
     }
-    __device__ inline void load(uint32_t lds, int j, int64_t kbyte, int wave) const {
-        direct_load(base + kbyte, off[j], lds + (j * WAVES + wave) * 1024);
-    }
-    // the last stage where K ends inside it: `chunks` of 8, zeros behind them
-    __device__ inline void load_tail(uint8_t* lds, int j, int64_t kbyte, int chunks, int wave, int lane) const {
-        u32x4 v = {0u, 0u, 0u, 0u};
-        if (chunk < chunks) v = *reinterpret_cast<const u32x4*>(base + kbyte + off[j]);
-        *reinterpret_cast<u32x4*>(lds + (j * WAVES + wave) * 1024 + lane * 16) = v;
+    // load j of stage kt of K elements `dim` (a multiple of 8); K beyond its end is zero
+    __device__ inline void load(uint32_t lds, int j, int kt, int dim, int wave) const {
+        const uint8_t* at = base + (int64_t)kt * (kHeadK * 2);
+        const uint32_t dst = lds + (j * WAVES + wave) * 1024;
+        if ((kt + 1) * kHeadK <= dim) direct_load(at, off[j], dst);
+        else direct_load_from(8 * chunk < dim - kt * kHeadK ? at + off[j] : kZeros, dst);
     }
     // fragment of 32 rows from `row`: lane l holds row perm(l % 32), K 16 kc + 8 (l / 32) .. + 7
     static __device__ inline u32x4 frag(const uint8_t* lds, int row, int kc, int lane) {
@@ -193,8 +197,7 @@ struct ColOperand {
 };
 
 // ---------------------------------------------------------------- K loop
-// acc += A B over `stages` stages of 64 K; the first `whole` stages consist of
-// direct loads only.  load_a(kt, slot, u), load_b issue load u of 4 of this
+// acc += A B over `stages` stages of 64 K.  load_a(kt, slot, u), load_b issue load u of 4 of this
 // wave for stage kt; a(slot, i, kc), b(slot, j, kc) read fragments of 16 K.
 //
 // LDS is a ring of five operand slots (all 160 KB): A of stage k is in slot
@@ -208,7 +211,7 @@ struct ColOperand {
 constexpr int kSlots = 5;
 constexpr size_t kRingBytes = (size_t)kSlots * kOperand;
 template <typename T, int TA, int TB, typename LoadA, typename LoadB, typename FragA, typename FragB>
-__device__ inline void k_loop(floatx16 (&acc)[TA][TB], int stages, int whole, LoadA load_a, LoadB load_b, FragA a, FragB b) {
+__device__ inline void k_loop(floatx16 (&acc)[TA][TB], int stages, LoadA load_a, LoadB load_b, FragA a, FragB b) {
     static_assert(kHeadK == 64, "four steps of 16 K per stage");
     u32x4 fa[2][TA], fb[2][TB];
     auto slot = [](int n) { return n >= kSlots ? n - kSlots : n; };
@@ -238,9 +241,8 @@ __device__ inline void k_loop(floatx16 (&acc)[TA][TB], int stages, int whole, Lo
     if (stages > 1)
 #pragma unroll
         for (int u = 0; u < 4; ++u) load_a(1, 2, u);
-    if (whole > 1) wait_loads<4>();
+    if (stages > 1) wait_loads<4>();
     else wait_loads<0>();
-    wait_lds();
     bare_barrier();
     read(0, 0, 1, 0);
     if (stages > 1) {
@@ -256,9 +258,9 @@ __device__ inline void k_loop(floatx16 (&acc)[TA][TB], int stages, int whole, Lo
         multiply(1, [&](int u) { if (kt + 2 < stages) load_a(kt + 2, sa2, u); });
         read(1, sa, sb, 3);
         multiply(0, [&](int u) { if (kt + 2 < stages) load_a(kt + 2, sa2, 2 + u); });
-        wait_lds();              // this wave's last fragments of stage kt, or its part of a tail
+        wait_lds();              // this wave's last fragments of stage kt
         if (kt + 1 < stages) {
-            if (kt + 2 < whole) wait_loads<4>();
+            if (kt + 2 < stages) wait_loads<4>();
             else wait_loads<0>();
             bare_barrier();
             read(0, sa1, sb1, 0);
@@ -370,12 +372,21 @@ __device__ inline void logits_epilogue(const HeadLogits& a, floatx16 (&acc)[TV][
     }
 }
 
+// Token tiles in groups of 8, vocabulary tiles within: the tiles that an XCD
+// works on at a time form a block, which shares operands in its L2.
+__device__ inline void tile_of(const HeadLogits& a, int item, int& tile_v, int& tile_t) {
+    const int group = item / (8 * a.tiles_v), in_group = item - group * 8 * a.tiles_v;
+    const int width = min(8, a.tiles_t - 8 * group);
+    tile_v = in_group / width;
+    tile_t = 8 * group + in_group % width;
+}
+
 // Tile of 256 vocabulary entries x 256 tokens: 8 waves of 128 x 64, 32x32x16
 // MFMAs.
 template <typename T, bool STORE, bool CAP>
 __global__ __launch_bounds__(512, 2) void head_logits_kernel(const HeadLogits a) {
     constexpr int WV = 2, WT = 4, TV = 4, TT = 2, BV = WV * TV * 32, BT = WT * TT * 32, NW = WV * WT;
-    static_assert(TV * 32 == kHeadSub, "one partial per wave");
+    static_assert(TV * 32 == logits_sub(kLogitsTile), "one partial per wave");
     extern __shared__ __align__(16) uint8_t lds[];
     if (blockIdx.x == gridDim.x - 1) {
         if (a.scalars.scalars) head_scalars<512>(a.scalars, lds);
@@ -383,23 +394,15 @@ __global__ __launch_bounds__(512, 2) void head_logits_kernel(const HeadLogits a)
     }
     const int item = xcd_item(a.tiles_v * a.tiles_t);
     if (item < 0) return;
-    // token tiles in groups of 8, vocabulary tiles within: the tiles that an XCD
-    // works on at a time form a block, which shares operands in its L2
-    const int group = item / (8 * a.tiles_v), in_group = item - group * 8 * a.tiles_v;
-    const int width = min(8, a.tiles_t - 8 * group);
-    const int tile_v = in_group / width, tile_t = 8 * group + in_group % width;
+    int tile_v, tile_t;
+    tile_of(a, item, tile_v, tile_t);
     const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), wv = wave / WT, wt = wave % WT;
 
-    typedef RowOperand<NW> Op;
+    typedef RowOperand<kHeadTile, NW> Op;
     Op W, H;
     W.init(a.w, a.w_pitch * 2, (int64_t)tile_v * BV, a.vocab, wave, lane);
     H.init(a.h, a.h_pitch * 2, (int64_t)tile_t * BT, a.tokens, wave, lane);
-    const int stages = (a.dim + kHeadK - 1) / kHeadK, whole = a.dim / kHeadK;
-    auto load = [&](const Op& op, int kt, int slot, int u) {
-        const int64_t k = (int64_t)kt * kHeadK * 2;
-        if (kt < whole) op.load(lds_address(lds) + slot * kOperand, u, k, wave);
-        else op.load_tail(lds + slot * kOperand, u, k, a.dim % kHeadK / 8, wave, lane);
-    };
+    const int stages = (a.dim + kHeadK - 1) / kHeadK;
     floatx16 acc[TV][TT];
 #pragma unroll
     for (int i = 0; i < TV; ++i)
@@ -407,19 +410,94 @@ __global__ __launch_bounds__(512, 2) void head_logits_kernel(const HeadLogits a)
         for (int j = 0; j < TT; ++j) acc[i][j] = floatx16(0.f);
     const int arow = wv * TV * 32 + swap23(lane % 32), brow = wt * TT * 32 + lane % 32;
     k_loop<T, TV, TT>(
-        acc, stages, whole, [&](int kt, int slot, int u) { load(W, kt, slot, u); },
-        [&](int kt, int slot, int u) { load(H, kt, slot, u); },
+        acc, stages, [&](int kt, int slot, int u) { W.load(lds_address(lds) + slot * kOperand, u, kt, a.dim, wave); },
+        [&](int kt, int slot, int u) { H.load(lds_address(lds) + slot * kOperand, u, kt, a.dim, wave); },
         [&](int slot, int i, int kc) { return Op::frag(lds + slot * kOperand, arow + 32 * i, kc, lane); },
         [&](int slot, int j, int kc) { return Op::frag(lds + slot * kOperand, brow + 32 * j, kc, lane); });
     logits_epilogue<TV, TT, STORE, CAP>(a, acc, tile_v * BV + wv * TV * 32, tile_t * BT + wt * TT * 32, tile_v * WV + wv, lane);
 }
 
-// Up to 32 TT tokens: a workgroup streams 32 vocabulary rows past all of them,
-// operands straight from memory (each row of W is used once), the waves take
-// every fourth 128 bytes of K and meet in LDS.
-template <typename T, int TT, bool STORE, bool CAP>
-__global__ __launch_bounds__(256) void head_logits_small_kernel(const HeadLogits a) {
-    __shared__ __align__(16) float part[4][TT][16][kWave];
+// Tile of 128 vocabulary entries x 32, 64 or 128 tokens, two workgroups of 4
+// waves per compute unit: for few tokens, where W streams past them (two or
+// three stages of 64 K in LDS keep its loads in flight), and for problems with too
+// few 256 x 256 tiles.
+template <int TOKENS> struct MidTile;
+template <> struct MidTile<32> { static constexpr int WV = 4, WT = 1, TV = 1, TT = 1, kBuffers = 3; };
+template <> struct MidTile<64> { static constexpr int WV = 4, WT = 1, TV = 1, TT = 2, kBuffers = 3; };
+template <> struct MidTile<128> { static constexpr int WV = 2, WT = 2, TV = 2, TT = 2, kBuffers = 2; };
+template <int TOKENS> constexpr size_t mid_bytes() {
+    return (size_t)MidTile<TOKENS>::kBuffers * (kHeadMidVocab + TOKENS) * kHeadK * 2;
+}
+
+template <typename T, int TOKENS, bool STORE, bool CAP>
+__global__ __launch_bounds__(256, 2) void head_logits_mid_kernel(const HeadLogits a) {
+    typedef MidTile<TOKENS> M;
+    constexpr int WV = M::WV, WT = M::WT, TV = M::TV, TT = M::TT, NW = WV * WT, kBuffers = M::kBuffers;
+    static_assert(WV * TV * 32 == kHeadMidVocab && WT * TT * 32 == TOKENS && NW == 4, "tile");
+    extern __shared__ __align__(16) uint8_t lds[];
+    if (blockIdx.x == gridDim.x - 1) {
+        if (a.scalars.scalars) head_scalars<256>(a.scalars, lds);
+        return;
+    }
+    const int item = xcd_item(a.tiles_v * a.tiles_t);
+    if (item < 0) return;
+    int tile_v, tile_t;
+    tile_of(a, item, tile_v, tile_t);
+    const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), wv = wave / WT, wt = wave % WT;
+    typedef RowOperand<kHeadMidVocab, NW> WOp;
+    typedef RowOperand<TOKENS, NW> HOp;
+    constexpr int kStage = WOp::kBytes + HOp::kBytes, kLoads = WOp::kLoads + HOp::kLoads;
+    WOp W;
+    HOp H;
+    W.init(a.w, a.w_pitch * 2, (int64_t)tile_v * kHeadMidVocab, a.vocab, wave, lane);
+    H.init(a.h, a.h_pitch * 2, (int64_t)tile_t * TOKENS, a.tokens, wave, lane);
+    const int stages = (a.dim + kHeadK - 1) / kHeadK;
+    auto load = [&](int kt) {
+        const uint32_t at = lds_address(lds) + kt % kBuffers * kStage;
+#pragma unroll
+        for (int u = 0; u < WOp::kLoads; ++u) W.load(at, u, kt, a.dim, wave);
+#pragma unroll
+        for (int u = 0; u < HOp::kLoads; ++u) H.load(at + WOp::kBytes, u, kt, a.dim, wave);
+    };
+    floatx16 acc[TV][TT];
+#pragma unroll
+    for (int i = 0; i < TV; ++i)
+#pragma unroll
+        for (int j = 0; j < TT; ++j) acc[i][j] = floatx16(0.f);
+    const int arow = wv * TV * 32 + swap23(lane % 32), brow = wt * TT * 32 + lane % 32;
+    for (int kt = 0; kt < kBuffers - 1 && kt < stages; ++kt) load(kt);
+    for (int kt = 0; kt < stages; ++kt) {
+        if (kt + kBuffers - 2 < stages) wait_loads<(kBuffers - 2) * kLoads>();    // stage kt of those under way
+        else wait_loads<0>();
+        wait_lds();
+        bare_barrier();      // stage kt is in LDS, and every wave is done with stage kt - 1
+        if (kt + kBuffers - 1 < stages) load(kt + kBuffers - 1);
+        const uint8_t* tw = lds + kt % kBuffers * kStage;
+        const uint8_t* th = tw + WOp::kBytes;
+#pragma unroll
+        for (int kc = 0; kc < kHeadK / 16; ++kc) {
+            u32x4 fa[TV], fb[TT];
+#pragma unroll
+            for (int i = 0; i < TV; ++i) fa[i] = WOp::frag(tw, arow + 32 * i, kc, lane);
+#pragma unroll
+            for (int j = 0; j < TT; ++j) fb[j] = HOp::frag(th, brow + 32 * j, kc, lane);
+#pragma unroll
+            for (int i = 0; i < TV; ++i)
+#pragma unroll
+                for (int j = 0; j < TT; ++j) acc[i][j] = mfma<T>(fa[i], fb[j], acc[i][j]);
+        }
+    }
+    logits_epilogue<TV, TT, STORE, CAP>(a, acc, tile_v * kHeadMidVocab + wv * TV * 32, tile_t * TOKENS + wt * TT * 32,
+                                        tile_v * WV + wv, lane);
+}
+
+// Up to 32 tokens and a small vocabulary, where there is little to read and
+// latency counts: a workgroup for every 32 vocabulary rows, operands straight
+// from memory (each row of W is used once), the waves take every fourth 128
+// bytes of K and meet in LDS.
+template <typename T, bool STORE, bool CAP>
+__global__ __launch_bounds__(256) void head_logits_stream_kernel(const HeadLogits a) {
+    __shared__ __align__(16) float part[4][16][kWave];
     if (blockIdx.x == gridDim.x - 1) {
         if (a.scalars.scalars) head_scalars<256>(a.scalars, part);
         return;
@@ -427,13 +505,8 @@ __global__ __launch_bounds__(256) void head_logits_small_kernel(const HeadLogits
     const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
     const int v0 = blockIdx.x * 32;
     const T* w = static_cast<const T*>(a.w) + (int64_t)min(v0 + swap23(lane % 32), a.vocab - 1) * a.w_pitch + 8 * (lane / 32);
-    const T* h[TT];
-#pragma unroll
-    for (int t = 0; t < TT; ++t)
-        h[t] = static_cast<const T*>(a.h) + (int64_t)min(32 * t + lane % 32, a.tokens - 1) * a.h_pitch + 8 * (lane / 32);
-    floatx16 acc[1][TT];
-#pragma unroll
-    for (int t = 0; t < TT; ++t) acc[0][t] = floatx16(0.f);
+    const T* h = static_cast<const T*>(a.h) + (int64_t)min(lane % 32, a.tokens - 1) * a.h_pitch + 8 * (lane / 32);
+    floatx16 acc = floatx16(0.f);
     const int left = a.dim - 8 * (lane / 32);     // this lane's K begins at 8 (l / 32)
     auto get = [&](const T* p, int k) -> u32x4 {
         u32x4 v = {0u, 0u, 0u, 0u};
@@ -441,62 +514,49 @@ __global__ __launch_bounds__(256) void head_logits_small_kernel(const HeadLogits
         return v;
     };
     for (int k0 = wave * 64; k0 < a.dim; k0 += 256) {
-        u32x4 fw[4], fh[4][TT];
+        u32x4 fw[4], fh[4];
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
             fw[s] = get(w, k0 + 16 * s);
-#pragma unroll
-            for (int t = 0; t < TT; ++t) fh[s][t] = get(h[t], k0 + 16 * s);
+            fh[s] = get(h, k0 + 16 * s);
         }
 #pragma unroll
-        for (int s = 0; s < 4; ++s)
-#pragma unroll
-            for (int t = 0; t < TT; ++t) acc[0][t] = mfma<T>(fw[s], fh[s][t], acc[0][t]);
+        for (int s = 0; s < 4; ++s) acc = mfma<T>(fw[s], fh[s], acc);
     }
 #pragma unroll
-    for (int t = 0; t < TT; ++t)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) part[wave][t][r][lane] = acc[0][t][r];
+    for (int r = 0; r < 16; ++r) part[wave][r][lane] = acc[r];
     __syncthreads();
-    if (wave >= TT) return;
+    if (wave != 0) return;
     floatx16 one[1][1];
 #pragma unroll
-    for (int r = 0; r < 16; ++r)
-        one[0][0][r] = (part[0][wave][r][lane] + part[1][wave][r][lane]) + (part[2][wave][r][lane] + part[3][wave][r][lane]);
-    logits_epilogue<1, 1, STORE, CAP>(a, one, v0, 32 * wave, blockIdx.x, lane);
+    for (int r = 0; r < 16; ++r) one[0][0][r] = (part[0][r][lane] + part[1][r][lane]) + (part[2][r][lane] + part[3][r][lane]);
+    logits_epilogue<1, 1, STORE, CAP>(a, one, v0, 0, blockIdx.x, lane);
 }
 
 // ---------------------------------------------------------------- rows
-// 256 threads on 256 / S tokens, S threads for each: the sub-tiles' partials
-// in a fixed order, the target's logit as a dot product of its own.
-template <typename T, int S>
-__global__ __launch_bounds__(256) void head_rows_kernel(const HeadRows a) {
-    constexpr int R = 256 / S;
-    __shared__ float red[256];
+// THREADS threads on R tokens, THREADS / R for each: the sub-tiles' partials, and
+// the target's logit as a dot product of its own, joined over a token's threads
+// in an order that depends on THREADS and R only.
+template <typename T, int THREADS, int R>
+__global__ __launch_bounds__(THREADS) void head_rows_kernel(const HeadRows a) {
+    constexpr int S = THREADS / R, kWaves = THREADS / kWave;
+    __shared__ float red[3][kWaves][R];
     const int r = threadIdx.x % R, s = threadIdx.x / R;
     const int row = blockIdx.x * R + r;
     const bool live = row < a.tokens, held = row < a.rows;
-    auto all = [&](float x, auto op) {   // over the S threads of a row, in a fixed order
-        __syncthreads();
-        red[threadIdx.x] = x;
-        __syncthreads();
-        for (int w = S / 2; w > 0; w >>= 1) {
-            if (s < w) red[threadIdx.x] = op(red[threadIdx.x], red[threadIdx.x + w * R]);
-            __syncthreads();
-        }
-        return red[r];
+    // two partials joined: the larger reference, the sums in units of it
+    auto join = [](float& top, float& sum, float top2, float sum2) {
+        const float m = fmaxf(top, top2);
+        // both -infinity: vocabulary padding only, nothing to add
+        sum = m == -INFINITY ? sum + sum2
+                             : sum * __builtin_amdgcn_exp2f(top - m) + sum2 * __builtin_amdgcn_exp2f(top2 - m);
+        top = m;
     };
-    float top = -INFINITY;
+    float top = -INFINITY, sum = 0.f;
     if (live)
-        for (int k = s; k < a.nsub; k += S) top = fmaxf(top, a.ref[(int64_t)k * a.stat_pitch + row]);
-    top = all(top, [](float x, float y) { return fmaxf(x, y); });
-    float sum = 0.f;
-    if (live)
+#pragma unroll 4
         for (int k = s; k < a.nsub; k += S)
-            sum += a.sum[(int64_t)k * a.stat_pitch + row] *
-                   __builtin_amdgcn_exp2f(a.ref[(int64_t)k * a.stat_pitch + row] - top);
-    sum = all(sum, [](float x, float y) { return x + y; });
-    const float lse2 = top + __builtin_amdgcn_logf(sum);
+            join(top, sum, a.ref[(int64_t)k * a.stat_pitch + row], a.sum[(int64_t)k * a.stat_pitch + row]);
 
     const int64_t t = live ? a.targets[row] : a.ignore_index;
     const bool counted = live && t != a.ignore_index, valid = t >= 0 && t < a.vocab;
@@ -512,7 +572,26 @@ __global__ __launch_bounds__(256) void head_rows_kernel(const HeadRows a) {
             for (int i = 0; i < 8; ++i) dot = fmaf(x[i], y[i], dot);
         }
     }
-    dot = all(dot, [](float x, float y) { return x + y; });
+#pragma unroll
+    for (int off = R; off < kWave; off <<= 1) {
+        join(top, sum, __shfl_xor(top, off, kWave), __shfl_xor(sum, off, kWave));
+        dot += __shfl_xor(dot, off, kWave);
+    }
+    if (threadIdx.x % kWave < R) {
+        red[0][threadIdx.x / kWave][r] = top;
+        red[1][threadIdx.x / kWave][r] = sum;
+        red[2][threadIdx.x / kWave][r] = dot;
+    }
+    __syncthreads();
+    top = red[0][0][r];
+    sum = red[1][0][r];
+    dot = red[2][0][r];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) {
+        join(top, sum, red[0][w][r], red[1][w][r]);
+        dot += red[2][w][r];
+    }
+    const float lse2 = top + __builtin_amdgcn_logf(sum);
     if (a.cap > 0.f) dot = capped(dot, a.cap, a.inv_cap);
     if (a.copy && held)
         for (int d = 8 * s; d < a.dim; d += 8 * S) {
@@ -607,7 +686,7 @@ __device__ inline void head_grad_tile(const HeadGrad& a, int item, uint8_t* lds)
     const int s0 = split * a.stages_per_split, s1 = min(a.k / kHeadK, s0 + a.stages_per_split);
 
     typedef ColOperand<NW> COp;
-    typedef RowOperand<NW> ROp;
+    typedef RowOperand<kHeadTile, NW> ROp;
     COp A, Q;
     ROp P;
     A.init(a.a, a.a_pitch * 2, d0, (a.dim + 7) / 8 * 8, wave, lane);
@@ -619,14 +698,13 @@ __device__ inline void head_grad_tile(const HeadGrad& a, int item, uint8_t* lds)
 #pragma unroll
         for (int j = 0; j < TC; ++j) acc[i][j] = floatx16(0.f);
     k_loop<T, TD, TC>(
-        acc, s1 - s0, s1 - s0,
+        acc, s1 - s0,
         [&](int kt, int slot, int u) {
             A.load(lds_address(lds) + slot * kOperand, u, (int64_t)(s0 + kt) * kHeadK, a.a_rows, wave);
         },
         [&](int kt, int slot, int u) {
-            const int64_t k = (int64_t)(s0 + kt) * kHeadK;
-            if constexpr (KTOKEN) Q.load(lds_address(lds) + slot * kOperand, u, k, a.p_rows, wave);
-            else P.load(lds_address(lds) + slot * kOperand, u, k * 2, wave);
+            if constexpr (KTOKEN) Q.load(lds_address(lds) + slot * kOperand, u, (int64_t)(s0 + kt) * kHeadK, a.p_rows, wave);
+            else P.load(lds_address(lds) + slot * kOperand, u, s0 + kt, a.k, wave);
         },
         [&](int slot, int i, int kc) {
             return COp::template frag<true>(lds + slot * kOperand, wd * TD * 32 + 32 * i, kc, lane);
@@ -744,14 +822,25 @@ hipError_t allow_lds(K kernel, size_t bytes) {
     return hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
 }
 
+template <typename T, int TOKENS, bool STORE, bool CAP>
+hipError_t mid_launch(const HeadLogits& a, hipStream_t s) {
+    constexpr size_t bytes = mid_bytes<TOKENS>();
+    const hipError_t allowed = allow_lds(&head_logits_mid_kernel<T, TOKENS, STORE, CAP>, bytes);
+    if (allowed != hipSuccess) return allowed;
+    head_logits_mid_kernel<T, TOKENS, STORE, CAP><<<xcd_grid(a.tiles_v * a.tiles_t) + 1, 256, bytes, s>>>(a);
+    return hipGetLastError();
+}
+
 template <typename T, bool STORE, bool CAP>
-hipError_t logits_launch(const HeadLogits& a, bool small, hipStream_t s) {
-    if (small) {
-        const int groups = (int)(a.e_pitch / kHeadSmallSub);   // the padded columns too: they become zeros
-        if (a.tokens <= 32) head_logits_small_kernel<T, 1, STORE, CAP><<<groups + 1, 256, 0, s>>>(a);
-        else head_logits_small_kernel<T, 2, STORE, CAP><<<groups + 1, 256, 0, s>>>(a);
+hipError_t logits_launch(const HeadLogits& a, int variant, hipStream_t s) {
+    if (variant == kLogitsStream) {
+        const int groups = (int)(a.e_pitch / kHeadStreamSub);   // the padded columns too: they become zeros
+        head_logits_stream_kernel<T, STORE, CAP><<<groups + 1, 256, 0, s>>>(a);
         return hipGetLastError();
     }
+    if (variant == kLogitsMid32) return mid_launch<T, 32, STORE, CAP>(a, s);
+    if (variant == kLogitsMid64) return mid_launch<T, 64, STORE, CAP>(a, s);
+    if (variant == kLogitsMid128) return mid_launch<T, 128, STORE, CAP>(a, s);
     const hipError_t allowed = allow_lds(&head_logits_kernel<T, STORE, CAP>, kRingBytes);
     if (allowed != hipSuccess) return allowed;
     head_logits_kernel<T, STORE, CAP><<<xcd_grid(a.tiles_v * a.tiles_t) + 1, 512, kRingBytes, s>>>(a);
@@ -759,16 +848,18 @@ hipError_t logits_launch(const HeadLogits& a, bool small, hipStream_t s) {
 }
 
 template <typename T>
-hipError_t logits_typed(const HeadLogits& a, bool small, hipStream_t s) {
-    if (a.e) return a.cap > 0.f ? logits_launch<T, true, true>(a, small, s) : logits_launch<T, true, false>(a, small, s);
-    return a.cap > 0.f ? logits_launch<T, false, true>(a, small, s) : logits_launch<T, false, false>(a, small, s);
+hipError_t logits_typed(const HeadLogits& a, int variant, hipStream_t s) {
+    if (a.e) return a.cap > 0.f ? logits_launch<T, true, true>(a, variant, s) : logits_launch<T, true, false>(a, variant, s);
+    return a.cap > 0.f ? logits_launch<T, false, true>(a, variant, s) : logits_launch<T, false, false>(a, variant, s);
 }
 
 template <typename T>
 hipError_t rows_typed(const HeadRows& a, hipStream_t s) {
-    // many tokens: 16 threads each; few: a workgroup each
-    if (a.rows > 256) head_rows_kernel<T, 16><<<(a.rows + 15) / 16, 256, 0, s>>>(a);
-    else head_rows_kernel<T, 256><<<a.rows, 256, 0, s>>>(a);
+    // many tokens: 16 per workgroup, which makes 64-byte pieces of the partials
+    // and, by their number, 16 or 64 threads for each; few: a workgroup each
+    if (a.rows <= 256) head_rows_kernel<T, 256, 1><<<a.rows, 256, 0, s>>>(a);
+    else if (a.nsub <= 128) head_rows_kernel<T, 256, 16><<<(a.rows + 15) / 16, 256, 0, s>>>(a);
+    else head_rows_kernel<T, 1024, 16><<<(a.rows + 15) / 16, 1024, 0, s>>>(a);
     return hipGetLastError();
 }
 
@@ -792,8 +883,8 @@ hipError_t grads_launch(const HeadGrads& a, hipStream_t s) {
 
 }  // namespace
 
-hipError_t launch_head_logits(const HeadLogits& a, int type, bool small, hipStream_t s) {
-    return type == kHeadBf16 ? logits_typed<bf16>(a, small, s) : logits_typed<f16>(a, small, s);
+hipError_t launch_head_logits(const HeadLogits& a, int type, int variant, hipStream_t s) {
+    return type == kHeadBf16 ? logits_typed<bf16>(a, variant, s) : logits_typed<f16>(a, variant, s);
 }
 hipError_t launch_head_rows(const HeadRows& a, int type, hipStream_t s) {
     return type == kHeadBf16 ? rows_typed<bf16>(a, s) : rows_typed<f16>(a, s);

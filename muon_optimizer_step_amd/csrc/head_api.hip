@@ -28,7 +28,8 @@ int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 
 // Offsets into the workspace (-1: not there) and sizes, from the problem alone.
 struct HeadPlan {
-    bool train, small, pack_h, pack_w, copy_h;
+    bool train, pack_h, pack_w, copy_h;
+    int variant, tile_v, tile_t;  // of the logits
     int64_t dim8;                 // dim rounded up to whole chunks
     int64_t piece, pieces;        // tokens per piece
     int64_t rows, cols;           // padded size of a piece's probabilities
@@ -68,6 +69,29 @@ void split_k(int64_t n, int a, int64_t m, int b, int& splits_a, int& splits_b) {
     }
 }
 
+// Kernel for the logits of a piece.  Measured (us, bf16, no gradients):
+//   tokens x vocab x dim      stream  128 x 32  128 x 64  128 x 128  256 x 256
+//   1 x 8192 x 512               6.8       8.5       9.5       10.2       18.5
+//   1 x 32768 x 1024            17.1      14.5      14.7       17.5       30.1
+//   64 x 131072 x 2048           282       123       109        128        144
+//   256 x 32768 x 1024             -         -      28.3       22.5       31.5
+//   2048 x 8192 x 512              -         -         -       24.8       22.6
+//   1024 x 50000 x 1024            -         -         -        114        123
+//   4096 x 8192 x 512              -         -         -       43.6       40.6
+// The last two differ in their rate (a 256 x 256 tile moves half the operand
+// bytes per product) and in the waste of their last round, counted here in
+// rounds of 256 tiles; two 128 x 128 tiles per compute unit overlap, less so
+// where a cap makes the vector work of the tile's end longer (1021 x 50021 x
+// 1000 capped: 161 against 150).
+int logits_variant(int64_t tokens, int64_t vocab, bool cap) {
+    if (tokens <= 32) return vocab < 16384 && tokens <= kHeadStream ? kLogitsStream : kLogitsMid32;
+    if (tokens <= 64) return kLogitsMid64;
+    auto tiles = [&](int64_t edge) { return ((tokens + edge - 1) / edge) * ((vocab + edge - 1) / edge); };
+    const double big = (double)((tiles(256) + kCus - 1) / kCus);
+    const double mid = (cap ? 0.65 : 0.57) * std::max(1.0, (double)tiles(128) / (2 * kCus) + 0.3);
+    return mid < big ? kLogitsMid128 : kLogitsTile;
+}
+
 HeadPlan make_head_plan(const head_loss_t& p) {
     HeadPlan q;
     q.train = p.loss || p.grad_hidden || p.grad_weight;
@@ -88,9 +112,11 @@ HeadPlan make_head_plan(const head_loss_t& p) {
     q.piece = std::min(q.piece, std::max<int64_t>(p.tokens, 1));
     q.pieces = (p.tokens + q.piece - 1) / q.piece;
     q.rows = round_up(q.piece, kHeadPad);
-    q.small = p.tokens <= kHeadSmall;
-    q.sub = q.small ? kHeadSmallSub : kHeadSub;
-    q.nsub = q.small ? (int)(q.cols / kHeadSmallSub) : (int)((p.vocab + kHeadTile - 1) / kHeadTile) * (kHeadTile / kHeadSub);
+    q.variant = logits_variant(q.piece, p.vocab, p.softcap > 0.f);
+    q.tile_v = q.variant == kLogitsTile ? kHeadTile : q.variant == kLogitsStream ? kHeadStreamSub : kHeadMidVocab;
+    q.tile_t = q.variant == kLogitsTile ? kHeadTile : q.variant == kLogitsMid128 ? 128 : q.variant == kLogitsMid32 ? 32 : 64;
+    q.sub = logits_sub(q.variant);
+    q.nsub = (int)(q.variant == kLogitsStream ? q.cols / q.sub : round_up(p.vocab, q.tile_v) / q.sub);
     const int64_t tiles_d = (p.dim + kHeadTile - 1) / kHeadTile;
     const int all_h = (int)(q.cols / kHeadK), all_w = (int)(q.rows / kHeadK);
     split_k(p.grad_hidden ? (q.piece + kHeadTile - 1) / kHeadTile * tiles_d : 0, all_h,
@@ -225,10 +251,10 @@ int enqueue_head(const head_loss_t& p, const HeadPlan& q, uint8_t* ws, hipStream
         a.dim = (int)(q.pack_h && q.pack_w ? q.dim8 : p.dim);
         a.cap = p.softcap;
         a.inv_cap = inv_cap;
-        a.tiles_v = (vocab + kHeadTile - 1) / kHeadTile;
-        a.tiles_t = (tokens + kHeadTile - 1) / kHeadTile;
+        a.tiles_v = (vocab + q.tile_v - 1) / q.tile_v;
+        a.tiles_t = (tokens + q.tile_t - 1) / q.tile_t;
         if (q.train && at == 0) a.scalars = {p.targets, p.token_weights, scalars, p.ignore_index, (int)p.tokens, p.dtype};
-        HEAD_TRY(q.small ? "head_logits_small" : "head_logits", launch_head_logits(a, p.dtype, q.small, s));
+        HEAD_TRY("head_logits", launch_head_logits(a, p.dtype, q.variant, s));
         HeadRows r;
         memset(&r, 0, sizeof(r));
         r.ref = ref;

@@ -6,7 +6,17 @@ import ctypes
 from typing import NamedTuple, Optional
 
 from . import _lib
-from .api import _stream_handle, _torch, _workspace_for
+from .api import _torch, _workspace_for
+
+
+def _stream_handle(stream, device):
+    """The HIP stream of a torch stream, or of the device's current one."""
+    torch = _torch()
+    if stream is not None:
+        return stream.cuda_stream
+    if device is None:
+        return torch.cuda.current_stream().cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _check(t, name: str, dtypes, numel: Optional[int] = None):
