@@ -122,7 +122,7 @@ int adamw8_decode(const void* exp_avg_codes, const float* exp_avg_scale, const v
 #define MUON_HEAD_MAX_TOKENS (1 << 24)
 #define MUON_HEAD_MAX_VOCAB (1 << 22)
 #define MUON_HEAD_MAX_DIM 65536
-#define MUON_HEAD_PIECE_BYTES ((int64_t)1 << 30)
+#define MUON_HEAD_PIECE_BYTES ((int64_t)2 << 30)
 typedef struct head_loss_t {
     const void* hidden;
     const void* weight;

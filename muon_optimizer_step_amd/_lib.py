@@ -28,7 +28,7 @@ MUON_HEAD_FP16 = 1
 MUON_HEAD_MAX_TOKENS = 1 << 24
 MUON_HEAD_MAX_VOCAB = 1 << 22
 MUON_HEAD_MAX_DIM = 65536
-MUON_HEAD_PIECE_BYTES = 1 << 30
+MUON_HEAD_PIECE_BYTES = 2 << 30
 
 
 class MuonTensor(ctypes.Structure):

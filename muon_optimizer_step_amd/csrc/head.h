@@ -41,6 +41,7 @@ struct HeadLogits {
     void* e;                 // nullable; e_rows x e_pitch
     int64_t e_pitch;
     int e_rows;              // rows that exist in e
+    int e_past;            // e is larger than the last cache: written past the caches
     float* ref;              // [sub][stat_pitch]
     float* sum;
     int stat_pitch;
@@ -50,11 +51,15 @@ struct HeadLogits {
     HeadScalars scalars;
 };
 
-// Per token: log-sum-exp, loss, and the factors of the gradient.
+// Per token: log-sum-exp and loss; with e also the probabilities' gradient in
+// its place.
 struct HeadRows {
     const float* ref;
-    float* sum;              // in: partial sums; out (train): factor from e to probability x weight
+    const float* sum;
     int stat_pitch, nsub;
+    void* e;                 // in: fp16 exp2 values; out: probability gradient, input type
+    int64_t e_pitch;
+    int sub;                 // vocabulary entries per partial
     const void* h;
     const void* w;
     int64_t h_pitch, w_pitch;
@@ -64,7 +69,6 @@ struct HeadRows {
     float* nll;
     float* lse;              // nullable
     float* row_weight;       // train: weight of the token in P
-    int* row_target;         // train: its target, -1 for none
     void* copy;              // nullable: rows x copy_pitch, hidden with zeros for tokens that do not count
     int64_t copy_pitch;
     int64_t ignore_index;
@@ -74,26 +78,13 @@ struct HeadRows {
 };
 
 // sum of weight x nll over all tokens of the call; by one more workgroup of the
-// last head_prob launch, or on its own.
+// last head_grads launch, or on its own.
 struct HeadLoss {
     const float* nll;
     const float* row_weight;
     const float* scalars;
     float* loss;             // NULL: nothing to do in this launch
     int tokens;
-};
-
-struct HeadProb {
-    void* e;                 // in: fp16 exp2 values; out: probability gradient, input type
-    int64_t e_pitch;
-    int rows, cols;          // padded
-    const float* ref;
-    const float* factor;     // [sub][stat_pitch]
-    int stat_pitch, sub;
-    const float* row_weight;
-    const int* row_target;
-    float inv_cap;           // 0: no cap
-    HeadLoss loss;
 };
 
 // out[col][d] = sum over k of P(k, col) A[k][d].
@@ -118,6 +109,7 @@ struct HeadGrad {
 // Both gradients of a piece; one without an output has tiles_c == 0.
 struct HeadGrads {
     HeadGrad hidden, weight;
+    HeadLoss loss;
 };
 
 // out[col][d] = sum over the splits' partials, for up to two gradients.
@@ -146,8 +138,8 @@ struct HeadPack {
 
 hipError_t launch_head_logits(const HeadLogits& a, int type, int variant, hipStream_t s);
 hipError_t launch_head_rows(const HeadRows& a, int type, hipStream_t s);
-hipError_t launch_head_prob(const HeadProb& a, int type, hipStream_t s);
-hipError_t launch_head_grads(const HeadGrads& a, int type, hipStream_t s);
+hipError_t launch_head_prob(const HeadRows& a, int type, hipStream_t s);
+hipError_t launch_head_grads(const HeadGrads& a, int type, bool mid, hipStream_t s);
 hipError_t launch_head_join(const HeadJoin& a, int type, hipStream_t s);
 hipError_t launch_head_pack(const HeadPack& a, hipStream_t s);
 hipError_t launch_head_loss(const HeadLoss& a, hipStream_t s);

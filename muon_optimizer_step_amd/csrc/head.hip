@@ -143,13 +143,16 @@ struct RowOperand {
 // one 16-byte store in a 16-bit type.
 __device__ inline int swap23(int r) { return (r & 0x13) | ((r & 4) << 1) | ((r & 8) >> 1); }
 
-// A column operand (K strided): 64 rows of K x 256 columns per stage (512 bytes
-// a row), read with the transposing LDS read.  The 16-byte chunk c of row k is
-// in slot c ^ 2 f(k % 4), f = 0, 2, 5, 7: the 4 rows x 32 bytes that 16 lanes
-// read, and the 4 rows x 64 bytes of 32 lanes, lie in different banks.
-template <int WAVES>
+// A column operand (K strided): 64 rows of K x COLS columns per stage, read
+// with the transposing LDS read.  The 16-byte chunk c of row k is in slot c ^ 2
+// f(k % 4), f = 0, 2, 5, 7: the 4 rows x 32 bytes that 16 lanes read, and the 4
+// rows x 64 bytes of 32 lanes, lie in different banks.
+template <int COLS, int WAVES>
 struct ColOperand {
-    static constexpr int kLoads = kHeadK / 2 / WAVES;
+    static constexpr int kRow = COLS * 2, kChunks = COLS / 8, kPer = 1024 / kRow;   // bytes and chunks of a row, rows per instruction
+    static constexpr int kBytes = kHeadK * kRow;
+    static constexpr int kLoads = kHeadK / kPer / WAVES;
+    static_assert(kChunks >= 16, "the slot of a chunk is in its row");
     const uint8_t* base;
     int64_t pitch;
     uint32_t off[kLoads];
@@ -162,8 +165,8 @@ struct ColOperand {
         const int last = (cols_pad - col0) / 8 - 1;
 #pragma unroll
         for (int j = 0; j < kLoads; ++j) {
-            row[j] = 2 * (j * WAVES + wave) + lane / 32;
-            chunk[j] = min((lane % 32) ^ slot_xor(row[j]), last) * 16;
+            row[j] = kPer * (j * WAVES + wave) + lane / kChunks;
+            chunk[j] = min((lane % kChunks) ^ slot_xor(row[j]), last) * 16;
             off[j] = (uint32_t)(row[j] * pitch) + chunk[j];
         }
     }
@@ -188,8 +191,8 @@ struct ColOperand {
         quad += 4 * ((lane / 16) % 2);
         const int at = ((col / 8 + quad / 2) ^ slot_xor(k)) * 16 + (quad & 1) * 8;
         typedef __attribute__((address_space(3))) short4v lds_short4;
-        const u32x2 a = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4*)(lds + k * 512 + at)));
-        const u32x2 b = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4*)(lds + (k + 4) * 512 + at)));
+        const u32x2 a = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4*)(lds + k * kRow + at)));
+        const u32x2 b = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4*)(lds + (k + 4) * kRow + at)));
         u32x4 r;
         r[0] = a[0]; r[1] = a[1]; r[2] = b[0]; r[3] = b[1];
         return r;
@@ -323,8 +326,15 @@ __device__ inline void head_scalars(const HeadScalars& a, void* lds) {
 // ---------------------------------------------------------------- logits
 // What one wave does with its logits: acc[tv][tt] holds 32 vocabulary entries
 // (v0 + 32 tv + 16 p + 8 (l / 32) + i in register 8 p + i) of token t0 + 32 tt + l % 32.
-template <int TV, int TT, bool STORE, bool CAP>
-__device__ inline void logits_epilogue(const HeadLogits& a, floatx16 (&acc)[TV][TT], int v0, int t0, int sub, int lane) {
+// e goes to memory through LDS (`stage`, this wave's 512 TV bytes per 8 tokens x
+// 4), so that a store instruction writes whole rows of 32 TV entries instead of
+// 32 bytes to each of 32 tokens.
+enum { kNoStore = 0, kStore, kStorePast };    // e not kept; kept; kept, written past the caches
+template <int TV> constexpr int kEpilogueBytes = 32 * TV * 64;
+template <int TV, int TT, int STORE, bool CAP>
+__device__ inline void logits_epilogue(const HeadLogits& a, floatx16 (&acc)[TV][TT], int v0, int t0, int sub, int lane,
+                                       uint8_t* stage) {
+    constexpr int kChunks = 4 * TV;       // 16-byte chunks of a token's row; chunk c of row r in slot c ^ (r % kChunks)
     const int half = lane / 32;
     const bool whole = v0 + 32 * TV <= a.vocab;
 #pragma unroll
@@ -358,12 +368,26 @@ __device__ inline void logits_epilogue(const HeadLogits& a, floatx16 (&acc)[TV][
                     e[i] = __builtin_amdgcn_exp2f(fmaf(acc[tv][tt][8 * p + i], kLog2e, minus));
                     sum += e[i];
                 }
-                if constexpr (STORE) {
-                    const int v = v0 + 32 * tv + 16 * p + 8 * half;
-                    if (token < a.e_rows && v < a.e_pitch)
-                        *reinterpret_cast<u32x4*>(static_cast<f16*>(a.e) + token * a.e_pitch + v) = pack8<f16>(e);
+                if constexpr (STORE != kNoStore) {
+                    const int c = 4 * tv + 2 * p + half, r = lane % 32;
+                    *reinterpret_cast<u32x4*>(stage + (r * kChunks + (c ^ (r % kChunks))) * 16) = pack8<f16>(e);
                 }
             }
+        if constexpr (STORE != kNoStore) {
+            // the same wave's data: LDS keeps its order
+#pragma unroll
+            for (int k = 0; k < kChunks / 2; ++k) {
+                const int r = k * (kWave / kChunks) + lane / kChunks, c = lane % kChunks;
+                const u32x4 w = *reinterpret_cast<const u32x4*>(stage + (r * kChunks + (c ^ (r % kChunks))) * 16);
+                const int64_t row = t0 + 32 * tt + r;
+                const int v = v0 + 8 * c;
+                u32x4* dst = reinterpret_cast<u32x4*>(static_cast<f16*>(a.e) + row * a.e_pitch + v);
+                if (row < a.e_rows && v < a.e_pitch) {
+                    if constexpr (STORE == kStorePast) __builtin_nontemporal_store(w, dst);
+                    else *dst = w;
+                }
+            }
+        }
         sum += __shfl_xor(sum, 32, kWave);
         if (half == 0 && token < a.stat_pitch) {
             a.ref[(int64_t)sub * a.stat_pitch + token] = ref;
@@ -383,7 +407,7 @@ __device__ inline void tile_of(const HeadLogits& a, int item, int& tile_v, int& 
 
 // Tile of 256 vocabulary entries x 256 tokens: 8 waves of 128 x 64, 32x32x16
 // MFMAs.
-template <typename T, bool STORE, bool CAP>
+template <typename T, int STORE, bool CAP>
 __global__ __launch_bounds__(512, 2) void head_logits_kernel(const HeadLogits a) {
     constexpr int WV = 2, WT = 4, TV = 4, TT = 2, BV = WV * TV * 32, BT = WT * TT * 32, NW = WV * WT;
     static_assert(TV * 32 == logits_sub(kLogitsTile), "one partial per wave");
@@ -414,7 +438,9 @@ __global__ __launch_bounds__(512, 2) void head_logits_kernel(const HeadLogits a)
         [&](int kt, int slot, int u) { H.load(lds_address(lds) + slot * kOperand, u, kt, a.dim, wave); },
         [&](int slot, int i, int kc) { return Op::frag(lds + slot * kOperand, arow + 32 * i, kc, lane); },
         [&](int slot, int j, int kc) { return Op::frag(lds + slot * kOperand, brow + 32 * j, kc, lane); });
-    logits_epilogue<TV, TT, STORE, CAP>(a, acc, tile_v * BV + wv * TV * 32, tile_t * BT + wt * TT * 32, tile_v * WV + wv, lane);
+    if (STORE != kNoStore) bare_barrier();      // every wave is done with the operands, whose slots e passes through
+    logits_epilogue<TV, TT, STORE, CAP>(a, acc, tile_v * BV + wv * TV * 32, tile_t * BT + wt * TT * 32, tile_v * WV + wv, lane,
+                                        lds + wave * kEpilogueBytes<TV>);
 }
 
 // Tile of 128 vocabulary entries x 32, 64 or 128 tokens, two workgroups of 4
@@ -429,7 +455,7 @@ template <int TOKENS> constexpr size_t mid_bytes() {
     return (size_t)MidTile<TOKENS>::kBuffers * (kHeadMidVocab + TOKENS) * kHeadK * 2;
 }
 
-template <typename T, int TOKENS, bool STORE, bool CAP>
+template <typename T, int TOKENS, int STORE, bool CAP>
 __global__ __launch_bounds__(256, 2) void head_logits_mid_kernel(const HeadLogits a) {
     typedef MidTile<TOKENS> M;
     constexpr int WV = M::WV, WT = M::WT, TV = M::TV, TT = M::TT, NW = WV * WT, kBuffers = M::kBuffers;
@@ -487,17 +513,19 @@ __global__ __launch_bounds__(256, 2) void head_logits_mid_kernel(const HeadLogit
                 for (int j = 0; j < TT; ++j) acc[i][j] = mfma<T>(fa[i], fb[j], acc[i][j]);
         }
     }
+    if (STORE != kNoStore) bare_barrier();
     logits_epilogue<TV, TT, STORE, CAP>(a, acc, tile_v * kHeadMidVocab + wv * TV * 32, tile_t * TOKENS + wt * TT * 32,
-                                        tile_v * WV + wv, lane);
+                                        tile_v * WV + wv, lane, lds + wave * kEpilogueBytes<TV>);
 }
 
 // Up to 32 tokens and a small vocabulary, where there is little to read and
 // latency counts: a workgroup for every 32 vocabulary rows, operands straight
 // from memory (each row of W is used once), the waves take every fourth 128
 // bytes of K and meet in LDS.
-template <typename T, bool STORE, bool CAP>
+template <typename T, int STORE, bool CAP>
 __global__ __launch_bounds__(256) void head_logits_stream_kernel(const HeadLogits a) {
     __shared__ __align__(16) float part[4][16][kWave];
+    __shared__ __align__(16) uint8_t stage[kEpilogueBytes<1>];
     if (blockIdx.x == gridDim.x - 1) {
         if (a.scalars.scalars) head_scalars<256>(a.scalars, part);
         return;
@@ -530,38 +558,41 @@ __global__ __launch_bounds__(256) void head_logits_stream_kernel(const HeadLogit
     floatx16 one[1][1];
 #pragma unroll
     for (int r = 0; r < 16; ++r) one[0][0][r] = (part[0][r][lane] + part[1][r][lane]) + (part[2][r][lane] + part[3][r][lane]);
-    logits_epilogue<1, 1, STORE, CAP>(a, one, v0, 0, blockIdx.x, lane);
+    logits_epilogue<1, 1, STORE, CAP>(a, one, v0, 0, blockIdx.x, lane, stage);
 }
 
 // ---------------------------------------------------------------- rows
-// THREADS threads on R tokens, THREADS / R for each: the sub-tiles' partials, and
-// the target's logit as a dot product of its own, joined over a token's threads
-// in an order that depends on THREADS and R only.
+// Two partials joined: the larger reference, the sums in units of it.
+__device__ inline void join_sums(float& top, float& sum, float top2, float sum2) {
+    const float m = fmaxf(top, top2);
+    // both -infinity: vocabulary padding only, nothing to add
+    sum = m == -INFINITY ? sum + sum2 : sum * __builtin_amdgcn_exp2f(top - m) + sum2 * __builtin_amdgcn_exp2f(top2 - m);
+    top = m;
+}
+
+// THREADS threads on R tokens, THREADS / R for each (thread t: token t % R): joins
+// the sub-tiles' partials of a token, in an order that depends on THREADS and R
+// only, to its base-2 log-sum-exp, and with `first` computes the target's logit as
+// a dot product of its own, writes loss and log-sum-exp and the copy of
+// hidden.  Every thread returns its token's values.
+struct Row {
+    float lse2, weight;      // weight in P; 0 for tokens that do not count, NaN for a target out of range
+    int target;              // -1 for none
+};
 template <typename T, int THREADS, int R>
-__global__ __launch_bounds__(THREADS) void head_rows_kernel(const HeadRows a) {
+__device__ inline Row head_row(const HeadRows& a, int row, bool first, float (*red)[THREADS / kWave][R]) {
     constexpr int S = THREADS / R, kWaves = THREADS / kWave;
-    __shared__ float red[3][kWaves][R];
     const int r = threadIdx.x % R, s = threadIdx.x / R;
-    const int row = blockIdx.x * R + r;
     const bool live = row < a.tokens, held = row < a.rows;
-    // two partials joined: the larger reference, the sums in units of it
-    auto join = [](float& top, float& sum, float top2, float sum2) {
-        const float m = fmaxf(top, top2);
-        // both -infinity: vocabulary padding only, nothing to add
-        sum = m == -INFINITY ? sum + sum2
-                             : sum * __builtin_amdgcn_exp2f(top - m) + sum2 * __builtin_amdgcn_exp2f(top2 - m);
-        top = m;
-    };
     float top = -INFINITY, sum = 0.f;
     if (live)
 #pragma unroll 4
         for (int k = s; k < a.nsub; k += S)
-            join(top, sum, a.ref[(int64_t)k * a.stat_pitch + row], a.sum[(int64_t)k * a.stat_pitch + row]);
-
+            join_sums(top, sum, a.ref[(int64_t)k * a.stat_pitch + row], a.sum[(int64_t)k * a.stat_pitch + row]);
     const int64_t t = live ? a.targets[row] : a.ignore_index;
     const bool counted = live && t != a.ignore_index, valid = t >= 0 && t < a.vocab;
     float dot = 0.f;
-    if (counted && valid) {
+    if (first && counted && valid) {
         const T* h = static_cast<const T*>(a.h) + (int64_t)row * a.h_pitch;
         const T* w = static_cast<const T*>(a.w) + t * a.w_pitch;
         for (int d = 8 * s; d < a.dim; d += 8 * S) {
@@ -572,9 +603,15 @@ __global__ __launch_bounds__(THREADS) void head_rows_kernel(const HeadRows a) {
             for (int i = 0; i < 8; ++i) dot = fmaf(x[i], y[i], dot);
         }
     }
+    if (first && a.copy && held)
+        for (int d = 8 * s; d < a.dim; d += 8 * S) {
+            u32x4 v = {0u, 0u, 0u, 0u};
+            if (counted) v = *reinterpret_cast<const u32x4*>(static_cast<const T*>(a.h) + (int64_t)row * a.h_pitch + d);
+            *reinterpret_cast<u32x4*>(static_cast<T*>(a.copy) + (int64_t)row * a.copy_pitch + d) = v;
+        }
 #pragma unroll
     for (int off = R; off < kWave; off <<= 1) {
-        join(top, sum, __shfl_xor(top, off, kWave), __shfl_xor(sum, off, kWave));
+        join_sums(top, sum, __shfl_xor(top, off, kWave), __shfl_xor(sum, off, kWave));
         dot += __shfl_xor(dot, off, kWave);
     }
     if (threadIdx.x % kWave < R) {
@@ -588,41 +625,90 @@ __global__ __launch_bounds__(THREADS) void head_rows_kernel(const HeadRows a) {
     dot = red[2][0][r];
 #pragma unroll
     for (int w = 1; w < kWaves; ++w) {
-        join(top, sum, red[0][w][r], red[1][w][r]);
+        join_sums(top, sum, red[0][w][r], red[1][w][r]);
         dot += red[2][w][r];
     }
-    const float lse2 = top + __builtin_amdgcn_logf(sum);
-    if (a.cap > 0.f) dot = capped(dot, a.cap, a.inv_cap);
-    if (a.copy && held)
-        for (int d = 8 * s; d < a.dim; d += 8 * S) {
-            u32x4 v = {0u, 0u, 0u, 0u};
-            if (counted) v = *reinterpret_cast<const u32x4*>(static_cast<const T*>(a.h) + (int64_t)row * a.h_pitch + d);
-            *reinterpret_cast<u32x4*>(static_cast<T*>(a.copy) + (int64_t)row * a.copy_pitch + d) = v;
+    Row out;
+    out.lse2 = top + __builtin_amdgcn_logf(sum);
+    out.target = counted && valid ? (int)t : -1;
+    out.weight = 0.f;
+    if (counted) out.weight = valid ? (a.train ? (a.weights ? a.weights[row] : 1.f) * a.scalars[0] : 1.f) : __builtin_nanf("");
+    if (first && s == 0) {
+        if (live) {
+            if (a.cap > 0.f) dot = capped(dot, a.cap, a.inv_cap);
+            const float lse = out.lse2 * kLn2;
+            float nll = valid ? lse - dot : __builtin_nanf("");
+            if (nll < 0.f) nll = 0.f;       // the target's logit is rounded apart from the sum it is part of
+            a.nll[row] = counted ? nll : 0.f;
+            if (a.lse) a.lse[row] = counted ? lse : 0.f;
         }
-    float weight = 0.f;
-    if (counted) weight = valid ? (a.train ? (a.weights ? a.weights[row] : 1.f) * a.scalars[0] : 1.f) : __builtin_nanf("");
-    if (s == 0 && live) {
-        const float lse = lse2 * kLn2;
-        float nll = valid ? lse - dot : __builtin_nanf("");
-        if (nll < 0.f) nll = 0.f;       // the target's logit is rounded apart from the sum it is part of
-        a.nll[row] = counted ? nll : 0.f;
-        if (a.lse) a.lse[row] = counted ? lse : 0.f;
+        if (a.train && held) a.row_weight[row] = out.weight;
     }
-    if (!a.train || !held) return;
-    if (s == 0) {
-        a.row_weight[row] = weight;
-        a.row_target[row] = counted && valid ? (int)t : -1;
-    }
-    for (int k = s; k < a.nsub; k += S) {
-        const int64_t i = (int64_t)k * a.stat_pitch + row;
-        a.sum[i] = counted ? __builtin_amdgcn_exp2f(a.ref[i] - lse2) * weight : 0.f;
+    return out;
+}
+
+template <typename T, int THREADS, int R>
+__global__ __launch_bounds__(THREADS) void head_rows_kernel(const HeadRows a) {
+    __shared__ float red[3][THREADS / kWave][R];
+    head_row<T, THREADS, R>(a, blockIdx.x * R + threadIdx.x % R, true, red);
+}
+
+// ---------------------------------------------------------------- probabilities
+// 8 tokens x `across` columns per workgroup: first the tokens' values (again by
+// each workgroup of their columns), then e -> P in place, 8 columns of the 8
+// tokens per thread at a time.  HBM-bound: reads and writes 2 bytes an entry.
+constexpr int kProbRows = 8;
+template <typename T, bool CAP, bool PAST>
+__global__ __launch_bounds__(256) void head_prob_kernel(const HeadRows a, int blocks, int across) {
+    __shared__ float red[3][4][kProbRows];
+    __shared__ Row rows[kProbRows];
+    const int row0 = blockIdx.x / blocks * kProbRows, col0 = blockIdx.x % blocks * across;
+    const Row mine = head_row<T, 256, kProbRows>(a, row0 + threadIdx.x % kProbRows, col0 == 0, red);
+    if (threadIdx.x < kProbRows) rows[threadIdx.x] = mine;
+    __syncthreads();
+    const int end = (int)min<int64_t>(col0 + across, a.e_pitch), live = min(kProbRows, a.rows - row0);
+    for (int col = col0 + 8 * threadIdx.x; col < end; col += 8 * 256) {
+        uint8_t* at = static_cast<uint8_t*>(a.e) + ((int64_t)row0 * a.e_pitch + col) * 2;
+        const float* ref = a.ref + (int64_t)(col / a.sub) * a.stat_pitch + row0;
+        u32x4 w[kProbRows];
+        float c[kProbRows];
+#pragma unroll
+        for (int k = 0; k < kProbRows; ++k) {
+            if (k >= live) continue;
+            const u32x4* src = reinterpret_cast<const u32x4*>(at + (int64_t)k * a.e_pitch * 2);
+            w[k] = PAST ? __builtin_nontemporal_load(src) : *src;
+            c[k] = ref[k];
+        }
+#pragma unroll
+        for (int k = 0; k < kProbRows; ++k) {
+            if (k >= live) continue;
+            const float weight = rows[k].weight;
+            u32x4 out = {0u, 0u, 0u, 0u};
+            if (weight != 0.f) {     // whatever an ignored token's logits are, its gradient is zero
+                const float f = __builtin_amdgcn_exp2f(c[k] - rows[k].lse2) * weight;
+                const int target = rows[k].target - col;
+                float e[8], p[8];
+                unpack8<f16>(w[k], e);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    p[i] = fmaf(e[i], f, i == target ? -weight : 0.f);
+                    if (CAP && e[i] > 0.f) {
+                        const float x = (c[k] + __builtin_amdgcn_logf(e[i])) * (kLn2 * a.inv_cap);
+                        p[i] *= fmaf(-x, x, 1.0f);
+                    }
+                }
+                out = pack8<T>(p);
+            }
+            u32x4* dst = reinterpret_cast<u32x4*>(at + (int64_t)k * a.e_pitch * 2);
+            if constexpr (PAST) __builtin_nontemporal_store(out, dst);
+            else *dst = out;
+        }
     }
 }
 
 // sum of weight x nll, in an order that depends on nothing but THREADS.
 template <int THREADS>
-__device__ inline void head_loss_sum(const HeadLoss& a) {
-    __shared__ float red[THREADS / kWave];
+__device__ inline void head_loss_sum(const HeadLoss& a, float* red) {
     float sum = 0.f;
 #pragma unroll 4
     for (int i = threadIdx.x; i < a.tokens; i += THREADS) sum = fmaf(a.row_weight[i], a.nll[i], sum);
@@ -634,96 +720,24 @@ __device__ inline void head_loss_sum(const HeadLoss& a) {
     *a.loss = sum * a.scalars[1];
 }
 
-// ---------------------------------------------------------------- probabilities
-// 8 rows x 2048 columns of the piece per workgroup, 8 columns of a row per thread.
-template <typename T, bool CAP>
-__global__ __launch_bounds__(256) void head_prob_kernel(const HeadProb a) {
-    if (blockIdx.x == gridDim.x - 1) {
-        if (a.loss.loss) head_loss_sum<256>(a.loss);
-        return;
-    }
-    const int across = (a.cols + 2047) / 2048, row0 = blockIdx.x / across * 8;
-    const int col = (blockIdx.x % across * 256 + threadIdx.x) * 8;
-    if (col >= a.cols) return;
-    const int sub = col / a.sub;
-#pragma unroll 2
-    for (int k = 0; k < 8; ++k) {
-        const int row = row0 + k;
-        if (row >= a.rows) return;
-        uint8_t* at = static_cast<uint8_t*>(a.e) + ((int64_t)row * a.e_pitch + col) * 2;
-        const float weight = a.row_weight[row];
-        u32x4 out = {0u, 0u, 0u, 0u};
-        if (weight != 0.f) {     // whatever an ignored token's logits are, its gradient is zero
-            const float f = a.factor[(int64_t)sub * a.stat_pitch + row];
-            const int target = a.row_target[row] - col;
-            float e[8], p[8];
-            unpack8<f16>(*reinterpret_cast<const u32x4*>(at), e);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                p[i] = fmaf(e[i], f, i == target ? -weight : 0.f);
-                if (CAP && e[i] > 0.f) {
-                    const float x = (a.ref[(int64_t)sub * a.stat_pitch + row] + __builtin_amdgcn_logf(e[i])) * (kLn2 * a.inv_cap);
-                    p[i] *= fmaf(-x, x, 1.0f);
-                }
-            }
-            out = pack8<T>(p);
-        }
-        *reinterpret_cast<u32x4*>(at) = out;
-    }
-}
-
 // ---------------------------------------------------------------- gradients
 // Tile of 256 output columns d x 256 rows, K split over workgroups where the
 // tiles alone would leave compute units idle.  A = W or H with K strided; P with K
 // contiguous (dH, K the vocabulary) or strided (dW, K the tokens).
-template <typename T, bool KTOKEN>
-__device__ inline void head_grad_tile(const HeadGrad& a, int item, uint8_t* lds) {
-    constexpr int WD = 2, WC = 4, TD = 4, TC = 2, NW = WD * WC;
-    const int split = item / (a.tiles_c * a.tiles_d), tile = item - split * a.tiles_c * a.tiles_d;
-    const int tile_c = tile / a.tiles_d, tile_d = tile % a.tiles_d;
-    const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), wd = wave / WC, wc = wave % WC;
-    const int d0 = tile_d * kHeadTile, c0 = tile_c * kHeadTile;
-    const int s0 = split * a.stages_per_split, s1 = min(a.k / kHeadK, s0 + a.stages_per_split);
-
-    typedef ColOperand<NW> COp;
-    typedef RowOperand<kHeadTile, NW> ROp;
-    COp A, Q;
-    ROp P;
-    A.init(a.a, a.a_pitch * 2, d0, (a.dim + 7) / 8 * 8, wave, lane);
-    if constexpr (KTOKEN) Q.init(a.p, a.p_pitch * 2, c0, a.p_cols, wave, lane);
-    else P.init(a.p, a.p_pitch * 2, c0, a.p_rows, wave, lane);
-    floatx16 acc[TD][TC];
-#pragma unroll
-    for (int i = 0; i < TD; ++i)
-#pragma unroll
-        for (int j = 0; j < TC; ++j) acc[i][j] = floatx16(0.f);
-    k_loop<T, TD, TC>(
-        acc, s1 - s0,
-        [&](int kt, int slot, int u) {
-            A.load(lds_address(lds) + slot * kOperand, u, (int64_t)(s0 + kt) * kHeadK, a.a_rows, wave);
-        },
-        [&](int kt, int slot, int u) {
-            if constexpr (KTOKEN) Q.load(lds_address(lds) + slot * kOperand, u, (int64_t)(s0 + kt) * kHeadK, a.p_rows, wave);
-            else P.load(lds_address(lds) + slot * kOperand, u, s0 + kt, a.k, wave);
-        },
-        [&](int slot, int i, int kc) {
-            return COp::template frag<true>(lds + slot * kOperand, wd * TD * 32 + 32 * i, kc, lane);
-        },
-        [&](int slot, int j, int kc) {
-            const int c = wc * TC * 32 + 32 * j;
-            if constexpr (KTOKEN) return COp::template frag<false>(lds + slot * kOperand, c, kc, lane);
-            else return ROp::frag(lds + slot * kOperand, c + lane % 32, kc, lane);
-        });
+// A wave's sums to memory: acc[i][j] holds columns d0 + 32 i + 16 p + 8 (l / 32) + e
+// (register 8 p + e) of row c0 + 32 j + l % 32.
+template <typename T, int TD, int TC>
+__device__ inline void grad_epilogue(const HeadGrad& a, floatx16 (&acc)[TD][TC], int split, int d0, int c0, int lane) {
     const float unscale = a.scalars[1];
 #pragma unroll
     for (int j = 0; j < TC; ++j) {
-        const int c = c0 + wc * TC * 32 + 32 * j + lane % 32;
+        const int c = c0 + 32 * j + lane % 32;
         if (c >= a.cols) continue;
 #pragma unroll
         for (int i = 0; i < TD; ++i)
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
-                const int d = d0 + wd * TD * 32 + 32 * i + 16 * p + 8 * (lane / 32);
+                const int d = d0 + 32 * i + 16 * p + 8 * (lane / 32);
                 if (d >= a.dim) continue;
                 float v[8];
 #pragma unroll
@@ -748,22 +762,146 @@ __device__ inline void head_grad_tile(const HeadGrad& a, int item, uint8_t* lds)
     }
 }
 
+// Which tile and part of K an item is.
+struct GradItem {
+    int split, d0, c0, s0, s1;
+};
+__device__ inline GradItem grad_item(const HeadGrad& a, int item, int edge) {
+    GradItem g;
+    g.split = item / (a.tiles_c * a.tiles_d);
+    const int tile = item - g.split * a.tiles_c * a.tiles_d;
+    g.c0 = tile / a.tiles_d * edge;
+    g.d0 = tile % a.tiles_d * edge;
+    g.s0 = g.split * a.stages_per_split;
+    g.s1 = min(a.k / kHeadK, g.s0 + a.stages_per_split);
+    return g;
+}
+
+// 256 x 256, 8 waves of 128 x 64.
+template <typename T, bool KTOKEN>
+__device__ inline void head_grad_tile(const HeadGrad& a, int item, uint8_t* lds) {
+    constexpr int WD = 2, WC = 4, TD = 4, TC = 2, NW = WD * WC;
+    static_assert(WD * TD * 32 == kHeadTile && WC * TC * 32 == kHeadTile, "tile");
+    const GradItem g = grad_item(a, item, kHeadTile);
+    const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), wd = wave / WC, wc = wave % WC;
+    typedef ColOperand<kHeadTile, NW> COp;
+    typedef RowOperand<kHeadTile, NW> ROp;
+    COp A, Q;
+    ROp P;
+    A.init(a.a, a.a_pitch * 2, g.d0, (a.dim + 7) / 8 * 8, wave, lane);
+    if constexpr (KTOKEN) Q.init(a.p, a.p_pitch * 2, g.c0, a.p_cols, wave, lane);
+    else P.init(a.p, a.p_pitch * 2, g.c0, a.p_rows, wave, lane);
+    floatx16 acc[TD][TC];
+#pragma unroll
+    for (int i = 0; i < TD; ++i)
+#pragma unroll
+        for (int j = 0; j < TC; ++j) acc[i][j] = floatx16(0.f);
+    k_loop<T, TD, TC>(
+        acc, g.s1 - g.s0,
+        [&](int kt, int slot, int u) {
+            A.load(lds_address(lds) + slot * kOperand, u, (int64_t)(g.s0 + kt) * kHeadK, a.a_rows, wave);
+        },
+        [&](int kt, int slot, int u) {
+            if constexpr (KTOKEN) Q.load(lds_address(lds) + slot * kOperand, u, (int64_t)(g.s0 + kt) * kHeadK, a.p_rows, wave);
+            else P.load(lds_address(lds) + slot * kOperand, u, g.s0 + kt, a.k, wave);
+        },
+        [&](int slot, int i, int kc) {
+            return COp::template frag<true>(lds + slot * kOperand, wd * TD * 32 + 32 * i, kc, lane);
+        },
+        [&](int slot, int j, int kc) {
+            const int c = wc * TC * 32 + 32 * j;
+            if constexpr (KTOKEN) return COp::template frag<false>(lds + slot * kOperand, c, kc, lane);
+            else return ROp::frag(lds + slot * kOperand, c + lane % 32, kc, lane);
+        });
+    grad_epilogue<T, TD, TC>(a, acc, g.split, g.d0 + wd * TD * 32, g.c0 + wc * TC * 32, lane);
+}
+
+// 128 x 128, 4 waves of 64 x 64, two workgroups per compute unit: for problems
+// whose few 256 x 256 tiles would need K split many times (each split's sums
+// go to memory and back), and output widths that waste much of a larger tile.
+constexpr int kMidEdge = 128;
+constexpr size_t kMidGradBytes = (size_t)2 * 2 * kMidEdge * kHeadK * 2;
+template <typename T, bool KTOKEN>
+__device__ inline void head_grad_mid_tile(const HeadGrad& a, int item, uint8_t* lds) {
+    constexpr int WD = 2, WC = 2, TD = 2, TC = 2, NW = WD * WC;
+    static_assert(WD * TD * 32 == kMidEdge && WC * TC * 32 == kMidEdge, "tile");
+    const GradItem g = grad_item(a, item, kMidEdge);
+    const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), wd = wave / WC, wc = wave % WC;
+    typedef ColOperand<kMidEdge, NW> COp;
+    typedef RowOperand<kMidEdge, NW> ROp;
+    constexpr int kStage = COp::kBytes + ROp::kBytes;
+    static_assert(2 * kStage == kMidGradBytes && COp::kBytes == ROp::kBytes, "LDS");
+    COp A, Q;
+    ROp P;
+    A.init(a.a, a.a_pitch * 2, g.d0, (a.dim + 7) / 8 * 8, wave, lane);
+    if constexpr (KTOKEN) Q.init(a.p, a.p_pitch * 2, g.c0, a.p_cols, wave, lane);
+    else P.init(a.p, a.p_pitch * 2, g.c0, a.p_rows, wave, lane);
+    auto load = [&](int kt) {
+        const uint32_t at = lds_address(lds) + (kt - g.s0) % 2 * kStage;
+#pragma unroll
+        for (int u = 0; u < COp::kLoads; ++u) A.load(at, u, (int64_t)kt * kHeadK, a.a_rows, wave);
+#pragma unroll
+        for (int u = 0; u < COp::kLoads; ++u) {
+            if constexpr (KTOKEN) Q.load(at + COp::kBytes, u, (int64_t)kt * kHeadK, a.p_rows, wave);
+            else P.load(at + COp::kBytes, u, kt, a.k, wave);
+        }
+    };
+    floatx16 acc[TD][TC];
+#pragma unroll
+    for (int i = 0; i < TD; ++i)
+#pragma unroll
+        for (int j = 0; j < TC; ++j) acc[i][j] = floatx16(0.f);
+    if (g.s0 < g.s1) load(g.s0);
+    for (int kt = g.s0; kt < g.s1; ++kt) {
+        wait_loads<0>();
+        wait_lds();
+        bare_barrier();      // stage kt is in LDS, and every wave is done with stage kt - 1
+        if (kt + 1 < g.s1) load(kt + 1);
+        const uint8_t* ta = lds + (kt - g.s0) % 2 * kStage;
+        const uint8_t* tp = ta + COp::kBytes;
+#pragma unroll
+        for (int kc = 0; kc < kHeadK / 16; ++kc) {
+            u32x4 fa[TD], fb[TC];
+#pragma unroll
+            for (int i = 0; i < TD; ++i) fa[i] = COp::template frag<true>(ta, wd * TD * 32 + 32 * i, kc, lane);
+#pragma unroll
+            for (int j = 0; j < TC; ++j) {
+                const int c = wc * TC * 32 + 32 * j;
+                if constexpr (KTOKEN) fb[j] = COp::template frag<false>(tp, c, kc, lane);
+                else fb[j] = ROp::frag(tp, c + lane % 32, kc, lane);
+            }
+#pragma unroll
+            for (int i = 0; i < TD; ++i)
+#pragma unroll
+                for (int j = 0; j < TC; ++j) acc[i][j] = mfma<T>(fa[i], fb[j], acc[i][j]);
+        }
+    }
+    grad_epilogue<T, TD, TC>(a, acc, g.split, g.d0 + wd * TD * 32, g.c0 + wc * TC * 32, lane);
+}
+
 // Both gradients of a piece in one launch, so that their tiles fill the
 // compute units together.
-template <typename T>
-__global__ __launch_bounds__(512, 2) void head_grads_kernel(const HeadGrads a) {
+template <typename T, bool MID>
+__global__ __launch_bounds__(MID ? 256 : 512, 2) void head_grads_kernel(const HeadGrads a) {
     extern __shared__ __align__(16) uint8_t lds[];
     // each XCD an equal number of items and its share of both kinds, those with K
     // the vocabulary (the longer ones) first
     const int items_h = a.hidden.tiles_c * a.hidden.tiles_d * a.hidden.splits;
     const int items_w = a.weight.tiles_c * a.weight.tiles_d * a.weight.splits;
+    if (blockIdx.x == gridDim.x - 1) {
+        if (a.loss.loss) head_loss_sum<MID ? 256 : 512>(a.loss, reinterpret_cast<float*>(lds));
+        return;
+    }
     const int per = gridDim.x / kXcds, xcd = blockIdx.x % kXcds, at = blockIdx.x / kXcds;
     const int begin = (int)((int64_t)xcd * items_h / kXcds), end = (int)((int64_t)(xcd + 1) * items_h / kXcds);
     if (at < end - begin) {
-        head_grad_tile<T, false>(a.hidden, begin + at, lds);
+        if constexpr (MID) head_grad_mid_tile<T, false>(a.hidden, begin + at, lds);
+        else head_grad_tile<T, false>(a.hidden, begin + at, lds);
     } else {
         const int i = xcd * per - begin + at - (end - begin);
-        if (i < items_w) head_grad_tile<T, true>(a.weight, i, lds);
+        if (i >= items_w) return;
+        if constexpr (MID) head_grad_mid_tile<T, true>(a.weight, i, lds);
+        else head_grad_tile<T, true>(a.weight, i, lds);
     }
 }
 
@@ -815,14 +953,17 @@ __global__ __launch_bounds__(256) void head_pack_kernel(const HeadPack a) {
     }
 }
 
-__global__ __launch_bounds__(1024) void head_loss_kernel(const HeadLoss a) { head_loss_sum<1024>(a); }
+__global__ __launch_bounds__(1024) void head_loss_kernel(const HeadLoss a) {
+    __shared__ float red[1024 / kWave];
+    head_loss_sum<1024>(a, red);
+}
 
 template <typename K>
 hipError_t allow_lds(K kernel, size_t bytes) {
     return hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
 }
 
-template <typename T, int TOKENS, bool STORE, bool CAP>
+template <typename T, int TOKENS, int STORE, bool CAP>
 hipError_t mid_launch(const HeadLogits& a, hipStream_t s) {
     constexpr size_t bytes = mid_bytes<TOKENS>();
     const hipError_t allowed = allow_lds(&head_logits_mid_kernel<T, TOKENS, STORE, CAP>, bytes);
@@ -831,7 +972,7 @@ hipError_t mid_launch(const HeadLogits& a, hipStream_t s) {
     return hipGetLastError();
 }
 
-template <typename T, bool STORE, bool CAP>
+template <typename T, int STORE, bool CAP>
 hipError_t logits_launch(const HeadLogits& a, int variant, hipStream_t s) {
     if (variant == kLogitsStream) {
         const int groups = (int)(a.e_pitch / kHeadStreamSub);   // the padded columns too: they become zeros
@@ -847,10 +988,15 @@ hipError_t logits_launch(const HeadLogits& a, int variant, hipStream_t s) {
     return hipGetLastError();
 }
 
+template <typename T, bool CAP>
+hipError_t logits_stored(const HeadLogits& a, int variant, hipStream_t s) {
+    if (!a.e) return logits_launch<T, kNoStore, CAP>(a, variant, s);
+    return a.e_past ? logits_launch<T, kStorePast, CAP>(a, variant, s) : logits_launch<T, kStore, CAP>(a, variant, s);
+}
+
 template <typename T>
 hipError_t logits_typed(const HeadLogits& a, int variant, hipStream_t s) {
-    if (a.e) return a.cap > 0.f ? logits_launch<T, true, true>(a, variant, s) : logits_launch<T, true, false>(a, variant, s);
-    return a.cap > 0.f ? logits_launch<T, false, true>(a, variant, s) : logits_launch<T, false, false>(a, variant, s);
+    return a.cap > 0.f ? logits_stored<T, true>(a, variant, s) : logits_stored<T, false>(a, variant, s);
 }
 
 template <typename T>
@@ -864,20 +1010,32 @@ hipError_t rows_typed(const HeadRows& a, hipStream_t s) {
 }
 
 template <typename T>
-hipError_t prob_typed(const HeadProb& a, hipStream_t s) {
-    const int grid = (a.cols + 2047) / 2048 * ((a.rows + 7) / 8) + 1;
-    if (a.inv_cap > 0.f) head_prob_kernel<T, true><<<grid, 256, 0, s>>>(a);
-    else head_prob_kernel<T, false><<<grid, 256, 0, s>>>(a);
+hipError_t prob_typed(const HeadRows& a, hipStream_t s) {
+    // a workgroup takes whole rows where there are rows enough for 4 on each compute unit
+    const int row_blocks = (a.rows + kProbRows - 1) / kProbRows;
+    const int wanted = std::max(1, 1024 / row_blocks);
+    const int across = (int)(((a.e_pitch + wanted - 1) / wanted + 2047) / 2048 * 2048);
+    const int blocks = (int)((a.e_pitch + across - 1) / across), grid = blocks * row_blocks;
+    // far more than the last-level cache holds: past it (8192 x 131072: 856 -> 731 us; 16384 x 8192: 86 -> 101)
+    const bool past = (int64_t)a.rows * a.e_pitch * 2 > (int64_t)1 << 30;
+    if (a.cap > 0.f) {
+        if (past) head_prob_kernel<T, true, true><<<grid, 256, 0, s>>>(a, blocks, across);
+        else head_prob_kernel<T, true, false><<<grid, 256, 0, s>>>(a, blocks, across);
+    } else {
+        if (past) head_prob_kernel<T, false, true><<<grid, 256, 0, s>>>(a, blocks, across);
+        else head_prob_kernel<T, false, false><<<grid, 256, 0, s>>>(a, blocks, across);
+    }
     return hipGetLastError();
 }
 
-template <typename T>
+template <typename T, bool MID>
 hipError_t grads_launch(const HeadGrads& a, hipStream_t s) {
-    const hipError_t allowed = allow_lds(&head_grads_kernel<T>, kRingBytes);
+    constexpr size_t bytes = MID ? kMidGradBytes : kRingBytes;
+    const hipError_t allowed = allow_lds(&head_grads_kernel<T, MID>, bytes);
     if (allowed != hipSuccess) return allowed;
     const int grid = xcd_grid(a.hidden.tiles_c * a.hidden.tiles_d * a.hidden.splits +
                               a.weight.tiles_c * a.weight.tiles_d * a.weight.splits);
-    head_grads_kernel<T><<<grid, 512, kRingBytes, s>>>(a);
+    head_grads_kernel<T, MID><<<grid + 1, MID ? 256 : 512, bytes, s>>>(a);
     return hipGetLastError();
 }
 
@@ -889,11 +1047,12 @@ hipError_t launch_head_logits(const HeadLogits& a, int type, int variant, hipStr
 hipError_t launch_head_rows(const HeadRows& a, int type, hipStream_t s) {
     return type == kHeadBf16 ? rows_typed<bf16>(a, s) : rows_typed<f16>(a, s);
 }
-hipError_t launch_head_prob(const HeadProb& a, int type, hipStream_t s) {
+hipError_t launch_head_prob(const HeadRows& a, int type, hipStream_t s) {
     return type == kHeadBf16 ? prob_typed<bf16>(a, s) : prob_typed<f16>(a, s);
 }
-hipError_t launch_head_grads(const HeadGrads& a, int type, hipStream_t s) {
-    return type == kHeadBf16 ? grads_launch<bf16>(a, s) : grads_launch<f16>(a, s);
+hipError_t launch_head_grads(const HeadGrads& a, int type, bool mid, hipStream_t s) {
+    if (type == kHeadBf16) return mid ? grads_launch<bf16, true>(a, s) : grads_launch<bf16, false>(a, s);
+    return mid ? grads_launch<f16, true>(a, s) : grads_launch<f16, false>(a, s);
 }
 hipError_t launch_head_join(const HeadJoin& a, int type, hipStream_t s) {
     const int64_t items = ((int64_t)a.part[0].cols + a.part[1].cols) * ((a.dim + 7) / 8);

@@ -5,9 +5,10 @@
 // One call enqueues, on the caller's stream:
 //   head_pack   only for inputs that are not 16-byte aligned
 //   for each piece of the tokens: head_logits (and the scale of the weights, one
-//   workgroup), head_rows (with a copy of hidden for the gradient of weight),
-//   and for gradients head_prob (and the loss, one workgroup), head_grads, with
-//   head_join where K was split or the pieces' sums had to be kept in fp32
+//   workgroup); without gradients head_rows; with them head_prob (the same for
+//   each token, a copy of hidden for the gradient of weight, and the
+//   probabilities) and head_grads (and the loss, one workgroup), with head_join
+//   where K was split or the pieces' sums had to be kept in fp32
 //   head_loss   only where the loss is wanted without gradients
 #include <algorithm>
 #include <cmath>
@@ -24,6 +25,12 @@ namespace {
 constexpr int kCus = 256;                 // compute units of an MI355X
 constexpr int kMinStagesPerSplit = 4;     // K stages a workgroup takes at least when K is split
 
+// Piece of probabilities from which head_logits writes past the caches: 256 MB
+// of last-level cache hold less of it than head_prob could use (16384 x 8192,
+// 268 MB: head_logits 197 -> 189 us, head_prob 102 -> 86; 1531 x 12345, 38 MB,
+// the other way round: head_prob 23 -> 34).
+constexpr int64_t kPastBytes = (int64_t)192 << 20;
+
 int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 
 // Offsets into the workspace (-1: not there) and sizes, from the problem alone.
@@ -34,39 +41,55 @@ struct HeadPlan {
     int64_t piece, pieces;        // tokens per piece
     int64_t rows, cols;           // padded size of a piece's probabilities
     int nsub, sub;
-    int splits_h, splits_w, stages_h, stages_w;   // K splits of the two gradients
+    int grad_edge, splits_h, splits_w, stages_h, stages_w;   // tiles and K splits of the two gradients
     bool partial_h, partial_w;
-    int64_t scalars, row_weight, row_target, ref, sum, e, hidden, weight, part_h, part_w, bytes;
+    int64_t scalars, row_weight, ref, sum, e, hidden, weight, part_h, part_w, bytes;
 };
 
-// Splits of K for the two gradients, of n and m tiles of `a` and `b` stages:
-// the pair that takes least by this estimate, in stages.  256 workgroups run
-// at a time; a tile costs kTileStages more for its prologue and epilogue; a
-// split's partial sums are written and read again, kPartStages per tile.
-// (Measured: a stage takes 1.8 us, prologue and epilogue 5 us, a partial
-// sum 13 us with head_join's share.)
-void split_k(int64_t n, int a, int64_t m, int b, int& splits_a, int& splits_b) {
-    constexpr double kTileStages = 3.0, kPartStages = 8.0;
+// Tile edge and splits of K for the two gradients (hidden: rows x dim, K the
+// vocabulary; weight: vocab x dim, K the rows), those that take least by this
+// estimate in stages of a 256 x 256 tile (1.8 us).  A tile costs a prologue and
+// an epilogue (5 us, 3 stages); a split's partial sums are written and read
+// again (13 us a tile with head_join's share).  One 256 x 256 tile or two 128 x
+// 128 tiles run on a compute unit at a time; the latter take 0.55 of a stage
+// each, both together.  Measured, gradients and join in us, 256 / 128 wide:
+//   2048 x 4096 x 512  44 / 38     1531 x 12345 x 600  77 / 68
+//   500 x 1000 x 256   27 / 19     8192 x 8192 x 512   149 / 139
+//   16384 x 8192 x 512 258 / 350   8192 x 131072 x 2048  7640 / 9523
+struct GradSplit {
+    int edge = kHeadTile, splits_h = 1, splits_w = 1;
+};
+GradSplit split_k(int64_t rows, int64_t vocab, int64_t dim, bool grad_hidden, bool grad_weight) {
     static const int tried[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32};
+    auto ceil_div = [](int64_t x, int64_t m) { return (x + m - 1) / m; };
+    const int a = (int)ceil_div(vocab, kHeadK), b = (int)ceil_div(rows, kHeadK);
     double best = 1e300;
-    splits_a = splits_b = 1;
-    for (int i : tried) {
-        if (i > 1 && (n == 0 || a / i < kMinStagesPerSplit)) break;
-        for (int j : tried) {
-            if (j > 1 && (m == 0 || b / j < kMinStagesPerSplit)) break;
-            const double la = n ? (a + i - 1) / i + kTileStages + (i > 1 ? kPartStages : 0.0) : 0.0;
-            const double lb = m ? (b + j - 1) / j + kTileStages + (j > 1 ? kPartStages : 0.0) : 0.0;
-            const int64_t items = n * i + m * j;
-            const double longest = std::max(la, lb), even = (n * i * la + m * j * lb) / kCus;
-            // the last items to start are gradient tiles of weight; their round is on average half full
-            const double cost = items <= kCus ? longest : std::max(longest, even + 0.5 * (m ? lb : la));
-            if (cost < best) {
-                best = cost;
-                splits_a = i;
-                splits_b = j;
+    GradSplit r;
+    for (int edge : {256, 128}) {
+        const int64_t tiles_d = ceil_div(dim, edge);
+        const int64_t n = grad_hidden ? ceil_div(rows, edge) * tiles_d : 0, m = grad_weight ? ceil_div(vocab, edge) * tiles_d : 0;
+        const double stage = edge == 256 ? 1.0 : 0.55, part = edge == 256 ? 8.0 : 3.0, ends = edge == 256 ? 3.0 : 2.0;
+        const int slots = edge == 256 ? kCus : 2 * kCus;
+        for (int i : tried) {
+            if (i > 1 && (n == 0 || a / i < kMinStagesPerSplit)) break;
+            for (int j : tried) {
+                if (j > 1 && (m == 0 || b / j < kMinStagesPerSplit)) break;
+                const double la = n ? ceil_div(a, i) * stage + ends + (i > 1 ? part : 0.0) : 0.0;
+                const double lb = m ? ceil_div(b, j) * stage + ends + (j > 1 ? part : 0.0) : 0.0;
+                const int64_t items = n * i + m * j;
+                const double longest = std::max(la, lb), even = (n * i * la + m * j * lb) / slots;
+                // the last items to start are gradient tiles of weight; their round is on average half full
+                const double cost = items <= slots ? longest : std::max(longest, even + 0.5 * (m ? lb : la));
+                if (cost < best) {
+                    best = cost;
+                    r.edge = edge;
+                    r.splits_h = i;
+                    r.splits_w = j;
+                }
             }
         }
     }
+    return r;
 }
 
 // Kernel for the logits of a piece.  Measured (us, bf16, no gradients):
@@ -117,10 +140,11 @@ HeadPlan make_head_plan(const head_loss_t& p) {
     q.tile_t = q.variant == kLogitsTile ? kHeadTile : q.variant == kLogitsMid128 ? 128 : q.variant == kLogitsMid32 ? 32 : 64;
     q.sub = logits_sub(q.variant);
     q.nsub = (int)(q.variant == kLogitsStream ? q.cols / q.sub : round_up(p.vocab, q.tile_v) / q.sub);
-    const int64_t tiles_d = (p.dim + kHeadTile - 1) / kHeadTile;
     const int all_h = (int)(q.cols / kHeadK), all_w = (int)(q.rows / kHeadK);
-    split_k(p.grad_hidden ? (q.piece + kHeadTile - 1) / kHeadTile * tiles_d : 0, all_h,
-            p.grad_weight ? (p.vocab + kHeadTile - 1) / kHeadTile * tiles_d : 0, all_w, q.splits_h, q.splits_w);
+    const GradSplit g = split_k(q.piece, p.vocab, p.dim, p.grad_hidden, p.grad_weight);
+    q.grad_edge = g.edge;
+    q.splits_h = g.splits_h;
+    q.splits_w = g.splits_w;
     q.stages_h = (all_h + q.splits_h - 1) / q.splits_h;
     q.stages_w = (all_w + q.splits_w - 1) / q.splits_w;
     q.partial_h = p.grad_hidden && q.splits_h > 1;
@@ -133,7 +157,6 @@ HeadPlan make_head_plan(const head_loss_t& p) {
     };
     q.scalars = take(true, 16);
     q.row_weight = take(q.train, 4 * (p.tokens + kHeadPad));
-    q.row_target = take(q.train, 4 * (p.tokens + kHeadPad));
     q.ref = take(true, 4 * (int64_t)q.nsub * q.rows);
     q.sum = take(true, 4 * (int64_t)q.nsub * q.rows);
     q.e = take(grads, 2 * q.rows * q.cols);
@@ -206,7 +229,6 @@ int validate_buffers(const head_loss_t& p, const void* workspace, size_t bytes) 
 int enqueue_head(const head_loss_t& p, const HeadPlan& q, uint8_t* ws, hipStream_t s) {
     float* scalars = reinterpret_cast<float*>(ws + q.scalars);
     float* row_weight = q.train ? reinterpret_cast<float*>(ws + q.row_weight) : nullptr;
-    int* row_target = q.train ? reinterpret_cast<int*>(ws + q.row_target) : nullptr;
     const int dim = (int)p.dim, vocab = (int)p.vocab;
     const uint8_t* h = static_cast<const uint8_t*>(p.hidden);
     const void* w = p.weight;
@@ -230,7 +252,7 @@ int enqueue_head(const head_loss_t& p, const HeadPlan& q, uint8_t* ws, hipStream
     auto vec = [&](const void* ptr, int64_t stride) {
         return dim % 8 == 0 && stride % 8 == 0 && reinterpret_cast<uintptr_t>(ptr) % 16 == 0;
     };
-    const int tiles_d = (dim + kHeadTile - 1) / kHeadTile;
+    const int tiles_d = (dim + q.grad_edge - 1) / q.grad_edge;
     for (int64_t at = 0; at < p.tokens; at += q.piece) {
         const int tokens = (int)std::min(q.piece, p.tokens - at), rows = (int)round_up(tokens, kHeadPad);
         const uint8_t* hp = h + at * h_pitch * 2;
@@ -243,6 +265,7 @@ int enqueue_head(const head_loss_t& p, const HeadPlan& q, uint8_t* ws, hipStream
         a.e = q.e >= 0 ? ws + q.e : nullptr;
         a.e_pitch = q.cols;
         a.e_rows = rows;
+        a.e_past = 2 * (int64_t)rows * q.cols > kPastBytes;
         a.ref = ref;
         a.sum = sum;
         a.stat_pitch = rows;
@@ -271,7 +294,6 @@ int enqueue_head(const head_loss_t& p, const HeadPlan& q, uint8_t* ws, hipStream
         r.nll = p.nll + at;
         r.lse = p.lse ? p.lse + at : nullptr;
         r.row_weight = q.train ? row_weight + at : nullptr;
-        r.row_target = q.train ? row_target + at : nullptr;
         r.copy = q.copy_h ? ws + q.hidden : nullptr;
         r.copy_pitch = q.dim8;
         r.ignore_index = p.ignore_index;
@@ -282,14 +304,18 @@ int enqueue_head(const head_loss_t& p, const HeadPlan& q, uint8_t* ws, hipStream
         r.cap = p.softcap;
         r.inv_cap = inv_cap;
         r.train = q.train;
-        HEAD_TRY("head_rows", launch_head_rows(r, p.dtype, s));
-        if (q.e < 0) continue;
+        r.e = q.e >= 0 ? ws + q.e : nullptr;
+        r.e_pitch = q.cols;
+        r.sub = q.sub;
+        if (q.e < 0) {
+            HEAD_TRY("head_rows", launch_head_rows(r, p.dtype, s));
+            continue;
+        }
+        HEAD_TRY("head_prob", launch_head_prob(r, p.dtype, s));
         const bool last = at + q.piece >= p.tokens;
-        HeadProb b = {ws + q.e, q.cols, rows, (int)q.cols, ref, sum, rows, q.sub, row_weight + at, row_target + at, inv_cap, {}};
-        if (last && p.loss) b.loss = {p.nll, row_weight, scalars, p.loss, (int)p.tokens};
-        HEAD_TRY("head_prob", launch_head_prob(b, p.dtype, s));
         HeadGrads g;
         memset(&g, 0, sizeof(g));
+        if (last && p.loss) g.loss = {p.nll, row_weight, scalars, p.loss, (int)p.tokens};
         auto common = [&](HeadGrad& x, int64_t cols) {
             x.p = ws + q.e;
             x.p_pitch = q.cols;
@@ -297,7 +323,7 @@ int enqueue_head(const head_loss_t& p, const HeadPlan& q, uint8_t* ws, hipStream
             x.p_cols = (int)q.cols;
             x.dim = dim;
             x.cols = (int)cols;
-            x.tiles_c = (int)((cols + kHeadTile - 1) / kHeadTile);
+            x.tiles_c = (int)((cols + q.grad_edge - 1) / q.grad_edge);
             x.tiles_d = tiles_d;
             x.partial_pitch = q.dim8;
             x.scalars = scalars;
@@ -337,7 +363,7 @@ int enqueue_head(const head_loss_t& p, const HeadPlan& q, uint8_t* ws, hipStream
             x.accumulate = at > 0;
             if (q.partial_w && last) j.part[1] = {x.partial, q.dim8, q.splits_w, vocab, x.out, x.out_pitch, x.out_vec};
         }
-        HEAD_TRY("head_grads", launch_head_grads(g, p.dtype, s));
+        HEAD_TRY("head_grads", launch_head_grads(g, p.dtype, q.grad_edge != kHeadTile, s));
         if (j.part[0].cols || j.part[1].cols) HEAD_TRY("head_join", launch_head_join(j, p.dtype, s));
     }
     if (p.tokens == 0 && (p.grad_weight || p.loss)) {
