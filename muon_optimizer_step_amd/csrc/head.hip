@@ -15,6 +15,7 @@
 // and P^T with H.  The logits thus cost one product, and only a piece of the
 // tokens is in memory at a time.
 #include <algorithm>
+#include <type_traits>
 
 #include "head.h"
 
@@ -78,43 +79,52 @@ __device__ inline float capped(float z, float cap, float inv_cap) {
     return fmaf(-2.0f * cap, __builtin_amdgcn_rcpf(t + 1.0f), cap);
 }
 
-// 16 bytes per lane, from base + off, straight into LDS at address dst + 16 x
-// lane (base and dst the wave's).  As assembly because the compiler makes every
-// transposing LDS read wait for all direct loads that it knows of, those of
-// later stages too; there is no result register, and the K loop waits for its
-// loads itself.
+// 16 bytes per lane, from base + off, straight into LDS at address dst + PLUS +
+// 16 x lane (base and dst the wave's).  As assembly because the compiler makes
+// every transposing LDS read wait for all direct loads that it knows of, those
+// of later stages too; there is no result register, and the K loop waits for
+// its loads itself.
+template <int PLUS>
 __device__ inline void direct_load(const uint8_t* base, uint32_t off, uint32_t dst) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(dst), "v"(off), "s"(base)
-                 : "memory");
+    asm volatile("s_add_u32 m0, %0, %3\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(dst), "v"(off), "s"(base), "n"(PLUS)
+                 : "memory", "scc");
 }
 // The same from an address of each lane's own.
+template <int PLUS>
 __device__ inline void direct_load_from(const uint8_t* src, uint32_t dst) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(dst), "v"(src) : "memory");
+    asm volatile("s_add_u32 m0, %0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(dst), "v"(src), "n"(PLUS)
+                 : "memory", "scc");
 }
 __device__ __align__(16) const uint8_t kZeros[16] = {};   // what K beyond its end is loaded from
 __device__ inline uint32_t lds_address(const uint8_t* p) { return (uint32_t)(uintptr_t)(lds_ptr)p; }
 
 // ---------------------------------------------------------------- operand staging
-// A stage is 64 K of both operands of a 256 x 256 tile, 32 KB each.
+// A stage is 64 K of both operands of a tile.  An operand knows the address of
+// the next stage to load (`next`, a scalar that moves by one addition a stage)
+// and the LDS addresses of its fragments within a stage's slot, so that a load
+// costs two scalar instructions and a fragment one read.
 //
 // A row operand (K contiguous): ROWS rows x 128 bytes of K per stage (a whole
 // cache line: 64-byte pieces cost the vector L1 twice the fills), the 16-byte
 // chunk c of row r in slot c ^ ((r / 2) % 8), which keeps the 16-byte fragment
 // reads of 32 rows free of bank conflicts.  Direct loads: one wave instruction
 // fills 8 rows.
-constexpr int kOperand = kHeadTile * kHeadK * 2;     // bytes of one operand of a stage
+constexpr int kOperand = kHeadTile * kHeadK * 2;     // bytes of one operand of a stage of a 256 x 256 tile
 template <int ROWS, int WAVES>
 struct RowOperand {
     static constexpr int kBytes = ROWS * kHeadK * 2;
     static constexpr int kLoads = ROWS / 8 / WAVES;
     static_assert(ROWS % (8 * WAVES) == 0 && WAVES % 2 == 0, "whole instructions per wave");
-    const uint8_t* base;
+    const uint8_t* next;
     uint32_t off[kLoads];
-    int chunk;      // source chunk of this lane within a stage
+    int chunk;               // source chunk of this lane within a stage
+    uint32_t at[kHeadK / 16];   // LDS address of the first fragment's chunk of each 16 K, less the slot's
 
-    // rows row0 .. row0 + ROWS - 1 of a matrix with `rows` rows; rows beyond its end repeat the last one
-    __device__ inline void init(const void* m, int64_t pitch_bytes, int64_t row0, int64_t rows, int wave, int lane) {
-        base = static_cast<const uint8_t*>(m) + row0 * pitch_bytes;
+    // rows row0 .. row0 + ROWS - 1 of a matrix with `rows` rows (rows beyond its
+    // end repeat the last one), from K element k0; `row` is this lane's row of the
+    // wave's first fragment
+    __device__ inline void init(const void* m, int64_t pitch_bytes, int64_t row0, int64_t rows, int64_t k0, int row, int wave, int lane) {
+        next = static_cast<const uint8_t*>(m) + row0 * pitch_bytes + k0 * 2;
         const int last = (int)min<int64_t>(rows - 1 - row0, ROWS - 1);
         chunk = 0;
 #pragma unroll
@@ -123,17 +133,20 @@ struct RowOperand {
             chunk = (lane % 8) ^ ((r >> 1) & 7);      // the same for every j
             off[j] = (uint32_t)(min(r, last) * pitch_bytes) + chunk * 16;
         }
+#pragma unroll
+        for (int kc = 0; kc < kHeadK / 16; ++kc) at[kc] = row * 128 + (((2 * kc + lane / 32) ^ ((row >> 1) & 7)) << 4);
     }
-    // load j of stage kt of K elements `dim` (a multiple of 8); K beyond its end is zero
-    __device__ inline void load(uint32_t lds, int j, int kt, int dim, int wave) const {
-        const uint8_t* at = base + (int64_t)kt * (kHeadK * 2);
-        const uint32_t dst = lds + (j * WAVES + wave) * 1024;
-        if ((kt + 1) * kHeadK <= dim) direct_load(at, off[j], dst);
-        else direct_load_from(8 * chunk < dim - kt * kHeadK ? at + off[j] : kZeros, dst);
+    // load J of the next stage to the slot at `dst` (with the wave's 1024 bytes in it)
+    template <int J> __device__ inline void load(uint32_t dst) const { direct_load<J * WAVES * 1024>(next, off[J], dst); }
+    // the same where K ends `left` elements (a multiple of 8) on: zeros behind it
+    template <int J> __device__ inline void load_tail(uint32_t dst, int left) const {
+        direct_load_from<J * WAVES * 1024>(8 * chunk < left ? next + off[J] : kZeros, dst);
     }
-    // fragment of 32 rows from `row`: lane l holds row perm(l % 32), K 16 kc + 8 (l / 32) .. + 7
-    static __device__ inline u32x4 frag(const uint8_t* lds, int row, int kc, int lane) {
-        return *reinterpret_cast<const u32x4*>(lds + row * 128 + (((2 * kc + lane / 32) ^ ((row >> 1) & 7)) << 4));
+    __device__ inline void advance() { next += kHeadK * 2; }
+    // fragment I (32 rows each): lane l holds K 16 kc + 8 (l / 32) .. + 7 of its row
+    template <int I> __device__ inline u32x4 frag(uint32_t slot, int kc) const {
+        typedef __attribute__((address_space(3))) const u32x4 lds_u32x4;
+        return *(lds_u32x4*)(uintptr_t)(at[kc] + slot + I * 32 * 128);
     }
 };
 
@@ -147,61 +160,91 @@ __device__ inline int swap23(int r) { return (r & 0x13) | ((r & 4) << 1) | ((r &
 // with the transposing LDS read.  The 16-byte chunk c of row k is in slot c ^ 2
 // f(k % 4), f = 0, 2, 5, 7: the 4 rows x 32 bytes that 16 lanes read, and the 4
 // rows x 64 bytes of 32 lanes, lie in different banks.
-template <int COLS, int WAVES>
+template <int COLS, int WAVES, int FRAGS>
 struct ColOperand {
     static constexpr int kRow = COLS * 2, kChunks = COLS / 8, kPer = 1024 / kRow;   // bytes and chunks of a row, rows per instruction
     static constexpr int kBytes = kHeadK * kRow;
     static constexpr int kLoads = kHeadK / kPer / WAVES;
     static_assert(kChunks >= 16, "the slot of a chunk is in its row");
-    const uint8_t* base;
-    int64_t pitch;
+    const uint8_t* next;
+    int64_t step;            // bytes of 64 rows
+    int pitch;
     uint32_t off[kLoads];
     int chunk[kLoads], row[kLoads];
+    uint32_t at[FRAGS];      // LDS address of each fragment's first row, less the slot's
     static __device__ inline int slot_xor(int k) { return 2 * ((0x7520 >> (4 * (k & 3))) & 7); }
-    // columns col0 .. of a matrix with cols_pad columns (a multiple of 8); chunks beyond repeat the last
-    __device__ inline void init(const void* m, int64_t pitch_bytes, int col0, int cols_pad, int wave, int lane) {
-        base = static_cast<const uint8_t*>(m) + (int64_t)col0 * 2;
-        pitch = pitch_bytes;
+    // columns col0 .. of a matrix with cols_pad columns (a multiple of 8; chunks
+    // beyond repeat the last), from K row k0; `frag0` is the wave's first fragment's
+    // column within the tile; `swap`: fragments hold columns swap23(l % 32)
+    __device__ inline void init(const void* m, int64_t pitch_bytes, int col0, int cols_pad, int64_t k0, int frag0, bool swap, int wave,
+                                int lane) {
+        next = static_cast<const uint8_t*>(m) + (int64_t)col0 * 2 + k0 * pitch_bytes;
+        step = kHeadK * pitch_bytes;
+        pitch = (int)pitch_bytes;
         const int last = (cols_pad - col0) / 8 - 1;
 #pragma unroll
         for (int j = 0; j < kLoads; ++j) {
             row[j] = kPer * (j * WAVES + wave) + lane / kChunks;
             chunk[j] = min((lane % kChunks) ^ slot_xor(row[j]), last) * 16;
-            off[j] = (uint32_t)(row[j] * pitch) + chunk[j];
+            off[j] = (uint32_t)(row[j] * pitch_bytes) + chunk[j];
         }
-    }
-    // K rows k0 .. k0 + 63 of `rows` rows; rows beyond repeat the last
-    __device__ inline void load(uint32_t lds, int j, int64_t k0, int64_t rows, int wave) const {
-        const uint32_t at = lds + (j * WAVES + wave) * 1024;
-        if (k0 + kHeadK <= rows) {
-            direct_load(base + k0 * pitch, off[j], at);
-        } else {
-            const int64_t first = min(k0, rows - 1);
-            const int last = (int)(rows - 1 - first);
-            direct_load(base + first * pitch, (uint32_t)(min(row[j], last) * pitch) + chunk[j], at);
-        }
-    }
-    // fragment of 32 columns from `col`: lane l holds column (perm of) l % 32, K 16 kc + 8 (l / 32) .. + 7.
-    // The transposing read gives lane l' of 16 element l' % 4 of the 8 bytes that lane 4 e + l' / 4 points at.
-    template <bool SWAP>
-    static __device__ inline u32x4 frag(const uint8_t* lds, int col, int kc, int lane) {
-        const int k = 16 * kc + 8 * (lane / 32) + (lane % 16) / 4;
+        // The transposing read gives lane l' of 16 element l' % 4 of the 8 bytes that lane 4 e + l' / 4 points at.
+        const int k = 8 * (lane / 32) + (lane % 16) / 4;
         int quad = lane % 4;
-        if (SWAP) quad = ((quad & 1) << 1) | (quad >> 1);
+        if (swap) quad = ((quad & 1) << 1) | (quad >> 1);
         quad += 4 * ((lane / 16) % 2);
-        const int at = ((col / 8 + quad / 2) ^ slot_xor(k)) * 16 + (quad & 1) * 8;
+#pragma unroll
+        for (int i = 0; i < FRAGS; ++i)
+            at[i] = k * kRow + ((((frag0 + 32 * i) / 8 + quad / 2) ^ slot_xor(k)) * 16) + (quad & 1) * 8;
+    }
+    template <int J> __device__ inline void load(uint32_t dst) const { direct_load<J * WAVES * 1024>(next, off[J], dst); }
+    // where only `left` rows of K remain: rows beyond repeat the last
+    template <int J> __device__ inline void load_tail(uint32_t dst, int left) const {
+        direct_load<J * WAVES * 1024>(next, (uint32_t)(min(row[J], left - 1) * (int64_t)pitch) + chunk[J], dst);
+    }
+    __device__ inline void advance() { next += step; }
+    // fragment I (32 columns): lane l holds K 16 kc + 8 (l / 32) .. + 7 of its column
+    template <int I> __device__ inline u32x4 frag(uint32_t slot, int kc) const {
         typedef __attribute__((address_space(3))) short4v lds_short4;
-        const u32x2 a = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4*)(lds + k * kRow + at)));
-        const u32x2 b = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4*)(lds + (k + 4) * kRow + at)));
+        const uint32_t p = at[I] + slot + kc * 16 * kRow;
+        const u32x2 a = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4*)(uintptr_t)p));
+        const u32x2 b = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4*)(uintptr_t)(p + 4 * kRow)));
         u32x4 r;
         r[0] = a[0]; r[1] = a[1]; r[2] = b[0]; r[3] = b[1];
         return r;
     }
 };
 
+// All fragments of one step of 16 K, and their products.
+template <typename OA, typename OB, int TA, int TB>
+__device__ inline void read_step(const OA& A, const OB& B, u32x4 (&fa)[TA], u32x4 (&fb)[TB], uint32_t slot_a, uint32_t slot_b, int kc) {
+    fa[0] = A.template frag<0>(slot_a, kc);
+    if constexpr (TA > 1) fa[1] = A.template frag<1>(slot_a, kc);
+    if constexpr (TA > 2) { fa[2] = A.template frag<2>(slot_a, kc); fa[3] = A.template frag<3>(slot_a, kc); }
+    fb[0] = B.template frag<0>(slot_b, kc);
+    if constexpr (TB > 1) fb[1] = B.template frag<1>(slot_b, kc);
+    static_assert((TA == 1 || TA == 2 || TA == 4) && (TB == 1 || TB == 2), "fragments of a wave");
+}
+
+// A whole stage's loads of one operand; `left` K from the stage's beginning.
+template <typename Op>
+__device__ inline void load_stage(Op& op, uint32_t dst, int left) {
+    static_assert(Op::kLoads == 1 || Op::kLoads == 2 || Op::kLoads == 4, "loads of a wave");
+    if (left >= kHeadK) {
+        op.template load<0>(dst);
+        if constexpr (Op::kLoads > 1) op.template load<1>(dst);
+        if constexpr (Op::kLoads > 2) { op.template load<2>(dst); op.template load<3>(dst); }
+    } else {
+        op.template load_tail<0>(dst, left);
+        if constexpr (Op::kLoads > 1) op.template load_tail<1>(dst, left);
+        if constexpr (Op::kLoads > 2) { op.template load_tail<2>(dst, left); op.template load_tail<3>(dst, left); }
+    }
+    op.advance();
+}
+
 // ---------------------------------------------------------------- K loop
-// acc += A B over `stages` stages of 64 K.  load_a(kt, slot, u), load_b issue load u of 4 of this
-// wave for stage kt; a(slot, i, kc), b(slot, j, kc) read fragments of 16 K.
+// acc += A B over `stages` stages of 64 K; the operands' K ends after left_a and
+// left_b elements, within the last stage.  Tile 256 x 256, 8 waves.
 //
 // LDS is a ring of five operand slots (all 160 KB): A of stage k is in slot
 // 2 k mod 5, B in 2 k + 1 mod 5.  The barrier at the end of stage k - 1 sits before
@@ -211,66 +254,126 @@ struct ColOperand {
 // not hold the MFMAs up; and it publishes stage k, whose first fragments
 // are read while the last MFMAs run.  At its end only B of stage k + 1, issued
 // in the first half of the window, has to have arrived; A of k + 2 may be under way.
+//
+// Measured on 16384 x 8192 x 512 (the gradient of hidden): two buffers filled
+// in a burst after the barrier 165 us, this 127; with scalar address work cut
+// from 300 to 40 instructions a stage, see head_grads.
 constexpr int kSlots = 5;
 constexpr size_t kRingBytes = (size_t)kSlots * kOperand;
-template <typename T, int TA, int TB, typename LoadA, typename LoadB, typename FragA, typename FragB>
-__device__ inline void k_loop(floatx16 (&acc)[TA][TB], int stages, LoadA load_a, LoadB load_b, FragA a, FragB b) {
-    static_assert(kHeadK == 64, "four steps of 16 K per stage");
+template <typename T, int TA, int TB, typename OA, typename OB>
+__device__ inline void k_loop(floatx16 (&acc)[TA][TB], int stages, OA& A, OB& B, int left_a, int left_b, uint32_t lds, int wave) {
+    static_assert(kHeadK == 64 && OA::kLoads == 4 && OB::kLoads == 4, "four steps of 16 K and eight loads per stage");
+    if (stages <= 0) return;
     u32x4 fa[2][TA], fb[2][TB];
-    auto slot = [](int n) { return n >= kSlots ? n - kSlots : n; };
-    auto read = [&](int set, int slot_a, int slot_b, int kc) {
-#pragma unroll
-        for (int i = 0; i < TA; ++i) fa[set][i] = a(slot_a, i, kc);
-#pragma unroll
-        for (int j = 0; j < TB; ++j) fb[set][j] = b(slot_b, j, kc);
-    };
-    // the MFMAs of one step with two loads between them
-    auto multiply = [&](int set, auto load) {
+    // the slots of A and B of stage kt, A and B of kt + 1, and A of kt + 2; B of kt + 2 takes the first
+    uint32_t s0 = lds, s1 = lds + kOperand, s2 = lds + 2 * kOperand, s3 = lds + 3 * kOperand, s4 = lds + 4 * kOperand;
+    const uint32_t mine = wave * 1024;
+    // the MFMAs of one step, with a load after the second and the sixth eighth
+    auto multiply = [&](int set, auto first, auto second) {
 #pragma unroll
         for (int n = 0; n < TA * TB; ++n) {
             acc[n / TB][n % TB] = mfma<T>(fa[set][n / TB], fb[set][n % TB], acc[n / TB][n % TB]);
             if (n == TA * TB / 4 || n == TA * TB * 3 / 4) {
                 __builtin_amdgcn_sched_barrier(0);
-                load(n == TA * TB / 4 ? 0 : 1);
+                if (n == TA * TB / 4) first(); else second();
                 __builtin_amdgcn_sched_barrier(0);
             }
         }
     };
-    if (stages <= 0) return;
-#pragma unroll
-    for (int u = 0; u < 4; ++u) load_a(0, 0, u);
-#pragma unroll
-    for (int u = 0; u < 4; ++u) load_b(0, 1, u);
-    if (stages > 1)
-#pragma unroll
-        for (int u = 0; u < 4; ++u) load_a(1, 2, u);
-    if (stages > 1) wait_loads<4>();
-    else wait_loads<0>();
-    bare_barrier();
-    read(0, 0, 1, 0);
+    load_stage(A, s0 + mine, left_a);
+    load_stage(B, s1 + mine, left_b);
     if (stages > 1) {
-        load_b(1, 3, 0);
-        load_b(1, 3, 1);
+        load_stage(A, s2 + mine, left_a - kHeadK);
+        wait_loads<4>();
+    } else {
+        wait_loads<0>();
     }
-    int at = 0;      // slot of A of stage kt
-    for (int kt = 0; kt < stages; ++kt) {
-        const int sa = at, sb = slot(at + 1), sa1 = slot(at + 2), sb1 = slot(at + 3), sa2 = slot(at + 4);
-        read(1, sa, sb, 1);
-        multiply(0, [&](int u) { if (kt + 1 < stages) load_b(kt + 1, sb1, 2 + u); });
-        read(0, sa, sb, 2);
-        multiply(1, [&](int u) { if (kt + 2 < stages) load_a(kt + 2, sa2, u); });
-        read(1, sa, sb, 3);
-        multiply(0, [&](int u) { if (kt + 2 < stages) load_a(kt + 2, sa2, 2 + u); });
+    bare_barrier();
+    read_step(A, B, fa[0], fb[0], s0, s1, 0);
+    const int whole = min(stages, min(left_a, left_b) / kHeadK);     // stages that are complete in both
+    // one stage; `fast`: the stages that it loads, kt + 1 and kt + 2, are complete
+    auto stage = [&](int kt, auto fast) {
+        constexpr bool kFast = decltype(fast)::value;
+        const int la = left_a - (kt + 2) * kHeadK, lb = left_b - (kt + 1) * kHeadK;
+        auto one = [&](auto& op, auto j, uint32_t dst, int ahead, int left) {
+            constexpr int J = decltype(j)::value;
+            if (kFast || (kt + ahead < stages && left >= kHeadK)) op.template load<J>(dst + mine);
+            else if (kt + ahead < stages) op.template load_tail<J>(dst + mine, left);
+        };
+        using std::integral_constant;
+        read_step(A, B, fa[1], fb[1], s0, s1, 1);
+        multiply(0, [&] { one(B, integral_constant<int, 2>(), s3, 1, lb); }, [&] { one(B, integral_constant<int, 3>(), s3, 1, lb); });
+        B.advance();
+        read_step(A, B, fa[0], fb[0], s0, s1, 2);
+        multiply(1, [&] { one(A, integral_constant<int, 0>(), s4, 2, la); }, [&] { one(A, integral_constant<int, 1>(), s4, 2, la); });
+        read_step(A, B, fa[1], fb[1], s0, s1, 3);
+        multiply(0, [&] { one(A, integral_constant<int, 2>(), s4, 2, la); }, [&] { one(A, integral_constant<int, 3>(), s4, 2, la); });
+        A.advance();
         wait_lds();              // this wave's last fragments of stage kt
-        if (kt + 1 < stages) {
-            if (kt + 2 < stages) wait_loads<4>();
+        if (kFast || kt + 1 < stages) {
+            if (kFast || kt + 2 < stages) wait_loads<4>();
             else wait_loads<0>();
             bare_barrier();
-            read(0, sa1, sb1, 0);
+            read_step(A, B, fa[0], fb[0], s2, s3, 0);
         }
-        multiply(1, [&](int u) { if (kt + 2 < stages) load_b(kt + 2, sa, u); });    // slot 2 (k + 2) + 1 = 2 k mod 5
-        at = sa1;
+        const int lb2 = lb - kHeadK;
+        multiply(1, [&] { one(B, integral_constant<int, 0>(), s0, 2, lb2); }, [&] { one(B, integral_constant<int, 1>(), s0, 2, lb2); });
+        const uint32_t t0 = s0, t1 = s1;
+        s0 = s2; s1 = s3; s2 = s4; s3 = t0; s4 = t1;
+    };
+    if (stages > 1) {            // the first half of B of stage 1; its slot is free from the start
+        if (left_b >= 2 * kHeadK) {
+            B.template load<0>(s3 + mine);
+            B.template load<1>(s3 + mine);
+        } else {
+            B.template load_tail<0>(s3 + mine, left_b - kHeadK);
+            B.template load_tail<1>(s3 + mine, left_b - kHeadK);
+        }
     }
+    int kt = 0;
+    for (; kt + 2 < whole; ++kt) stage(kt, std::true_type());
+    for (; kt < stages; ++kt) stage(kt, std::false_type());
+}
+
+// The same for the smaller tiles: 4 waves, BUFFERS stages of LDS, two
+// workgroups on a compute unit that fill each other's waits.
+template <typename T, int BUFFERS, int TA, int TB, typename OA, typename OB>
+__device__ inline void k_loop_mid(floatx16 (&acc)[TA][TB], int stages, OA& A, OB& B, int left_a, int left_b, uint32_t lds, int wave) {
+    constexpr uint32_t kStage = OA::kBytes + OB::kBytes;
+    constexpr int kLoads = OA::kLoads + OB::kLoads;
+    const uint32_t mine = wave * 1024;
+    uint32_t put = lds, get = lds;
+    auto load = [&](int kt) {
+        load_stage(A, put + mine, left_a - kt * kHeadK);
+        load_stage(B, put + OA::kBytes + mine, left_b - kt * kHeadK);
+        put = put == lds + (BUFFERS - 1) * kStage ? lds : put + kStage;
+    };
+    for (int kt = 0; kt < BUFFERS - 1 && kt < stages; ++kt) load(kt);
+    for (int kt = 0; kt < stages; ++kt) {
+        if (kt + BUFFERS - 2 < stages) wait_loads<(BUFFERS - 2) * kLoads>();    // stage kt of those under way
+        else wait_loads<0>();
+        wait_lds();
+        bare_barrier();      // stage kt is in LDS, and every wave is done with stage kt - 1
+        if (kt + BUFFERS - 1 < stages) load(kt + BUFFERS - 1);
+#pragma unroll
+        for (int kc = 0; kc < kHeadK / 16; ++kc) {
+            u32x4 fa[TA], fb[TB];
+            read_step(A, B, fa, fb, get, get + OA::kBytes, kc);
+#pragma unroll
+            for (int i = 0; i < TA; ++i)
+#pragma unroll
+                for (int j = 0; j < TB; ++j) acc[i][j] = mfma<T>(fa[i], fb[j], acc[i][j]);
+        }
+        get = get == lds + (BUFFERS - 1) * kStage ? lds : get + kStage;
+    }
+}
+
+template <int TA, int TB>
+__device__ inline void clear(floatx16 (&acc)[TA][TB]) {
+#pragma unroll
+    for (int i = 0; i < TA; ++i)
+#pragma unroll
+        for (int j = 0; j < TB; ++j) acc[i][j] = floatx16(0.f);
 }
 
 // Work item of this workgroup: workgroups go round-robin over the XCDs, and
@@ -422,22 +525,12 @@ __global__ __launch_bounds__(512, 2) void head_logits_kernel(const HeadLogits a)
     tile_of(a, item, tile_v, tile_t);
     const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), wv = wave / WT, wt = wave % WT;
 
-    typedef RowOperand<kHeadTile, NW> Op;
-    Op W, H;
-    W.init(a.w, a.w_pitch * 2, (int64_t)tile_v * BV, a.vocab, wave, lane);
-    H.init(a.h, a.h_pitch * 2, (int64_t)tile_t * BT, a.tokens, wave, lane);
-    const int stages = (a.dim + kHeadK - 1) / kHeadK;
+    RowOperand<kHeadTile, NW> W, H;
+    W.init(a.w, a.w_pitch * 2, (int64_t)tile_v * BV, a.vocab, 0, wv * TV * 32 + swap23(lane % 32), wave, lane);
+    H.init(a.h, a.h_pitch * 2, (int64_t)tile_t * BT, a.tokens, 0, wt * TT * 32 + lane % 32, wave, lane);
     floatx16 acc[TV][TT];
-#pragma unroll
-    for (int i = 0; i < TV; ++i)
-#pragma unroll
-        for (int j = 0; j < TT; ++j) acc[i][j] = floatx16(0.f);
-    const int arow = wv * TV * 32 + swap23(lane % 32), brow = wt * TT * 32 + lane % 32;
-    k_loop<T, TV, TT>(
-        acc, stages, [&](int kt, int slot, int u) { W.load(lds_address(lds) + slot * kOperand, u, kt, a.dim, wave); },
-        [&](int kt, int slot, int u) { H.load(lds_address(lds) + slot * kOperand, u, kt, a.dim, wave); },
-        [&](int slot, int i, int kc) { return Op::frag(lds + slot * kOperand, arow + 32 * i, kc, lane); },
-        [&](int slot, int j, int kc) { return Op::frag(lds + slot * kOperand, brow + 32 * j, kc, lane); });
+    clear(acc);
+    k_loop<T, TV, TT>(acc, (a.dim + kHeadK - 1) / kHeadK, W, H, a.dim, a.dim, lds_address(lds), wave);
     if (STORE != kNoStore) bare_barrier();      // every wave is done with the operands, whose slots e passes through
     logits_epilogue<TV, TT, STORE, CAP>(a, acc, tile_v * BV + wv * TV * 32, tile_t * BT + wt * TT * 32, tile_v * WV + wv, lane,
                                         lds + wave * kEpilogueBytes<TV>);
@@ -458,7 +551,7 @@ template <int TOKENS> constexpr size_t mid_bytes() {
 template <typename T, int TOKENS, int STORE, bool CAP>
 __global__ __launch_bounds__(256, 2) void head_logits_mid_kernel(const HeadLogits a) {
     typedef MidTile<TOKENS> M;
-    constexpr int WV = M::WV, WT = M::WT, TV = M::TV, TT = M::TT, NW = WV * WT, kBuffers = M::kBuffers;
+    constexpr int WV = M::WV, WT = M::WT, TV = M::TV, TT = M::TT, NW = WV * WT;
     static_assert(WV * TV * 32 == kHeadMidVocab && WT * TT * 32 == TOKENS && NW == 4, "tile");
     extern __shared__ __align__(16) uint8_t lds[];
     if (blockIdx.x == gridDim.x - 1) {
@@ -470,49 +563,13 @@ __global__ __launch_bounds__(256, 2) void head_logits_mid_kernel(const HeadLogit
     int tile_v, tile_t;
     tile_of(a, item, tile_v, tile_t);
     const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), wv = wave / WT, wt = wave % WT;
-    typedef RowOperand<kHeadMidVocab, NW> WOp;
-    typedef RowOperand<TOKENS, NW> HOp;
-    constexpr int kStage = WOp::kBytes + HOp::kBytes, kLoads = WOp::kLoads + HOp::kLoads;
-    WOp W;
-    HOp H;
-    W.init(a.w, a.w_pitch * 2, (int64_t)tile_v * kHeadMidVocab, a.vocab, wave, lane);
-    H.init(a.h, a.h_pitch * 2, (int64_t)tile_t * TOKENS, a.tokens, wave, lane);
-    const int stages = (a.dim + kHeadK - 1) / kHeadK;
-    auto load = [&](int kt) {
-        const uint32_t at = lds_address(lds) + kt % kBuffers * kStage;
-#pragma unroll
-        for (int u = 0; u < WOp::kLoads; ++u) W.load(at, u, kt, a.dim, wave);
-#pragma unroll
-        for (int u = 0; u < HOp::kLoads; ++u) H.load(at + WOp::kBytes, u, kt, a.dim, wave);
-    };
+    RowOperand<kHeadMidVocab, NW> W;
+    RowOperand<TOKENS, NW> H;
+    W.init(a.w, a.w_pitch * 2, (int64_t)tile_v * kHeadMidVocab, a.vocab, 0, wv * TV * 32 + swap23(lane % 32), wave, lane);
+    H.init(a.h, a.h_pitch * 2, (int64_t)tile_t * TOKENS, a.tokens, 0, wt * TT * 32 + lane % 32, wave, lane);
     floatx16 acc[TV][TT];
-#pragma unroll
-    for (int i = 0; i < TV; ++i)
-#pragma unroll
-        for (int j = 0; j < TT; ++j) acc[i][j] = floatx16(0.f);
-    const int arow = wv * TV * 32 + swap23(lane % 32), brow = wt * TT * 32 + lane % 32;
-    for (int kt = 0; kt < kBuffers - 1 && kt < stages; ++kt) load(kt);
-    for (int kt = 0; kt < stages; ++kt) {
-        if (kt + kBuffers - 2 < stages) wait_loads<(kBuffers - 2) * kLoads>();    // stage kt of those under way
-        else wait_loads<0>();
-        wait_lds();
-        bare_barrier();      // stage kt is in LDS, and every wave is done with stage kt - 1
-        if (kt + kBuffers - 1 < stages) load(kt + kBuffers - 1);
-        const uint8_t* tw = lds + kt % kBuffers * kStage;
-        const uint8_t* th = tw + WOp::kBytes;
-#pragma unroll
-        for (int kc = 0; kc < kHeadK / 16; ++kc) {
-            u32x4 fa[TV], fb[TT];
-#pragma unroll
-            for (int i = 0; i < TV; ++i) fa[i] = WOp::frag(tw, arow + 32 * i, kc, lane);
-#pragma unroll
-            for (int j = 0; j < TT; ++j) fb[j] = HOp::frag(th, brow + 32 * j, kc, lane);
-#pragma unroll
-            for (int i = 0; i < TV; ++i)
-#pragma unroll
-                for (int j = 0; j < TT; ++j) acc[i][j] = mfma<T>(fa[i], fb[j], acc[i][j]);
-        }
-    }
+    clear(acc);
+    k_loop_mid<T, M::kBuffers>(acc, (a.dim + kHeadK - 1) / kHeadK, W, H, a.dim, a.dim, lds_address(lds), wave);
     if (STORE != kNoStore) bare_barrier();
     logits_epilogue<TV, TT, STORE, CAP>(a, acc, tile_v * kHeadMidVocab + wv * TV * 32, tile_t * TOKENS + wt * TT * 32,
                                         tile_v * WV + wv, lane, lds + wave * kEpilogueBytes<TV>);
@@ -657,7 +714,7 @@ __global__ __launch_bounds__(THREADS) void head_rows_kernel(const HeadRows a) {
 // 8 tokens x `across` columns per workgroup: first the tokens' values (again by
 // each workgroup of their columns), then e -> P in place, 8 columns of the 8
 // tokens per thread at a time.  HBM-bound: reads and writes 2 bytes an entry.
-constexpr int kProbRows = 8;
+constexpr int kProbRows = 8, kProbBatch = 4;
 template <typename T, bool CAP, bool PAST>
 __global__ __launch_bounds__(256) void head_prob_kernel(const HeadRows a, int blocks, int across) {
     __shared__ float red[3][4][kProbRows];
@@ -670,38 +727,41 @@ __global__ __launch_bounds__(256) void head_prob_kernel(const HeadRows a, int bl
     for (int col = col0 + 8 * threadIdx.x; col < end; col += 8 * 256) {
         uint8_t* at = static_cast<uint8_t*>(a.e) + ((int64_t)row0 * a.e_pitch + col) * 2;
         const float* ref = a.ref + (int64_t)(col / a.sub) * a.stat_pitch + row0;
-        u32x4 w[kProbRows];
-        float c[kProbRows];
+#pragma unroll 1
+        for (int k0 = 0; k0 < live; k0 += kProbBatch) {
+            u32x4 w[kProbBatch];
+            float c[kProbBatch];
 #pragma unroll
-        for (int k = 0; k < kProbRows; ++k) {
-            if (k >= live) continue;
-            const u32x4* src = reinterpret_cast<const u32x4*>(at + (int64_t)k * a.e_pitch * 2);
-            w[k] = PAST ? __builtin_nontemporal_load(src) : *src;
-            c[k] = ref[k];
-        }
-#pragma unroll
-        for (int k = 0; k < kProbRows; ++k) {
-            if (k >= live) continue;
-            const float weight = rows[k].weight;
-            u32x4 out = {0u, 0u, 0u, 0u};
-            if (weight != 0.f) {     // whatever an ignored token's logits are, its gradient is zero
-                const float f = __builtin_amdgcn_exp2f(c[k] - rows[k].lse2) * weight;
-                const int target = rows[k].target - col;
-                float e[8], p[8];
-                unpack8<f16>(w[k], e);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    p[i] = fmaf(e[i], f, i == target ? -weight : 0.f);
-                    if (CAP && e[i] > 0.f) {
-                        const float x = (c[k] + __builtin_amdgcn_logf(e[i])) * (kLn2 * a.inv_cap);
-                        p[i] *= fmaf(-x, x, 1.0f);
-                    }
-                }
-                out = pack8<T>(p);
+            for (int k = 0; k < kProbBatch; ++k) {
+                if (k0 + k >= live) continue;
+                const u32x4* src = reinterpret_cast<const u32x4*>(at + (int64_t)(k0 + k) * a.e_pitch * 2);
+                w[k] = PAST ? __builtin_nontemporal_load(src) : *src;
+                c[k] = ref[k0 + k];
             }
-            u32x4* dst = reinterpret_cast<u32x4*>(at + (int64_t)k * a.e_pitch * 2);
-            if constexpr (PAST) __builtin_nontemporal_store(out, dst);
-            else *dst = out;
+#pragma unroll
+            for (int k = 0; k < kProbBatch; ++k) {
+                if (k0 + k >= live) continue;
+                const Row row = rows[k0 + k];
+                u32x4 out = {0u, 0u, 0u, 0u};
+                if (row.weight != 0.f) {     // whatever an ignored token's logits are, its gradient is zero
+                    const float f = __builtin_amdgcn_exp2f(c[k] - row.lse2) * row.weight;
+                    const int target = row.target - col;
+                    float e[8], p[8];
+                    unpack8<f16>(w[k], e);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        p[i] = fmaf(e[i], f, i == target ? -row.weight : 0.f);
+                        if (CAP && e[i] > 0.f) {
+                            const float x = (c[k] + __builtin_amdgcn_logf(e[i])) * (kLn2 * a.inv_cap);
+                            p[i] *= fmaf(-x, x, 1.0f);
+                        }
+                    }
+                    out = pack8<T>(p);
+                }
+                u32x4* dst = reinterpret_cast<u32x4*>(at + (int64_t)(k0 + k) * a.e_pitch * 2);
+                if constexpr (PAST) __builtin_nontemporal_store(out, dst);
+                else *dst = out;
+            }
         }
     }
 }
@@ -784,35 +844,20 @@ __device__ inline void head_grad_tile(const HeadGrad& a, int item, uint8_t* lds)
     static_assert(WD * TD * 32 == kHeadTile && WC * TC * 32 == kHeadTile, "tile");
     const GradItem g = grad_item(a, item, kHeadTile);
     const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), wd = wave / WC, wc = wave % WC;
-    typedef ColOperand<kHeadTile, NW> COp;
-    typedef RowOperand<kHeadTile, NW> ROp;
-    COp A, Q;
-    ROp P;
-    A.init(a.a, a.a_pitch * 2, g.d0, (a.dim + 7) / 8 * 8, wave, lane);
-    if constexpr (KTOKEN) Q.init(a.p, a.p_pitch * 2, g.c0, a.p_cols, wave, lane);
-    else P.init(a.p, a.p_pitch * 2, g.c0, a.p_rows, wave, lane);
+    ColOperand<kHeadTile, NW, TD> A;
+    A.init(a.a, a.a_pitch * 2, g.d0, (a.dim + 7) / 8 * 8, (int64_t)g.s0 * kHeadK, wd * TD * 32, true, wave, lane);
+    const int stages = g.s1 - g.s0, left_a = a.a_rows - g.s0 * kHeadK, left_p = a.k - g.s0 * kHeadK;
     floatx16 acc[TD][TC];
-#pragma unroll
-    for (int i = 0; i < TD; ++i)
-#pragma unroll
-        for (int j = 0; j < TC; ++j) acc[i][j] = floatx16(0.f);
-    k_loop<T, TD, TC>(
-        acc, g.s1 - g.s0,
-        [&](int kt, int slot, int u) {
-            A.load(lds_address(lds) + slot * kOperand, u, (int64_t)(g.s0 + kt) * kHeadK, a.a_rows, wave);
-        },
-        [&](int kt, int slot, int u) {
-            if constexpr (KTOKEN) Q.load(lds_address(lds) + slot * kOperand, u, (int64_t)(g.s0 + kt) * kHeadK, a.p_rows, wave);
-            else P.load(lds_address(lds) + slot * kOperand, u, g.s0 + kt, a.k, wave);
-        },
-        [&](int slot, int i, int kc) {
-            return COp::template frag<true>(lds + slot * kOperand, wd * TD * 32 + 32 * i, kc, lane);
-        },
-        [&](int slot, int j, int kc) {
-            const int c = wc * TC * 32 + 32 * j;
-            if constexpr (KTOKEN) return COp::template frag<false>(lds + slot * kOperand, c, kc, lane);
-            else return ROp::frag(lds + slot * kOperand, c + lane % 32, kc, lane);
-        });
+    clear(acc);
+    if constexpr (KTOKEN) {
+        ColOperand<kHeadTile, NW, TC> P;
+        P.init(a.p, a.p_pitch * 2, g.c0, a.p_cols, (int64_t)g.s0 * kHeadK, wc * TC * 32, false, wave, lane);
+        k_loop<T, TD, TC>(acc, stages, A, P, left_a, left_p, lds_address(lds), wave);
+    } else {
+        RowOperand<kHeadTile, NW> P;
+        P.init(a.p, a.p_pitch * 2, g.c0, a.p_rows, (int64_t)g.s0 * kHeadK, wc * TC * 32 + lane % 32, wave, lane);
+        k_loop<T, TD, TC>(acc, stages, A, P, left_a, left_p, lds_address(lds), wave);
+    }
     grad_epilogue<T, TD, TC>(a, acc, g.split, g.d0 + wd * TD * 32, g.c0 + wc * TC * 32, lane);
 }
 
@@ -827,54 +872,19 @@ __device__ inline void head_grad_mid_tile(const HeadGrad& a, int item, uint8_t* 
     static_assert(WD * TD * 32 == kMidEdge && WC * TC * 32 == kMidEdge, "tile");
     const GradItem g = grad_item(a, item, kMidEdge);
     const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), wd = wave / WC, wc = wave % WC;
-    typedef ColOperand<kMidEdge, NW> COp;
-    typedef RowOperand<kMidEdge, NW> ROp;
-    constexpr int kStage = COp::kBytes + ROp::kBytes;
-    static_assert(2 * kStage == kMidGradBytes && COp::kBytes == ROp::kBytes, "LDS");
-    COp A, Q;
-    ROp P;
-    A.init(a.a, a.a_pitch * 2, g.d0, (a.dim + 7) / 8 * 8, wave, lane);
-    if constexpr (KTOKEN) Q.init(a.p, a.p_pitch * 2, g.c0, a.p_cols, wave, lane);
-    else P.init(a.p, a.p_pitch * 2, g.c0, a.p_rows, wave, lane);
-    auto load = [&](int kt) {
-        const uint32_t at = lds_address(lds) + (kt - g.s0) % 2 * kStage;
-#pragma unroll
-        for (int u = 0; u < COp::kLoads; ++u) A.load(at, u, (int64_t)kt * kHeadK, a.a_rows, wave);
-#pragma unroll
-        for (int u = 0; u < COp::kLoads; ++u) {
-            if constexpr (KTOKEN) Q.load(at + COp::kBytes, u, (int64_t)kt * kHeadK, a.p_rows, wave);
-            else P.load(at + COp::kBytes, u, kt, a.k, wave);
-        }
-    };
+    ColOperand<kMidEdge, NW, TD> A;
+    A.init(a.a, a.a_pitch * 2, g.d0, (a.dim + 7) / 8 * 8, (int64_t)g.s0 * kHeadK, wd * TD * 32, true, wave, lane);
+    const int stages = g.s1 - g.s0, left_a = a.a_rows - g.s0 * kHeadK, left_p = a.k - g.s0 * kHeadK;
     floatx16 acc[TD][TC];
-#pragma unroll
-    for (int i = 0; i < TD; ++i)
-#pragma unroll
-        for (int j = 0; j < TC; ++j) acc[i][j] = floatx16(0.f);
-    if (g.s0 < g.s1) load(g.s0);
-    for (int kt = g.s0; kt < g.s1; ++kt) {
-        wait_loads<0>();
-        wait_lds();
-        bare_barrier();      // stage kt is in LDS, and every wave is done with stage kt - 1
-        if (kt + 1 < g.s1) load(kt + 1);
-        const uint8_t* ta = lds + (kt - g.s0) % 2 * kStage;
-        const uint8_t* tp = ta + COp::kBytes;
-#pragma unroll
-        for (int kc = 0; kc < kHeadK / 16; ++kc) {
-            u32x4 fa[TD], fb[TC];
-#pragma unroll
-            for (int i = 0; i < TD; ++i) fa[i] = COp::template frag<true>(ta, wd * TD * 32 + 32 * i, kc, lane);
-#pragma unroll
-            for (int j = 0; j < TC; ++j) {
-                const int c = wc * TC * 32 + 32 * j;
-                if constexpr (KTOKEN) fb[j] = COp::template frag<false>(tp, c, kc, lane);
-                else fb[j] = ROp::frag(tp, c + lane % 32, kc, lane);
-            }
-#pragma unroll
-            for (int i = 0; i < TD; ++i)
-#pragma unroll
-                for (int j = 0; j < TC; ++j) acc[i][j] = mfma<T>(fa[i], fb[j], acc[i][j]);
-        }
+    clear(acc);
+    if constexpr (KTOKEN) {
+        ColOperand<kMidEdge, NW, TC> P;
+        P.init(a.p, a.p_pitch * 2, g.c0, a.p_cols, (int64_t)g.s0 * kHeadK, wc * TC * 32, false, wave, lane);
+        k_loop_mid<T, 2>(acc, stages, A, P, left_a, left_p, lds_address(lds), wave);
+    } else {
+        RowOperand<kMidEdge, NW> P;
+        P.init(a.p, a.p_pitch * 2, g.c0, a.p_rows, (int64_t)g.s0 * kHeadK, wc * TC * 32 + lane % 32, wave, lane);
+        k_loop_mid<T, 2>(acc, stages, A, P, left_a, left_p, lds_address(lds), wave);
     }
     grad_epilogue<T, TD, TC>(a, acc, g.split, g.d0 + wd * TD * 32, g.c0 + wc * TC * 32, lane);
 }
