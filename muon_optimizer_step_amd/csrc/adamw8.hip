@@ -31,7 +31,6 @@ constexpr int kQBlock = MUON_ADAMW8_BLOCK;
 constexpr int kA8Threads = 256;
 constexpr int kA8Blocks = 2;                                         // blocks of 256 values per wave
 constexpr int kA8Elems = kA8Threads / kWave * kA8Blocks * kQBlock;   // values per workgroup
-constexpr int kA8Chunk = 48;                                         // tensors per launch
 static_assert(kQBlock == 4 * kWave, "one wave covers a block with 4 values per lane");
 
 // One launch holds at most 2^23 workgroups (2^32 threads is the grid's limit),
@@ -55,14 +54,20 @@ struct A8Tensor {
     uint16_t flags;
     uint16_t place;      // index in the call's list (MUON_MAX_TENSORS fits)
 };
-struct A8Args {
-    A8Tensor t[kA8Chunk];
+struct A8Scalars {
     int n;
     float keep, beta1, omb1, beta2, omb2, step_size, inv_sqrt_bc2, eps, decay, one_minus_decay;
     int dither;
     uint32_t key;        // mixed bits of seed and step
 };
-static_assert(sizeof(A8Args) <= 4096, "AdamW kernel arguments exceed 4 KiB");
+// A launch's table is a kernel argument; its size is one of two, so that a
+// single tensor's call does not copy a long one.
+template <int CHUNK>
+struct A8Args {
+    A8Scalars s;
+    A8Tensor t[CHUNK];
+};
+constexpr int kA8Short = 8, kA8Chunk = 192;     // tensors per launch
 
 // 32 mixed bits: xor-shifts and odd multipliers (the leading fraction bits of
 // sqrt 2 and sqrt 3).
@@ -111,7 +116,7 @@ constexpr uint32_t kHalfDown = 0x7FFFF;   // nearest code, halves to the smaller
 
 // One value: moments, parameter.  Every operation rounds by itself, so that the
 // result is the plain formula's in any implementation.
-__device__ inline void update_one(const A8Args& a, float g, float& m, float& v, float& root, float& p) {
+__device__ inline void update_one(const A8Scalars& a, float g, float& m, float& v, float& root, float& p) {
 #pragma clang fp contract(off)
     m = m * a.beta1 + g * a.omb1;
     v = v * a.beta2 + (g * g) * a.omb2;
@@ -119,7 +124,7 @@ __device__ inline void update_one(const A8Args& a, float g, float& m, float& v, 
     p = p * a.keep - (m / (root * a.inv_sqrt_bc2 + a.eps)) * a.step_size;
 }
 
-__device__ inline float ema_one(const A8Args& a, float e, float p) {
+__device__ inline float ema_one(const A8Scalars& a, float e, float p) {
 #pragma clang fp contract(off)
     return e * a.decay + p * a.one_minus_decay;
 }
@@ -145,7 +150,7 @@ __device__ inline int find_entry(const Tab* t, int n, int blk) {
 
 // One block of 256 values (or what is left of the tensor) by one wave.
 template <bool VEC>
-__device__ inline void adamw8_block(const A8Args& a, const A8Tensor& T, int64_t base, uint32_t key) {
+__device__ inline void adamw8_block(const A8Scalars& a, const A8Tensor& T, int64_t base, uint32_t key) {
     const int lane = threadIdx.x % kWave;
     const int64_t i0 = base + 4 * lane;
     const int left = VEC ? 4 : (int)max((int64_t)0, min((int64_t)4, T.numel - i0));   // values of this lane
@@ -290,9 +295,11 @@ __device__ inline void adamw8_block(const A8Args& a, const A8Tensor& T, int64_t 
     }
 }
 
-__global__ __launch_bounds__(kA8Threads) void adamw8_kernel(const A8Args a) {
-    const int ti = find_entry(a.t, a.n, blockIdx.x);
-    const A8Tensor& T = a.t[ti];
+template <int CHUNK>
+__global__ __launch_bounds__(kA8Threads) void adamw8_kernel(const A8Args<CHUNK> args) {
+    const A8Scalars& a = args.s;
+    const int ti = find_entry(args.t, a.n, blockIdx.x);
+    const A8Tensor& T = args.t[ti];
     const uint32_t key = mix32(a.key + T.place);
     const int64_t first = (int64_t)(blockIdx.x - T.block_begin) * kA8Elems;
     const bool vec = (T.flags & kA8Vec) != 0;
@@ -370,6 +377,49 @@ int validate_moments(const void* mc, const void* ms, const void* rc, const void*
     return check_overlaps(spans, what);
 }
 
+// The kernels over a validated list: table entries of whole tensors, CHUNK per launch.
+template <int CHUNK>
+int enqueue_adamw8(const adamw8_tensor_t* tensors, int32_t n, const A8Scalars& scalars, hipStream_t s) {
+    A8Args<CHUNK> a;
+    a.s = scalars;
+    for (int i = 0; i < n;) {
+        a.s.n = 0;
+        int64_t blocks = 0;
+        for (; i < n && a.s.n < CHUNK; ++i) {
+            const adamw8_tensor_t& x = tensors[i];
+            if (x.numel == 0) continue;
+            const int64_t nb = (x.numel + kA8Elems - 1) / kA8Elems;
+            if (blocks + nb > kA8MaxGroups) break;
+            A8Tensor& T = a.t[a.s.n++];
+            T.param = x.param;
+            T.grad = x.grad;
+            T.m = x.exp_avg;
+            T.v = x.rms;
+            T.m_scale = x.exp_avg_scale;
+            T.v_scale = x.rms_scale;
+            T.ema = x.ema;
+            T.copy = static_cast<bf16*>(x.copy);
+            T.numel = x.numel;
+            T.block_begin = (int)blocks;
+            T.place = (uint16_t)i;
+            const uintptr_t wide = reinterpret_cast<uintptr_t>(x.param) | reinterpret_cast<uintptr_t>(x.ema);
+            const uintptr_t half = reinterpret_cast<uintptr_t>(x.copy) | (x.grad_bf16 ? reinterpret_cast<uintptr_t>(x.grad) : 0);
+            const uintptr_t codes = reinterpret_cast<uintptr_t>(x.exp_avg) | reinterpret_cast<uintptr_t>(x.rms);
+            const bool vec = wide % 16 == 0 && (x.grad_bf16 || reinterpret_cast<uintptr_t>(x.grad) % 16 == 0) && half % 8 == 0 &&
+                             codes % (x.exp_avg_scale ? 4 : 16) == 0;
+            T.flags = (uint16_t)((vec ? kA8Vec : 0) | (x.grad_bf16 ? kA8GradBf16 : 0));
+            blocks += nb;
+        }
+        if (a.s.n == 0) continue;
+        hipError_t err = timed_launch("adamw8", s, [&] {
+            adamw8_kernel<CHUNK><<<(int)blocks, kA8Threads, 0, s>>>(a);
+            return hipGetLastError();
+        });
+        if (err != hipSuccess) return fail(MUON_ERR_HIP, "adamw8 launch failed: %s", hipGetErrorString(err));
+    }
+    return MUON_OK;
+}
+
 }  // namespace
 }  // namespace muon
 
@@ -420,9 +470,9 @@ int adamw8_step(const adamw8_tensor_t* tensors, int32_t n, float lr, float beta1
     }
     const int rc = check_overlaps(spans, "adamw8_step");
     if (rc) return rc;
-    A8Args a;
-    memset(&a, 0, sizeof(a));
+    A8Scalars a;
     const float decayed = lr * weight_decay;
+    a.n = 0;
     a.keep = 1.0f - decayed;
     a.beta1 = beta1;
     a.omb1 = 1.0f - beta1;
@@ -437,43 +487,7 @@ int adamw8_step(const adamw8_tensor_t* tensors, int32_t n, float lr, float beta1
     a.dither = dither;
     a.key = mix32((uint32_t)seed + 0x9E3779B9u * (uint32_t)step);
     hipStream_t s = static_cast<hipStream_t>(stream);
-    // table entries of whole tensors, kA8Chunk per launch
-    for (int i = 0; i < n;) {
-        a.n = 0;
-        int64_t blocks = 0;
-        for (; i < n && a.n < kA8Chunk; ++i) {
-            const adamw8_tensor_t& x = tensors[i];
-            if (x.numel == 0) continue;
-            const int64_t nb = (x.numel + kA8Elems - 1) / kA8Elems;
-            if (blocks + nb > kA8MaxGroups) break;
-            A8Tensor& T = a.t[a.n++];
-            T.param = x.param;
-            T.grad = x.grad;
-            T.m = x.exp_avg;
-            T.v = x.rms;
-            T.m_scale = x.exp_avg_scale;
-            T.v_scale = x.rms_scale;
-            T.ema = x.ema;
-            T.copy = static_cast<bf16*>(x.copy);
-            T.numel = x.numel;
-            T.block_begin = (int)blocks;
-            T.place = (uint16_t)i;
-            const uintptr_t wide = reinterpret_cast<uintptr_t>(x.param) | reinterpret_cast<uintptr_t>(x.ema);
-            const uintptr_t half = reinterpret_cast<uintptr_t>(x.copy) | (x.grad_bf16 ? reinterpret_cast<uintptr_t>(x.grad) : 0);
-            const uintptr_t codes = reinterpret_cast<uintptr_t>(x.exp_avg) | reinterpret_cast<uintptr_t>(x.rms);
-            const bool vec = wide % 16 == 0 && (x.grad_bf16 || reinterpret_cast<uintptr_t>(x.grad) % 16 == 0) && half % 8 == 0 &&
-                             codes % (x.exp_avg_scale ? 4 : 16) == 0;
-            T.flags = (uint16_t)((vec ? kA8Vec : 0) | (x.grad_bf16 ? kA8GradBf16 : 0));
-            blocks += nb;
-        }
-        if (a.n == 0) continue;
-        hipError_t err = timed_launch("adamw8", s, [&] {
-            adamw8_kernel<<<(int)blocks, kA8Threads, 0, s>>>(a);
-            return hipGetLastError();
-        });
-        if (err != hipSuccess) return fail(MUON_ERR_HIP, "adamw8 launch failed: %s", hipGetErrorString(err));
-    }
-    return MUON_OK;
+    return n <= kA8Short ? enqueue_adamw8<kA8Short>(tensors, n, a, s) : enqueue_adamw8<kA8Chunk>(tensors, n, a, s);
 }
 
 int adamw8_encode(const float* exp_avg, const float* exp_avg_sq, void* exp_avg_codes, float* exp_avg_scale,

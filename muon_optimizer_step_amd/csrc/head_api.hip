@@ -48,14 +48,15 @@ struct HeadPlan {
 
 // Tile edge and splits of K for the two gradients (hidden: rows x dim, K the
 // vocabulary; weight: vocab x dim, K the rows), those that take least by this
-// estimate in stages of a 256 x 256 tile (1.8 us).  A tile costs a prologue and
+// estimate in stages of a 256 x 256 tile (1.6 us).  A tile costs a prologue and
 // an epilogue (5 us, 3 stages); a split's partial sums are written and read
 // again (13 us a tile with head_join's share).  One 256 x 256 tile or two 128 x
-// 128 tiles run on a compute unit at a time; the latter take 0.55 of a stage
+// 128 tiles run on a compute unit at a time; the latter take 0.62 of a stage
 // each, both together.  Measured, gradients and join in us, 256 / 128 wide:
-//   2048 x 4096 x 512  44 / 38     1531 x 12345 x 600  77 / 68
-//   500 x 1000 x 256   27 / 19     8192 x 8192 x 512   149 / 139
-//   16384 x 8192 x 512 258 / 350   8192 x 131072 x 2048  7640 / 9523
+//   2048 x 4096 x 512  44 / 38     1531 x 12345 x 600  67 / 69
+//   500 x 1000 x 256   25 / 18     8192 x 8192 x 512   133 / 145
+//   1000 x 20000 x 200 46 / 39     300 x 50000 x 768   86 / 81
+//   16384 x 8192 x 512 244 / 344   8192 x 131072 x 2048  6780 / 9520
 struct GradSplit {
     int edge = kHeadTile, splits_h = 1, splits_w = 1;
 };
@@ -68,7 +69,7 @@ GradSplit split_k(int64_t rows, int64_t vocab, int64_t dim, bool grad_hidden, bo
     for (int edge : {256, 128}) {
         const int64_t tiles_d = ceil_div(dim, edge);
         const int64_t n = grad_hidden ? ceil_div(rows, edge) * tiles_d : 0, m = grad_weight ? ceil_div(vocab, edge) * tiles_d : 0;
-        const double stage = edge == 256 ? 1.0 : 0.55, part = edge == 256 ? 8.0 : 3.0, ends = edge == 256 ? 3.0 : 2.0;
+        const double stage = edge == 256 ? 1.0 : 0.62, part = edge == 256 ? 8.0 : 3.0, ends = edge == 256 ? 3.0 : 2.0;
         const int slots = edge == 256 ? kCus : 2 * kCus;
         for (int i : tried) {
             if (i > 1 && (n == 0 || a / i < kMinStagesPerSplit)) break;
@@ -94,24 +95,25 @@ GradSplit split_k(int64_t rows, int64_t vocab, int64_t dim, bool grad_hidden, bo
 
 // Kernel for the logits of a piece.  Measured (us, bf16, no gradients):
 //   tokens x vocab x dim      stream  128 x 32  128 x 64  128 x 128  256 x 256
-//   1 x 8192 x 512               6.8       8.5       9.5       10.2       18.5
-//   1 x 32768 x 1024            17.1      14.5      14.7       17.5       30.1
-//   64 x 131072 x 2048           282       123       109        128        144
-//   256 x 32768 x 1024             -         -      28.3       22.5       31.5
-//   2048 x 8192 x 512              -         -         -       24.8       22.6
-//   1024 x 50000 x 1024            -         -         -        114        123
-//   4096 x 8192 x 512              -         -         -       43.6       40.6
+//   1 x 8192 x 512               7.8       9.2       9.4       10.6       18.4
+//   1 x 32768 x 1024            17.0      14.1      15.3       18.1       28.0
+//   64 x 131072 x 2048             -       123       111        129        140
+//   256 x 32768 x 1024             -         -      29.2       22.8       28.4
+//   1531 x 12345 x 600             -         -         -       40.7       42.9
+//   2048 x 8192 x 512              -         -         -       25.0       21.9
+//   1024 x 50000 x 1024            -         -         -        119        114
+//   4096 x 8192 x 512              -         -         -       44.2       39.2
 // The last two differ in their rate (a 256 x 256 tile moves half the operand
 // bytes per product) and in the waste of their last round, counted here in
 // rounds of 256 tiles; two 128 x 128 tiles per compute unit overlap, less so
 // where a cap makes the vector work of the tile's end longer (1021 x 50021 x
-// 1000 capped: 161 against 150).
+// 1000 capped: 161 against 143).
 int logits_variant(int64_t tokens, int64_t vocab, bool cap) {
     if (tokens <= 32) return vocab < 16384 && tokens <= kHeadStream ? kLogitsStream : kLogitsMid32;
     if (tokens <= 64) return kLogitsMid64;
     auto tiles = [&](int64_t edge) { return ((tokens + edge - 1) / edge) * ((vocab + edge - 1) / edge); };
     const double big = (double)((tiles(256) + kCus - 1) / kCus);
-    const double mid = (cap ? 0.65 : 0.57) * std::max(1.0, (double)tiles(128) / (2 * kCus) + 0.3);
+    const double mid = (cap ? 0.70 : 0.64) * std::max(1.0, (double)tiles(128) / (2 * kCus) + 0.3);
     return mid < big ? kLogitsMid128 : kLogitsTile;
 }
 

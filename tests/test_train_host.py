@@ -92,12 +92,12 @@ def test_head_loss_workspace_is_bounded_by_the_piece():
     lib = _lib.load()
     big = dict(vocab=131072, dim=2048, hidden_stride=2048, weight_stride=2048, grad_hidden_stride=2048,
                grad_weight_stride=2048)
-    size = {n: lib.head_loss_workspace_size(_problem(tokens=n, **big)) for n in (4096, 8192, 65536)}
+    size = {n: lib.head_loss_workspace_size(_problem(tokens=n, **big)) for n in (4096, 16384, 65536)}
     # one piece of probabilities, whatever the batch; beyond one piece the fp32 sums of grad_weight join it
     sums = 4 * 131072 * 2048
     assert size[4096] < _lib.MUON_HEAD_PIECE_BYTES + (1 << 28)
-    assert size[8192] < _lib.MUON_HEAD_PIECE_BYTES + sums + (1 << 28)
-    assert size[65536] - size[8192] < 1 << 20
+    assert size[16384] < _lib.MUON_HEAD_PIECE_BYTES + sums + (1 << 28)
+    assert size[65536] - size[16384] < 1 << 20
     # scoring needs the partial sums only
     score = _problem(tokens=8192, loss=None, grad_hidden=None, grad_weight=None, **big)
     assert lib.head_loss_workspace_size(score) < 1 << 27
