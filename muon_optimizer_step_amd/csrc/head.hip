@@ -1021,9 +1021,9 @@ hipError_t rows_typed(const HeadRows& a, hipStream_t s) {
 
 template <typename T>
 hipError_t prob_typed(const HeadRows& a, hipStream_t s) {
-    // a workgroup takes whole rows where there are rows enough for 4 on each compute unit
+    // a workgroup takes whole rows where there are rows enough for 8 on each compute unit
     const int row_blocks = (a.rows + kProbRows - 1) / kProbRows;
-    const int wanted = std::max(1, 1024 / row_blocks);
+    const int wanted = std::max(1, 2048 / row_blocks);
     const int across = (int)(((a.e_pitch + wanted - 1) / wanted + 2047) / 2048 * 2048);
     const int blocks = (int)((a.e_pitch + across - 1) / across), grid = blocks * row_blocks;
     // far more than the last-level cache holds: past it (8192 x 131072: 856 -> 731 us; 16384 x 8192: 86 -> 101)
