@@ -79,6 +79,12 @@ __device__ inline float capped(float z, float cap, float inv_cap) {
     return fmaf(-2.0f * cap, __builtin_amdgcn_rcpf(t + 1.0f), cap);
 }
 
+// The cap's derivative 1 - tanh(z / cap)^2 = 4 t / (1 + t)^2, t = exp(-2 |z| / cap).
+__device__ inline float cap_slope(float z, float inv_cap) {
+    const float t = __builtin_amdgcn_exp2f(-fabsf(z) * inv_cap * (2.0f * kLog2e)), u = __builtin_amdgcn_rcpf(t + 1.0f);
+    return 4.0f * t * u * u;
+}
+
 // 16 bytes per lane, from base + off, straight into LDS at address dst + PLUS +
 // 16 x lane (base and dst the wave's).  As assembly because the compiler makes
 // every transposing LDS read wait for all direct loads that it knows of, those
@@ -619,46 +625,115 @@ __global__ __launch_bounds__(256) void head_logits_stream_kernel(const HeadLogit
 }
 
 // ---------------------------------------------------------------- rows
-// Two partials joined: the larger reference, the sums in units of it.
+// Two partials joined: the larger reference, the sums in units of it.  The same
+// bits in either order of the two.
 __device__ inline void join_sums(float& top, float& sum, float top2, float sum2) {
     const float m = fmaxf(top, top2);
+    const bool first = top >= top2;
     // both -infinity: vocabulary padding only, nothing to add
-    sum = m == -INFINITY ? sum + sum2 : sum * __builtin_amdgcn_exp2f(top - m) + sum2 * __builtin_amdgcn_exp2f(top2 - m);
+    const float d = m == -INFINITY ? 0.f : -fabsf(top - top2);
+    sum = fmaf(first ? sum2 : sum, __builtin_amdgcn_exp2f(d), first ? sum : sum2);
     top = m;
 }
 
 // THREADS threads on R tokens, THREADS / R for each (thread t: token t % R): joins
-// the sub-tiles' partials of a token, in an order that depends on THREADS and R
-// only, to its base-2 log-sum-exp, and with `first` computes the target's logit as
-// a dot product of its own, writes loss and log-sum-exp and the copy of
-// hidden.  Every thread returns its token's values.
+// the sub-tiles' partials of a token to its base-2 log-sum-exp, and with `first`
+// computes the target's logit as a dot product of its own, writes loss and
+// log-sum-exp and the copy of hidden.  Under a cap the target's logit is also
+// computed where the target is among the vocabulary entries col0 .. end - 1.
+// Every thread returns its token's values.
+//
+// Both sums run over 64 classes (partials, or 8 elements of the dot product,
+// modulo 64), the partials' classes in four parts (partials modulo 256) of their
+// own.  Parts meet in pairs, then classes in pairs, fours, eights and sixteens, and the four
+// sixteens in turn: an order that does not depend on THREADS and R, so that a
+// token's loss has the same bits with and without gradients.
 struct Row {
     float lse2, weight;      // weight in P; 0 for tokens that do not count, NaN for a target out of range
+    float slope;             // the cap's derivative at the target's logit, where that is computed
     int target;              // -1 for none
 };
+constexpr int kClasses = 64, kParts = 4, kGroup = 16;
+template <int THREADS, int R>
+struct RowShape {
+    static constexpr int S = THREADS / R;                             // threads of a token
+    static constexpr int kOwn = S < kClasses ? kClasses / S : 1;      // classes of a thread
+    static constexpr int kHeld = kOwn * (kWave / R < S ? kWave / R : S);   // classes of a token within a wave
+    static constexpr int kShared = kHeld < kGroup ? kHeld : kGroup;   // of those, how many meet by shuffles
+    static constexpr int kSlots = kClasses / kShared;                 // what then meets through LDS
+    static constexpr bool kSpread = S == kClasses * kParts;           // each part of a class has a thread
+    static_assert(S <= kClasses || kSpread, "threads of a token");
+};
 template <typename T, int THREADS, int R>
-__device__ inline Row head_row(const HeadRows& a, int row, bool first, float (*red)[THREADS / kWave][R]) {
-    constexpr int S = THREADS / R, kWaves = THREADS / kWave;
+__device__ inline Row head_row(const HeadRows& a, int row, bool first, int col0, int end,
+                               float (*red)[RowShape<THREADS, R>::kSlots][R]) {
+    typedef RowShape<THREADS, R> Shape;
+    constexpr int S = Shape::S, C = Shape::kOwn, kShared = Shape::kShared, kSlots = Shape::kSlots;
     const int r = threadIdx.x % R, s = threadIdx.x / R;
-    const bool live = row < a.tokens, held = row < a.rows;
-    float top = -INFINITY, sum = 0.f;
-    if (live)
+    const bool live = row < a.tokens, held = row < a.rows, works = s < kClasses;   // the dot product's threads
+    float tops[C], sums[C], dots[C];
+    auto part = [&](int k, float& top, float& sum) {
+        if (k < a.nsub) join_sums(top, sum, a.ref[(int64_t)k * a.stat_pitch + row], a.sum[(int64_t)k * a.stat_pitch + row]);
+    };
+    if constexpr (Shape::kSpread) {
+        __shared__ float meet[2][kParts][kClasses];
+        static_assert(C == 1 && R == 1, "one token, one class a thread");
+        float top = -INFINITY, sum = 0.f;
+        if (live)
 #pragma unroll 4
-        for (int k = s; k < a.nsub; k += S)
-            join_sums(top, sum, a.ref[(int64_t)k * a.stat_pitch + row], a.sum[(int64_t)k * a.stat_pitch + row]);
+            for (int k = s; k < a.nsub; k += kClasses * kParts) part(k, top, sum);
+        meet[0][s / kClasses][s % kClasses] = top;
+        meet[1][s / kClasses][s % kClasses] = sum;
+        __syncthreads();
+        const int c = s % kClasses;
+        tops[0] = meet[0][0][c];
+        sums[0] = meet[1][0][c];
+        join_sums(tops[0], sums[0], meet[0][1][c], meet[1][1][c]);
+        float top2 = meet[0][2][c], sum2 = meet[1][2][c];
+        join_sums(top2, sum2, meet[0][3][c], meet[1][3][c]);
+        join_sums(tops[0], sums[0], top2, sum2);
+    } else {
+        float top[kParts][C], sum[kParts][C];
+#pragma unroll
+        for (int q = 0; q < kParts; ++q)
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                top[q][c] = -INFINITY;
+                sum[q][c] = 0.f;
+            }
+        if (live)
+            for (int k0 = s * C; k0 < a.nsub; k0 += kClasses * kParts)
+#pragma unroll
+                for (int q = 0; q < kParts; ++q)
+#pragma unroll
+                    for (int c = 0; c < C; ++c) part(k0 + q * kClasses + c, top[q][c], sum[q][c]);
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            join_sums(top[0][c], sum[0][c], top[1][c], sum[1][c]);
+            join_sums(top[2][c], sum[2][c], top[3][c], sum[3][c]);
+            join_sums(top[0][c], sum[0][c], top[2][c], sum[2][c]);
+            tops[c] = top[0][c];
+            sums[c] = sum[0][c];
+        }
+    }
+#pragma unroll
+    for (int c = 0; c < C; ++c) dots[c] = 0.f;
     const int64_t t = live ? a.targets[row] : a.ignore_index;
     const bool counted = live && t != a.ignore_index, valid = t >= 0 && t < a.vocab;
-    float dot = 0.f;
-    if (first && counted && valid) {
+    if (counted && valid && works && (first || (a.cap > 0.f && t >= col0 && t < end))) {
         const T* h = static_cast<const T*>(a.h) + (int64_t)row * a.h_pitch;
         const T* w = static_cast<const T*>(a.w) + t * a.w_pitch;
-        for (int d = 8 * s; d < a.dim; d += 8 * S) {
-            float x[8], y[8];
-            unpack8<T>(*reinterpret_cast<const u32x4*>(h + d), x);
-            unpack8<T>(*reinterpret_cast<const u32x4*>(w + d), y);
+        for (int d0 = 8 * C * s; d0 < a.dim; d0 += 8 * kClasses)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) dot = fmaf(x[i], y[i], dot);
-        }
+            for (int c = 0; c < C; ++c) {
+                const int d = d0 + 8 * c;
+                if (d >= a.dim) continue;
+                float x[8], y[8];
+                unpack8<T>(*reinterpret_cast<const u32x4*>(h + d), x);
+                unpack8<T>(*reinterpret_cast<const u32x4*>(w + d), y);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) dots[c] = fmaf(x[i], y[i], dots[c]);
+            }
     }
     if (first && a.copy && held)
         for (int d = 8 * s; d < a.dim; d += 8 * S) {
@@ -667,27 +742,51 @@ __device__ inline Row head_row(const HeadRows& a, int row, bool first, float (*r
             *reinterpret_cast<u32x4*>(static_cast<T*>(a.copy) + (int64_t)row * a.copy_pitch + d) = v;
         }
 #pragma unroll
-    for (int off = R; off < kWave; off <<= 1) {
+    for (int w = 1; w < C; w <<= 1)
+#pragma unroll
+        for (int c = 0; c < C; c += 2 * w) {
+            join_sums(tops[c], sums[c], tops[c + w], sums[c + w]);
+            dots[c] += dots[c + w];
+        }
+    float top = tops[0], sum = sums[0], dot = dots[0];
+#pragma unroll
+    for (int w = C; w < kShared; w <<= 1) {
+        const int off = w / C * R;
         join_sums(top, sum, __shfl_xor(top, off, kWave), __shfl_xor(sum, off, kWave));
         dot += __shfl_xor(dot, off, kWave);
     }
-    if (threadIdx.x % kWave < R) {
-        red[0][threadIdx.x / kWave][r] = top;
-        red[1][threadIdx.x / kWave][r] = sum;
-        red[2][threadIdx.x / kWave][r] = dot;
+    if (works && s * C % kShared == 0) {
+        const int at = s * C / kShared;
+        red[0][at][r] = top;
+        red[1][at][r] = sum;
+        red[2][at][r] = dot;
     }
     __syncthreads();
-    top = red[0][0][r];
-    sum = red[1][0][r];
-    dot = red[2][0][r];
+    constexpr int kEach = kGroup / kShared;       // slots of a sixteen
+    static_assert(kEach == 1 || kEach == 4, "one sixteen per slot, or four slots per sixteen");
 #pragma unroll
-    for (int w = 1; w < kWaves; ++w) {
-        join_sums(top, sum, red[0][w][r], red[1][w][r]);
-        dot += red[2][w][r];
+    for (int g = 0; g < kSlots / kEach; ++g) {
+        float gt = red[0][g * kEach][r], gs = red[1][g * kEach][r], gd = red[2][g * kEach][r];
+        if constexpr (kEach == 4) {
+            join_sums(gt, gs, red[0][4 * g + 1][r], red[1][4 * g + 1][r]);
+            gd += red[2][4 * g + 1][r];
+            float ht = red[0][4 * g + 2][r], hs = red[1][4 * g + 2][r], hd = red[2][4 * g + 2][r];
+            join_sums(ht, hs, red[0][4 * g + 3][r], red[1][4 * g + 3][r]);
+            hd += red[2][4 * g + 3][r];
+            join_sums(gt, gs, ht, hs);
+            gd += hd;
+        }
+        if (g == 0) {
+            top = gt; sum = gs; dot = gd;
+        } else {
+            join_sums(top, sum, gt, gs);
+            dot += gd;
+        }
     }
     Row out;
     out.lse2 = top + __builtin_amdgcn_logf(sum);
     out.target = counted && valid ? (int)t : -1;
+    out.slope = a.cap > 0.f ? cap_slope(dot, a.inv_cap) : 1.f;
     out.weight = 0.f;
     if (counted) out.weight = valid ? (a.train ? (a.weights ? a.weights[row] : 1.f) * a.scalars[0] : 1.f) : __builtin_nanf("");
     if (first && s == 0) {
@@ -706,24 +805,27 @@ __device__ inline Row head_row(const HeadRows& a, int row, bool first, float (*r
 
 template <typename T, int THREADS, int R>
 __global__ __launch_bounds__(THREADS) void head_rows_kernel(const HeadRows a) {
-    __shared__ float red[3][THREADS / kWave][R];
-    head_row<T, THREADS, R>(a, blockIdx.x * R + threadIdx.x % R, true, red);
+    __shared__ float red[3][RowShape<THREADS, R>::kSlots][R];
+    head_row<T, THREADS, R>(a, blockIdx.x * R + threadIdx.x % R, true, 0, 0, red);
 }
 
 // ---------------------------------------------------------------- probabilities
 // 8 tokens x `across` columns per workgroup: first the tokens' values (again by
 // each workgroup of their columns), then e -> P in place, 8 columns of the 8
 // tokens per thread at a time.  HBM-bound: reads and writes 2 bytes an entry.
+// Under a cap the derivative 1 - (l / cap)^2 is taken from log e, off by 2^-11 /
+// cap: less than the rounding of P to 16 bits unless it is below 1 / cap itself;
+// the target's, in P of the size of the weight even where e is zero, from its logit.
 constexpr int kProbRows = 8, kProbBatch = 4;
 template <typename T, bool CAP, bool PAST>
 __global__ __launch_bounds__(256) void head_prob_kernel(const HeadRows a, int blocks, int across) {
-    __shared__ float red[3][4][kProbRows];
+    __shared__ float red[3][RowShape<256, kProbRows>::kSlots][kProbRows];
     __shared__ Row rows[kProbRows];
     const int row0 = blockIdx.x / blocks * kProbRows, col0 = blockIdx.x % blocks * across;
-    const Row mine = head_row<T, 256, kProbRows>(a, row0 + threadIdx.x % kProbRows, col0 == 0, red);
+    const int end = (int)min<int64_t>(col0 + across, a.e_pitch), live = min(kProbRows, a.rows - row0);
+    const Row mine = head_row<T, 256, kProbRows>(a, row0 + threadIdx.x % kProbRows, col0 == 0, col0, end, red);
     if (threadIdx.x < kProbRows) rows[threadIdx.x] = mine;
     __syncthreads();
-    const int end = (int)min<int64_t>(col0 + across, a.e_pitch), live = min(kProbRows, a.rows - row0);
     for (int col = col0 + 8 * threadIdx.x; col < end; col += 8 * 256) {
         uint8_t* at = static_cast<uint8_t*>(a.e) + ((int64_t)row0 * a.e_pitch + col) * 2;
         const float* ref = a.ref + (int64_t)(col / a.sub) * a.stat_pitch + row0;
@@ -753,8 +855,10 @@ __global__ __launch_bounds__(256) void head_prob_kernel(const HeadRows a, int bl
                         p[i] = fmaf(e[i], f, i == target ? -row.weight : 0.f);
                         if (CAP && e[i] > 0.f) {
                             const float x = (c[k] + __builtin_amdgcn_logf(e[i])) * (kLn2 * a.inv_cap);
-                            p[i] *= fmaf(-x, x, 1.0f);
+                            p[i] = fmaf(-x, x, 1.0f) * e[i] * f;
                         }
+                        // the target's term is no small one, whatever its e: its derivative comes from the logit itself
+                        if (CAP && i == target) p[i] = fmaf(e[i], f, -row.weight) * row.slope;
                     }
                     out = pack8<T>(p);
                 }

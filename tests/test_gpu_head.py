@@ -36,7 +36,7 @@ def _f64(x):
     return x.double().numpy()
 
 
-def _check(r, want, dim, dtype, cap, grads, label):
+def _check(r, want, dim, dtype, cap, grads, label, target=None):
     lim = (dim + 16) * 2.0 ** -24 * want["abs_logit"] + 8 * 2.0 ** -23 * cap
     lse_tol = lim + 2.0 ** -20 * (1 + np.abs(want["lse"]))
     for k, tol in (("lse", lse_tol), ("nll", 2 * lse_tol)):
@@ -53,6 +53,8 @@ def _check(r, want, dim, dtype, cap, grads, label):
             continue
         got = got.double().cpu().numpy()
         tol = share * want[mag] + 1.01 * U[dtype] * np.abs(want[k]) + TINY[dtype]
+        if target is not None:
+            tol += target[k](2 * lse_tol)
         err = np.abs(got - want[k])
         assert (err <= tol).all(), f"{label} {k}: worst {np.max(err / tol):.3g} of the tolerance"
 
@@ -132,6 +134,32 @@ def test_a_target_outside_the_vocabulary_gives_nan(target):
     assert np.isnan(nll[17]) and np.isfinite(np.delete(nll, 17)).all() and np.isnan(float(r.loss))
     gh = r.grad_hidden.float().cpu().numpy()
     assert np.isnan(gh[17]).all() and np.isfinite(np.delete(gh, 17, axis=0)).all()
+
+
+@pytest.mark.parametrize("n,v", [(40, 300), (300, 3000), (60, 20000)])
+def test_capped_target_far_below_the_maximum(n, v):
+    """The target's share of the gradient is - weight x the cap's derivative however small its probability is: targets
+    up to 56 below another token's logit, near and far from it in the vocabulary."""
+    import torch
+    import muon_optimizer_step_amd as ms
+    d, cap = 256, 30.0
+    h, w, t = _inputs(n, v, d, "bf16", seed=13, ignored=0.0)
+    other = (t + torch.randint(1, 40, (n,), generator=torch.Generator().manual_seed(14)) * (1 + 11 * (torch.arange(n) % 2))) % v
+    unit = lambda i: w[i].float() / w[i].float().square().sum(1, keepdim=True)  # noqa: E731
+    down = torch.linspace(0.0, 50.0, n)[:, None]
+    h = (40.0 * unit(other) - down * unit(t)).bfloat16()
+    want = oh.head_loss(_f64(h), _f64(w), t.numpy(), softcap=cap)
+    assert want["nll"].max() > 50
+    r = ms.linear_cross_entropy_grad(h.cuda(), w.cuda(), t.cuda(), softcap=cap)
+
+    # The target's entry is a difference, softmax - 1: an error x of the exponent (of the logit and the log-sum-exp) is
+    # x of the softmax, at most x itself, also where the difference is far smaller.
+    def in_weight(x):
+        out = np.zeros((v, d))
+        np.add.at(out, t.numpy(), (x / n)[:, None] * np.abs(_f64(h)))
+        return out
+    target = {"grad_hidden": lambda x: (x / n)[:, None] * np.abs(_f64(w))[t.numpy()], "grad_weight": in_weight}
+    _check(r, want, d, "bf16", cap, 1.0, "far target", target)
 
 
 def test_infinite_and_huge_logits():
@@ -262,6 +290,19 @@ def test_same_bits_every_time_on_any_stream_and_workspace(n, v, d):
     torch.cuda.current_stream().wait_stream(side)
     for a, b, c in zip(first, second, third):
         assert torch.equal(a, b) and torch.equal(a, c)
+
+
+@pytest.mark.parametrize("n,v,d", [(1, 300, 64), (20, 17000, 600), (64, 33000, 512), (300, 2000, 64), (300, 20000, 1040),
+                                   (2050, 8450, 136), (1100, 40000, 64)])
+@pytest.mark.parametrize("cap", [0.0, 12.0])
+def test_scores_have_the_bits_of_the_gradients_call(n, v, d, cap):
+    """Sums over a token are taken in one order whatever the launch: few and many tokens, few and many partials."""
+    import torch
+    import muon_optimizer_step_amd as ms
+    h, w, t = (x.cuda() for x in _inputs(n, v, d, "bf16", seed=15))
+    s, r = ms.linear_cross_entropy(h, w, t, softcap=cap), ms.linear_cross_entropy_grad(h, w, t, softcap=cap)
+    only = ms.linear_cross_entropy_grad(h, w, t, softcap=cap, grad_hidden=False, grad_weight=False)
+    assert torch.equal(s.nll, r.nll) and torch.equal(s.lse, r.lse) and torch.equal(s.nll, only.nll)
 
 
 @pytest.mark.parametrize("n,v,d", [(20, 900, 64), (300, 3000, 100)])
