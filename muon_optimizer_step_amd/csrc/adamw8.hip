@@ -485,7 +485,7 @@ int adamw8_step(const adamw8_tensor_t* tensors, int32_t n, float lr, float beta1
     a.decay = ema_decay;
     a.one_minus_decay = 1.0f - ema_decay;
     a.dither = dither;
-    a.key = mix32((uint32_t)seed + 0x9E3779B9u * (uint32_t)step);
+    a.key = mix32(((uint32_t)seed ^ mix32((uint32_t)(seed >> 32))) + 0x9E3779B9u * (uint32_t)step);
     hipStream_t s = static_cast<hipStream_t>(stream);
     return n <= kA8Short ? enqueue_adamw8<kA8Short>(tensors, n, a, s) : enqueue_adamw8<kA8Chunk>(tensors, n, a, s);
 }

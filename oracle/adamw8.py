@@ -74,6 +74,7 @@ def dithers(n: int, seed, step: int, place: int):
     if seed is None:
         d = np.full(n, 0x7FFFF, dtype=np.int64)
         return d, d
+    seed = (seed & 0xFFFFFFFF) ^ int(mix(seed >> 32 & 0xFFFFFFFF))
     key = mix(mix((seed + 0x9E3779B9 * step) & 0xFFFFFFFF) + np.uint64(place))
     x = mix(key + np.arange(n, dtype=np.uint64)).astype(np.int64)
     return (x >> 16) << 4, (x & 0xFFFF) << 4

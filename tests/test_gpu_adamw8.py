@@ -200,6 +200,22 @@ def test_stochastic_rounding_keeps_small_decay_on_the_average():
     assert abs(mean[None] - 0.5) <= 0.02 * 0.5
 
 
+def test_every_bit_of_the_seed_counts():
+    import torch
+    import muon_optimizer_step_amd as ms
+    n = 4096
+    rng = np.random.default_rng(16)
+    p, g = rng.standard_normal(n).astype(np.float32), gu.dev(rng.standard_normal(n).astype(np.float32))
+    seen = []
+    for seed in [7] + [7 ^ (1 << b) for b in range(64)] + [-7]:
+        s = ms.AdamW8State.zeros_like(g)
+        ms.adamw8_step([gu.dev(p)], [g], [s], lr=1e-3, step=1, seed=seed)
+        seen.append((s.exp_avg.view(torch.uint8), s.rms.view(torch.uint8)))
+    for i, a in enumerate(seen):
+        for b in seen[:i]:
+            assert not torch.equal(a[0], b[0]) and not torch.equal(a[1], b[1])
+
+
 @pytest.mark.parametrize("n", [1, 255, 256, 1000, 70000])
 def test_conversion_from_and_to_float32_moments(n):
     import torch
