@@ -11,9 +11,13 @@
 // the sub-tile's maximum less 15, so the largest e is 2^15: 11 significant
 // bits down to 2^-29 of the maximum, which leaves the rounding of P to its
 // 16-bit type as the only one that counts).  head_rows joins the sub-tiles of a
-// token, head_prob turns e into P in place, and head_grad multiplies P with W
+// token, head_prob turns e into P in place, and head_grads multiplies P with W
 // and P^T with H.  The logits thus cost one product, and only a piece of the
 // tokens is in memory at a time.
+//
+// Bound: the three products (6 x tokens x vocab x dim operations), on MFMA, and
+// for training the piece's way through HBM (6 bytes per token and vocabulary entry, the
+// products' reads of P not counted, which the caches serve in part).
 #include <algorithm>
 #include <type_traits>
 
@@ -262,8 +266,10 @@ __device__ inline void load_stage(Op& op, uint32_t dst, int left) {
 // in the first half of the window, has to have arrived; A of k + 2 may be under way.
 //
 // Measured on 16384 x 8192 x 512 (the gradient of hidden): two buffers filled
-// in a burst after the barrier 165 us, this 127; with scalar address work cut
-// from 300 to 40 instructions a stage, see head_grads.
+// in a burst after the barrier 165 us, this 127.  Counters of the three products of
+// 8192 x 131072 x 2048: no LDS bank conflicts, MFMA busy in 67 % of the cycles of
+// head_logits and 77 % of head_grads, cycles of a clock of about 1.6 GHz by the
+// same counters.
 constexpr int kSlots = 5;
 constexpr size_t kRingBytes = (size_t)kSlots * kOperand;
 template <typename T, int TA, int TB, typename OA, typename OB>
@@ -435,11 +441,11 @@ __device__ inline void head_scalars(const HeadScalars& a, void* lds) {
 // ---------------------------------------------------------------- logits
 // What one wave does with its logits: acc[tv][tt] holds 32 vocabulary entries
 // (v0 + 32 tv + 16 p + 8 (l / 32) + i in register 8 p + i) of token t0 + 32 tt + l % 32.
-// e goes to memory through LDS (`stage`, this wave's 512 TV bytes per 8 tokens x
-// 4), so that a store instruction writes whole rows of 32 TV entries instead of
-// 32 bytes to each of 32 tokens.
+// e goes to memory through LDS (`stage`, this wave's own), so that a store
+// instruction writes whole rows of 32 TV entries instead of 32 bytes to each of
+// 32 tokens.
 enum { kNoStore = 0, kStore, kStorePast };    // e not kept; kept; kept, written past the caches
-template <int TV> constexpr int kEpilogueBytes = 32 * TV * 64;
+template <int TV> constexpr int kEpilogueBytes = 32 * TV * 64;     // 32 tokens x 32 TV entries of 2 bytes
 template <int TV, int TT, int STORE, bool CAP>
 __device__ inline void logits_epilogue(const HeadLogits& a, floatx16 (&acc)[TV][TT], int v0, int t0, int sub, int lane,
                                        uint8_t* stage) {
@@ -515,7 +521,11 @@ __device__ inline void tile_of(const HeadLogits& a, int item, int& tile_v, int& 
 }
 
 // Tile of 256 vocabulary entries x 256 tokens: 8 waves of 128 x 64, 32x32x16
-// MFMAs.
+// MFMAs, so that an operand byte from LDS serves the most products that 128
+// accumulator registers hold.  Bound by MFMA where dim is long (16384 x 32768 x
+// 1024: 885 us, 1.24 PFLOP/s; 8192 x 131072 x 2048: 3.33 ms, 1.32), by the tile's
+// ends where it is short (16384 x 8192 x 512: 143 us, 0.96; with e stored
+// 184, of which 44 are e's 268 MB).
 template <typename T, int STORE, bool CAP>
 __global__ __launch_bounds__(512, 2) void head_logits_kernel(const HeadLogits a) {
     constexpr int WV = 2, WT = 4, TV = 4, TT = 2, BV = WV * TV * 32, BT = WT * TT * 32, NW = WV * WT;
@@ -545,7 +555,9 @@ __global__ __launch_bounds__(512, 2) void head_logits_kernel(const HeadLogits a)
 // Tile of 128 vocabulary entries x 32, 64 or 128 tokens, two workgroups of 4
 // waves per compute unit: for few tokens, where W streams past them (two or
 // three stages of 64 K in LDS keep its loads in flight), and for problems with too
-// few 256 x 256 tiles.
+// few 256 x 256 tiles.  Bound for few tokens by HBM (64 x 131072 x 2048: 108 us,
+// 4.9 TB/s), otherwise by the vector work and the waits of its shorter tiles
+// (2048 x 4096 x 512: 15 us, 0.57 PFLOP/s).
 template <int TOKENS> struct MidTile;
 template <> struct MidTile<32> { static constexpr int WV = 4, WT = 1, TV = 1, TT = 1, kBuffers = 3; };
 template <> struct MidTile<64> { static constexpr int WV = 4, WT = 1, TV = 1, TT = 2, kBuffers = 3; };
@@ -584,7 +596,8 @@ __global__ __launch_bounds__(256, 2) void head_logits_mid_kernel(const HeadLogit
 // Up to 32 tokens and a small vocabulary, where there is little to read and
 // latency counts: a workgroup for every 32 vocabulary rows, operands straight
 // from memory (each row of W is used once), the waves take every fourth 128
-// bytes of K and meet in LDS.
+// bytes of K and meet in LDS.  1 x 8192 x 512: 5.0 us for 8.4 MB, head_rows 2.8;
+// a launch alone is over 2.
 template <typename T, int STORE, bool CAP>
 __global__ __launch_bounds__(256) void head_logits_stream_kernel(const HeadLogits a) {
     __shared__ __align__(16) float part[4][16][kWave];
@@ -803,6 +816,9 @@ __device__ inline Row head_row(const HeadRows& a, int row, bool first, int col0,
     return out;
 }
 
+// Bound by latency: 3 us for one token's 256 partials, 13 for 64 tokens' 4096
+// (which 64 threads for each token, the classes alone, took 21 for), 24 for 16384
+// tokens' 256.
 template <typename T, int THREADS, int R>
 __global__ __launch_bounds__(THREADS) void head_rows_kernel(const HeadRows a) {
     __shared__ float red[3][RowShape<THREADS, R>::kSlots][R];
@@ -812,7 +828,10 @@ __global__ __launch_bounds__(THREADS) void head_rows_kernel(const HeadRows a) {
 // ---------------------------------------------------------------- probabilities
 // 8 tokens x `across` columns per workgroup: first the tokens' values (again by
 // each workgroup of their columns), then e -> P in place, 8 columns of the 8
-// tokens per thread at a time.  HBM-bound: reads and writes 2 bytes an entry.
+// tokens per thread at a time.  HBM-bound: reads and writes 2 bytes an entry
+// (8192 x 131072: 935 us, 4.6 TB/s; 16384 x 8192: 101 us, 5.3 TB/s).  An XCD
+// takes consecutive workgroups, whose partials share cache lines (987 and 104
+// us without).
 // Under a cap the derivative 1 - (l / cap)^2 is taken from log e, off by 2^-11 /
 // cap: less than the rounding of P to 16 bits unless it is below 1 / cap itself;
 // the target's, in P of the size of the weight even where e is zero, from its logit.
@@ -821,7 +840,9 @@ template <typename T, bool CAP, bool PAST>
 __global__ __launch_bounds__(256) void head_prob_kernel(const HeadRows a, int blocks, int across) {
     __shared__ float red[3][RowShape<256, kProbRows>::kSlots][kProbRows];
     __shared__ Row rows[kProbRows];
-    const int row0 = blockIdx.x / blocks * kProbRows, col0 = blockIdx.x % blocks * across;
+    const int item = xcd_item((a.rows + kProbRows - 1) / kProbRows * blocks);
+    if (item < 0) return;
+    const int row0 = item / blocks * kProbRows, col0 = item % blocks * across;
     const int end = (int)min<int64_t>(col0 + across, a.e_pitch), live = min(kProbRows, a.rows - row0);
     const Row mine = head_row<T, 256, kProbRows>(a, row0 + threadIdx.x % kProbRows, col0 == 0, col0, end, red);
     if (threadIdx.x < kProbRows) rows[threadIdx.x] = mine;
@@ -887,7 +908,10 @@ __device__ inline void head_loss_sum(const HeadLoss& a, float* red) {
 // ---------------------------------------------------------------- gradients
 // Tile of 256 output columns d x 256 rows, K split over workgroups where the
 // tiles alone would leave compute units idle.  A = W or H with K strided; P with K
-// contiguous (dH, K the vocabulary) or strided (dW, K the tokens).
+// contiguous (dH, K the vocabulary) or strided (dW, K the tokens).  Bound by MFMA:
+// 8192 x 131072 x 2048, both gradients 6.69 ms, 1.32 PFLOP/s; 16384 x 8192 x 512,
+// 226 us, 1.22, where splits and their partial sums cost the difference.
+//
 // A wave's sums to memory: acc[i][j] holds columns d0 + 32 i + 16 p + 8 (l / 32) + e
 // (register 8 p + e) of row c0 + 32 j + l % 32.
 template <typename T, int TD, int TC>
@@ -1019,7 +1043,8 @@ __global__ __launch_bounds__(MID ? 256 : 512, 2) void head_grads_kernel(const He
     }
 }
 
-// The splits' sums in order, rounded once.
+// The splits' sums in order, rounded once.  HBM-bound where large: 8 us for 42 MB
+// (16384 x 8192 x 512); otherwise latency.
 template <typename T>
 __global__ __launch_bounds__(256) void head_join_kernel(const HeadJoin a) {
     const int64_t octs = (a.dim + 7) / 8, first = octs * a.part[0].cols, items = first + octs * a.part[1].cols;
@@ -1047,7 +1072,8 @@ __global__ __launch_bounds__(256) void head_join_kernel(const HeadJoin a) {
 }
 
 // ---------------------------------------------------------------- small passes
-// Copy with rows padded to whole chunks, ignored rows and rows beyond the end zero.
+// Copy with rows padded to whole chunks, ignored rows and rows beyond the end
+// zero: for inputs whose rows are not 16-byte aligned, which nothing else here reads.
 __global__ __launch_bounds__(256) void head_pack_kernel(const HeadPack a) {
     const int64_t per = a.dst_pitch / 8, items = per * a.rows;
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < items; i += (int64_t)gridDim.x * 256) {
@@ -1129,7 +1155,7 @@ hipError_t prob_typed(const HeadRows& a, hipStream_t s) {
     const int row_blocks = (a.rows + kProbRows - 1) / kProbRows;
     const int wanted = std::max(1, 2048 / row_blocks);
     const int across = (int)(((a.e_pitch + wanted - 1) / wanted + 2047) / 2048 * 2048);
-    const int blocks = (int)((a.e_pitch + across - 1) / across), grid = blocks * row_blocks;
+    const int blocks = (int)((a.e_pitch + across - 1) / across), grid = xcd_grid(blocks * row_blocks);
     // far more than the last-level cache holds: past it (8192 x 131072: 856 -> 731 us; 16384 x 8192: 86 -> 101)
     const bool past = (int64_t)a.rows * a.e_pitch * 2 > (int64_t)1 << 30;
     if (a.cap > 0.f) {
