@@ -829,16 +829,18 @@ __global__ __launch_bounds__(THREADS) void head_rows_kernel(const HeadRows a) {
 // 8 tokens x `across` columns per workgroup: first the tokens' values (again by
 // each workgroup of their columns), then e -> P in place, 8 columns of the 8
 // tokens per thread at a time.  HBM-bound: reads and writes 2 bytes an entry
-// (8192 x 131072: 935 us, 4.6 TB/s; 16384 x 8192: 101 us, 5.3 TB/s).  An XCD
-// takes consecutive workgroups, whose partials share cache lines (987 and 104
-// us without).
+// (8192 x 131072: 894 us, 4.8 TB/s; 16384 x 8192: 101 us, 5.3 TB/s).  An XCD
+// takes consecutive workgroups, whose partials share cache lines (987 against 935
+// and 104 against 101 us).  All 8 tokens' loads at a time where e is past the
+// caches (935 -> 894 us), 4 where it is not (8: 1531 x 12345 capped 22 -> 26).
 // Under a cap the derivative 1 - (l / cap)^2 is taken from log e, off by 2^-11 /
 // cap: less than the rounding of P to 16 bits unless it is below 1 / cap itself;
 // the target's, in P of the size of the weight even where e is zero, from its logit.
-constexpr int kProbRows = 8, kProbBatch = 4;
+constexpr int kProbRows = 8;
 template <typename T, bool CAP, bool PAST>
 __global__ __launch_bounds__(256) void head_prob_kernel(const HeadRows a, int blocks, int across) {
     __shared__ float red[3][RowShape<256, kProbRows>::kSlots][kProbRows];
+    constexpr int kBatch = PAST ? kProbRows : kProbRows / 2;
     __shared__ Row rows[kProbRows];
     const int item = xcd_item((a.rows + kProbRows - 1) / kProbRows * blocks);
     if (item < 0) return;
@@ -851,18 +853,18 @@ __global__ __launch_bounds__(256) void head_prob_kernel(const HeadRows a, int bl
         uint8_t* at = static_cast<uint8_t*>(a.e) + ((int64_t)row0 * a.e_pitch + col) * 2;
         const float* ref = a.ref + (int64_t)(col / a.sub) * a.stat_pitch + row0;
 #pragma unroll 1
-        for (int k0 = 0; k0 < live; k0 += kProbBatch) {
-            u32x4 w[kProbBatch];
-            float c[kProbBatch];
+        for (int k0 = 0; k0 < live; k0 += kBatch) {
+            u32x4 w[kBatch];
+            float c[kBatch];
 #pragma unroll
-            for (int k = 0; k < kProbBatch; ++k) {
+            for (int k = 0; k < kBatch; ++k) {
                 if (k0 + k >= live) continue;
                 const u32x4* src = reinterpret_cast<const u32x4*>(at + (int64_t)(k0 + k) * a.e_pitch * 2);
                 w[k] = PAST ? __builtin_nontemporal_load(src) : *src;
                 c[k] = ref[k0 + k];
             }
 #pragma unroll
-            for (int k = 0; k < kProbBatch; ++k) {
+            for (int k = 0; k < kBatch; ++k) {
                 if (k0 + k >= live) continue;
                 const Row row = rows[k0 + k];
                 u32x4 out = {0u, 0u, 0u, 0u};
