@@ -111,7 +111,12 @@ int adamw8_decode(const void* exp_avg_codes, const float* exp_avg_scale, const v
  *   tokens >= 0, vocab >= 1, dim >= 1 (limits below); softcap finite, >= 0.
  * Products take their 16-bit inputs as they are and sum in float32; the
  * probabilities are rounded to 16 bits once, before they are multiplied with
- * weight and hidden; gradients are rounded once.  dim a multiple of 8 with
+ * weight and hidden; gradients are rounded once.  Probabilities come from
+ * exponentials kept in float16 in units of the largest of 32, 64 or 128
+ * neighbours: they have 11 significant bits down to 2^-29 of it and end at
+ * 2^-40.  Under a softcap the factor 1 - (l / softcap)^2 has an absolute error of
+ * 2^-11 / softcap (at the target: float32's).  nll and lse have the same bits
+ * whatever else is asked for.  dim a multiple of 8 with
  * 16-byte aligned rows is read in place, anything else through a padded copy
  * in the workspace.
  * For gradients the tokens go through the workspace in pieces of at most
