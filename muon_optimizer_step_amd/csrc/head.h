@@ -14,6 +14,7 @@ constexpr int kHeadTile = 256;     // output tile edge of the products
 constexpr int kHeadMidVocab = 128; // vocabulary entries of a tile of the kernels for few tokens or small problems
 constexpr int kHeadStream = 32;    // tokens that the streaming kernel takes at most
 constexpr int kHeadStreamSub = 32; // vocabulary entries of its workgroups
+constexpr int kHeadRowGroups = 256; // tokens up to which head_rows takes a workgroup for each
 
 // Kernels for the logits, and the vocabulary entries of their partial maxima
 // and sums (what one wave holds).
@@ -31,6 +32,15 @@ struct HeadScalars {
     int type;
 };
 
+// The partials of a piece: a reference and a sum for each sub-tile and token.
+struct HeadStats {
+    float* ref;
+    float* sum;
+    int rows;                // tokens that there is room for
+    int per_sub, per_token;  // elements from one to the next
+    __host__ __device__ int64_t at(int sub, int token) const { return (int64_t)sub * per_sub + (int64_t)token * per_token; }
+};
+
 // Logits of a piece of the tokens against the whole vocabulary, reduced to a
 // reference exponent and a sum per token and `sub` vocabulary entries, and (e
 // set) kept as fp16 exp2(logit - reference).
@@ -42,9 +52,7 @@ struct HeadLogits {
     int64_t e_pitch;
     int e_rows;              // rows that exist in e
     int e_past;            // e is larger than the last cache: written past the caches
-    float* ref;              // [sub][stat_pitch]
-    float* sum;
-    int stat_pitch;
+    HeadStats stats;
     int tokens, vocab, dim;
     float cap, inv_cap;      // 0: no cap
     int tiles_v, tiles_t;
@@ -54,9 +62,8 @@ struct HeadLogits {
 // Per token: log-sum-exp and loss; with e also the probabilities' gradient in
 // its place.
 struct HeadRows {
-    const float* ref;
-    const float* sum;
-    int stat_pitch, nsub;
+    HeadStats stats;
+    int nsub;
     void* e;                 // in: fp16 exp2 values; out: probability gradient, input type
     int64_t e_pitch;
     int sub;                 // vocabulary entries per partial

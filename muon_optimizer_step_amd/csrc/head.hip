@@ -504,9 +504,9 @@ __device__ inline void logits_epilogue(const HeadLogits& a, floatx16 (&acc)[TV][
             }
         }
         sum += __shfl_xor(sum, 32, kWave);
-        if (half == 0 && token < a.stat_pitch) {
-            a.ref[(int64_t)sub * a.stat_pitch + token] = ref;
-            a.sum[(int64_t)sub * a.stat_pitch + token] = sum;
+        if (half == 0 && token < a.stats.rows) {
+            a.stats.ref[a.stats.at(sub, token)] = ref;
+            a.stats.sum[a.stats.at(sub, token)] = sum;
         }
     }
 }
@@ -685,8 +685,15 @@ __device__ inline Row head_row(const HeadRows& a, int row, bool first, int col0,
     const int r = threadIdx.x % R, s = threadIdx.x / R;
     const bool live = row < a.tokens, held = row < a.rows, works = s < kClasses;   // the dot product's threads
     float tops[C], sums[C], dots[C];
-    auto part = [&](int k, float& top, float& sum) {
-        if (k < a.nsub) join_sums(top, sum, a.ref[(int64_t)k * a.stat_pitch + row], a.sum[(int64_t)k * a.stat_pitch + row]);
+    // a partial, nothing beyond the last one: loads without a branch, so that many are under way
+    auto load = [&](int k, float& top, float& sum) {
+        const int64_t at = a.stats.at(min(k, a.nsub - 1), row);
+        top = a.stats.ref[at];
+        sum = a.stats.sum[at];
+        if (k >= a.nsub) {
+            top = -INFINITY;
+            sum = 0.f;
+        }
     };
     if constexpr (Shape::kSpread) {
         __shared__ float meet[2][kParts][kClasses];
@@ -694,7 +701,11 @@ __device__ inline Row head_row(const HeadRows& a, int row, bool first, int col0,
         float top = -INFINITY, sum = 0.f;
         if (live)
 #pragma unroll 4
-            for (int k = s; k < a.nsub; k += kClasses * kParts) part(k, top, sum);
+            for (int k = s; k < a.nsub; k += kClasses * kParts) {
+                float top2, sum2;
+                load(k, top2, sum2);
+                join_sums(top, sum, top2, sum2);
+            }
         meet[0][s / kClasses][s % kClasses] = top;
         meet[1][s / kClasses][s % kClasses] = sum;
         __syncthreads();
@@ -715,11 +726,17 @@ __device__ inline Row head_row(const HeadRows& a, int row, bool first, int col0,
                 sum[q][c] = 0.f;
             }
         if (live)
-            for (int k0 = s * C; k0 < a.nsub; k0 += kClasses * kParts)
+            for (int k0 = s * C; k0 < a.nsub; k0 += kClasses * kParts) {
+                float top2[kParts][C], sum2[kParts][C];
 #pragma unroll
                 for (int q = 0; q < kParts; ++q)
 #pragma unroll
-                    for (int c = 0; c < C; ++c) part(k0 + q * kClasses + c, top[q][c], sum[q][c]);
+                    for (int c = 0; c < C; ++c) load(k0 + q * kClasses + c, top2[q][c], sum2[q][c]);
+#pragma unroll
+                for (int q = 0; q < kParts; ++q)
+#pragma unroll
+                    for (int c = 0; c < C; ++c) join_sums(top[q][c], sum[q][c], top2[q][c], sum2[q][c]);
+            }
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             join_sums(top[0][c], sum[0][c], top[1][c], sum[1][c]);
@@ -851,7 +868,7 @@ __global__ __launch_bounds__(256) void head_prob_kernel(const HeadRows a, int bl
     __syncthreads();
     for (int col = col0 + 8 * threadIdx.x; col < end; col += 8 * 256) {
         uint8_t* at = static_cast<uint8_t*>(a.e) + ((int64_t)row0 * a.e_pitch + col) * 2;
-        const float* ref = a.ref + (int64_t)(col / a.sub) * a.stat_pitch + row0;
+        const float* ref = a.stats.ref + a.stats.at(col / a.sub, row0);
 #pragma unroll 1
         for (int k0 = 0; k0 < live; k0 += kBatch) {
             u32x4 w[kBatch];
@@ -861,7 +878,7 @@ __global__ __launch_bounds__(256) void head_prob_kernel(const HeadRows a, int bl
                 if (k0 + k >= live) continue;
                 const u32x4* src = reinterpret_cast<const u32x4*>(at + (int64_t)(k0 + k) * a.e_pitch * 2);
                 w[k] = PAST ? __builtin_nontemporal_load(src) : *src;
-                c[k] = ref[k0 + k];
+                c[k] = ref[(int64_t)(k0 + k) * a.stats.per_token];
             }
 #pragma unroll
             for (int k = 0; k < kBatch; ++k) {
@@ -1145,7 +1162,7 @@ template <typename T>
 hipError_t rows_typed(const HeadRows& a, hipStream_t s) {
     // many tokens: 16 per workgroup, which makes 64-byte pieces of the partials
     // and, by their number, 16 or 64 threads for each; few: a workgroup each
-    if (a.rows <= 256) head_rows_kernel<T, 256, 1><<<a.rows, 256, 0, s>>>(a);
+    if (a.rows <= kHeadRowGroups) head_rows_kernel<T, 256, 1><<<a.rows, 256, 0, s>>>(a);
     else if (a.nsub <= 128) head_rows_kernel<T, 256, 16><<<(a.rows + 15) / 16, 256, 0, s>>>(a);
     else head_rows_kernel<T, 1024, 16><<<(a.rows + 15) / 16, 1024, 0, s>>>(a);
     return hipGetLastError();

@@ -268,9 +268,9 @@ int enqueue_head(const head_loss_t& p, const HeadPlan& q, uint8_t* ws, hipStream
         a.e_pitch = q.cols;
         a.e_rows = rows;
         a.e_past = 2 * (int64_t)rows * q.cols > kPastBytes;
-        a.ref = ref;
-        a.sum = sum;
-        a.stat_pitch = rows;
+        // a token's partials side by side where head_rows has a workgroup for each token, a partial's tokens otherwise
+        const bool by_token = q.e < 0 && rows <= kHeadRowGroups;
+        a.stats = {ref, sum, rows, by_token ? 1 : rows, by_token ? q.nsub : 1};
         a.tokens = tokens;
         a.vocab = vocab;
         a.dim = (int)(q.pack_h && q.pack_w ? q.dim8 : p.dim);
@@ -282,9 +282,7 @@ int enqueue_head(const head_loss_t& p, const HeadPlan& q, uint8_t* ws, hipStream
         HEAD_TRY("head_logits", launch_head_logits(a, p.dtype, q.variant, s));
         HeadRows r;
         memset(&r, 0, sizeof(r));
-        r.ref = ref;
-        r.sum = sum;
-        r.stat_pitch = rows;
+        r.stats = a.stats;
         r.nsub = q.nsub;
         r.h = hp;
         r.w = w;
