@@ -833,9 +833,9 @@ __device__ inline Row head_row(const HeadRows& a, int row, bool first, int col0,
     return out;
 }
 
-// Bound by latency: 3 us for one token's 256 partials, 13 for 64 tokens' 4096
-// (which 64 threads for each token, the classes alone, took 21 for), 24 for 16384
-// tokens' 256.
+// Bound by latency: 3 us for one token's 256 partials, 7 for 64 tokens' 4096 (13
+// where a token's partials lie a row apart, 21 with the 64 threads of the classes
+// alone), 24 for 16384 tokens' 256.
 template <typename T, int THREADS, int R>
 __global__ __launch_bounds__(THREADS) void head_rows_kernel(const HeadRows a) {
     __shared__ float red[3][RowShape<THREADS, R>::kSlots][R];
