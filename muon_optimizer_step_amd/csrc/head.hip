@@ -77,10 +77,21 @@ __device__ inline void bare_barrier() {
     asm volatile("" ::: "memory");
 }
 
-// cap tanh(z / cap); exact to a few ulp of cap, which is the scale that counts.
+// cap tanh(z / cap), to a few ulp of itself whatever the cap.  Up to half a cap from
+// zero z + z y p(y), y = (z / cap)^2, with p fitted to (tanh(x) / x - 1) / x^2 (minimax
+// on 0 .. 1/4, off by 1.5e-8 of tanh): the cap enters only through y, and far
+// above z the result is z itself.  Beyond, cap (1 - t) / (1 + t) with t = exp(-2 |z| / cap),
+// where nothing cancels.
+constexpr float kCapNear = 0.5f;
+__device__ inline float capped_near(float z, float inv_cap) {
+    const float x = z * inv_cap, y = x * x;
+    const float p = fmaf(fmaf(fmaf(0.017256994f, y, -0.05305295f), y, 0.13325988f), y, -0.3333315f);
+    return fmaf(z * y, p, z);
+}
 __device__ inline float capped(float z, float cap, float inv_cap) {
-    const float t = __builtin_amdgcn_exp2f(z * inv_cap * (2.0f * kLog2e));
-    return fmaf(-2.0f * cap, __builtin_amdgcn_rcpf(t + 1.0f), cap);
+    const float x = fabsf(z) * inv_cap, t = __builtin_amdgcn_exp2f(x * (-2.0f * kLog2e));
+    const float far = cap * ((1.0f - t) * __builtin_amdgcn_rcpf(1.0f + t));
+    return x < kCapNear ? capped_near(z, inv_cap) : copysignf(far, z);
 }
 
 // The cap's derivative 1 - tanh(z / cap)^2 = 4 t / (1 + t)^2, t = exp(-2 |z| / cap).
@@ -458,15 +469,31 @@ __device__ inline void logits_epilogue(const HeadLogits& a, floatx16 (&acc)[TV][
         int end = a.vocab - v0 - 8 * half;
         asm volatile("" : "+v"(end));     // compared with anew for each tt: the masks of all registers do not fit in scalars
         float top = -INFINITY;
+        if constexpr (CAP) {
+            // few logits are far from zero in units of the cap: the exponential form only where the wave has one
+            float most = 0.f;
+#pragma unroll
+            for (int tv = 0; tv < TV; ++tv)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) most = fmaxf(most, fabsf(acc[tv][tt][r]));
+            auto cap_all = [&](auto far) {
+#pragma unroll
+                for (int tv = 0; tv < TV; ++tv)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) {
+                        const float z = acc[tv][tt][r];
+                        acc[tv][tt][r] = decltype(far)::value ? capped(z, a.cap, a.inv_cap) : capped_near(z, a.inv_cap);
+                    }
+            };
+            if (__any(!(most * a.inv_cap < kCapNear))) cap_all(std::true_type());
+            else cap_all(std::false_type());
+        }
 #pragma unroll
         for (int tv = 0; tv < TV; ++tv)
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
-                float z = acc[tv][tt][r];
-                if (CAP) z = capped(z, a.cap, a.inv_cap);
-                if (!whole && 32 * tv + 16 * (r / 8) + r % 8 >= end) z = -INFINITY;
-                acc[tv][tt][r] = z;
-                top = fmaxf(top, z);
+                if (!whole && 32 * tv + 16 * (r / 8) + r % 8 >= end) acc[tv][tt][r] = -INFINITY;
+                top = fmaxf(top, acc[tv][tt][r]);
             }
         top = fmaxf(top, __shfl_xor(top, 32, kWave));
         // entries beyond the vocabulary only: nothing to add, and no reference

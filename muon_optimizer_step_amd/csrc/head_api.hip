@@ -11,6 +11,7 @@
 //   where K was split or the pieces' sums had to be kept in fp32
 //   head_loss   only where the loss is wanted without gradients
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 #include <cstring>
 #include <vector>
@@ -250,7 +251,8 @@ int enqueue_head(const head_loss_t& p, const HeadPlan& q, uint8_t* ws, hipStream
     }
     float* ref = reinterpret_cast<float*>(ws + q.ref);
     float* sum = reinterpret_cast<float*>(ws + q.sum);
-    const float inv_cap = p.softcap > 0.f ? 1.0f / p.softcap : 0.f;
+    // finite: zero times it has to stay zero
+    const float inv_cap = p.softcap > 0.f ? std::min(1.0f / p.softcap, FLT_MAX) : 0.f;
     auto vec = [&](const void* ptr, int64_t stride) {
         return dim % 8 == 0 && stride % 8 == 0 && reinterpret_cast<uintptr_t>(ptr) % 16 == 0;
     };
