@@ -114,8 +114,9 @@ int adamw8_decode(const void* exp_avg_codes, const float* exp_avg_scale, const v
  * weight and hidden; gradients are rounded once.  Probabilities come from
  * exponentials kept in float16 in units of the largest of 32, 64 or 128
  * neighbours: they have 11 significant bits down to 2^-29 of it and end at
- * 2^-40.  Under a softcap the factor 1 - (l / softcap)^2 has an absolute error of
- * 2^-11 / softcap (at the target: float32's).  nll and lse have the same bits
+ * 2^-40.  Under a softcap l and the factor 1 - (l / softcap)^2 are off by a few ulp of
+ * themselves, and the exponential is kept multiplied by the factor: the same bounds
+ * hold for the two together.  nll and lse have the same bits
  * whatever else is asked for.  dim a multiple of 8 with
  * 16-byte aligned rows is read in place, anything else through a padded copy
  * in the workspace.

@@ -43,10 +43,12 @@ struct HeadStats {
 
 // Logits of a piece of the tokens against the whole vocabulary, reduced to a
 // reference exponent and a sum per token and `sub` vocabulary entries, and (e
-// set) kept as fp16 exp2(logit - reference).
+// set) kept as fp16 exp2(logit - reference), times the cap's
+// derivative but at the target.
 struct HeadLogits {
     const void* h;           // tokens x dim
     const void* w;           // vocab x dim
+    const int64_t* targets;  // per token
     int64_t h_pitch, w_pitch;   // elements
     void* e;                 // nullable; e_rows x e_pitch
     int64_t e_pitch;
@@ -64,7 +66,7 @@ struct HeadLogits {
 struct HeadRows {
     HeadStats stats;
     int nsub;
-    void* e;                 // in: fp16 exp2 values; out: probability gradient, input type
+    void* e;                 // in: fp16 values of head_logits; out: probability gradient, input type
     int64_t e_pitch;
     int sub;                 // vocabulary entries per partial
     const void* h;

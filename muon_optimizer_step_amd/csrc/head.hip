@@ -7,9 +7,9 @@
 //   dH = P W;  dW = P^T H
 // head_logits multiplies H W^T tile by tile and reduces each token's logits of
 // one sub-tile of the vocabulary to a reference exponent c (base 2) and the sum of
-// e_ij = 2^(l_ij log2 e - c); for training it also writes e_ij in fp16 (c is
-// the sub-tile's maximum less 15, so the largest e is 2^15: 11 significant
-// bits down to 2^-29 of the maximum, which leaves the rounding of P to its
+// e_ij = 2^(l_ij log2 e - c); for training it also writes e_ij, times 1 - (l_ij / cap)^2
+// but at the target, in fp16 (c is the sub-tile's maximum less 15, so the largest e is 2^15: 11
+// significant bits down to 2^-29 of the maximum, which leaves the rounding of P to its
 // 16-bit type as the only one that counts).  head_rows joins the sub-tiles of a
 // token, head_prob turns e into P in place, and head_grads multiplies P with W
 // and P^T with H.  The logits thus cost one product, and only a piece of the
@@ -77,27 +77,32 @@ __device__ inline void bare_barrier() {
     asm volatile("" ::: "memory");
 }
 
-// cap tanh(z / cap), to a few ulp of itself whatever the cap.  Up to half a cap from
-// zero z + z y p(y), y = (z / cap)^2, with p fitted to (tanh(x) / x - 1) / x^2 (minimax
-// on 0 .. 1/4, off by 1.5e-8 of tanh): the cap enters only through y, and far
-// above z the result is z itself.  Beyond, cap (1 - t) / (1 + t) with t = exp(-2 |z| / cap),
-// where nothing cancels.
+// cap tanh(z / cap) and its derivative 1 - tanh(z / cap)^2, each to a few ulp of itself
+// whatever the cap.  Up to half a cap from zero the value is z + z y p(y), y = (z / cap)^2,
+// with p fitted to (tanh(x) / x - 1) / x^2 (minimax on 0 .. 1/4, off by 1.5e-8 of
+// tanh): the cap enters only through y, and far above z the result is z itself.
+// Beyond, cap (1 - t) / (1 + t) and 4 t / (1 + t)^2 with t = exp(-2 |z| / cap), where
+// nothing cancels.
+struct Capped {
+    float value, slope;
+};
 constexpr float kCapNear = 0.5f;
-__device__ inline float capped_near(float z, float inv_cap) {
+__device__ inline Capped capped_near(float z, float inv_cap) {
     const float x = z * inv_cap, y = x * x;
     const float p = fmaf(fmaf(fmaf(0.017256994f, y, -0.05305295f), y, 0.13325988f), y, -0.3333315f);
-    return fmaf(z * y, p, z);
+    Capped r;
+    r.value = fmaf(z * y, p, z);
+    const float tanh = r.value * inv_cap;
+    r.slope = fmaf(-tanh, tanh, 1.0f);
+    return r;
 }
-__device__ inline float capped(float z, float cap, float inv_cap) {
-    const float x = fabsf(z) * inv_cap, t = __builtin_amdgcn_exp2f(x * (-2.0f * kLog2e));
-    const float far = cap * ((1.0f - t) * __builtin_amdgcn_rcpf(1.0f + t));
-    return x < kCapNear ? capped_near(z, inv_cap) : copysignf(far, z);
-}
-
-// The cap's derivative 1 - tanh(z / cap)^2 = 4 t / (1 + t)^2, t = exp(-2 |z| / cap).
-__device__ inline float cap_slope(float z, float inv_cap) {
-    const float t = __builtin_amdgcn_exp2f(-fabsf(z) * inv_cap * (2.0f * kLog2e)), u = __builtin_amdgcn_rcpf(t + 1.0f);
-    return 4.0f * t * u * u;
+__device__ inline Capped capped(float z, float cap, float inv_cap) {
+    const float x = fabsf(z) * inv_cap, t = __builtin_amdgcn_exp2f(x * (-2.0f * kLog2e)), u = __builtin_amdgcn_rcpf(1.0f + t);
+    const Capped near = capped_near(z, inv_cap);
+    Capped r;
+    r.value = x < kCapNear ? near.value : copysignf(cap * ((1.0f - t) * u), z);
+    r.slope = x < kCapNear ? near.slope : 4.0f * t * u * u;
+    return r;
 }
 
 // 16 bytes per lane, from base + off, straight into LDS at address dst + PLUS +
@@ -467,54 +472,55 @@ __device__ inline void logits_epilogue(const HeadLogits& a, floatx16 (&acc)[TV][
     for (int tt = 0; tt < TT; ++tt) {
         const int token = t0 + 32 * tt + lane % 32;
         int end = a.vocab - v0 - 8 * half;
-        asm volatile("" : "+v"(end));     // compared with anew for each tt: the masks of all registers do not fit in scalars
-        float top = -INFINITY;
-        if constexpr (CAP) {
-            // few logits are far from zero in units of the cap: the exponential form only where the wave has one
-            float most = 0.f;
-#pragma unroll
-            for (int tv = 0; tv < TV; ++tv)
-#pragma unroll
-                for (int r = 0; r < 16; ++r) most = fmaxf(most, fabsf(acc[tv][tt][r]));
-            auto cap_all = [&](auto far) {
-#pragma unroll
-                for (int tv = 0; tv < TV; ++tv)
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) {
-                        const float z = acc[tv][tt][r];
-                        acc[tv][tt][r] = decltype(far)::value ? capped(z, a.cap, a.inv_cap) : capped_near(z, a.inv_cap);
-                    }
-            };
-            if (__any(!(most * a.inv_cap < kCapNear))) cap_all(std::true_type());
-            else cap_all(std::false_type());
-        }
+        asm volatile("" : "+v"(end));     // compared with anew for each pass: the masks of all registers do not fit in scalars
+        auto beyond = [&](int tv, int r) { return !whole && 32 * tv + 16 * (r / 8) + r % 8 >= end; };
+        float top = -INFINITY, most = 0.f;
 #pragma unroll
         for (int tv = 0; tv < TV; ++tv)
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
-                if (!whole && 32 * tv + 16 * (r / 8) + r % 8 >= end) acc[tv][tt][r] = -INFINITY;
-                top = fmaxf(top, acc[tv][tt][r]);
+                const float z = beyond(tv, r) ? -INFINITY : acc[tv][tt][r];
+                top = fmaxf(top, z);
+                if (CAP) most = fmaxf(most, fabsf(acc[tv][tt][r]));
+                else acc[tv][tt][r] = z;
             }
         top = fmaxf(top, __shfl_xor(top, 32, kWave));
-        // entries beyond the vocabulary only: nothing to add, and no reference
-        const float ref = top == -INFINITY ? -INFINITY : top * kLog2e - 15.0f;
-        const float minus = top == -INFINITY ? 0.f : -ref;
+        // entries beyond the vocabulary only: nothing to add, and no reference (under a cap -infinity is a logit of -cap)
+        const bool none = CAP ? v0 >= a.vocab : top == -INFINITY;
+        if (CAP) top = capped(top, a.cap, a.inv_cap).value;
+        const float ref = none ? -INFINITY : top * kLog2e - 15.0f;
+        const float minus = none ? 0.f : -ref;
         float sum = 0.f;
+        int target = -1;        // among this lane's entries
+        if constexpr (CAP && STORE != kNoStore) {
+            const int64_t t = a.targets[min(token, a.tokens - 1)];
+            if (t >= v0 + 8 * half && t < a.vocab) target = (int)t - v0 - 8 * half;
+        }
+        auto exponentials = [&](auto far) {
+            if (CAP) asm volatile("" : "+v"(end));
 #pragma unroll
-        for (int tv = 0; tv < TV; ++tv)
+            for (int tv = 0; tv < TV; ++tv)
 #pragma unroll
-            for (int p = 0; p < 2; ++p) {
-                float e[8];
+                for (int p = 0; p < 2; ++p) {
+                    float e[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    e[i] = __builtin_amdgcn_exp2f(fmaf(acc[tv][tt][8 * p + i], kLog2e, minus));
-                    sum += e[i];
+                    for (int i = 0; i < 8; ++i) {
+                        Capped l = {acc[tv][tt][8 * p + i], 1.f};
+                        if (CAP) l = decltype(far)::value ? capped(l.value, a.cap, a.inv_cap) : capped_near(l.value, a.inv_cap);
+                        e[i] = __builtin_amdgcn_exp2f(fmaf(l.value, kLog2e, minus));
+                        if (CAP && beyond(tv, 8 * p + i)) e[i] = l.slope = 0.f;
+                        sum += e[i];
+                        if (CAP && STORE != kNoStore) e[i] *= 32 * tv + 16 * p + i == target ? 1.f : l.slope;
+                    }
+                    if constexpr (STORE != kNoStore) {
+                        const int c = 4 * tv + 2 * p + half, r = lane % 32;
+                        *reinterpret_cast<u32x4*>(stage + (r * kChunks + (c ^ (r % kChunks))) * 16) = pack8<f16>(e);
+                    }
                 }
-                if constexpr (STORE != kNoStore) {
-                    const int c = 4 * tv + 2 * p + half, r = lane % 32;
-                    *reinterpret_cast<u32x4*>(stage + (r * kChunks + (c ^ (r % kChunks))) * 16) = pack8<f16>(e);
-                }
-            }
+        };
+        // few logits are far from zero in units of the cap: the exponential form only where the wave has one
+        if (CAP && __any(!(most * a.inv_cap < kCapNear))) exponentials(std::true_type());
+        else exponentials(std::false_type());
         if constexpr (STORE != kNoStore) {
             // the same wave's data: LDS keeps its order
 #pragma unroll
@@ -843,14 +849,14 @@ __device__ inline Row head_row(const HeadRows& a, int row, bool first, int col0,
     Row out;
     out.lse2 = top + __builtin_amdgcn_logf(sum);
     out.target = counted && valid ? (int)t : -1;
-    out.slope = a.cap > 0.f ? cap_slope(dot, a.inv_cap) : 1.f;
+    const Capped logit = a.cap > 0.f ? capped(dot, a.cap, a.inv_cap) : Capped{dot, 1.f};
+    out.slope = logit.slope;
     out.weight = 0.f;
     if (counted) out.weight = valid ? (a.train ? (a.weights ? a.weights[row] : 1.f) * a.scalars[0] : 1.f) : __builtin_nanf("");
     if (first && s == 0) {
         if (live) {
-            if (a.cap > 0.f) dot = capped(dot, a.cap, a.inv_cap);
             const float lse = out.lse2 * kLn2;
-            float nll = valid ? lse - dot : __builtin_nanf("");
+            float nll = valid ? lse - logit.value : __builtin_nanf("");
             if (nll < 0.f) nll = 0.f;       // the target's logit is rounded apart from the sum it is part of
             a.nll[row] = counted ? nll : 0.f;
             if (a.lse) a.lse[row] = counted ? lse : 0.f;
@@ -877,9 +883,9 @@ __global__ __launch_bounds__(THREADS) void head_rows_kernel(const HeadRows a) {
 // takes consecutive workgroups, whose partials share cache lines (987 against 935
 // and 104 against 101 us).  All 8 tokens' loads at a time where e is past the
 // caches (935 -> 894 us), 4 where it is not (8: 1531 x 12345 capped 22 -> 26).
-// Under a cap the derivative 1 - (l / cap)^2 is taken from log e, off by 2^-11 /
-// cap: less than the rounding of P to 16 bits unless it is below 1 / cap itself;
-// the target's, in P of the size of the weight even where e is zero, from its logit.
+// Under a cap head_logits has multiplied e by the derivative 1 - (l / cap)^2, taken from
+// the product in fp32, but for the target's e: there the softmax and -1 cancel
+// before the derivative, taken from the target's logit, multiplies both.
 constexpr int kProbRows = 8;
 template <typename T, bool CAP, bool PAST>
 __global__ __launch_bounds__(256) void head_prob_kernel(const HeadRows a, int blocks, int across) {
@@ -920,12 +926,7 @@ __global__ __launch_bounds__(256) void head_prob_kernel(const HeadRows a, int bl
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         p[i] = fmaf(e[i], f, i == target ? -row.weight : 0.f);
-                        if (CAP && e[i] > 0.f) {
-                            const float x = (c[k] + __builtin_amdgcn_logf(e[i])) * (kLn2 * a.inv_cap);
-                            p[i] = fmaf(-x, x, 1.0f) * e[i] * f;
-                        }
-                        // the target's term is no small one, whatever its e: its derivative comes from the logit itself
-                        if (CAP && i == target) p[i] = fmaf(e[i], f, -row.weight) * row.slope;
+                        if (CAP) p[i] *= i == target ? row.slope : 1.f;
                     }
                     out = pack8<T>(p);
                 }

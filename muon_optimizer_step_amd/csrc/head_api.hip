@@ -264,6 +264,7 @@ int enqueue_head(const head_loss_t& p, const HeadPlan& q, uint8_t* ws, hipStream
         memset(&a, 0, sizeof(a));
         a.h = hp;
         a.w = w;
+        a.targets = p.targets + at;
         a.h_pitch = h_pitch;
         a.w_pitch = w_pitch;
         a.e = q.e >= 0 ? ws + q.e : nullptr;
