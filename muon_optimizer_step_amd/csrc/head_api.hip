@@ -130,15 +130,19 @@ HeadPlan make_head_plan(const head_loss_t& p) {
     q.pack_w = odd(p.weight, p.weight_stride);
     const bool grads = p.grad_hidden || p.grad_weight;
     q.cols = round_up(p.vocab, kHeadPad);
-    q.piece = std::max<int64_t>(p.tokens, 1);
+    auto piece = [&](int64_t most) {
+        const int64_t all = std::max<int64_t>(p.tokens, 1);
+        return all * q.cols > most ? std::min(all, std::max<int64_t>(kHeadTile, most / q.cols / kHeadTile * kHeadTile)) : all;
+    };
     // gradients: what the workspace holds of the probabilities; scoring: 2^32
     // logits a launch, whose partial sums take 256 MB
-    const int64_t most = grads ? MUON_HEAD_PIECE_BYTES / 2 : (int64_t)1 << 32;
-    if (q.piece * q.cols > most) q.piece = std::max<int64_t>(kHeadTile, most / q.cols / kHeadTile * kHeadTile);
-    q.piece = std::min(q.piece, std::max<int64_t>(p.tokens, 1));
+    const int64_t grads_piece = piece(MUON_HEAD_PIECE_BYTES / 2);
+    q.piece = grads ? grads_piece : piece((int64_t)1 << 32);
     q.pieces = (p.tokens + q.piece - 1) / q.piece;
     q.rows = round_up(q.piece, kHeadPad);
-    q.variant = logits_variant(q.piece, p.vocab, p.softcap > 0.f);
+    // the kernel for the pieces of a call with gradients, whatever is asked for: a
+    // token's sums are then grouped alike, and its loss has the same bits
+    q.variant = logits_variant(grads_piece, p.vocab, p.softcap > 0.f);
     q.tile_v = q.variant == kLogitsTile ? kHeadTile : q.variant == kLogitsStream ? kHeadStreamSub : kHeadMidVocab;
     q.tile_t = q.variant == kLogitsTile ? kHeadTile : q.variant == kLogitsMid128 ? 128 : q.variant == kLogitsMid32 ? 32 : 64;
     q.sub = logits_sub(q.variant);

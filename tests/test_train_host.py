@@ -103,6 +103,35 @@ def test_head_loss_workspace_is_bounded_by_the_piece():
     assert lib.head_loss_workspace_size(score) < 1 << 27
 
 
+@pytest.mark.parametrize("n,v", [(200, 4194304), (300, 4194304), (384, 2800000), (257, 4194304), (500, 3000000),
+                                 (3000, 400000), (9000, 131072), (20000, 70000), (1 << 20, 1100), (1 << 23, 200)])
+@pytest.mark.parametrize("cap", [0.0, 30.0])
+def test_scores_and_gradients_group_a_tokens_sums_alike(n, v, cap):
+    """Vocabulary entries of a partial sum, read off the workspace: the bits of nll depend on them."""
+    lib = _lib.load()
+    d = 8
+    kw = dict(vocab=v, dim=d, hidden_stride=d, weight_stride=d, grad_hidden_stride=d, grad_weight_stride=d, softcap=cap,
+              grad_weight=None)
+    up = lambda x, m: -(-x // m) * m  # noqa: E731
+    cols = up(v, 64)
+
+    def partials(grads):
+        most = _lib.MUON_HEAD_PIECE_BYTES // 2 if grads else 1 << 32
+        piece = n if n * cols <= most else max(256, most // cols // 256 * 256)
+        rows = up(piece, 64)
+        p = _problem(tokens=n, **kw) if grads else _problem(tokens=n, **dict(kw, loss=None, grad_hidden=None))
+        size = lib.head_loss_workspace_size(p)
+        assert size > 0
+        rest = 256 + (up(4 * (n + 64), 256) + up(2 * rows * cols, 256) if grads else 0)
+        # what K splits add (at most 32 of piece x dim sums) is small beside a reference and a sum for 128 entries
+        slack = 4 * 32 * piece * d if grads else 0
+        fits = [sub for sub in (32, 64, 128) if 0 <= size - rest - 8 * rows * (up(v, sub) // sub) <= slack + 8 * rows * 256 // sub + 512]
+        assert len(fits) == 1, (size, rest, fits)
+        return fits[0]
+
+    assert partials(False) == partials(True)
+
+
 def test_binding_refuses_what_is_not_on_a_gpu_or_not_16_bit():
     import torch
     import muon_optimizer_step_amd as ms
