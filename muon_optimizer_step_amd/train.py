@@ -6,7 +6,7 @@ import ctypes
 from typing import NamedTuple, Optional
 
 from . import _lib
-from .api import _torch, _workspace_for
+from .api import _torch
 
 
 def _stream_handle(stream, device):
@@ -268,30 +268,24 @@ class PreparedLinearCrossEntropy:
         return self.result
 
 
-def _one_call(hidden, weight, targets, workspace, stream, **kw):
-    """A prepared loss run once on the stream's cached workspace."""
-    torch = _torch()
-    if workspace is None and isinstance(hidden, torch.Tensor) and hidden.device.type == "cuda":
-        s = stream if stream is not None else torch.cuda.current_stream(hidden.device)
-        probe = PreparedLinearCrossEntropy(hidden, weight, targets, workspace=torch.empty(0, dtype=torch.uint8,
-                                           device=hidden.device), stream=s, **kw)
-        need = int(probe._lib.head_loss_workspace_size(probe.problem))
-        ws = _workspace_for(need, hidden.device, s)
-        probe.workspace, probe._ws = ws, (ws.data_ptr(), ws.numel())
-        return probe(stream=s)
-    return PreparedLinearCrossEntropy(hidden, weight, targets, workspace=workspace, stream=stream, **kw)(stream=stream)
-
-
 def linear_cross_entropy(hidden, weight, targets, *, ignore_index: int = -100, softcap: float = 0.0, workspace=None,
                          stream=None) -> LinearCrossEntropy:
-    """Scores tokens: nll and log-sum-exp of each under softmax(hidden @ weight.T), float32, without the logits."""
-    return _one_call(hidden, weight, targets, workspace, stream, ignore_index=ignore_index, softcap=softcap)
+    """Scores tokens: nll and log-sum-exp of each under softmax(hidden @ weight.T), float32, without the logits.
+
+    workspace: None takes one for this call from the stream's memory (calls from several threads, and calls captured in
+    a graph, do not share any).
+    """
+    return PreparedLinearCrossEntropy(hidden, weight, targets, ignore_index=ignore_index, softcap=softcap,
+                                      workspace=workspace, stream=stream)(stream)
 
 
 def linear_cross_entropy_grad(hidden, weight, targets, *, token_weights=None, ignore_index: int = -100,
                               softcap: float = 0.0, grad_hidden=None, grad_weight=None, workspace=None,
                               stream=None) -> LinearCrossEntropy:
-    """The loss of a training step with the gradients of hidden and weight (see PreparedLinearCrossEntropy)."""
-    return _one_call(hidden, weight, targets, workspace, stream, token_weights=token_weights,
-                     ignore_index=ignore_index, softcap=softcap, grads=True, grad_hidden=grad_hidden,
-                     grad_weight=grad_weight)
+    """The loss of a training step with the gradients of hidden and weight (see PreparedLinearCrossEntropy).
+
+    workspace: as in linear_cross_entropy.
+    """
+    return PreparedLinearCrossEntropy(hidden, weight, targets, token_weights=token_weights, ignore_index=ignore_index,
+                                      softcap=softcap, grads=True, grad_hidden=grad_hidden, grad_weight=grad_weight,
+                                      workspace=workspace, stream=stream)(stream)

@@ -1,0 +1,75 @@
+"""GPU: what the binding of include/muonstep_train.h promises about buffers, streams and arguments."""
+
+import threading
+
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+
+def _small(n=40, v=300, d=64, seed=0):
+    import torch
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(n, d, generator=g).bfloat16().cuda(), torch.randn(v, d, generator=g).bfloat16().cuda(),
+            torch.randint(0, v, (n,), generator=g).cuda())
+
+
+def test_one_shot_calls_share_no_workspace():
+    """The buffers that muon_step's calls share, one for each stream, are not theirs."""
+    import muon_optimizer_step_amd as ms
+    from muon_optimizer_step_amd import api
+    api._workspaces.clear()
+    ms.linear_cross_entropy_grad(*_small(2000, 4000, 512))
+    ms.linear_cross_entropy(*_small())
+    assert not api._workspaces
+
+
+def test_one_shot_calls_of_two_threads_on_one_stream():
+    import torch
+    import muon_optimizer_step_amd as ms
+    inputs = [_small(600, 5000, 128, seed=1), _small(500, 7000, 136, seed=2)]
+    want = [[x.clone() for x in ms.linear_cross_entropy_grad(*i)] for i in inputs]
+    torch.cuda.synchronize()
+    wrong, start = [], threading.Barrier(2)
+
+    def work(k):
+        start.wait()
+        kept = [ms.linear_cross_entropy_grad(*inputs[k]) for _ in range(50)]
+        torch.cuda.synchronize()
+        wrong.extend((k, n) for n, r in enumerate(kept) if not all(torch.equal(a, b) for a, b in zip(r, want[k])))
+
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert wrong == []
+
+
+def test_one_shot_call_in_a_graph_keeps_its_workspace():
+    """Calls after the capture, larger ones on its stream and on many others, neither change what the graph computes nor
+    lose memory to it."""
+    import torch
+    import muon_optimizer_step_amd as ms
+    h, w, t = _small(300, 3000, 96)
+    ms.linear_cross_entropy_grad(h, w, t)
+    want = [x.clone() for x in ms.linear_cross_entropy_grad(h, w, t)]
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        r = ms.linear_cross_entropy_grad(h, w, t)
+    large = _small(4000, 9000, 256, seed=3)
+    for s in [torch.cuda.Stream() for _ in range(6)] + [None]:
+        if s is not None:
+            s.wait_stream(torch.cuda.current_stream())
+        ms.linear_cross_entropy_grad(*large, stream=s)
+        torch.cuda.synchronize()
+    others = [torch.full((1 << 20,), 7, dtype=torch.int32, device="cuda") for _ in range(64)]
+    for k in range(4):
+        for x in r:
+            x.fill_(float("nan"))
+        g.replay()
+        float(torch.randn(1 << 16, device="cuda").sum())
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(r, want)), k
+        assert all(bool((x == 7).all()) for x in others), k
