@@ -202,6 +202,17 @@ def _check_rows(t, name: str, dtype=None, shape=None):
         raise ValueError(f"{name}'s rows overlap, strides {t.stride()}")
 
 
+def _check_workspace(t, device):
+    """A contiguous tensor of any type on the call's device: the library writes to it."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("workspace must be a torch.Tensor")
+    if t.device != device:
+        raise ValueError(f"workspace must be on {device}, got {t.device}")
+    if not t.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+
+
 class PreparedLinearCrossEntropy:
     """The head's loss with the tensors marshalled once (same tensors and result buffers every call).
 
@@ -259,6 +270,7 @@ class PreparedLinearCrossEntropy:
             # allocated on the stream the calls run on, so that its memory is reused only in that stream's order
             with torch.cuda.stream(s):
                 workspace = torch.empty(int(need), dtype=torch.uint8, device=device)
+        _check_workspace(workspace, device)
         self.workspace = workspace
         self._ws = (workspace.data_ptr(), workspace.numel() * workspace.element_size())
         self.device = device

@@ -73,3 +73,18 @@ def test_one_shot_call_in_a_graph_keeps_its_workspace():
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(r, want)), k
         assert all(bool((x == 7).all()) for x in others), k
+
+
+def test_a_workspace_elsewhere_is_refused():
+    import torch
+    import muon_optimizer_step_amd as ms
+    h, w, t = _small()
+    need = 1 << 24
+    for bad, error in ((torch.empty(need, dtype=torch.uint8), ValueError), (torch.empty(need, dtype=torch.uint8).pin_memory(), ValueError),
+                       (torch.empty(4096, need // 2048, dtype=torch.uint8, device="cuda")[:, :need // 4096], ValueError),
+                       (need, TypeError)):
+        for call in (ms.linear_cross_entropy, ms.linear_cross_entropy_grad, ms.PreparedLinearCrossEntropy):
+            with pytest.raises(error, match="workspace"):
+                call(h, w, t, workspace=bad)
+    a = ms.linear_cross_entropy(h, w, t, workspace=torch.empty(need // 4, device="cuda"))
+    assert torch.equal(a.nll, ms.linear_cross_entropy(h, w, t).nll)

@@ -103,6 +103,20 @@ def test_head_loss_workspace_is_bounded_by_the_piece():
     assert lib.head_loss_workspace_size(score) < 1 << 27
 
 
+def test_binding_refuses_a_workspace_that_the_gpu_cannot_write():
+    import torch
+    from muon_optimizer_step_amd import train
+    for ws in (torch.empty(1 << 20, dtype=torch.uint8), torch.empty(1 << 20, device="meta")):
+        with pytest.raises(ValueError, match="workspace"):
+            train._check_workspace(ws, torch.device("cuda", 0))
+    cpu = torch.device("cpu")
+    train._check_workspace(torch.empty(16), cpu)
+    with pytest.raises(ValueError, match="contiguous"):
+        train._check_workspace(torch.empty(16, 16)[:, :8], cpu)
+    with pytest.raises(TypeError, match="workspace"):
+        train._check_workspace(1 << 44, cpu)
+
+
 @pytest.mark.parametrize("n,v", [(200, 4194304), (300, 4194304), (384, 2800000), (257, 4194304), (500, 3000000),
                                  (3000, 400000), (9000, 131072), (20000, 70000), (1 << 20, 1100), (1 << 23, 200)])
 @pytest.mark.parametrize("cap", [0.0, 30.0])
