@@ -138,15 +138,15 @@ def _adamw8_entries(params, grads, states, emas, copies):
         seen.extend(tensors)
         entries.append(tuple(t.data_ptr() if t is not None else 0 for t in tensors)
                        + (p.numel(), int(g.dtype == torch.bfloat16)))
-    return entries, _same_device(seen, "adamw8")
+    return entries, seen, _same_device(seen, "adamw8")
 
 
 class PreparedAdamW8:
     """adamw8_step with the tensor table marshalled once."""
 
     def __init__(self, params, grads, states, *, emas=None, copies=None):
-        self._keep = (list(params), list(grads), list(states), emas, copies)
-        entries, self.device = _adamw8_entries(params, grads, states, emas, copies)
+        # the tensors themselves: the caller's lists and states may change
+        entries, self._keep, self.device = _adamw8_entries(params, grads, states, emas, copies)
         self.n = len(entries)
         self.table = _lib.adamw8_table(entries)
 

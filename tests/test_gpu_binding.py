@@ -1,6 +1,8 @@
 """GPU: what the binding of include/muonstep_train.h promises about buffers, streams and arguments."""
 
+import gc
 import threading
+import weakref
 
 import pytest
 
@@ -88,3 +90,21 @@ def test_a_workspace_elsewhere_is_refused():
                 call(h, w, t, workspace=bad)
     a = ms.linear_cross_entropy(h, w, t, workspace=torch.empty(need // 4, device="cuda"))
     assert torch.equal(a.nll, ms.linear_cross_entropy(h, w, t).nll)
+
+
+def test_prepared_adamw8_keeps_its_tensors():
+    import torch
+    import muon_optimizer_step_amd as ms
+    x = lambda dtype=torch.float32: [torch.zeros(512, device="cuda", dtype=dtype)]  # noqa: E731
+    params, grads, emas, copies = x(), x(), x(), x(torch.bfloat16)
+    states = [ms.AdamW8State.zeros_like(params[0])]
+    call = ms.PreparedAdamW8(params, grads, states, emas=emas, copies=copies)
+    s = states[0]
+    refs = [weakref.ref(t) for t in (params[0], grads[0], emas[0], copies[0], s.exp_avg, s.exp_avg_scale, s.rms, s.rms_scale)]
+    for lst in (params, grads, states, emas, copies):
+        lst.clear()
+    s.exp_avg = s.exp_avg_scale = s.rms = s.rms_scale = None
+    del s
+    gc.collect()
+    assert [i for i, r in enumerate(refs) if r() is None] == []
+    call(lr=1e-3, step=1)
