@@ -9,14 +9,23 @@ from . import _lib
 from .api import _torch
 
 
-def _stream_handle(stream, device):
-    """The HIP stream of a torch stream, or of the device's current one."""
+def _run(entry, args, stream, device):
+    """entry(*args, HIP stream) with the tensors' device current: on a torch stream of that device, or on its current one."""
     torch = _torch()
-    if stream is not None:
-        return stream.cuda_stream
     if device is None:
-        return torch.cuda.current_stream().cuda_stream
-    return torch._C._cuda_getCurrentRawStream(device.index)
+        device = torch.device("cuda", torch.cuda.current_device())
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(device.index)
+    elif stream.device != device:
+        raise ValueError(f"stream of {stream.device}, tensors on {device}")
+    else:
+        handle = stream.cuda_stream
+    if torch._C._cuda_getDevice() == device.index:
+        rc = entry(*args, handle)
+    else:
+        with torch.cuda.device(device):
+            rc = entry(*args, handle)
+    _lib.check(rc)
 
 
 def _check(t, name: str, dtypes, numel: Optional[int] = None):
@@ -88,9 +97,9 @@ class AdamW8State:
         device = _same_device((exp_avg, exp_avg_sq), "from_moments")
         with torch.cuda.stream(stream):
             s = cls.zeros_like(exp_avg)
-        _lib.check(_lib.load().adamw8_encode(
+        _run(_lib.load().adamw8_encode, (
             exp_avg.data_ptr(), exp_avg_sq.data_ptr(), s.exp_avg.data_ptr(), s.exp_avg_scale.data_ptr(),
-            s.rms.data_ptr(), s.rms_scale.data_ptr(), exp_avg.numel(), _stream_handle(stream, device)))
+            s.rms.data_ptr(), s.rms_scale.data_ptr(), exp_avg.numel()), stream, device)
         return s
 
     def moments(self, stream=None):
@@ -99,9 +108,9 @@ class AdamW8State:
         device = self.exp_avg.device
         with torch.cuda.stream(stream):
             m, v = (torch.empty(self.exp_avg.shape, dtype=torch.float32, device=device) for _ in "mv")
-        _lib.check(_lib.load().adamw8_decode(
+        _run(_lib.load().adamw8_decode, (
             self.exp_avg.data_ptr(), self.exp_avg_scale.data_ptr(), self.rms.data_ptr(), self.rms_scale.data_ptr(),
-            m.data_ptr(), v.data_ptr(), m.numel(), _stream_handle(stream, device)))
+            m.data_ptr(), v.data_ptr(), m.numel()), stream, device)
         return m, v
 
 
@@ -152,10 +161,9 @@ class PreparedAdamW8:
 
     def __call__(self, *, lr: float, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay: float = 0.01, step: int,
                  seed: Optional[int] = None, ema_decay: float = 0.0, stream=None) -> None:
-        rc = _lib.load().adamw8_step(self.table, self.n, lr, betas[0], betas[1], eps, weight_decay, step, ema_decay,
-                                     0 if seed is None else 1, 0 if seed is None else seed & 0xFFFFFFFFFFFFFFFF,
-                                     _stream_handle(stream, self.device))
-        _lib.check(rc)
+        _run(_lib.load().adamw8_step,
+             (self.table, self.n, lr, betas[0], betas[1], eps, weight_decay, step, ema_decay, 0 if seed is None else 1,
+              0 if seed is None else seed & 0xFFFFFFFFFFFFFFFF), stream, self.device)
 
 
 def adamw8_step(params, grads, states, *, lr: float, betas=(0.9, 0.999), eps: float = 1e-8,
@@ -276,7 +284,7 @@ class PreparedLinearCrossEntropy:
         self.device = device
 
     def __call__(self, stream=None) -> LinearCrossEntropy:
-        _lib.check(self._lib.head_loss(self.problem, *self._ws, _stream_handle(stream, self.device)))
+        _run(self._lib.head_loss, (self.problem, *self._ws), stream, self.device)
         return self.result
 
 

@@ -117,6 +117,41 @@ def test_binding_refuses_a_workspace_that_the_gpu_cannot_write():
         train._check_workspace(1 << 44, cpu)
 
 
+def test_binding_calls_with_the_tensors_device_current(monkeypatch):
+    """With stand-ins for torch's device functions: two devices, on either of which the caller may be."""
+    import contextlib
+    import types
+    import torch
+    from muon_optimizer_step_amd import train
+    now, seen = [0], []
+
+    @contextlib.contextmanager
+    def device(d):
+        before, now[0] = now[0], d.index
+        yield
+        now[0] = before
+
+    fake = types.SimpleNamespace(
+        device=torch.device, cuda=types.SimpleNamespace(device=device, current_device=lambda: now[0]),
+        _C=types.SimpleNamespace(_cuda_getDevice=lambda: now[0], _cuda_getCurrentRawStream=lambda i: 100 + i))
+    monkeypatch.setattr(train, "_torch", lambda: fake)
+    entry = lambda *a: seen.append((now[0], *a)) or 0  # noqa: E731
+    dev = [torch.device("cuda", i) for i in range(2)]
+    for now[0] in (0, 1):
+        for d in dev:
+            train._run(entry, ("x",), None, d)
+            assert seen.pop() == (d.index, "x", 100 + d.index)
+            train._run(entry, (), types.SimpleNamespace(device=d, cuda_stream=7), d)
+            assert seen.pop() == (d.index, 7)
+        train._run(entry, (), None, None)
+        assert seen.pop() == (now[0], 100 + now[0])
+    with pytest.raises(ValueError, match="stream of cuda:1"):
+        train._run(entry, (), types.SimpleNamespace(device=dev[1], cuda_stream=7), dev[0])
+    with pytest.raises(_lib.MuonError):
+        train._run(lambda *a: -1, (), None, dev[0])
+    assert not seen
+
+
 @pytest.mark.parametrize("n,v", [(200, 4194304), (300, 4194304), (384, 2800000), (257, 4194304), (500, 3000000),
                                  (3000, 400000), (9000, 131072), (20000, 70000), (1 << 20, 1100), (1 << 23, 200)])
 @pytest.mark.parametrize("cap", [0.0, 30.0])
