@@ -264,7 +264,8 @@ class PreparedLinearCrossEntropy:
         self.result = LinearCrossEntropy(nll, lse, loss, grad_hidden, grad_weight)
         self._keep = (hidden, weight, targets, token_weights)
         ptr = lambda t: t.data_ptr() if t is not None else 0  # noqa: E731
-        pitch = lambda t: max(t.stride(0), dim) if t is not None else dim  # noqa: E731
+        # a single row has no row stride, whatever its tensor says
+        pitch = lambda t: t.stride(0) if t is not None and t.shape[0] > 1 else dim  # noqa: E731
         self.problem = _lib.HeadLoss(
             ptr(hidden), ptr(weight), ptr(targets), ptr(token_weights), ptr(loss), ptr(nll), ptr(lse), ptr(grad_hidden),
             ptr(grad_weight), tokens, vocab, dim, pitch(hidden), pitch(weight), pitch(grad_hidden), pitch(grad_weight),

@@ -108,3 +108,14 @@ def test_prepared_adamw8_keeps_its_tensors():
     gc.collect()
     assert [i for i, r in enumerate(refs) if r() is None] == []
     call(lr=1e-3, step=1)
+
+
+def test_a_single_row_has_no_row_stride():
+    """The last token of one long sequence: a view whose stride is the sequence's."""
+    import torch
+    import muon_optimizer_step_amd as ms
+    h, w, t = _small(1)
+    wide = torch.as_strided(h, (1, 64), (1 << 23, 1))
+    assert wide.stride(0) == 1 << 23
+    a, b = ms.linear_cross_entropy(wide, w, t), ms.linear_cross_entropy(h, w, t)
+    assert torch.equal(a.nll, b.nll) and torch.equal(a.lse, b.lse)
