@@ -161,9 +161,13 @@ class PreparedAdamW8:
 
     def __call__(self, *, lr: float, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay: float = 0.01, step: int,
                  seed: Optional[int] = None, ema_decay: float = 0.0, stream=None) -> None:
+        step = int(step)
+        if abs(step) >= 1 << 31:
+            raise ValueError(f"step = {step} does not fit 32 bits")
         _run(_lib.load().adamw8_step,
-             (self.table, self.n, lr, betas[0], betas[1], eps, weight_decay, step, ema_decay, 0 if seed is None else 1,
-              0 if seed is None else seed & 0xFFFFFFFFFFFFFFFF), stream, self.device)
+             (self.table, self.n, float(lr), float(betas[0]), float(betas[1]), float(eps), float(weight_decay), step,
+              float(ema_decay), 0 if seed is None else 1, 0 if seed is None else int(seed) & 0xFFFFFFFFFFFFFFFF),
+             stream, self.device)
 
 
 def adamw8_step(params, grads, states, *, lr: float, betas=(0.9, 0.999), eps: float = 1e-8,

@@ -4,6 +4,7 @@ import gc
 import threading
 import weakref
 
+import numpy as np
 import pytest
 
 pytestmark = pytest.mark.gpu
@@ -119,3 +120,21 @@ def test_a_single_row_has_no_row_stride():
     assert wide.stride(0) == 1 << 23
     a, b = ms.linear_cross_entropy(wide, w, t), ms.linear_cross_entropy(h, w, t)
     assert torch.equal(a.nll, b.nll) and torch.equal(a.lse, b.lse)
+
+
+def test_scalars_of_numpy_and_torch():
+    import torch
+    import muon_optimizer_step_amd as ms
+    rng = np.random.default_rng(0)
+    p0, g = torch.from_numpy(rng.standard_normal(700)).float().cuda(), torch.from_numpy(rng.standard_normal(700)).float().cuda()
+    out = []
+    for f, i in ((float, int), (np.float64, np.int64), (torch.tensor, torch.tensor), (np.float32, np.int32)):
+        p, s = p0.clone(), ms.AdamW8State.zeros_like(p0)
+        ms.adamw8_step([p], [g], [s], lr=f(2.0 ** -7), betas=(f(0.5), f(0.75)), eps=f(2.0 ** -20), weight_decay=f(0.25),
+                       step=i(3), seed=i(11), ema_decay=f(0.5))
+        out.append((p, s.exp_avg.view(torch.uint8), s.rms.view(torch.uint8)))
+    for o in out[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(o, out[0]))
+    for step in ((1 << 32) + 3, 1 << 31):
+        with pytest.raises(ValueError, match="32 bits"):
+            ms.adamw8_step([p0], [g], [s], lr=0.0, step=step)
