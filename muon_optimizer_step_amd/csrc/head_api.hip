@@ -218,7 +218,7 @@ int validate_buffers(const head_loss_t& p, const void* workspace, size_t bytes) 
         const uintptr_t lo = reinterpret_cast<uintptr_t>(buf[i].p);
         if (lo % buf[i].align) return fail(MUON_ERR_INVALID_ARG, "buffer %d is not %d-byte aligned", i, buf[i].align);
         for (int j = 0; j < i; ++j) {
-            if (!buf[j].p || !(buf[i].written || buf[j].written)) continue;
+            if (!buf[j].p || buf[j].bytes == 0 || !(buf[i].written || buf[j].written)) continue;
             const uintptr_t lj = reinterpret_cast<uintptr_t>(buf[j].p);
             if (lo < lj + buf[j].bytes && lj < lo + buf[i].bytes)
                 return fail(MUON_ERR_UNSUPPORTED, "head_loss: buffers %d and %d overlap", j, i);

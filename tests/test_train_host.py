@@ -88,6 +88,17 @@ def test_head_loss_rejects_a_bad_workspace():
     assert lib.head_loss_workspace_size(_problem(dim=0)) == 0
 
 
+def test_head_loss_without_tokens_has_no_per_token_buffers_to_overlap():
+    """Addresses of nothing, inside grad_weight: the call gets as far as its next check, the workspace's alignment."""
+    lib = _lib.load()
+    inside = BASE + (7 << 32) + 64
+    for kw in (dict(nll=inside), dict(lse=inside), dict(targets=inside), dict(hidden=inside), dict(grad_hidden=inside)):
+        p = _problem(tokens=0, **kw)
+        assert lib.head_loss(p, BASE + (9 << 32) + 16, 1 << 40, None) == -1, kw
+        assert "aligned" in lib.muon_last_error().decode(), kw
+        assert lib.head_loss(_problem(**kw), BASE + (9 << 32) + 16, 1 << 40, None) == -2, kw
+
+
 def test_head_loss_workspace_is_bounded_by_the_piece():
     lib = _lib.load()
     big = dict(vocab=131072, dim=2048, hidden_stride=2048, weight_stride=2048, grad_hidden_stride=2048,
