@@ -28,6 +28,14 @@ def _run(entry, args, stream, device):
     _lib.check(rc)
 
 
+def _used_on(stream, tensors):
+    """Tells the allocator that work on `stream` uses the tensors, which the caller may drop before it has run."""
+    if stream is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
 def _check(t, name: str, dtypes, numel: Optional[int] = None):
     """A contiguous HIP tensor of one of these dtypes (and this many elements)."""
     torch = _torch()
@@ -100,6 +108,7 @@ class AdamW8State:
         _run(_lib.load().adamw8_encode, (
             exp_avg.data_ptr(), exp_avg_sq.data_ptr(), s.exp_avg.data_ptr(), s.exp_avg_scale.data_ptr(),
             s.rms.data_ptr(), s.rms_scale.data_ptr(), exp_avg.numel()), stream, device)
+        _used_on(stream, (exp_avg, exp_avg_sq))
         return s
 
     def moments(self, stream=None):
@@ -111,6 +120,7 @@ class AdamW8State:
         _run(_lib.load().adamw8_decode, (
             self.exp_avg.data_ptr(), self.exp_avg_scale.data_ptr(), self.rms.data_ptr(), self.rms_scale.data_ptr(),
             m.data_ptr(), v.data_ptr(), m.numel()), stream, device)
+        _used_on(stream, (self.exp_avg, self.exp_avg_scale, self.rms, self.rms_scale))
         return m, v
 
 
@@ -181,9 +191,9 @@ def adamw8_step(params, grads, states, *, lr: float, betas=(0.9, 0.999), eps: fl
     index).  emas: optional list of float32 tensors (or None entries) advanced as ema = d*ema + (1-d)*param' with
     d = ema_decay.  copies: optional list of bfloat16 tensors (or None entries) that receive the updated parameter.
     """
-    PreparedAdamW8(params, grads, states, emas=emas, copies=copies)(
-        lr=lr, betas=betas, eps=eps, weight_decay=weight_decay, step=step, seed=seed, ema_decay=ema_decay,
-        stream=stream)
+    call = PreparedAdamW8(params, grads, states, emas=emas, copies=copies)
+    call(lr=lr, betas=betas, eps=eps, weight_decay=weight_decay, step=step, seed=seed, ema_decay=ema_decay, stream=stream)
+    _used_on(stream, call._keep)
 
 
 # ------------------------------------------------------------- loss of the language-model head
@@ -266,7 +276,7 @@ class PreparedLinearCrossEntropy:
             _check_rows(grad_weight, "grad_weight", hidden.dtype, (vocab, dim))
         _same_device((hidden, grad_hidden, grad_weight), "linear_cross_entropy")
         self.result = LinearCrossEntropy(nll, lse, loss, grad_hidden, grad_weight)
-        self._keep = (hidden, weight, targets, token_weights)
+        self._keep = (hidden, weight, targets, token_weights, grad_hidden, grad_weight, workspace)
         ptr = lambda t: t.data_ptr() if t is not None else 0  # noqa: E731
         # a single row has no row stride, whatever its tensor says
         pitch = lambda t: t.stride(0) if t is not None and t.shape[0] > 1 else dim  # noqa: E731
@@ -293,6 +303,13 @@ class PreparedLinearCrossEntropy:
         return self.result
 
 
+def _once(hidden, weight, targets, stream, **kw):
+    call = PreparedLinearCrossEntropy(hidden, weight, targets, stream=stream, **kw)
+    result = call(stream)
+    _used_on(stream, call._keep)
+    return result
+
+
 def linear_cross_entropy(hidden, weight, targets, *, ignore_index: int = -100, softcap: float = 0.0, workspace=None,
                          stream=None) -> LinearCrossEntropy:
     """Scores tokens: nll and log-sum-exp of each under softmax(hidden @ weight.T), float32, without the logits.
@@ -300,8 +317,7 @@ def linear_cross_entropy(hidden, weight, targets, *, ignore_index: int = -100, s
     workspace: None takes one for this call from the stream's memory (calls from several threads, and calls captured in
     a graph, do not share any).
     """
-    return PreparedLinearCrossEntropy(hidden, weight, targets, ignore_index=ignore_index, softcap=softcap,
-                                      workspace=workspace, stream=stream)(stream)
+    return _once(hidden, weight, targets, stream, ignore_index=ignore_index, softcap=softcap, workspace=workspace)
 
 
 def linear_cross_entropy_grad(hidden, weight, targets, *, token_weights=None, ignore_index: int = -100,
@@ -311,6 +327,5 @@ def linear_cross_entropy_grad(hidden, weight, targets, *, token_weights=None, ig
 
     workspace: as in linear_cross_entropy.
     """
-    return PreparedLinearCrossEntropy(hidden, weight, targets, token_weights=token_weights, ignore_index=ignore_index,
-                                      softcap=softcap, grads=True, grad_hidden=grad_hidden, grad_weight=grad_weight,
-                                      workspace=workspace, stream=stream)(stream)
+    return _once(hidden, weight, targets, stream, token_weights=token_weights, ignore_index=ignore_index, softcap=softcap,
+                 grads=True, grad_hidden=grad_hidden, grad_weight=grad_weight, workspace=workspace)

@@ -138,3 +138,41 @@ def test_scalars_of_numpy_and_torch():
     for step in ((1 << 32) + 3, 1 << 31):
         with pytest.raises(ValueError, match="32 bits"):
             ms.adamw8_step([p0], [g], [s], lr=0.0, step=step)
+
+
+def test_inputs_dropped_after_a_call_on_another_stream():
+    """The caller's references end before the stream gets to the call; what takes their memory's place must not show."""
+    import torch
+    import muon_optimizer_step_amd as ms
+    h, w, t = _small(700, 3000, 128)
+    weights = torch.rand(700, device="cuda") / 700
+    want = [x.clone() for x in ms.linear_cross_entropy_grad(h, w, t, token_weights=weights)]
+    p = torch.randn(50000, device="cuda")
+    grad, m, v = torch.randn_like(p), torch.randn_like(p), torch.rand_like(p)
+    state = ms.AdamW8State.from_moments(m, v)
+    want_m, want_v = state.moments()
+    p1 = p.clone()
+    ms.adamw8_step([p1], [grad], [state], lr=0.1, step=3)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+
+    def late(call, *tensors):
+        """call(copies of the tensors) on the busy side stream; the copies' memory is taken over at once."""
+        copies = [x.clone() for x in tensors]
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(5_000_000)
+        out = call(*copies)
+        del copies
+        junk = [torch.full_like(x, 0 if x.dtype == torch.int64 else float("nan")) for x in tensors for _ in range(3)]
+        torch.cuda.synchronize()
+        del junk
+        return out
+
+    r = late(lambda h, w, t, g: ms.linear_cross_entropy_grad(h, w, t, token_weights=g, stream=side), h, w, t, weights)
+    assert all(torch.equal(a, b) for a, b in zip(r, want))
+    s = late(lambda m, v: ms.AdamW8State.from_moments(m, v, stream=side), m, v)
+    assert all(torch.equal(a, b) for a, b in zip(s.moments(), (want_m, want_v)))
+    p2 = p.clone()
+    late(lambda g: ms.adamw8_step([p2], [g], [s], lr=0.1, step=3, stream=side), grad)
+    assert torch.equal(p1, p2)
