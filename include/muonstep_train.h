@@ -64,11 +64,15 @@ typedef struct adamw8_tensor_t {
  *               (to 2^-16), from 32 mixed bits of (seed, step, tensor's place
  *               in the list, value's index): the moments' averages then keep
  *               increments below half a step on the average, and the same
- *               arguments give the same bits.
+ *               arguments give the same bits.  All tensors draw from one
+ *               sequence of 2^32, each from a place of its own: long ones may
+ *               share a stretch of it, and beyond 2^32 values it repeats.
  * A v above zero never becomes the zero code.  A block with a value that is
  * not finite gets a NaN scale: its states are lost as a whole, as the
  * parameters are.  Blocks whose largest value is below 2^-100 are written as zero
  * (sqrt(v): as the smallest code).
+ * The scalars, step and seed among them, are arguments of the launches: a captured
+ * graph repeats the step that was captured.
  * Argument limits as adamw_step; tensors with numel == 0 are skipped.  param,
  * exp_avg, rms, scales, ema: 4-byte aligned (8-bit codes: any); grad, copy: aligned to
  * their type.  Aligned to 16 bytes (codes: 4, bfloat16: 8) they take the
@@ -108,6 +112,8 @@ int adamw8_decode(const void* exp_avg_codes, const float* exp_avg_scale, const v
  *   grad_hidden, grad_weight   NULL or rows like hidden and weight, overwritten
  *                (not added to).  Each is computed only if given; with both and
  *                loss NULL the call only scores.
+ *   A buffer reaches from its first element to its last, the gaps of strided
+ *   rows included: what is written may overlap nothing else.
  *   tokens >= 0, vocab >= 1, dim >= 1 (limits below); softcap finite, >= 0.
  * Products take their 16-bit inputs as they are and sum in float32; the
  * probabilities are rounded to 16 bits once, before they are multiplied with

@@ -11,9 +11,11 @@
 //
 // Bound: HBM.  Per value 8 bytes of param, 2 or 4 of grad, 4 of codes and
 // 16/256 of scales, 8 more with an EMA, 2 with a bf16 copy.  Measured: 134.2 M values
-// of 96 tensors, bf16 gradients and copies, 2.16 GB: 377 us, 5.7 TB/s (a copy of
-// 4 GiB: 4.8, reads and writes together); 4.2 M values: 15.6 us, launch included,
-// and one small tensor 5.5, which is what the host takes to enqueue it.
+// of 96 tensors, bf16 gradients and copies, 2.16 GB: 380 us, 5.7 TB/s (a copy of
+// 4 GiB: 4.8, reads and writes together); fp32 gradients of one such tensor 365 us, with
+// 32-bit states 759, 5.0 TB/s; 4.2 M values: 15.6 us, launch included.  A small
+// tensor is bound by latency: 65536 values are 32 workgroups, each wave of which takes
+// two blocks one after the other, 5.4 us, about what the host takes to enqueue it.
 //
 // Layout: one wave per block of 256 values, 4 consecutive values per lane
 // (16-byte param and EMA accesses, 4-byte code accesses: 256 contiguous bytes

@@ -283,7 +283,7 @@ __device__ inline void load_stage(Op& op, uint32_t dst, int left) {
 //
 // Measured on 16384 x 8192 x 512 (the gradient of hidden): two buffers filled
 // in a burst after the barrier 165 us, this 127.  Counters of the three products of
-// 8192 x 131072 x 2048: no LDS bank conflicts, MFMA busy in 67 % of the cycles of
+// 8192 x 131072 x 2048: no LDS bank conflicts, MFMA busy in 66 % of the cycles of
 // head_logits and 77 % of head_grads, cycles of a clock of about 1.6 GHz by the
 // same counters.
 constexpr int kSlots = 5;
@@ -556,9 +556,10 @@ __device__ inline void tile_of(const HeadLogits& a, int item, int& tile_v, int& 
 // Tile of 256 vocabulary entries x 256 tokens: 8 waves of 128 x 64, 32x32x16
 // MFMAs, so that an operand byte from LDS serves the most products that 128
 // accumulator registers hold.  Bound by MFMA where dim is long (16384 x 32768 x
-// 1024: 885 us, 1.24 PFLOP/s; 8192 x 131072 x 2048: 3.33 ms, 1.32), by the tile's
-// ends where it is short (16384 x 8192 x 512: 143 us, 0.96; with e stored
-// 184, of which 44 are e's 268 MB).
+// 1024: 882 us, 1.25 PFLOP/s; 8192 x 131072 x 2048: 3.38 ms, 1.30, with e stored
+// 3.76, 1.17), by the tile's ends where it is short (16384 x 8192 x 512: 149 us,
+// 0.92; with e's 268 MB stored 187).  A cap's polynomial at the tile's end, in bf16:
+// 1021 x 50021 x 1000 119 -> 135 us, 155 where the logits reach several caps.
 template <typename T, int STORE, bool CAP>
 __global__ __launch_bounds__(512, 2) void head_logits_kernel(const HeadLogits a) {
     constexpr int WV = 2, WT = 4, TV = 4, TT = 2, BV = WV * TV * 32, BT = WT * TT * 32, NW = WV * WT;
@@ -588,9 +589,9 @@ __global__ __launch_bounds__(512, 2) void head_logits_kernel(const HeadLogits a)
 // Tile of 128 vocabulary entries x 32, 64 or 128 tokens, two workgroups of 4
 // waves per compute unit: for few tokens, where W streams past them (two or
 // three stages of 64 K in LDS keep its loads in flight), and for problems with too
-// few 256 x 256 tiles.  Bound for few tokens by HBM (64 x 131072 x 2048: 108 us,
-// 4.9 TB/s), otherwise by the vector work and the waits of its shorter tiles
-// (2048 x 4096 x 512: 15 us, 0.57 PFLOP/s).
+// few 256 x 256 tiles.  Bound for few tokens by HBM (64 x 131072 x 2048: 108
+// to 113 us, 4.8 TB/s), otherwise by the vector work and the waits of its shorter
+// tiles (2048 x 4096 x 512: 13 us, 0.67 PFLOP/s; with e stored 17).
 template <int TOKENS> struct MidTile;
 template <> struct MidTile<32> { static constexpr int WV = 4, WT = 1, TV = 1, TT = 1, kBuffers = 3; };
 template <> struct MidTile<64> { static constexpr int WV = 4, WT = 1, TV = 1, TT = 2, kBuffers = 3; };
@@ -629,7 +630,7 @@ __global__ __launch_bounds__(256, 2) void head_logits_mid_kernel(const HeadLogit
 // Up to 32 tokens and a small vocabulary, where there is little to read and
 // latency counts: a workgroup for every 32 vocabulary rows, operands straight
 // from memory (each row of W is used once), the waves take every fourth 128
-// bytes of K and meet in LDS.  1 x 8192 x 512: 5.0 us for 8.4 MB, head_rows 2.8;
+// bytes of K and meet in LDS.  1 x 8192 x 512: 5.0 us for 8.4 MB, head_rows 2.5;
 // a launch alone is over 2.
 template <typename T, int STORE, bool CAP>
 __global__ __launch_bounds__(256) void head_logits_stream_kernel(const HeadLogits a) {
@@ -866,9 +867,9 @@ __device__ inline Row head_row(const HeadRows& a, int row, bool first, int col0,
     return out;
 }
 
-// Bound by latency: 3 us for one token's 256 partials, 7 for 64 tokens' 4096 (13
+// Bound by latency: 2.5 us for one token's 256 partials, 7 for 64 tokens' 4096 (13
 // where a token's partials lie a row apart, 21 with the 64 threads of the classes
-// alone), 24 for 16384 tokens' 256.
+// alone), 23 for 16384 tokens' 256.
 template <typename T, int THREADS, int R>
 __global__ __launch_bounds__(THREADS) void head_rows_kernel(const HeadRows a) {
     __shared__ float red[3][RowShape<THREADS, R>::kSlots][R];
@@ -879,10 +880,11 @@ __global__ __launch_bounds__(THREADS) void head_rows_kernel(const HeadRows a) {
 // 8 tokens x `across` columns per workgroup: first the tokens' values (again by
 // each workgroup of their columns), then e -> P in place, 8 columns of the 8
 // tokens per thread at a time.  HBM-bound: reads and writes 2 bytes an entry
-// (8192 x 131072: 894 us, 4.8 TB/s; 16384 x 8192: 101 us, 5.3 TB/s).  An XCD
-// takes consecutive workgroups, whose partials share cache lines (987 against 935
-// and 104 against 101 us).  All 8 tokens' loads at a time where e is past the
-// caches (935 -> 894 us), 4 where it is not (8: 1531 x 12345 capped 22 -> 26).
+// (8192 x 131072: 887 us, 4.8 TB/s; 16384 x 8192: 100 us, 5.4 TB/s).  An XCD
+// takes consecutive workgroups, whose partials share cache lines (5 % at 8192 x
+// 131072, 3 % at 16384 x 8192 when it was built).  All 8 tokens' loads at a time where
+// e is past the caches (another 4 %), 4 where it is not (8: 1531 x 12345 capped 22 ->
+// 26 us then, 20 now).
 // Under a cap head_logits has multiplied e by the derivative 1 - (l / cap)^2, taken from
 // the product in fp32, but for the target's e: there the softmax and -1 cancel
 // before the derivative, taken from the target's logit, multiplies both.
@@ -956,8 +958,8 @@ __device__ inline void head_loss_sum(const HeadLoss& a, float* red) {
 // Tile of 256 output columns d x 256 rows, K split over workgroups where the
 // tiles alone would leave compute units idle.  A = W or H with K strided; P with K
 // contiguous (dH, K the vocabulary) or strided (dW, K the tokens).  Bound by MFMA:
-// 8192 x 131072 x 2048, both gradients 6.69 ms, 1.32 PFLOP/s; 16384 x 8192 x 512,
-// 226 us, 1.22, where splits and their partial sums cost the difference.
+// 8192 x 131072 x 2048, both gradients 6.71 ms, 1.31 PFLOP/s; 16384 x 8192 x 512,
+// 233 us, 1.18, where splits and their partial sums cost the difference.
 //
 // A wave's sums to memory: acc[i][j] holds columns d0 + 32 i + 16 p + 8 (l / 32) + e
 // (register 8 p + e) of row c0 + 32 j + l % 32.
@@ -1203,7 +1205,8 @@ hipError_t prob_typed(const HeadRows& a, hipStream_t s) {
     const int wanted = std::max(1, 2048 / row_blocks);
     const int across = (int)(((a.e_pitch + wanted - 1) / wanted + 2047) / 2048 * 2048);
     const int blocks = (int)((a.e_pitch + across - 1) / across), grid = xcd_grid(blocks * row_blocks);
-    // far more than the last-level cache holds: past it (8192 x 131072: 856 -> 731 us; 16384 x 8192: 86 -> 101)
+    // far more than the last-level cache holds: past it (8192 x 131072, 2.1 GB: 949 -> 887 us; 16384 x 8192, 268 MB:
+    // 100 -> 122)
     const bool past = (int64_t)a.rows * a.e_pitch * 2 > (int64_t)1 << 30;
     if (a.cap > 0.f) {
         if (past) head_prob_kernel<T, true, true><<<grid, 256, 0, s>>>(a, blocks, across);

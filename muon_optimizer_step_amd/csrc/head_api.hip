@@ -28,8 +28,9 @@ constexpr int kMinStagesPerSplit = 4;     // K stages a workgroup takes at least
 
 // Piece of probabilities from which head_logits writes past the caches: 256 MB
 // of last-level cache hold less of it than head_prob could use (16384 x 8192,
-// 268 MB: head_logits 197 -> 189 us, head_prob 102 -> 86; 1531 x 12345, 38 MB,
-// the other way round: head_prob 23 -> 34).
+// 268 MB: head_logits 201 -> 187 us, head_prob 102 -> 100; 8192 x 131072, 2.1 GB:
+// 3712 -> 3765, but head_prob, past them too, 949 -> 887; 1531 x 12345, 38 MB, the
+// other way round: head_logits 57 -> 54, head_prob 20 -> 25).
 constexpr int64_t kPastBytes = (int64_t)192 << 20;
 
 int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
@@ -110,7 +111,7 @@ GradSplit split_k(int64_t rows, int64_t vocab, int64_t dim, bool grad_hidden, bo
 // where a cap makes the vector work of the tile's end longer (1021 x 50021 x
 // 1000 capped: 161 against 143).
 int logits_variant(int64_t tokens, int64_t vocab, bool cap) {
-    if (tokens <= 32) return vocab < 16384 && tokens <= kHeadStream ? kLogitsStream : kLogitsMid32;
+    if (tokens <= kHeadStream) return vocab < 16384 ? kLogitsStream : kLogitsMid32;
     if (tokens <= 64) return kLogitsMid64;
     auto tiles = [&](int64_t edge) { return ((tokens + edge - 1) / edge) * ((vocab + edge - 1) / edge); };
     const double big = (double)((tiles(256) + kCus - 1) / kCus);

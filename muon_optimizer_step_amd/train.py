@@ -188,7 +188,7 @@ def adamw8_step(params, grads, states, *, lr: float, betas=(0.9, 0.999), eps: fl
     grads: float32 or bfloat16.  states: an AdamW8State per tensor, or a pair (exp_avg, exp_avg_sq) of float32
     tensors.  step counts the AdamW steps including this one (>= 1).  seed: None rounds the 8-bit states to the
     nearest code; an int rounds them stochastically, from (seed, step, the tensor's place in the list, the value's
-    index).  emas: optional list of float32 tensors (or None entries) advanced as ema = d*ema + (1-d)*param' with
+    index); a captured graph repeats the step and seed that were captured.  emas: optional list of float32 tensors (or None entries) advanced as ema = d*ema + (1-d)*param' with
     d = ema_decay.  copies: optional list of bfloat16 tensors (or None entries) that receive the updated parameter.
     """
     call = PreparedAdamW8(params, grads, states, emas=emas, copies=copies)
@@ -199,7 +199,11 @@ def adamw8_step(params, grads, states, *, lr: float, betas=(0.9, 0.999), eps: fl
 # ------------------------------------------------------------- loss of the language-model head
 
 class LinearCrossEntropy(NamedTuple):
-    """What the head's loss returns: per-token nll and lse; with gradients also the loss and both gradients."""
+    """What the head's loss returns: per-token nll and lse; with gradients also the loss and both gradients.
+
+    None of them is part of an autograd graph, also where hidden or weight require gradients: hand grad_hidden on with
+    `output.backward(grad_hidden)` or `torch.autograd.grad(output, inputs, grad_hidden)`, and add grad_weight where it belongs.
+    """
     nll: object
     lse: object
     loss: object = None
@@ -243,6 +247,8 @@ class PreparedLinearCrossEntropy:
     that one out; a tensor given there receives it).  token_weights: float32 [tokens], or None for the mean over the
     tokens whose target is not ignore_index.  softcap: logits are softcap * tanh(z / softcap), 0 for none.
     Each call returns the same LinearCrossEntropy of result tensors, overwritten.
+    stream: whose memory the results and the workspace are (None: the current one).  Calls on another one, and from
+    another thread, have to be ordered with those before and with the use of the results.
     """
 
     def __init__(self, hidden, weight, targets, *, token_weights=None, ignore_index: int = -100, softcap: float = 0.0,
