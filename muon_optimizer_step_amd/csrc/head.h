@@ -3,14 +3,13 @@
 #pragma once
 
 #include "common.h"
+#include "tiles.h"
 
 namespace muon {
 
 enum HeadType { kHeadBf16 = 0, kHeadFp16 = 1 };
 
-constexpr int kHeadK = 64;         // K elements per LDS stage
 constexpr int kHeadPad = 64;       // rows and columns of the probability piece are padded to it
-constexpr int kHeadTile = 256;     // output tile edge of the products
 constexpr int kHeadMidVocab = 128; // vocabulary entries of a tile of the kernels for few tokens or small problems
 constexpr int kHeadStream = 32;    // tokens that the streaming kernel and the narrowest tile take at most
 constexpr int kHeadStreamSub = 32; // vocabulary entries of its workgroups
