@@ -1,4 +1,4 @@
-"""ctypes declarations of the C ABI in include/muonstep.h and include/muonstep_train.h (no torch needed here)."""
+"""ctypes declarations of the C ABI in include/muonstep.h, muonstep_train.h and muonstep_linear8.h (no torch needed here)."""
 
 from __future__ import annotations
 
@@ -29,6 +29,17 @@ MUON_HEAD_MAX_TOKENS = 1 << 24
 MUON_HEAD_MAX_VOCAB = 1 << 22
 MUON_HEAD_MAX_DIM = 65536
 MUON_HEAD_PIECE_BYTES = 2 << 30
+MUON_T_BF16 = 0
+MUON_T_FP16 = 1
+MUON_T_FP32 = 2
+MUON_ACT_NONE = 0
+MUON_ACT_RELU2 = 1
+MUON_ACT_SILU = 2
+MUON_ACT_GELU = 3
+MUON_BLOCK8 = 128
+MUON_SCALE8_LOW = 10
+MUON_LINEAR8_MAX_ROWS = 1 << 24
+MUON_LINEAR8_MAX_DIM = 1 << 18
 
 
 class MuonTensor(ctypes.Structure):
@@ -75,6 +86,37 @@ class HeadLoss(ctypes.Structure):
     _fields_ += [(n, ctypes.c_int64) for n in ("tokens", "vocab", "dim", "hidden_stride", "weight_stride",
                                                "grad_hidden_stride", "grad_weight_stride", "ignore_index")]
     _fields_ += [("softcap", ctypes.c_float), ("dtype", ctypes.c_int32)]
+
+
+class Blocks8(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("stride", ctypes.c_int64),
+                ("scale_stride", ctypes.c_int64)]
+
+
+def _fields(**kinds):
+    """Fields of a structure: names by their type, in order."""
+    types = {"ptr": ctypes.c_void_p, "i64": ctypes.c_int64, "i32": ctypes.c_int32, "blocks": Blocks8}
+    return [(name, types[kind.rstrip("_")]) for kind, names in kinds.items() for name in names.split()]
+
+
+class Act8Encode(ctypes.Structure):
+    _fields_ = _fields(ptr="x", i64="rows dim x_stride", i32="dtype activation", blocks="codes out")
+
+
+class Act8Backward(ctypes.Structure):
+    _fields_ = _fields(blocks="u", ptr="grad out", i64="rows dim grad_stride out_stride", i32="dtype activation", blocks_="out8")
+
+
+class Weight8Encode(ctypes.Structure):
+    _fields_ = _fields(ptr="weight", i64="rows dim weight_stride", i32="dtype", blocks="codes transposed")
+
+
+class Matmul8(ctypes.Structure):
+    _fields_ = _fields(blocks="a b", ptr="y", i64="rows cols dim y_stride", i32="dtype")
+
+
+class Act8GradWeight(ctypes.Structure):
+    _fields_ = _fields(blocks="x", ptr="grad out", i64="rows cols dim grad_stride out_stride", i32="accumulate")
 
 
 class MuonError(RuntimeError):
@@ -149,6 +191,20 @@ def load() -> ctypes.CDLL:
     lib.head_loss_workspace_size.restype = ctypes.c_size_t
     lib.head_loss.argtypes = [ctypes.POINTER(HeadLoss), ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
     lib.head_loss.restype = ctypes.c_int
+    for name, problem in (("act8_encode", Act8Encode), ("act8_backward", Act8Backward), ("weight8_encode", Weight8Encode)):
+        f = getattr(lib, name)
+        f.argtypes = [ctypes.POINTER(problem), ctypes.c_void_p]
+        f.restype = ctypes.c_int
+    lib.act8_decode.argtypes = [ctypes.POINTER(Blocks8), ctypes.c_int32, ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p,
+                                ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p]
+    lib.act8_decode.restype = ctypes.c_int
+    for name, problem in (("matmul8", Matmul8), ("act8_grad_weight", Act8GradWeight)):
+        f = getattr(lib, name)
+        f.argtypes = [ctypes.POINTER(problem), ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
+        f.restype = ctypes.c_int
+        f = getattr(lib, name + "_workspace_size")
+        f.argtypes = [ctypes.POINTER(problem)]
+        f.restype = ctypes.c_size_t
     lib.muon_set_ns_schedule.argtypes = [ctypes.c_int32]
     lib.muon_set_ns_schedule.restype = ctypes.c_int
     lib.muon_plan_cache_stats.argtypes = [ctypes.POINTER(ctypes.c_int64), ctypes.POINTER(ctypes.c_int64)]

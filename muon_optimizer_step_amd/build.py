@@ -15,7 +15,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libmuonstep.so")
 SOURCES = ["api.hip", "elementwise.hip", "ns.hip", "chain.hip", "adamw8.hip", "head.hip",
-           "head_api.hip"]
+           "head_api.hip", "blocks8.hip", "matmul8.hip", "grad8.hip", "linear8_api.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = [

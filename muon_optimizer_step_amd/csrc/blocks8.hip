@@ -1,0 +1,435 @@
+// Row-wise passes of the linear layers in 8 bits on gfx950: activations and
+// weights to e4m3 codes with a power of two as scale for each block, back, and the
+// gradient of an activation function from such codes.
+//
+// Mathematics.  For a block with largest finite magnitude t = m 2^p (1 <= m < 2) the
+// scale is 2^e, e = p - 8, or p - 7 where m > 448 / 256: the smallest power with
+// t / 2^e <= 448.  It comes from t's bits; value / 2^e is exact (a power of two), so a
+// code has the conversion's rounding only, and is the same in any
+// implementation.
+//
+// Bound: HBM; every value is read once and written once.
+#include <algorithm>
+
+#include "linear8.h"
+#include "tiles.h"
+
+namespace muon {
+namespace {
+
+constexpr int kLanes = 16;        // lanes of a block: 8 values each, a row of the DPP operations
+constexpr int kThreads = 256;
+constexpr int kUnits = kThreads / kLanes;
+static_assert(kLanes * 8 == kBlock8, "lanes of a block");
+
+// The largest bits over the 16 lanes of a block, in all of them.
+__device__ inline uint32_t block_max(uint32_t x) {
+    auto step = [&](uint32_t y) { x = x > y ? x : y; };
+    step((uint32_t)__builtin_amdgcn_mov_dpp((int)x, 0x128, 15, 15, true));    // row_ror:8
+    step((uint32_t)__builtin_amdgcn_mov_dpp((int)x, 0x124, 15, 15, true));
+    step((uint32_t)__builtin_amdgcn_mov_dpp((int)x, 0x122, 15, 15, true));
+    step((uint32_t)__builtin_amdgcn_mov_dpp((int)x, 0x121, 15, 15, true));
+    return x;
+}
+__device__ inline uint32_t finite_bits(float x) {
+    const uint32_t b = __builtin_bit_cast(uint32_t, x) & 0x7FFFFFFFu;
+    return b < 0x7F800000u ? b : 0u;
+}
+// The scale's byte from the bits of the block's largest magnitude.
+__device__ inline int scale_byte(uint32_t top) {
+    const int s = (int)(top >> 23) - 8 + ((top & 0x7FFFFFu) > 0x600000u);
+    return s > kScale8Low ? s : kScale8Low;
+}
+__device__ inline float scale_value(int byte) { return __builtin_bit_cast(float, (uint32_t)byte << 23); }
+__device__ inline float scale_inverse(int byte) { return __builtin_bit_cast(float, (uint32_t)(254 - byte) << 23); }
+
+__device__ inline uint32_t codes4(const float* v, float inverse) {
+    int w = __builtin_amdgcn_cvt_pk_fp8_f32(v[0] * inverse, v[1] * inverse, 0, false);
+    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[2] * inverse, v[3] * inverse, w, true);
+}
+// A lane's 8 values of a block to codes; every lane of the block takes part.
+__device__ inline u32x2 encode8(const float* v, int& byte) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const uint32_t b = finite_bits(v[k]);
+        top = top > b ? top : b;
+    }
+    byte = scale_byte(block_max(top));
+    const float inverse = scale_inverse(byte);
+    return u32x2{codes4(v, inverse), codes4(v + 4, inverse)};
+}
+__device__ inline void decode8(const u32x2& w, float scale, float* v) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const f32x2 lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[k], false), hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[k], true);
+        v[4 * k] = lo[0] * scale;
+        v[4 * k + 1] = lo[1] * scale;
+        v[4 * k + 2] = hi[0] * scale;
+        v[4 * k + 3] = hi[1] * scale;
+    }
+}
+
+// 8 values as they lie in memory.
+template <typename T> struct Raw { u32x4 w[sizeof(T) / 2]; };
+template <typename T> __device__ inline void to_float(const Raw<T>& r, float* v) {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = as_float(r.w[k / 4][k % 4]);
+    } else {
+        unpack8<T>(r.w[0], v);
+    }
+}
+template <typename T> __device__ inline Raw<T> from_float(const float* v) {
+    Raw<T> r;
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) r.w[k / 4][k % 4] = __builtin_bit_cast(uint32_t, v[k]);
+    } else {
+        r.w[0] = pack8<T>(v);
+    }
+    return r;
+}
+// `left` values are there (zeros behind them); vec: p is 16-byte aligned.
+template <typename T> __device__ inline Raw<T> load8(const T* p, int left, bool vec) {
+    Raw<T> r;
+    if (vec && left >= 8) {
+#pragma unroll
+        for (int k = 0; k < (int)sizeof(T) / 2; ++k) r.w[k] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p) + k);
+        return r;
+    }
+    uint32_t word[4 * (sizeof(T) / 2)] = {};
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        if (k < left) {
+            if constexpr (sizeof(T) == 4) word[k] = __builtin_bit_cast(uint32_t, p[k]);
+            else word[k / 2] |= (uint32_t)__builtin_bit_cast(uint16_t, p[k]) << (16 * (k % 2));
+        }
+#pragma unroll
+    for (int k = 0; k < 4 * ((int)sizeof(T) / 2); ++k) r.w[k / 4][k % 4] = word[k];
+    return r;
+}
+template <typename T> __device__ inline void store8(T* p, const Raw<T>& r, int left, bool vec) {
+    if (vec && left >= 8) {
+#pragma unroll
+        for (int k = 0; k < (int)sizeof(T) / 2; ++k) reinterpret_cast<u32x4*>(p)[k] = r.w[k];
+        return;
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        if (k < left) {
+            if constexpr (sizeof(T) == 4) p[k] = as_float(r.w[k / 4][k % 4]);
+            else p[k] = __builtin_bit_cast(T, (uint16_t)(r.w[0][k / 2] >> (16 * (k % 2))));
+        }
+}
+
+// ---------------------------------------------------------------- activation functions
+// gelu's F(u) = erfc(-u / sqrt 2) / 2 keeps its digits where F is small.
+constexpr float kHalfRoot = 0.70710678118654752440f, kInvRoot2Pi = 0.39894228040143267794f;
+__device__ inline float positive(float u) { return u <= 0.f ? 0.f : u; }     // NaN stays
+template <int ACT> __device__ inline float act(float u) {
+    if (ACT == kActRelu2) {
+        const float t = positive(u);
+        return t * t;
+    }
+    if (ACT == kActSilu) return u / (1.f + expf(-u));
+    if (ACT == kActGelu) return u * (0.5f * erfcf(-kHalfRoot * u));
+    return u;
+}
+template <int ACT> __device__ inline float act_slope(float u) {
+    if (ACT == kActRelu2) {
+        const float t = positive(u);
+        return t + t;
+    }
+    if (ACT == kActSilu) {
+        const float s = 1.f / (1.f + expf(-u));
+        return s * fmaf(u, 1.f - s, 1.f);
+    }
+    return fmaf(u * kInvRoot2Pi, expf(-0.5f * u * u), 0.5f * erfcf(-kHalfRoot * u));
+}
+
+// ---------------------------------------------------------------- rows
+// A workgroup takes kBatch rows of each of its units at a time: their loads are
+// under way together.
+constexpr int kBatch = 4;
+struct Unit {
+    int d;               // the lane's first column
+    int block;
+    int64_t row, step;   // first row, and from one row of the batch to the next
+};
+template <typename F>
+__device__ inline void for_units(const Rows8& r, F work) {
+    const int unit = threadIdx.x / kLanes, across = 1 << r.unit_log;
+    const int64_t per = (int64_t)kBatch * (kUnits >> r.unit_log);
+    const uint32_t items = (uint32_t)r.row_groups * r.col_groups;
+    for (uint32_t item = blockIdx.x; item < items; item += gridDim.x) {
+        const uint32_t rg = item / (uint32_t)r.col_groups;
+        Unit u;
+        u.block = (int)(item - rg * r.col_groups) * across + (unit & (across - 1));
+        u.d = u.block * kBlock8 + 8 * (threadIdx.x % kLanes);
+        u.step = kUnits >> r.unit_log;
+        u.row = rg * per + (unit >> r.unit_log);
+        work(u);
+    }
+}
+__device__ inline void store_codes(const Rows8& r, const Blocks8& b, const Unit& u, int64_t row, const u32x2& w, int byte) {
+    if (row >= r.rows || u.d >= r.dim16) return;
+    *reinterpret_cast<u32x2*>(b.codes + row * b.stride + u.d) = w;
+    if (threadIdx.x % kLanes == 0) b.scale[row * b.scale_stride + u.block] = (uint8_t)byte;
+}
+
+template <typename T, int ACT, bool KEEP>
+__global__ __launch_bounds__(kThreads) void encode8_kernel(const Encode8 a) {
+    for_units(a.r, [&](const Unit& u) {
+        Raw<T> raw[kBatch];
+        const int left = a.r.dim - u.d;
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const int64_t row = u.row + k * u.step;
+            raw[k] = load8(static_cast<const T*>(a.x) + row * a.x_stride + u.d, row < a.r.rows ? left : 0, a.vec);
+        }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const int64_t row = u.row + k * u.step;
+            float v[8];
+            int byte;
+            to_float<T>(raw[k], v);
+            if (KEEP) {
+                const u32x2 w = encode8(v, byte);
+                store_codes(a.r, a.codes, u, row, w, byte);
+            }
+            if (ACT != kActNone) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = act<ACT>(v[e]);
+                const u32x2 w = encode8(v, byte);
+                store_codes(a.r, a.out, u, row, w, byte);
+            }
+        }
+    });
+}
+
+template <typename T, int ACT>
+__global__ __launch_bounds__(kThreads) void backward8_kernel(const Backward8 a) {
+    for_units(a.r, [&](const Unit& u) {
+        Raw<T> grad[kBatch];
+        u32x2 code[kBatch];
+        int byte[kBatch];
+        const int left = a.r.dim - u.d;
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const int64_t row = u.row + k * u.step;
+            const bool there = row < a.r.rows && left > 0;
+            grad[k] = load8(static_cast<const T*>(a.grad) + row * a.grad_stride + u.d, there ? left : 0, a.grad_vec);
+            code[k] = u32x2{0u, 0u};
+            byte[k] = kScale8Low;
+            if (there) {
+                code[k] = *reinterpret_cast<const u32x2*>(a.u.codes + row * a.u.stride + u.d);
+                byte[k] = a.u.scale[row * a.u.scale_stride + u.block];
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const int64_t row = u.row + k * u.step;
+            float v[8], g[8];
+            decode8(code[k], scale_value(byte[k]), v);
+            to_float<T>(grad[k], g);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) g[e] *= act_slope<ACT>(v[e]);
+            if (a.out && row < a.r.rows)
+                store8(static_cast<T*>(a.out) + row * a.out_stride + u.d, from_float<T>(g), left, a.out_vec);
+            if (a.out8.codes) {
+                int b;
+                const u32x2 w = encode8(g, b);
+                store_codes(a.r, a.out8, u, row, w, b);
+            }
+        }
+    });
+}
+
+template <typename T>
+__global__ __launch_bounds__(kThreads) void decode8_kernel(const Decode8 a) {
+    for_units(a.r, [&](const Unit& u) {
+        const int left = a.r.dim - u.d;
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const int64_t row = u.row + k * u.step;
+            if (row >= a.r.rows || left <= 0) continue;
+            const u32x2 w = *reinterpret_cast<const u32x2*>(a.x.codes + row * a.x.stride + u.d);
+            float v[8];
+            decode8(w, scale_value(a.x.scale[row / a.tall * a.x.scale_stride + u.block]), v);
+            store8(static_cast<T*>(a.out) + row * a.out_stride + u.d, from_float<T>(v), left, a.vec);
+        }
+    });
+}
+
+// ---------------------------------------------------------------- weights
+// A workgroup for each 128 x 128 block.  A lane holds 4 x 4 values of each of 4 pieces:
+// 4 rows of 4 consecutive columns, so that both layouts are written from registers
+// in words: rows straight to memory (32 lanes cover a row's 128 bytes), columns
+// through LDS, whose word (column, 4 rows) sits in slot rows ^ column / 4 of its
+// column: the 32 lanes that write a row group meet 32 different banks.
+template <typename T>
+__global__ __launch_bounds__(kThreads) void weight8_kernel(const Weight8 a) {
+    __shared__ uint32_t tops[kThreads / kWave];
+    __shared__ uint32_t turned[kBlock8][kBlock8 / 4];
+    const int across = (a.dim + kBlock8 - 1) / kBlock8;
+    const int br = blockIdx.x / across, bd = blockIdx.x % across;
+    const int col = 4 * (threadIdx.x % 32), group = threadIdx.x / 32;     // rows 4 (group + 8 q) + j
+    const int d = bd * kBlock8 + col, row0 = br * kBlock8;
+    float v[4][4][4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int row = row0 + 4 * (group + 8 * q) + j;
+            const T* p = static_cast<const T*>(a.w) + (int64_t)row * a.w_stride + d;
+            if (row < a.rows && a.vec && d + 4 <= a.dim) {
+                if constexpr (sizeof(T) == 4) {
+                    const u32x4 w = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[q][j][e] = as_float(w[e]);
+                } else {
+                    const u32x2 w = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(p));
+                    const u32x4 both = {w[0], w[1], 0u, 0u};
+                    float x[8];
+                    unpack8<T>(both, x);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[q][j][e] = x[e];
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[q][j][e] = row < a.rows && d + e < a.dim ? (float)p[e] : 0.f;
+            }
+        }
+    uint32_t top = 0;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t b = finite_bits(v[q][j][e]);
+                top = top > b ? top : b;
+            }
+    top = block_max(top);
+#pragma unroll
+    for (int off = 16; off < kWave; off <<= 1) {
+        const uint32_t y = (uint32_t)__shfl_xor((int)top, off, kWave);
+        top = top > y ? top : y;
+    }
+    if (threadIdx.x % kWave == 0) tops[threadIdx.x / kWave] = top;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kThreads / kWave; ++w) top = top > tops[w] ? top : tops[w];
+    const int byte = scale_byte(top);
+    const float inverse = scale_inverse(byte);
+    const int dim16 = (a.dim + 15) / 16 * 16, rows16 = (a.rows + 15) / 16 * 16;
+    if (threadIdx.x == 0) {
+        a.codes.scale[br * a.codes.scale_stride + bd] = (uint8_t)byte;
+        if (a.transposed.codes) a.transposed.scale[bd * a.transposed.scale_stride + br] = (uint8_t)byte;
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int row = row0 + 4 * (group + 8 * q) + j;
+            w[j] = codes4(v[q][j], inverse);
+            if (row < a.rows && d < dim16) *reinterpret_cast<uint32_t*>(a.codes.codes + row * a.codes.stride + d) = w[j];
+        }
+        if (a.transposed.codes) {
+            // 4 x 4 bytes turned: pairs of rows, then pairs of pairs
+            const uint32_t lo01 = __builtin_amdgcn_perm(w[1], w[0], 0x05010400u), hi01 = __builtin_amdgcn_perm(w[1], w[0], 0x07030602u);
+            const uint32_t lo23 = __builtin_amdgcn_perm(w[3], w[2], 0x05010400u), hi23 = __builtin_amdgcn_perm(w[3], w[2], 0x07030602u);
+            const int slot = (group + 8 * q) ^ (col / 4);
+            turned[col][slot] = __builtin_amdgcn_perm(lo23, lo01, 0x05040100u);
+            turned[col + 1][slot] = __builtin_amdgcn_perm(lo23, lo01, 0x07060302u);
+            turned[col + 2][slot] = __builtin_amdgcn_perm(hi23, hi01, 0x05040100u);
+            turned[col + 3][slot] = __builtin_amdgcn_perm(hi23, hi01, 0x07060302u);
+        }
+    }
+    if (!a.transposed.codes) return;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int c = threadIdx.x / 8 + 32 * k, chunk = threadIdx.x % 8;
+        const int out_row = bd * kBlock8 + c, out_col = row0 + 16 * chunk;
+        u32x4 w;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[e] = turned[c][(4 * chunk + e) ^ (c / 4)];
+        if (out_row < a.dim && out_col < rows16)
+            *reinterpret_cast<u32x4*>(a.transposed.codes + out_row * a.transposed.stride + out_col) = w;
+    }
+}
+
+// Workgroups of a row-wise pass: enough to fill the chip many times over, the rest
+// by the kernel's own loop.
+int rows_grid(const Rows8& r) { return (int)std::min<int64_t>((int64_t)r.row_groups * r.col_groups, 1 << 20); }
+
+template <typename T, int ACT>
+hipError_t encode_typed(const Encode8& a, hipStream_t s) {
+    const int grid = rows_grid(a.r);
+    if (ACT == kActNone || a.codes.codes) encode8_kernel<T, ACT, true><<<grid, kThreads, 0, s>>>(a);
+    else encode8_kernel<T, ACT, ACT == kActNone><<<grid, kThreads, 0, s>>>(a);
+    return hipGetLastError();
+}
+template <typename T>
+hipError_t encode_act(const Encode8& a, int act, hipStream_t s) {
+    if (act == kActRelu2) return encode_typed<T, kActRelu2>(a, s);
+    if (act == kActSilu) return encode_typed<T, kActSilu>(a, s);
+    if (act == kActGelu) return encode_typed<T, kActGelu>(a, s);
+    return encode_typed<T, kActNone>(a, s);
+}
+template <typename T>
+hipError_t backward_act(const Backward8& a, int act, hipStream_t s) {
+    const int grid = rows_grid(a.r);
+    if (act == kActRelu2) backward8_kernel<T, kActRelu2><<<grid, kThreads, 0, s>>>(a);
+    else if (act == kActSilu) backward8_kernel<T, kActSilu><<<grid, kThreads, 0, s>>>(a);
+    else backward8_kernel<T, kActGelu><<<grid, kThreads, 0, s>>>(a);
+    return hipGetLastError();
+}
+
+Rows8 plan(const Rows8& r) {
+    Rows8 q = r;
+    const int blocks = (q.dim + kBlock8 - 1) / kBlock8;
+    q.dim16 = (q.dim + 15) / 16 * 16;
+    q.unit_log = 0;
+    while (q.unit_log < 4 && (1 << q.unit_log) < blocks) ++q.unit_log;
+    q.col_groups = (blocks + (1 << q.unit_log) - 1) >> q.unit_log;
+    const int64_t per = (int64_t)kBatch * (kUnits >> q.unit_log);
+    q.row_groups = (int)((q.rows + per - 1) / per);
+    return q;
+}
+
+}  // namespace
+
+hipError_t launch_encode8(const Encode8& a0, int type, int act, hipStream_t s) {
+    Encode8 a = a0;
+    a.r = plan(a0.r);
+    if (type == kTypeBf16) return encode_act<bf16>(a, act, s);
+    return type == kTypeFp16 ? encode_act<f16>(a, act, s) : encode_act<float>(a, act, s);
+}
+hipError_t launch_backward8(const Backward8& a0, int type, int act, hipStream_t s) {
+    Backward8 a = a0;
+    a.r = plan(a0.r);
+    if (type == kTypeBf16) return backward_act<bf16>(a, act, s);
+    return type == kTypeFp16 ? backward_act<f16>(a, act, s) : backward_act<float>(a, act, s);
+}
+hipError_t launch_decode8(const Decode8& a0, int type, hipStream_t s) {
+    Decode8 a = a0;
+    a.r = plan(a0.r);
+    const int grid = rows_grid(a.r);
+    if (type == kTypeBf16) decode8_kernel<bf16><<<grid, kThreads, 0, s>>>(a);
+    else if (type == kTypeFp16) decode8_kernel<f16><<<grid, kThreads, 0, s>>>(a);
+    else decode8_kernel<float><<<grid, kThreads, 0, s>>>(a);
+    return hipGetLastError();
+}
+hipError_t launch_weight8(const Weight8& a, int type, hipStream_t s) {
+    const int64_t grid = (int64_t)((a.rows + kBlock8 - 1) / kBlock8) * ((a.dim + kBlock8 - 1) / kBlock8);
+    if (type == kTypeBf16) weight8_kernel<bf16><<<(int)grid, kThreads, 0, s>>>(a);
+    else if (type == kTypeFp16) weight8_kernel<f16><<<(int)grid, kThreads, 0, s>>>(a);
+    else weight8_kernel<float><<<(int)grid, kThreads, 0, s>>>(a);
+    return hipGetLastError();
+}
+
+}  // namespace muon

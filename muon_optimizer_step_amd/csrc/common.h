@@ -57,6 +57,8 @@ __device__ inline float lo8_decode(float hi, uint32_t word, int b) {
     return hi + ldexpf(u - 128.0f, __builtin_amdgcn_frexp_expf(hi) - 16);
 }
 
+// A vector's element goes through a value: __builtin_bit_cast of the element itself reads the first one.
+__device__ inline float as_float(uint32_t x) { return __builtin_bit_cast(float, x); }
 __device__ inline uint32_t bf16_bits(bf16 x) { return (uint32_t)__builtin_bit_cast(uint16_t, x); }
 __device__ inline bf16 bits_bf16(uint32_t b) { return __builtin_bit_cast(bf16, (uint16_t)b); }
 

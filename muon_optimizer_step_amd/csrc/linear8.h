@@ -1,0 +1,104 @@
+// Kernel arguments and launchers of the linear layers in 8 bits (blocks8.hip,
+// matmul8.hip, grad8.hip); the host side is linear8_api.hip.
+#pragma once
+
+#include "common.h"
+
+namespace muon {
+
+enum Linear8Type { kTypeBf16 = 0, kTypeFp16, kTypeFp32 };
+enum Linear8Act { kActNone = 0, kActRelu2, kActSilu, kActGelu };
+
+constexpr int kBlock8 = 128;      // values of a row that share a scale
+constexpr int kScale8Low = 10;    // the smallest scale's byte
+
+// A matrix in 8 bits: codes and scales, strides in bytes.
+struct Blocks8 {
+    uint8_t* codes;
+    uint8_t* scale;
+    int64_t stride, scale_stride;
+};
+
+// Which rows and blocks of a row-wise pass a workgroup takes: 2^unit_log units of 16
+// lanes side by side on a row, 16 >> unit_log rows of them at a time.
+struct Rows8 {
+    int64_t rows;
+    int dim, dim16;          // dim rounded up to 16
+    int unit_log, col_groups, row_groups;      // at most 2^29 of both together
+};
+
+struct Encode8 {
+    Rows8 r;
+    const void* x;
+    int64_t x_stride;        // elements
+    int vec;                 // rows of x 16-byte aligned
+    Blocks8 codes, out;      // codes NULL: not wanted
+};
+struct Backward8 {
+    Rows8 r;
+    Blocks8 u, out8;
+    const void* grad;
+    void* out;
+    int64_t grad_stride, out_stride;
+    int grad_vec, out_vec;
+};
+struct Decode8 {
+    Rows8 r;
+    Blocks8 x;
+    int tall;                // rows of a block: 1 or kBlock8
+    void* out;
+    int64_t out_stride;
+    int vec;
+};
+struct Weight8 {
+    const void* w;
+    int64_t w_stride;
+    int rows, dim, vec;
+    Blocks8 codes, transposed;
+};
+
+hipError_t launch_encode8(const Encode8& a, int type, int act, hipStream_t s);
+hipError_t launch_backward8(const Backward8& a, int type, int act, hipStream_t s);
+hipError_t launch_decode8(const Decode8& a, int type, hipStream_t s);
+hipError_t launch_weight8(const Weight8& a, int type, hipStream_t s);
+
+// y = a b^T.
+enum Matmul8Variant { kMatmulStream = 0, kMatmulMid, kMatmulTile };
+struct Matmul8 {
+    Blocks8 a, b;
+    void* y;
+    int64_t y_stride;
+    int rows, cols, dim;
+    int y_vec;               // rows of y 16-byte aligned, cols a multiple of 8
+    int tiles_v, tiles_t;    // tiles along cols and rows
+};
+hipError_t launch_matmul8(const Matmul8& a, int type, int variant, hipStream_t s);
+
+// out[c][d] = sum over r of grad[r][c] x[r][d].
+struct Grad8 {
+    Blocks8 x;
+    const void* grad;        // bf16, rows of whole 16-byte chunks
+    int64_t grad_stride;     // elements
+    int rows, cols, dim;
+    int cols8;               // cols rounded up to 8
+    int splits, stages_per_split;
+    int tiles_c, tiles_d;
+    float* out;
+    int64_t out_stride;
+    int out_vec;             // rows of out 16-byte aligned, dim a multiple of 4
+    int accumulate;
+    float* partial;          // nullable: [split][cols][partial_pitch]
+    int64_t partial_pitch;
+};
+struct Join8 {
+    const float* partial;
+    int64_t partial_pitch;
+    int splits, cols, dim;   // splits == 0: zeros
+    float* out;
+    int64_t out_stride;
+    int out_vec, accumulate;
+};
+hipError_t launch_grad8(const Grad8& a, bool mid, hipStream_t s);
+hipError_t launch_join8(const Join8& a, hipStream_t s);
+
+}  // namespace muon

@@ -185,6 +185,10 @@ struct ColOperand {
     template <int J> __device__ inline void load_tail(uint32_t dst, int left) const {
         direct_load<J * WAVES * 1024>(next, (uint32_t)(min(row[J], left - 1) * (int64_t)pitch) + chunk[J], dst);
     }
+    // where rows beyond count as zero, whatever the last one holds
+    template <int J> __device__ inline void load_zeros(uint32_t dst, int left) const {
+        direct_load_from<J * WAVES * 1024>(row[J] < left ? next + off[J] : kZeros, dst);
+    }
     __device__ inline void advance() { next += step; }
     // fragment I (32 columns): lane l holds K 16 kc + 8 (l / 32) .. + 7 of its column
     template <int I> __device__ inline u32x4 frag(uint32_t slot, int kc) const {
