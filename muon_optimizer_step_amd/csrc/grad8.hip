@@ -17,128 +17,239 @@
 namespace muon {
 namespace {
 
-// Columns of x for a tile: 64 rows of K x COLS values per stage, decoded, in the layout of
-// ColOperand<COLS>.
-template <int COLS, int WAVES, int FRAGS>
+// Columns of x for a tile: 64 rows of K x COLS values per stage, decoded and turned: LDS
+// holds a row of 128 bytes for each column, K contiguous, so that a fragment is one 16-byte read
+// (the transposing reads that the gradient takes have half the rate: 64 bytes a clock). The
+// 16-byte chunk c of column d is in slot c ^ f(d), f = d / 2 ^ d / 16 modulo 8: the 8 lanes that are
+// served at a time lie in different banks, in fragments (8 columns) and in writes
+// (every fourth of 32 columns).
+//
+// A lane takes 4 columns of 8 rows: a word of codes from each row and one scale's byte, which
+// the 16 lanes that share the rows pass on.
+template <int COLS, int THREADS>
 struct CodeOperand {
-    typedef ColOperand<COLS, WAVES, FRAGS> Col;
-    static constexpr int kAcross = COLS / 16, kPer = WAVES * kWave / kAcross, kLoads = kHeadK / kPer;
-    static_assert(kPer % 4 == 0 && kLoads >= 1, "the swizzle of a lane's rows is the same");
-    const uint8_t* code;
+    static constexpr int kAcross = COLS / 4, kBytes = COLS * kHeadK * 2;
+    static_assert(THREADS / kAcross * 8 == kHeadK && kAcross % 16 == 0, "a stage");
+    struct Codes {
+        uint32_t w[8], byte;
+    };
+    const uint8_t* code;     // of the next stage to load
     const uint8_t* scale;
-    int64_t code_stride, scale_stride;
-    int row;
-    uint32_t put[2];         // LDS addresses of the lane's two chunks in its first row, less the slot's
-    uint32_t at[FRAGS];
-    u32x4 w[kLoads];
-    uint32_t byte[kLoads];
-    __device__ inline void init(const Blocks8& x, int d0, int dim, int64_t k0, int frag0, int thread, int lane) {
-        const int chunk = thread % kAcross;
-        row = thread / kAcross;
-        const int d = min(d0 + 16 * chunk, (dim + 15) / 16 * 16 - 16);
-        code_stride = x.stride;
-        scale_stride = x.scale_stride;
-        code = x.codes + (k0 + row) * code_stride + d;
-        scale = x.scale + (k0 + row) * scale_stride + d / kBlock8;
+    int64_t code_step, scale_step;
+    uint32_t code_stride, scale_stride, code_at, scale_at;
+    int row, scale_row;
+    uint32_t put[2];         // LDS address of the lane's first and third column's chunk, less the slot's
+    uint32_t at[4];          // of its chunk of fragment 0, by step ^ fragment
+    // frag0: the wave's first column, step0 its first step (of 16 K) of a stage
+    __device__ inline void init(const Blocks8& x, int d0, int dim, int64_t k0, int frag0, int step0, int thread, int lane) {
+        const int col = 4 * (thread % kAcross), group = thread / kAcross;
+        const int d = min(col, (dim + 15) / 16 * 16 - 4 - d0);
+        row = 8 * group;
+        scale_row = 8 * group + lane % 8;
+        code_stride = (uint32_t)x.stride;
+        scale_stride = (uint32_t)x.scale_stride;
+        code_step = kHeadK * x.stride;
+        scale_step = kHeadK * x.scale_stride;
+        code = x.codes + k0 * x.stride + d0;
+        scale = x.scale + k0 * x.scale_stride + d0 / kBlock8;
+        code_at = d;
+        scale_at = d / kBlock8;
+        auto f = [](int c) { return ((c >> 1) ^ (c >> 4)) & 7; };
 #pragma unroll
-        for (int h = 0; h < 2; ++h) put[h] = row * Col::kRow + (((2 * chunk + h) ^ Col::slot_xor(row)) * 16);
-        const int k = 8 * (lane / 32) + (lane % 16) / 4;
-        int quad = lane % 4;
-        quad = ((quad & 1) << 1) | (quad >> 1);
-        quad += 4 * ((lane / 16) % 2);
+        for (int h = 0; h < 2; ++h) put[h] = (col + 2 * h) * 128 + ((group ^ f(col + 2 * h)) << 4);
+        const int r = frag0 + swap23(lane % 32);
 #pragma unroll
-        for (int i = 0; i < FRAGS; ++i)
-            at[i] = k * Col::kRow + ((((frag0 + 32 * i) / 8 + quad / 2) ^ Col::slot_xor(k)) * 16) + (quad & 1) * 8;
+        for (int j = 0; j < 4; ++j) at[j] = r * 128 + (((2 * (j ^ step0) + lane / 32) ^ f(r)) << 4);
     }
-    // the next stage, of which `left` rows exist (zeros behind them)
-    __device__ inline void load(int left) {
+    // the next stage, whose last row is `last` (rows beyond repeat it)
+    template <int FIRST, int END> __device__ inline void load(Codes& c, int last) const {
 #pragma unroll
-        for (int j = 0; j < kLoads; ++j) {
-            w[j] = u32x4{0u, 0u, 0u, 0u};
-            byte[j] = kScale8Low;
-            if (row + j * kPer < left) {
-                w[j] = *reinterpret_cast<const u32x4*>(code + j * kPer * code_stride);
-                byte[j] = scale[j * kPer * scale_stride];
-            }
-        }
-        code += kHeadK * code_stride;
-        scale += kHeadK * scale_stride;
+        for (int j = FIRST; j < END; ++j)
+            c.w[j] = *reinterpret_cast<const uint32_t*>(code + (__umul24(min(row + j, last), code_stride) + code_at));
+        if (END == 8) c.byte = scale[__umul24(min(scale_row, last), scale_stride) + scale_at];
     }
-    __device__ inline void store(uint32_t slot) const {
+    __device__ inline void advance(bool there) {
+        code += there ? code_step : 0;
+        scale += there ? scale_step : 0;
+    }
+    // rows 2 M and 2 M + 1: word M of each column's eight values
+    struct Decoded {
+        u32x4 col[4];
+    };
+    template <int M> __device__ inline void decode(const Codes& c, Decoded& out) const {
+        const int bits = (int)(c.byte << 23);       // row_newbcast: lane n of each 16
+        const float f0 = as_float((uint32_t)__builtin_amdgcn_update_dpp(0, bits, 0x150 + 2 * M, 15, 15, false));
+        const float f1 = as_float((uint32_t)__builtin_amdgcn_update_dpp(0, bits, 0x151 + 2 * M, 15, 15, false));
+        auto half = [&](auto h) {
+            constexpr bool H = decltype(h)::value;
+            const uint32_t a = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)c.w[2 * M], f0, H));
+            const uint32_t b = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)c.w[2 * M + 1], f1, H));
+            out.col[2 * H][M] = __builtin_amdgcn_perm(b, a, 0x05040100u);
+            out.col[2 * H + 1][M] = __builtin_amdgcn_perm(b, a, 0x07060302u);
+        };
+        half(std::false_type());
+        half(std::true_type());
+    }
+    template <int C> __device__ inline void store(const Decoded& v, uint32_t slot) const {
         typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
-#pragma unroll
-        for (int j = 0; j < kLoads; ++j) {
-            const float f = __builtin_bit_cast(float, byte[j] << 23);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                u32x4 v;
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    v[2 * k] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)w[j][2 * h + k], f, false));
-                    v[2 * k + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)w[j][2 * h + k], f, true));
-                }
-                *(lds_u32x4*)(uintptr_t)(slot + put[h] + j * kPer * Col::kRow) = v;
-            }
-        }
+        *(lds_u32x4*)(uintptr_t)(slot + put[C / 2] + C % 2 * 128) = v.col[C];
     }
-    template <int I> __device__ inline u32x4 frag(uint32_t slot, int kc) const {
-        typedef __attribute__((address_space(3))) short4v lds_short4;
-        const uint32_t p = at[I] + slot + kc * 16 * Col::kRow;
-        const u32x2 a = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4*)(uintptr_t)p));
-        const u32x2 b = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4*)(uintptr_t)(p + 4 * Col::kRow)));
-        return u32x4{a[0], a[1], b[0], b[1]};
+    __device__ inline void decode_all(const Codes& c, uint32_t slot) const {
+        Decoded v;
+        decode<0>(c, v);
+        decode<1>(c, v);
+        decode<2>(c, v);
+        decode<3>(c, v);
+        store<0>(v, slot);
+        store<1>(v, slot);
+        store<2>(v, slot);
+        store<3>(v, slot);
+    }
+    template <int I> __device__ inline u32x4 frag(uint32_t slot, int step) const {
+        typedef __attribute__((address_space(3))) const u32x4 lds_u32x4;
+        return *(lds_u32x4*)(uintptr_t)(at[step ^ I] + slot + I * 32 * 128);
     }
 };
 
-template <typename Op> __device__ inline void load_zeros(Op& op, uint32_t dst, int left) {
-    if (left >= kHeadK) {
-        load_stage(op, dst, left);
-        return;
-    }
-    static_assert(Op::kLoads == 4, "loads of a wave");
-    op.template load_zeros<0>(dst, left);
-    op.template load_zeros<1>(dst, left);
-    op.template load_zeros<2>(dst, left);
-    op.template load_zeros<3>(dst, left);
-    op.advance();
-}
-
-// acc += x^T grad over `stages` stages of 64 rows, `left` rows in all.  Two buffers: while a
-// stage is multiplied, the next one's gradient is loaded straight to the other buffer,
-// its codes, loaded a stage before, are decoded to it, and the codes of the one after are loaded.
-template <int TD, int TC, typename OX, typename OG>
-__device__ inline void k_loop_coded(floatx16 (&acc)[TD][TC], int stages, OX& X, OG& G, int left, uint32_t lds, int wave) {
-    if (stages <= 0) return;
-    constexpr uint32_t kX = kHeadK * OX::Col::kRow, kStage = kX + OG::kBytes;
+// acc += x^T grad over `stages` stages of 64 rows, `left` rows in all; STEPS steps of 16 rows from
+// step0 on are this wave's.  LDS holds two stages of x and three of the gradient.  While
+// stage k is multiplied, x of k + 1 is decoded from registers (loaded at the end of k - 2), the
+// gradient of k + 2 is loaded straight to LDS and the codes of k + 3 to registers, a piece after every
+// second product.  The barrier sits before the products of a stage's last step, whose
+// fragments are in registers by then; the next stage's first ones are read behind it.
+// Near the end the last stage is loaded again, which nothing reads, so that the body has no branch;
+// rows behind the last are zero in the gradient's fragments of the last stage (x has the last
+// row again there).
+template <int STEPS, int TD, int TC, typename OX, typename OG>
+__device__ inline void k_loop_coded(floatx16 (&acc)[TD][TC], int stages, OX& X, OG& G, int left, int step0, uint32_t lds, int wave, int lane) {
+    static_assert(OG::kLoads == 4 && TD * TC == 8 && (STEPS == 2 || STEPS == 4), "pieces of a stage");
+    constexpr int kUnderWay = 9 + OG::kLoads;      // loads of a stage of x and of the gradient
+    using std::integral_constant;
+    constexpr uint32_t kX = OX::kBytes, kG = OG::kBytes;
     const uint32_t mine = wave * 1024;
-    uint32_t now = lds, other = lds + kStage;
-    X.load(left);
-    X.store(now);
-    load_zeros(G, now + kX + mine, left);
-    if (stages > 1) X.load(left - kHeadK);
-    for (int kt = 0; kt < stages; ++kt) {
-        wait_loads<0>();
-        wait_lds();
-        bare_barrier();      // stage kt is in LDS, and every wave is done with stage kt - 1
-        u32x4 fa[TD], fb[TC];
-        auto multiply = [&](int kc) {
-            read_step(X, G, fa, fb, now, now + kX, kc);
+    uint32_t x0 = lds, x1 = lds + kX, g0 = lds + 2 * kX, g1 = g0 + kG, g2 = g1 + kG;
+    u32x4 fa[2][TD], fb[2][TC];
+    typename OX::Codes c0, c1;
+    int left_x = left, left_g = left;      // rows from the stage that X and G load next
+    auto next_x = [&] {
+        const bool more = left_x > kHeadK;
+        X.advance(more);
+        left_x -= more ? kHeadK : 0;
+    };
+    auto load_x = [&](typename OX::Codes& c) {
+        X.template load<0, 8>(c, min(kHeadK, left_x) - 1);
+        next_x();
+    };
+    auto load_g = [&](auto j, uint32_t slot) { G.template load_clamped<decltype(j)::value>(slot + mine, min(kHeadK, left_g) - 1); };
+    auto next_g = [&] {
+        const bool more = left_g > kHeadK;
+        G.next += more ? G.step : 0;
+        left_g -= more ? kHeadK : 0;
+    };
+    auto whole_g = [&](uint32_t slot) {
+        load_g(integral_constant<int, 0>(), slot);
+        load_g(integral_constant<int, 1>(), slot);
+        load_g(integral_constant<int, 2>(), slot);
+        load_g(integral_constant<int, 3>(), slot);
+        next_g();
+    };
+    load_x(c1);
+    load_x(c0);
+    whole_g(g0);
+    X.decode_all(c1, x0);
+    whole_g(g1);
+    load_x(c1);
+    wait_loads<kUnderWay>(); // the gradient of stage 0
+    wait_lds();
+    bare_barrier();
+    auto read = [&](int set, uint32_t x, uint32_t g, int step) { read_step(X, G, fa[set], fb[set], x, g, step); };
+    auto mask = [&](u32x4 (&f)[TC], int step) {      // of the last stage
+        const int rows = (left - 1) % kHeadK + 1 - 16 * (step0 + step) - 8 * (lane / 32);
 #pragma unroll
-            for (int i = 0; i < TD; ++i)
+        for (int j = 0; j < TC; ++j)
 #pragma unroll
-                for (int j = 0; j < TC; ++j) acc[i][j] = mfma<bf16>(fa[i], fb[j], acc[i][j]);
+            for (int e = 0; e < 4; ++e) f[j][e] &= (2 * e < rows ? 0xFFFFu : 0u) | (2 * e + 1 < rows ? 0xFFFF0000u : 0u);
+    };
+    // the products of a step, with a piece of other work after each
+    auto multiply = [&](int set, auto piece) {
+        auto one = [&](auto n) {
+            constexpr int N = decltype(n)::value;
+            acc[N / TC][N % TC] = mfma<bf16>(fa[set][N / TC], fb[set][N % TC], acc[N / TC][N % TC]);
+            __builtin_amdgcn_sched_barrier(0);
+            piece(n);
+            __builtin_amdgcn_sched_barrier(0);
         };
-        if (kt + 1 < stages) {
-            X.store(other);
-            load_zeros(G, other + kX + mine, left - (kt + 1) * kHeadK);
-            if (kt + 2 < stages) X.load(left - (kt + 2) * kHeadK);
+        one(integral_constant<int, 0>());
+        one(integral_constant<int, 1>());
+        one(integral_constant<int, 2>());
+        one(integral_constant<int, 3>());
+        one(integral_constant<int, 4>());
+        one(integral_constant<int, 5>());
+        one(integral_constant<int, 6>());
+        one(integral_constant<int, 7>());
+    };
+    read(0, x0, g0, 0);
+    // a stage that another follows; c: x of the next stage, then of the third after
+    auto stage = [&](typename OX::Codes& c) {
+        typename OX::Decoded v;
+        auto piece_g = [&](auto n) {      // 0 .. 3
+            load_g(n, g2);
+            if (decltype(n)::value == 3) next_g();
+        };
+        read(1, x0, g0, 1);
+        if constexpr (STEPS == 2) {
+            multiply(0, [&](auto n) {
+                constexpr int N = decltype(n)::value;
+                if constexpr (N < 4) X.template decode<N>(c, v);
+                if constexpr (N >= 4) {
+                    X.template store<N - 4>(v, x1);
+                    piece_g(integral_constant<int, N - 4>());
+                }
+            });
+        } else {
+            multiply(0, [&](auto n) {
+                constexpr int N = decltype(n)::value;
+                if constexpr (N % 2 == 0) X.template decode<N / 2>(c, v);
+            });
+            read(0, x0, g0, 2);
+            multiply(1, [&](auto n) {
+                constexpr int N = decltype(n)::value;
+                if constexpr (N % 2 == 0) X.template store<N / 2>(v, x1);
+            });
+            read(1, x0, g0, 3);
+            multiply(0, [&](auto n) {
+                constexpr int N = decltype(n)::value;
+                if constexpr (N % 2 == 0) piece_g(integral_constant<int, N / 2>());
+            });
         }
-#pragma unroll
-        for (int kc = 0; kc < kHeadK / 16; ++kc) multiply(kc);
-        const uint32_t t = now;
-        now = other;
-        other = t;
+        wait_lds();          // this wave's last fragments of the stage, and its share of the next one's x
+        wait_loads<kUnderWay>();     // all but the newest of x and of the gradient
+        bare_barrier();
+        read(0, x1, g1, 0);
+        const int last = min(kHeadK, left_x) - 1;
+        multiply(1, [&](auto n) {
+            constexpr int N = decltype(n)::value;
+            X.template load<N, N + 1>(c, last);
+            if (N == 7) next_x();
+        });
+        const uint32_t tx = x0, tg = g0;
+        x0 = x1; x1 = tx;
+        g0 = g1; g1 = g2; g2 = tg;
+    };
+    int kt = 0;
+#pragma unroll 1
+    for (; kt + 2 < stages; kt += 2) {
+        stage(c0);
+        stage(c1);
     }
+    if (kt + 1 < stages) stage(c0);
+#pragma unroll
+    for (int step = 0; step < STEPS; ++step) {
+        if (step + 1 < STEPS) read((step + 1) % 2, x0, g0, step + 1);
+        mask(fb[step % 2], step);
+        multiply(step % 2, [](auto) {});
+    }
+    wait_loads<0>();         // nothing under way to LDS behind the end
 }
 
 // A wave's sums to memory: acc[i][j] holds columns d0 + 32 i + 16 p + 8 (l / 32) + e
@@ -182,34 +293,75 @@ __device__ inline void store_tile(const Grad8& a, floatx16 (&acc)[TD][TC], int s
     }
 }
 
-// EDGE x EDGE: 256 with 8 waves of 128 x 64, or 128 with 4 waves of 64 x 64 and two workgroups
-// per compute unit.
-template <int EDGE> struct GradTile;
-template <> struct GradTile<256> { static constexpr int WD = 2, WC = 4, TD = 4, TC = 2; };
-template <> struct GradTile<128> { static constexpr int WD = 2, WC = 2, TD = 2, TC = 2; };
-template <int EDGE> constexpr int kGradThreads = GradTile<EDGE>::WD * GradTile<EDGE>::WC * kWave;
-template <int EDGE> constexpr size_t kGradBytes = (size_t)2 * 2 * EDGE * kHeadK * 2;
+// EDGE x EDGE, waves of 128 x 64: 256 with 8 waves; 128 with 4 and two workgroups per compute
+// unit, two pairs of waves that take half of every stage's K each and meet in LDS (64 x 64 a
+// wave would read a third more fragments for its products).
+template <int EDGE> struct GradTile {
+    static constexpr int WD = EDGE / 128, WC = EDGE / 64, kParts = EDGE == 256 ? 1 : 2, NW = WD * WC * kParts, kThreads = NW * kWave;
+    static constexpr size_t kBytes = (size_t)5 * EDGE * kHeadK * 2;
+    static_assert(kParts == 1 || (size_t)NW * 16 * 1024 <= kBytes, "the pairs' meeting");
+};
 
 template <int EDGE>
-__global__ __launch_bounds__(kGradThreads<EDGE>, 2) void grad8_kernel(const Grad8 a) {
+__global__ __launch_bounds__((GradTile<EDGE>::kThreads), 2) void grad8_kernel(const Grad8 a) {
     typedef GradTile<EDGE> S;
-    constexpr int NW = S::WD * S::WC;
-    static_assert(S::WD * S::TD * 32 == EDGE && S::WC * S::TC * 32 == EDGE, "tile");
+    constexpr int TD = 4, TC = 2, NW = S::NW, kSteps = kHeadK / 16 / S::kParts;
     extern __shared__ __align__(16) uint8_t lds[];
     const int item = xcd_item(a.tiles_c * a.tiles_d * a.splits);
     if (item < 0) return;
     const int split = item / (a.tiles_c * a.tiles_d), tile = item - split * a.tiles_c * a.tiles_d;
     const int c0 = tile / a.tiles_d * EDGE, d0 = tile % a.tiles_d * EDGE;
     const int s0 = split * a.stages_per_split, s1 = min((a.rows + kHeadK - 1) / kHeadK, s0 + a.stages_per_split);
-    const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), wd = wave / S::WC, wc = wave % S::WC;
-    CodeOperand<EDGE, NW, S::TD> X;
-    ColOperand<EDGE, NW, S::TC> G;
-    X.init(a.x, d0, a.dim, (int64_t)s0 * kHeadK, wd * S::TD * 32, threadIdx.x, lane);
-    G.init(a.grad, a.grad_stride * 2, c0, a.cols8, (int64_t)s0 * kHeadK, wc * S::TC * 32, false, wave, lane);
-    floatx16 acc[S::TD][S::TC];
+    const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int part = wave / (S::WD * S::WC), wd = wave / S::WC % S::WD, wc = wave % S::WC;
+    CodeOperand<EDGE, S::kThreads> X;
+    ColOperand<EDGE, NW, TC> G;
+    X.init(a.x, d0, a.dim, (int64_t)s0 * kHeadK, wd * TD * 32, part * kSteps, threadIdx.x, lane);
+    G.init(a.grad, a.grad_stride * 2, c0, a.cols8, (int64_t)s0 * kHeadK, wc * TC * 32, false, wave, lane);
+#pragma unroll
+    for (int j = 0; j < TC; ++j) G.at[j] += part * kSteps * 16 * G.kRow;
+    floatx16 acc[TD][TC];
     clear(acc);
-    k_loop_coded<S::TD, S::TC>(acc, s1 - s0, X, G, a.rows - s0 * kHeadK, lds_address(lds), wave);
-    store_tile<S::TD, S::TC>(a, acc, split, d0 + wd * S::TD * 32, c0 + wc * S::TC * 32, lane);
+    k_loop_coded<kSteps, TD, TC>(acc, s1 - s0, X, G, min(a.rows - s0 * kHeadK, (s1 - s0) * kHeadK), part * kSteps, lds_address(lds),
+                                 wave, lane);
+    if constexpr (S::kParts == 1) {
+        store_tile<TD, TC>(a, acc, split, d0 + wd * TD * 32, c0 + wc * TC * 32, lane);
+    } else {
+        // each pair keeps half of the columns and gives the other half away
+        constexpr int kHalf = TD / 2;
+        static_assert(kHalf * TC * 16 * kWave * 4 == 16 * 1024, "what a wave gives");
+        floatx4* given = reinterpret_cast<floatx4*>(lds);
+        floatx16 mine[kHalf][TC];
+        wait_lds();
+        bare_barrier();      // every wave is done with the operands
+#pragma unroll
+        for (int i = 0; i < kHalf; ++i)
+#pragma unroll
+            for (int j = 0; j < TC; ++j) {
+                mine[i][j] = part ? acc[kHalf + i][j] : acc[i][j];
+                const floatx16 give = part ? acc[i][j] : acc[kHalf + i][j];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    floatx4 v;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[e] = give[4 * q + e];
+                    given[((wave * kHalf + i) * TC + j) * 4 * kWave + q * kWave + lane] = v;
+                }
+            }
+        __syncthreads();
+        const int other = wave ^ (S::WD * S::WC);
+#pragma unroll
+        for (int i = 0; i < kHalf; ++i)
+#pragma unroll
+            for (int j = 0; j < TC; ++j)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const floatx4 v = given[((other * kHalf + i) * TC + j) * 4 * kWave + q * kWave + lane];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) mine[i][j][4 * q + e] += v[e];
+                }
+        store_tile<kHalf, TC>(a, mine, split, d0 + wd * TD * 32 + part * kHalf * 32, c0 + wc * TC * 32, lane);
+    }
 }
 
 // The splits' sums in order, added to what is there.
@@ -234,16 +386,17 @@ __global__ __launch_bounds__(256) void join8_kernel(const Join8 a) {
 
 template <int EDGE>
 hipError_t launch(const Grad8& a, hipStream_t s) {
+    typedef GradTile<EDGE> S;
     const hipError_t allowed = hipFuncSetAttribute(reinterpret_cast<const void*>(&grad8_kernel<EDGE>),
-                                                   hipFuncAttributeMaxDynamicSharedMemorySize, (int)kGradBytes<EDGE>);
+                                                   hipFuncAttributeMaxDynamicSharedMemorySize, (int)S::kBytes);
     if (allowed != hipSuccess) return allowed;
-    grad8_kernel<EDGE><<<xcd_grid(a.tiles_c * a.tiles_d * a.splits), kGradThreads<EDGE>, kGradBytes<EDGE>, s>>>(a);
+    grad8_kernel<EDGE><<<xcd_grid(a.tiles_c * a.tiles_d * a.splits), S::kThreads, S::kBytes, s>>>(a);
     return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_grad8(const Grad8& a, bool mid, hipStream_t s) { return mid ? launch<128>(a, s) : launch<256>(a, s); }
+hipError_t launch_grad8(const Grad8& a, int edge, hipStream_t s) { return edge == 128 ? launch<128>(a, s) : launch<256>(a, s); }
 
 hipError_t launch_join8(const Join8& a, hipStream_t s) {
     const int64_t items = (int64_t)a.cols * ((a.dim + 3) / 4);

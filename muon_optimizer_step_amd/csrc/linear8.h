@@ -63,7 +63,8 @@ hipError_t launch_decode8(const Decode8& a, int type, hipStream_t s);
 hipError_t launch_weight8(const Weight8& a, int type, hipStream_t s);
 
 // y = a b^T.
-enum Matmul8Variant { kMatmulStream = 0, kMatmulMid, kMatmulTile };
+// Kernels: up to 16 rows; 32 x 32 with K split over the waves; tiles of 64, 128 and 256.
+enum Matmul8Variant { kMatmulRows = 0, kMatmulSplit, kMatmulSmall, kMatmulMid, kMatmulTile };
 struct Matmul8 {
     Blocks8 a, b;
     void* y;
@@ -71,7 +72,11 @@ struct Matmul8 {
     int rows, cols, dim;
     int y_vec;               // rows of y 16-byte aligned, cols a multiple of 8
     int tiles_v, tiles_t;    // tiles along cols and rows
+    int splits, stages_per_split;    // parts of K (kMatmulSmall, kMatmulMid; 1 otherwise), a multiple of 4 stages of 128 each
+    float* partial;          // nullable: [split][rows][partial_pitch]
+    int64_t partial_pitch;
 };
+hipError_t launch_matmul8_join(const Matmul8& a, int type, hipStream_t s);
 hipError_t launch_matmul8(const Matmul8& a, int type, int variant, hipStream_t s);
 
 // out[c][d] = sum over r of grad[r][c] x[r][d].
@@ -98,7 +103,7 @@ struct Join8 {
     int64_t out_stride;
     int out_vec, accumulate;
 };
-hipError_t launch_grad8(const Grad8& a, bool mid, hipStream_t s);
+hipError_t launch_grad8(const Grad8& a, int edge, hipStream_t s);     // tiles of 128 or 256
 hipError_t launch_join8(const Join8& a, hipStream_t s);
 
 }  // namespace muon

@@ -118,11 +118,34 @@ Rows8 rows8(int64_t rows, int64_t dim) {
 
 // ---------------------------------------------------------------- the product
 struct MatmulPlan {
-    int variant, tile;
+    int variant, tile_v, tile_t, splits, stages;     // stages of a split
+    int64_t bytes;
 };
 MatmulPlan plan_matmul(const matmul8_t& p) {
-    if (p.rows <= 16) return {kMatmulStream, 16};
-    return {kMatmulMid, 128};
+    const int all = (int)ceil_div(p.dim, kBlock8);
+    MatmulPlan best = {kMatmulRows, 16, 16, 1, all, 256};
+    if (p.rows <= 16) return best;
+    double least = 1e300;
+    auto consider = [&](int variant, int tile, double start, double stage, double ends, int most_splits) {
+        const int64_t tiles = ceil_div(p.rows, tile) * ceil_div(p.cols, tile);
+        for (int splits = 1; splits <= most_splits; splits *= 2) {
+            const int stages = splits == 1 ? all : (int)round_up(ceil_div(all, splits), 4);
+            const int parts = (int)ceil_div(all, stages);
+            if (splits > 1 && (parts < 2 || tiles * parts > kCus)) break;
+            const double partial = (double)parts * p.rows * p.cols * 8;      // bytes, written and read
+            const double us = start + ceil_div(tiles * parts, kCus) * (stages * stage + ends) + (parts > 1 ? 2.5 + partial * 2e-7 : 0.0);
+            if (us < least) {
+                least = us;
+                best = {variant, tile, tile, parts, stages, 256};
+            }
+        }
+    };
+    consider(kMatmulSplit, 32, 2.5, 0.20, 0.6, 1);
+    consider(kMatmulSmall, 64, 2.6, 0.24, 0.9, 16);
+    consider(kMatmulMid, 128, 3.5, 0.56, 0.75, 8);
+    consider(kMatmulTile, 256, 3.5, 1.55, 4.4, 1);
+    if (best.splits > 1) best.bytes = 4 * (int64_t)best.splits * p.rows * round_up(p.cols, 8);
+    return best;
 }
 
 int check_matmul_sizes(const matmul8_t* p) {
@@ -136,8 +159,9 @@ int check_matmul_sizes(const matmul8_t* p) {
 }
 
 // ---------------------------------------------------------------- the weight's gradient
+constexpr int kMinStages = 4;     // of a split
 struct GradPlan {
-    bool pack, mid;
+    bool pack;
     int edge, splits, stages;     // stages of a split
     int64_t cols8, dim8;
     int64_t grad, partial, bytes; // offsets, -1: not there
@@ -147,13 +171,25 @@ GradPlan plan_grad(const act8_grad_weight_t& p) {
     q.pack = p.cols % 8 || !whole_rows(p.grad, p.grad_stride, 2);
     q.cols8 = round_up(p.cols, 8);
     q.dim8 = round_up(p.dim, 8);
-    q.edge = 128;
     const int64_t all = std::max<int64_t>(1, ceil_div(p.rows, kHeadK));
-    const int64_t tiles = ceil_div(p.cols, q.edge) * ceil_div(p.dim, q.edge);
-    q.splits = (int)std::max<int64_t>(1, std::min<int64_t>({all / 4, 32, 2 * kCus / tiles}));
-    q.stages = (int)ceil_div(all, q.splits);
-    q.splits = (int)ceil_div(all, q.stages);
-    q.mid = q.edge == 128;
+    static const int tried[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32};
+    double least = 1e300;
+    auto consider = [&](int edge, double stage, double ends) {
+        const int64_t tiles = ceil_div(p.cols, edge) * ceil_div(p.dim, edge);
+        for (int splits : tried) {
+            if (splits > 1 && all / splits < kMinStages) break;
+            const int64_t stages = ceil_div(all, splits), parts = ceil_div(all, stages);
+            const double mb = (double)parts * p.cols * p.dim * 4e-6;         // a part's sums, written and read again
+            const double us = 4.5 + ceil_div(tiles * parts, kCus) * (stages * stage + ends) + (parts > 1 ? 2.0 + mb * 0.3 : 0.0);
+            if (us >= least) continue;
+            least = us;
+            q.edge = edge;
+            q.splits = (int)parts;
+            q.stages = (int)stages;
+        }
+    };
+    consider(128, 0.48, 2.5);
+    consider(256, 1.5, 5.0);
     int64_t off = 0;
     auto take = [&](bool there, int64_t bytes) {
         const int64_t at = there ? off : -1;
@@ -275,25 +311,27 @@ int weight8_encode(const weight8_encode_t* problem, void* stream) {
 
 size_t matmul8_workspace_size(const matmul8_t* problem) {
     if (check_matmul_sizes(problem)) return 0;
-    return 256;
+    return (size_t)plan_matmul(*problem).bytes;
 }
 
 int matmul8(const matmul8_t* problem, void* workspace, size_t workspace_bytes, void* stream) {
     if (const int rc = check_matmul_sizes(problem)) return rc;
     const matmul8_t& p = *problem;
     const MatmulPlan q = plan_matmul(p);
-    if (const int rc = check_workspace("matmul8", workspace, workspace_bytes, 256)) return rc;
+    if (const int rc = check_workspace("matmul8", workspace, workspace_bytes, q.bytes)) return rc;
     Checks c("matmul8");
     c.coded("a", p.a, p.rows, p.dim, 1, false);
     c.coded("b", p.b, p.cols, p.dim, MUON_BLOCK8, false);
     if (!c.rc) c.matrix("y", p.y, p.rows, p.cols, p.y_stride, 2, true);
-    c.buffer("workspace", workspace, 256, 256, true);
+    c.buffer("workspace", workspace, q.bytes, 256, true);
     if (const int rc = c.done()) return rc;
     if (p.rows == 0) return MUON_OK;
     hipStream_t s = static_cast<hipStream_t>(stream);
     const Matmul8 a = {blocks(p.a), blocks(p.b), p.y, p.y_stride, (int)p.rows, (int)p.cols, (int)p.dim,
-                       whole_rows(p.y, p.y_stride, 2), (int)ceil_div(p.cols, q.tile), (int)ceil_div(p.rows, q.tile)};
+                       whole_rows(p.y, p.y_stride, 2), (int)ceil_div(p.cols, q.tile_v), (int)ceil_div(p.rows, q.tile_t),
+                       q.splits, q.stages, q.splits > 1 ? static_cast<float*>(workspace) : nullptr, round_up(p.cols, 8)};
     LINEAR8_TRY("matmul8", launch_matmul8(a, p.dtype, q.variant, s));
+    if (q.splits > 1) LINEAR8_TRY("matmul8_join", launch_matmul8_join(a, p.dtype, s));
     return MUON_OK;
 }
 
@@ -349,7 +387,7 @@ int act8_grad_weight(const act8_grad_weight_t* problem, void* workspace, size_t 
     a.accumulate = p.accumulate != 0;
     a.partial = q.partial >= 0 ? reinterpret_cast<float*>(ws + q.partial) : nullptr;
     a.partial_pitch = q.dim8;
-    LINEAR8_TRY("act8_grad_weight", launch_grad8(a, q.mid, s));
+    LINEAR8_TRY("act8_grad_weight", launch_grad8(a, q.edge, s));
     if (a.partial) {
         j.partial = a.partial;
         LINEAR8_TRY("act8_grad_join", launch_join8(j, s));

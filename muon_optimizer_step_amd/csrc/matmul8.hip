@@ -38,7 +38,10 @@ constexpr int kScaleStages = 16;
 struct RowScales {
     const uint32_t* row;
     uint32_t w[kScaleStages / 4];
-    __device__ inline void init(const Blocks8& b, int64_t r) { row = reinterpret_cast<const uint32_t*>(b.scale + r * b.scale_stride); }
+    // stage0: a multiple of 4
+    __device__ inline void init(const Blocks8& b, int64_t r, int stage0) {
+        row = reinterpret_cast<const uint32_t*>(b.scale + r * b.scale_stride + stage0);
+    }
     __device__ inline void load(int stage, int stages) {
 #pragma unroll
         for (int k = 0; k < kScaleStages / 4; ++k) w[k] = stage + 4 * k < stages ? row[stage / 4 + k] : 0u;
@@ -54,10 +57,10 @@ struct RowScales {
 template <int TV, int TT>
 struct Scales {
     RowScales b, a[TT];
-    __device__ inline void init(const Matmul8& m, int v0, int t0, int lane) {
-        b.init(m.b, min(v0, m.cols - 1) / kBlock8);
+    __device__ inline void init(const Matmul8& m, int v0, int t0, int stage0, int lane) {
+        b.init(m.b, min(v0, m.cols - 1) / kBlock8, stage0);
 #pragma unroll
-        for (int j = 0; j < TT; ++j) a[j].init(m.a, min(t0 + 32 * j + lane % 32, m.rows - 1));
+        for (int j = 0; j < TT; ++j) a[j].init(m.a, min(t0 + 32 * j + lane % 32, m.rows - 1), stage0);
     }
     __device__ inline void load(int stage, int stages) {
         b.load(stage, stages);
@@ -92,107 +95,285 @@ template <typename Op, int N> __device__ inline void read8(const Op& op, v8i (&f
 // every wave has the fragments of its second half in registers: it frees the stage's two
 // slots, which B of stage k + 2 and, half a stage later, A of stage k + 3 are loaded to, and
 // publishes stage k + 1, whose first fragments are read while the second half is multiplied.
+// A fragment is read into its own registers as soon as its last product is issued, four
+// products before the next one that needs it, and one load follows every second product.
+//
+// Where K ends inside the last stage, the chunks behind it are loaded from the stage's
+// beginning, so that nothing is read out of range, and B's fragments of them are zero (what A
+// has there is of the same row: a NaN is in the row's sums anyway).  The body of the loop then has no
+// branch, across which the compiler would move products away from what they are to overlap.
 template <int TA, int TB, typename OA, typename OB>
-__device__ inline void k_loop8(floatx16 (&acc)[TA][TB], int stages, OA& A, OB& B, int left, uint32_t lds, int wave, Scales<TA, TB>& s) {
+__device__ inline void k_loop8(floatx16 (&acc)[TA][TB], int stages, OA& A, OB& B, int left, uint32_t lds, int wave, int lane,
+                               Scales<TA, TB>& s) {
     static_assert(TA == 4 && TB == 2 && OA::kLoads == 4 && OB::kLoads == 4, "eight products and eight loads");
     using std::integral_constant;
-    v8i fa[TA], fb[2][TB];
+    v8i fa[TA], fb, fc[2];       // of A; of B: the first, and the second for each half
     uint32_t s0 = lds, s1 = lds + kOperand, s2 = lds + 2 * kOperand, s3 = lds + 3 * kOperand, s4 = lds + 4 * kOperand;
     const uint32_t mine = wave * 1024;
+    const int part = left % kHeadK;
+    const uint32_t behind = part && 8 * A.chunk >= part ? 16 * A.chunk : 0;      // the same chunk of B
+    auto load_all = [&](auto& op, uint32_t dst, uint32_t less) {
+        op.template load_before<0>(dst, less);
+        op.template load_before<1>(dst, less);
+        op.template load_before<2>(dst, less);
+        op.template load_before<3>(dst, less);
+        op.advance();
+    };
+    // fragment I of B in half `step` of the last stage
+    auto frag_last = [&](auto i, uint32_t slot, int step) {
+        u32x4 w[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            w[k] = B.template frag<decltype(i)::value>(slot, 2 * step + k);
+            const bool there = !part || 16 * (2 * step + k) + 8 * (lane / 32) < part;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[k][e] = there ? w[k][e] : 0u;
+        }
+        return join(w[0], w[1]);
+    };
     s.load(0, stages);
-    load_stage(A, s0 + mine, left);
-    load_stage(B, s1 + mine, left);
+    load_all(A, s0 + mine, stages == 1 ? behind : 0);
+    load_all(B, s1 + mine, stages == 1 ? behind : 0);
     if (stages > 1) {
-        load_stage(A, s2 + mine, left - kHeadK);
-        load_stage(B, s3 + mine, left - kHeadK);
+        load_all(A, s2 + mine, stages == 2 ? behind : 0);
+        load_all(B, s3 + mine, stages == 2 ? behind : 0);
         wait_loads<8>();
     } else {
         wait_loads<0>();
     }
     bare_barrier();
     read8(A, fa, s0, 0);
-    read8(B, fb[0], s1, 0);
-    auto one = [&](auto& op, auto j, uint32_t dst, bool there, int rest) {
-        constexpr int J = decltype(j)::value;
-        if (!there) return;
-        if (rest >= kHeadK) op.template load<J>(dst + mine);
-        else op.template load_tail<J>(dst + mine, rest);
-    };
-    for (int kt = 0; kt < stages; ++kt) {
-        const int rest = left - (kt + 2) * kHeadK;
-        const bool ahead = kt + 2 < stages;
-        // first half; the second half's fragments; A of stage kt + 2
-        read8(B, fb[1], s1, 1);
-        auto half = [&](int set, uint32_t slot_a, int step, bool next, auto& op, uint32_t dst) {
-            auto row = [&](auto i) {
+    if (stages > 1) {
+        fb = frag8<0>(B, s1, 0);
+        fc[0] = frag8<1>(B, s1, 0);
+    } else {
+        fb = frag_last(integral_constant<int, 0>(), s1, 0);
+        fc[0] = frag_last(integral_constant<int, 1>(), s1, 0);
+    }
+    // a stage that loads another one; the last but one, the last
+    enum { kLoads, kBeforeLast, kLast };
+    auto stage = [&](auto kind, uint32_t less) {
+        constexpr int kKind = decltype(kind)::value;
+        // half a stage: its products, four loads of `op`, and the fragments of the half that follows
+        auto half = [&](auto second, auto& op, uint32_t dst, uint32_t next_a, uint32_t next_b) {
+            constexpr int H = decltype(second)::value;
+            constexpr bool kNext = !(kKind == kLast && H == 1), kMasked = kKind == kLast || (kKind == kBeforeLast && H == 1);
+            auto next_of_b = [&](auto i) {
+                if constexpr (kMasked) return frag_last(i, next_b, 1 - H);
+                else return frag8<decltype(i)::value>(B, next_b, 1 - H);
+            };
+            auto first = [&](auto i) {
                 constexpr int I = decltype(i)::value;
-                acc[I][0] = mfma8(fa[I], fb[set][0], acc[I][0], s.b.w[0], s.a[0].w[0]);
-                acc[I][1] = mfma8(fa[I], fb[set][1], acc[I][1], s.b.w[0], s.a[1].w[0]);
+                acc[I][0] = mfma8(fa[I], fb, acc[I][0], s.b.w[0], s.a[0].w[0]);
+                if (I % 2 == 1) {
+                    __builtin_amdgcn_sched_barrier(0);
+                    if (kKind == kLoads) op.template load_before<I / 2>(dst + mine, less);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            };
+            auto then = [&](auto i) {
+                constexpr int I = decltype(i)::value;
+                acc[I][1] = mfma8(fa[I], fc[H], acc[I][1], s.b.w[0], s.a[1].w[0]);
                 __builtin_amdgcn_sched_barrier(0);
-                if (next) fa[I] = frag8<I>(A, slot_a, step);
-                one(op, i, dst, ahead, rest);
+                if constexpr (kNext) fa[I] = frag8<I>(A, next_a, 1 - H);
+                if (I % 2 == 1 && kKind == kLoads) op.template load_before<2 + I / 2>(dst + mine, less);
                 __builtin_amdgcn_sched_barrier(0);
             };
-            row(integral_constant<int, 0>());
-            row(integral_constant<int, 1>());
-            row(integral_constant<int, 2>());
-            row(integral_constant<int, 3>());
+            if constexpr (kNext) fc[1 - H] = next_of_b(integral_constant<int, 1>());
+            first(integral_constant<int, 0>());
+            first(integral_constant<int, 1>());
+            first(integral_constant<int, 2>());
+            first(integral_constant<int, 3>());
+            if constexpr (kNext) fb = next_of_b(integral_constant<int, 0>());
+            then(integral_constant<int, 0>());
+            then(integral_constant<int, 1>());
+            then(integral_constant<int, 2>());
+            then(integral_constant<int, 3>());
         };
-        half(0, s0, 1, true, A, s4);
+        half(integral_constant<int, 0>(), A, s4, s0, s1);
         A.advance();
-        wait_lds();
-        const bool next = kt + 1 < stages;
-        if (next) {
-            if (ahead) wait_loads<4>();
-            else wait_loads<0>();
+        if constexpr (kKind != kLast) {
+            wait_lds();          // this wave's last fragments of the stage
+            wait_loads<kKind == kLoads ? 4 : 0>();
             bare_barrier();
-            read8(B, fb[0], s3, 0);
         }
-        half(1, s2, 0, next, B, s0);
+        half(integral_constant<int, 1>(), B, s0, s2, s3);
         B.advance();
         s.advance();
-        if (next && (kt + 1) % kScaleStages == 0) s.load(kt + 1, stages);
         const uint32_t t0 = s0, t1 = s1;
         s0 = s2; s1 = s3; s2 = s4; s3 = t0; s4 = t1;
+    };
+    int kt = 0;
+    while (kt < stages - 2) {
+        const int end = min(stages - 2, kt + kScaleStages);
+#pragma unroll 1
+        for (; kt < end; ++kt) stage(integral_constant<int, kLoads>(), kt + 3 == stages ? behind : 0);
+        if (kt % kScaleStages == 0) s.load(kt, stages);
+    }
+    if (stages > 1) {
+        stage(integral_constant<int, kBeforeLast>(), 0);
+        if (++kt % kScaleStages == 0) s.load(kt, stages);
+    }
+    stage(integral_constant<int, kLast>(), 0);
+}
+
+// Waits until at most `stages` stages of LOADS loads are under way.
+template <int LOADS> __device__ inline void wait_stages(int stages) {
+    static_assert(6 * LOADS < 64, "the counter's range");
+    switch (stages) {
+        case 0: wait_loads<0>(); break;
+        case 1: wait_loads<LOADS>(); break;
+        case 2: wait_loads<2 * LOADS>(); break;
+        case 3: wait_loads<3 * LOADS>(); break;
+        case 4: wait_loads<4 * LOADS>(); break;
+        case 5: wait_loads<5 * LOADS>(); break;
+        default: wait_loads<6 * LOADS>();
     }
 }
 
-// The same for smaller tiles: 4 waves, BUFFERS stages of LDS.
-template <int BUFFERS, int TA, int TB, typename OA, typename OB>
+// The same for smaller tiles of 4 waves, two buffers, two workgroups on a compute unit that fill
+// each other's waits.
+template <int TA, int TB, typename OA, typename OB>
 __device__ inline void k_loop8_mid(floatx16 (&acc)[TA][TB], int stages, OA& A, OB& B, int left, uint32_t lds, int wave,
                                    Scales<TA, TB>& s) {
     constexpr uint32_t kStage = OA::kBytes + OB::kBytes;
-    constexpr int kLoads = OA::kLoads + OB::kLoads;
     const uint32_t mine = wave * 1024;
-    uint32_t put = lds, get = lds;
-    auto load = [&](int kt) {
-        load_stage(A, put + mine, left - kt * kHeadK);
-        load_stage(B, put + OA::kBytes + mine, left - kt * kHeadK);
-        put = put == lds + (BUFFERS - 1) * kStage ? lds : put + kStage;
-    };
-    for (int kt = 0; kt < BUFFERS - 1 && kt < stages; ++kt) load(kt);
+    uint32_t now = lds, other = lds + kStage;
+    load_stage(A, now + mine, left);
+    load_stage(B, now + OA::kBytes + mine, left);
     for (int k0 = 0; k0 < stages; k0 += kScaleStages) {
         s.load(k0, stages);
         const int end = min(stages, k0 + kScaleStages);
         for (int kt = k0; kt < end; ++kt) {
-            if (kt + BUFFERS - 2 < stages) wait_loads<(BUFFERS - 2) * kLoads>();
-            else wait_loads<0>();
+            wait_loads<0>();
             wait_lds();
             bare_barrier();      // stage kt is in LDS, and every wave is done with stage kt - 1
-            if (kt + BUFFERS - 1 < stages) load(kt + BUFFERS - 1);
+            if (kt + 1 < stages) {
+                load_stage(A, other + mine, left - (kt + 1) * kHeadK);
+                load_stage(B, other + OA::kBytes + mine, left - (kt + 1) * kHeadK);
+            }
 #pragma unroll
             for (int step = 0; step < 2; ++step) {
                 v8i fa[TA], fb[TB];
-                read8(A, fa, get, step);
-                read8(B, fb, get + OA::kBytes, step);
+                read8(A, fa, now, step);
+                read8(B, fb, now + OA::kBytes, step);
 #pragma unroll
                 for (int i = 0; i < TA; ++i)
 #pragma unroll
                     for (int j = 0; j < TB; ++j) acc[i][j] = mfma8(fa[i], fb[j], acc[i][j], s.b.w[0], s.a[j].w[0]);
             }
             s.advance();
-            get = get == lds + (BUFFERS - 1) * kStage ? lds : get + kStage;
+            const uint32_t t = now;
+            now = other;
+            other = t;
         }
+    }
+}
+
+// The same for still smaller tiles, which are for problems that leave compute units idle: 4
+// waves, BUFFERS stages of LDS.  A wave multiplies a stage from
+// registers while it reads the next one's fragments into others, so that a stage costs its
+// products or one barrier and its issue, whichever is longer, and not the LDS's latency.
+template <int BUFFERS, int TA, int TB, typename OA, typename OB>
+__device__ inline void k_loop8_small(floatx16 (&acc)[TA][TB], int stages, OA& A, OB& B, int left, uint32_t lds, int wave, int lane,
+                                     Scales<TA, TB>& s) {
+    static_assert(BUFFERS % 2 == 0 && kScaleStages % 2 == 0, "stages in pairs");
+    constexpr uint32_t kStage = OA::kBytes + OB::kBytes;
+    constexpr int kLoads = OA::kLoads + OB::kLoads;
+    const int part = left % kHeadK;
+    const uint32_t behind = part && 8 * A.chunk >= part ? 16 * A.chunk : 0;      // as in k_loop8
+    const uint32_t mine = wave * 1024;
+    uint32_t put = lds, get = lds;
+    auto after = [&](uint32_t slot) { return slot == lds + (BUFFERS - 1) * kStage ? lds : slot + kStage; };
+    auto load_all = [&](auto& op, uint32_t dst, uint32_t less) {
+        typedef std::remove_reference_t<decltype(op)> Op;
+        op.template load_before<0>(dst, less);
+        if constexpr (Op::kLoads > 1) op.template load_before<1>(dst, less);
+        if constexpr (Op::kLoads > 2) {
+            op.template load_before<2>(dst, less);
+            op.template load_before<3>(dst, less);
+        }
+        op.advance();
+    };
+    auto load = [&](int kt) {
+        const uint32_t less = kt + 1 == stages ? behind : 0;
+        load_all(A, put + mine, less);
+        load_all(B, put + OA::kBytes + mine, less);
+        put = after(put);
+    };
+    struct Frags {
+        v8i a[2][TA], b[2][TB];
+    };
+    auto read = [&](Frags& f) {
+#pragma unroll
+        for (int step = 0; step < 2; ++step) {
+            read8(A, f.a[step], get, step);
+            read8(B, f.b[step], get + OA::kBytes, step);
+        }
+        get = after(get);
+    };
+    auto mask = [&](Frags& f) {      // of the last stage
+#pragma unroll
+        for (int step = 0; step < 2; ++step)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const bool there = !part || 16 * (2 * step + k) + 8 * (lane / 32) < part;
+#pragma unroll
+                for (int j = 0; j < TB; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) f.b[step][j][4 * k + e] = there ? f.b[step][j][4 * k + e] : 0;
+            }
+    };
+    auto multiply = [&](const Frags& f) {
+#pragma unroll
+        for (int step = 0; step < 2; ++step)
+#pragma unroll
+            for (int i = 0; i < TA; ++i)
+#pragma unroll
+                for (int j = 0; j < TB; ++j) acc[i][j] = mfma8(f.a[step][i], f.b[step][j], acc[i][j], s.b.w[0], s.a[j].w[0]);
+        s.advance();
+    };
+    s.load(0, stages);
+    const int first = min(BUFFERS, stages);
+    for (int kt = 0; kt < first; ++kt) load(kt);
+    wait_stages<kLoads>(first - 1);
+    bare_barrier();
+    Frags f, g;
+    read(f);
+    if (stages == 1) mask(f);
+    // multiplies one stage, reads the next, loads the one BUFFERS on
+    auto stage = [&](Frags& now, Frags& next, int kt) {
+        wait_loads<(BUFFERS - 2) * kLoads>();
+        wait_lds();
+        bare_barrier();      // stage kt + 1 is in LDS, and every wave has read stage kt
+        load(kt + BUFFERS);
+        read(next);
+        multiply(now);
+    };
+    int kt = 0;
+    const int pairs_end = stages - BUFFERS - 1;
+    while (kt < pairs_end) {
+        const int end = min(pairs_end, (kt / kScaleStages + 1) * kScaleStages);
+#pragma unroll 1
+        for (; kt < end; kt += 2) {
+            stage(f, g, kt);
+            stage(g, f, kt + 1);
+        }
+        if (kt % kScaleStages == 0) s.load(kt, stages);
+    }
+    for (; kt < stages; ++kt) {
+        const bool next = kt + 1 < stages;
+        if (next) {
+            wait_stages<kLoads>(min(BUFFERS - 2, stages - 2 - kt));
+            wait_lds();
+            bare_barrier();
+            if (kt + BUFFERS < stages) load(kt + BUFFERS);
+            read(g);
+            if (kt + 2 == stages) mask(g);
+        }
+        multiply(f);
+        if (next && (kt + 1) % kScaleStages == 0) s.load(kt + 1, stages);
+        f = g;
     }
 }
 
@@ -236,6 +417,31 @@ __device__ inline void store_tile(const Matmul8& a, floatx16 (&acc)[TV][TT], int
     }
 }
 
+// The same as float32 sums of a part of K, straight from the registers.
+template <int TV, int TT>
+__device__ inline void store_partial(const Matmul8& a, floatx16 (&acc)[TV][TT], int split, int v0, int t0, int lane) {
+#pragma unroll
+    for (int tt = 0; tt < TT; ++tt) {
+        const int row = t0 + 32 * tt + lane % 32;
+        if (row >= a.rows) continue;
+#pragma unroll
+        for (int tv = 0; tv < TV; ++tv)
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                const int v = v0 + 32 * tv + 16 * p + 8 * (lane / 32);
+                if (v >= a.cols) continue;
+                floatx4* dst = reinterpret_cast<floatx4*>(a.partial + ((int64_t)split * a.rows + row) * a.partial_pitch + v);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    floatx4 x;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x[e] = acc[tv][tt][8 * p + 4 * h + e];
+                    dst[h] = x;
+                }
+            }
+    }
+}
+
 // Row tiles in groups of 8, column tiles within: the tiles that an XCD works on at a
 // time form a block, which shares operands in its L2.
 __device__ inline void tile_of(const Matmul8& a, int item, int& tile_v, int& tile_t) {
@@ -260,75 +466,233 @@ __global__ __launch_bounds__(512, 2) void matmul8_kernel(const Matmul8 a) {
     B.init(a.b.codes, a.b.stride, (int64_t)tile_v * kHeadTile, a.cols, 0, wv * TV * 32 + swap23(lane % 32), wave, lane);
     A.init(a.a.codes, a.a.stride, (int64_t)tile_t * kHeadTile, a.rows, 0, wt * TT * 32 + lane % 32, wave, lane);
     Scales<TV, TT> s;
-    s.init(a, v0, t0, lane);
+    s.init(a, v0, t0, 0, lane);
     floatx16 acc[TV][TT];
     clear(acc);
-    k_loop8<TV, TT>(acc, (a.dim + kBlock8 - 1) / kBlock8, B, A, (a.dim + 15) / 16 * 8, lds_address(lds), wave, s);
+    k_loop8<TV, TT>(acc, (a.dim + kBlock8 - 1) / kBlock8, B, A, (a.dim + 15) / 16 * 8, lds_address(lds), wave, lane, s);
     bare_barrier();      // every wave is done with the operands, whose slots y passes through
     store_tile<T, TV, TT>(a, acc, v0, t0, lane, lds + wave * kStageBytes<TV>);
 }
 
-// 128 x 128, 4 waves of 64 x 64, two workgroups per compute unit.
-constexpr int kMid = 128;
-constexpr size_t kMidBytes = (size_t)2 * 2 * kMid * kBlock8;
+// 32 WV TV columns x 32 WT TT rows by 4 waves, BUFFERS stages, two workgroups per compute
+// unit; K in a.splits parts, whose sums matmul8_join adds.
+template <int WV, int WT, int TV, int TT, int BUFFERS> struct SmallTile {
+    static constexpr int kCols = 32 * WV * TV, kRows = 32 * WT * TT;
+    static constexpr size_t kBytes = (size_t)BUFFERS * (kCols + kRows) * kBlock8;
+    static_assert(WV * WT == 4 && kBlock8 % (32 * TV) == 0 && kStageBytes<TV> * 4 <= (int)kBytes, "tile");
+};
+template <typename T, int WV, int WT, int TV, int TT, int BUFFERS>
+__global__ __launch_bounds__(256, 2) void matmul8_small_kernel(const Matmul8 a) {
+    typedef SmallTile<WV, WT, TV, TT, BUFFERS> S;
+    extern __shared__ __align__(16) uint8_t lds[];
+    const int tiles = a.tiles_v * a.tiles_t, item = xcd_item(tiles * a.splits);
+    if (item < 0) return;
+    int tile_v, tile_t;
+    const int split = item / tiles;
+    tile_of(a, item - split * tiles, tile_v, tile_t);
+    const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), wv = wave / WT, wt = wave % WT;
+    const int v0 = tile_v * S::kCols + wv * TV * 32, t0 = tile_t * S::kRows + wt * TT * 32;
+    const int all = (a.dim + kBlock8 - 1) / kBlock8, s0 = split * a.stages_per_split, stages = min(all - s0, a.stages_per_split);
+    RowOperand<S::kCols, 4> B;
+    RowOperand<S::kRows, 4> A;
+    B.init(a.b.codes, a.b.stride, (int64_t)tile_v * S::kCols, a.cols, s0 * kHeadK, wv * TV * 32 + swap23(lane % 32), wave, lane);
+    A.init(a.a.codes, a.a.stride, (int64_t)tile_t * S::kRows, a.rows, s0 * kHeadK, wt * TT * 32 + lane % 32, wave, lane);
+    Scales<TV, TT> s;
+    s.init(a, v0, t0, s0, lane);
+    floatx16 acc[TV][TT];
+    clear(acc);
+    const int left = min((a.dim + 15) / 16 * 8 - s0 * kHeadK, stages * kHeadK);
+    if constexpr (BUFFERS == 2) k_loop8_mid(acc, stages, B, A, left, lds_address(lds), wave, s);
+    else k_loop8_small<BUFFERS>(acc, stages, B, A, left, lds_address(lds), wave, lane, s);
+    if (a.partial) {
+        store_partial<TV, TT>(a, acc, split, v0, t0, lane);
+        return;
+    }
+    bare_barrier();
+    store_tile<T, TV, TT>(a, acc, v0, t0, lane, lds + wave * kStageBytes<TV>);
+}
+
+// The sums of the parts of K in order, rounded once.
 template <typename T>
-__global__ __launch_bounds__(256, 2) void matmul8_mid_kernel(const Matmul8 a) {
-    constexpr int WV = 2, WT = 2, TV = 2, TT = 2, NW = WV * WT;
-    static_assert(kStageBytes<TV> * NW <= (int)kMidBytes, "tile");
+__global__ __launch_bounds__(256) void matmul8_join_kernel(const Matmul8 a) {
+    const int64_t octs = (a.cols + 7) / 8, items = octs * a.rows;
+    for (int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x; n < items; n += (int64_t)gridDim.x * 256) {
+        const int64_t row = n / octs;
+        const int v = (int)(n - row * octs) * 8;
+        floatx4 lo = {0.f, 0.f, 0.f, 0.f}, hi = lo;
+        const float* src = a.partial + row * a.partial_pitch + v;
+        for (int s = 0; s < a.splits; ++s, src += (int64_t)a.rows * a.partial_pitch) {
+            lo += reinterpret_cast<const floatx4*>(src)[0];
+            hi += reinterpret_cast<const floatx4*>(src)[1];
+        }
+        const float sums[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+        T* dst = static_cast<T*>(a.y) + row * a.y_stride + v;
+        if (a.y_vec && v + 8 <= a.cols) {
+            *reinterpret_cast<u32x4*>(dst) = pack8<T>(sums);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (v + e < a.cols) dst[e] = (T)sums[e];
+        }
+    }
+}
+
+// Few rows or few tiles: K is split over the waves of a workgroup, which meet in LDS; operands
+// straight from memory, the next stage's under way while one is multiplied.
+//
+// Up to 16 rows: 16 columns of y a workgroup, 16x16x128 products, each row of b used once.
+template <typename T, int NW>
+__global__ __launch_bounds__(NW * kWave) void matmul8_rows_kernel(const Matmul8 a) {
+    constexpr int kEdge = 16;
+    __shared__ float part[NW][kEdge][kEdge + 1];
+    const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int v0 = blockIdx.x * kEdge;
+    const int v = min(v0 + lane % 16, a.cols - 1), t = min(lane % 16, a.rows - 1);
+    const uint8_t* b = a.b.codes + (int64_t)v * a.b.stride + 32 * (lane / 16);
+    const uint8_t* x = a.a.codes + (int64_t)t * a.a.stride + 32 * (lane / 16);
+    const uint8_t* sb = a.b.scale + (int64_t)(v / kBlock8) * a.b.scale_stride;
+    const uint8_t* sa = a.a.scale + (int64_t)t * a.a.scale_stride;
+    const int stages = (a.dim + kBlock8 - 1) / kBlock8, end = (a.dim + 15) / 16 * 16 - 32 * (lane / 16);
+    floatx4 acc = {0.f, 0.f, 0.f, 0.f};
+    struct Stage {
+        u32x4 b[2], x[2];
+        int sb, sa;
+    };
+    auto load = [&](Stage& s, int kt) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int k = kt * kBlock8 + 16 * h;
+            s.b[h] = s.x[h] = u32x4{0u, 0u, 0u, 0u};
+            if (k < end) {
+                s.b[h] = *reinterpret_cast<const u32x4*>(b + k);
+                s.x[h] = *reinterpret_cast<const u32x4*>(x + k);
+            }
+        }
+        s.sb = sb[kt];
+        s.sa = sa[kt];
+    };
+    auto multiply = [&](const Stage& s) {
+        acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(join(s.b[0], s.b[1]), join(s.x[0], s.x[1]), acc, 0, 0, 0, s.sb, 0, s.sa);
+    };
+    constexpr int kAhead = 4;        // stages under way together
+    for (int kt = wave; kt < stages; kt += kAhead * NW) {
+        Stage s[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+            if (kt + k * NW < stages) load(s[k], kt + k * NW);
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+            if (kt + k * NW < stages) multiply(s[k]);
+    }
+    // register e of lane l: column 4 (l / 16) + e, row l % 16
+#pragma unroll
+    for (int e = 0; e < 4; ++e) part[wave][lane % 16][4 * (lane / 16) + e] = acc[e];
+    __syncthreads();
+    for (int i = threadIdx.x; i < kEdge * kEdge; i += NW * kWave) {
+        const int c = i % kEdge, r = i / kEdge;
+        float sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) sum += part[w][r][c];
+        if (v0 + c < a.cols && r < a.rows) static_cast<T*>(a.y)[(int64_t)r * a.y_stride + v0 + c] = (T)sum;
+    }
+}
+
+// Otherwise 32 TV columns x 32 TT rows a workgroup.
+template <int TV, int TT, int NW> constexpr size_t kSplitBytes = (size_t)NW * TV * TT * 16 * kWave * 4;
+template <typename T, int TV, int TT, int NW>
+__global__ __launch_bounds__(NW * kWave) void matmul8_split_kernel(const Matmul8 a) {
     extern __shared__ __align__(16) uint8_t lds[];
     const int item = xcd_item(a.tiles_v * a.tiles_t);
     if (item < 0) return;
     int tile_v, tile_t;
     tile_of(a, item, tile_v, tile_t);
-    const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), wv = wave / WT, wt = wave % WT;
-    const int v0 = tile_v * kMid + wv * TV * 32, t0 = tile_t * kMid + wt * TT * 32;
-    RowOperand<kMid, NW> B, A;
-    B.init(a.b.codes, a.b.stride, (int64_t)tile_v * kMid, a.cols, 0, wv * TV * 32 + swap23(lane % 32), wave, lane);
-    A.init(a.a.codes, a.a.stride, (int64_t)tile_t * kMid, a.rows, 0, wt * TT * 32 + lane % 32, wave, lane);
-    Scales<TV, TT> s;
-    s.init(a, v0, t0, lane);
+    const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), half = lane / 32;
+    const int v0 = tile_v * 32 * TV, t0 = tile_t * 32 * TT;
+    const int stages = (a.dim + kBlock8 - 1) / kBlock8, end = (a.dim + 15) / 16 * 16 - 16 * half;
+    const uint8_t* code[TV + TT];
+    const uint8_t* scale[1 + TT];        // the columns of a tile share a block
+    static_assert(kBlock8 % (32 * TV) == 0, "one block of weights");
+#pragma unroll
+    for (int i = 0; i < TV; ++i) code[i] = a.b.codes + (int64_t)min(v0 + 32 * i + swap23(lane % 32), a.cols - 1) * a.b.stride + 16 * half;
+    scale[0] = a.b.scale + (int64_t)(v0 / kBlock8) * a.b.scale_stride;
+#pragma unroll
+    for (int j = 0; j < TT; ++j) {
+        const int64_t t = min(t0 + 32 * j + lane % 32, a.rows - 1);
+        code[TV + j] = a.a.codes + t * a.a.stride + 16 * half;
+        scale[1 + j] = a.a.scale + t * a.a.scale_stride;
+    }
+    struct Stage {
+        u32x4 w[TV + TT][4];
+        int s[1 + TT];
+    };
     floatx16 acc[TV][TT];
     clear(acc);
-    k_loop8_mid<2>(acc, (a.dim + kBlock8 - 1) / kBlock8, B, A, (a.dim + 15) / 16 * 8, lds_address(lds), wave, s);
-    bare_barrier();
-    store_tile<T, TV, TT>(a, acc, v0, t0, lane, lds + wave * kStageBytes<TV>);
-}
-
-// Up to 16 rows: a workgroup for every 16 columns of y, operands straight from memory
-// (each row of b is used once), the waves take K in turn, 128 at a time, and meet in LDS.
-constexpr int kStreamRows = 16, kStreamCols = 16;
-template <typename T, int NW>
-__global__ __launch_bounds__(NW * kWave) void matmul8_stream_kernel(const Matmul8 a) {
-    __shared__ float part[NW][kStreamCols][kStreamRows];
-    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
-    const int v0 = blockIdx.x * kStreamCols, t0 = blockIdx.y * kStreamRows;
-    const int v = min(v0 + lane % 16, a.cols - 1), t = min(t0 + lane % 16, a.rows - 1);
-    const uint8_t* b = a.b.codes + (int64_t)v * a.b.stride;
-    const uint8_t* x = a.a.codes + (int64_t)t * a.a.stride;
-    const uint8_t* sb = a.b.scale + (int64_t)(v / kBlock8) * a.b.scale_stride;
-    const uint8_t* sa = a.a.scale + (int64_t)t * a.a.scale_stride;
-    const int stages = (a.dim + kBlock8 - 1) / kBlock8, dim16 = (a.dim + 15) / 16 * 16;
-    floatx4 acc = {0.f, 0.f, 0.f, 0.f};
-    auto get = [&](const uint8_t* p, int k) -> u32x4 {
-        u32x4 w = {0u, 0u, 0u, 0u};
-        if (k < dim16) w = *reinterpret_cast<const u32x4*>(p + k);
-        return w;
+    auto load = [&](Stage& s, int kt) {
+#pragma unroll
+        for (int i = 0; i < TV + TT; ++i)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const int k = kt * kBlock8 + 32 * c;
+                s.w[i][c] = u32x4{0u, 0u, 0u, 0u};
+                if (k < end) s.w[i][c] = *reinterpret_cast<const u32x4*>(code[i] + k);
+            }
+#pragma unroll
+        for (int i = 0; i < 1 + TT; ++i) s.s[i] = scale[i][kt];
     };
-    for (int kt = wave; kt < stages; kt += NW) {
-        const int k = kt * kBlock8 + 32 * (lane / 16);
-        const v8i fb = join(get(b, k), get(b, k + 16)), fx = join(get(x, k), get(x, k + 16));
-        acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fb, fx, acc, 0, 0, 0, sb[kt], 0, sa[kt]);
+    auto multiply = [&](const Stage& s) {
+#pragma unroll
+        for (int step = 0; step < 2; ++step)
+#pragma unroll
+            for (int i = 0; i < TV; ++i)
+#pragma unroll
+                for (int j = 0; j < TT; ++j)
+                    acc[i][j] = mfma8(join(s.w[i][2 * step], s.w[i][2 * step + 1]), join(s.w[TV + j][2 * step], s.w[TV + j][2 * step + 1]),
+                                      acc[i][j], s.s[0], s.s[1 + j]);
+    };
+    Stage now, next;
+    if (wave < stages) load(now, wave);
+    for (int kt = wave; kt < stages; kt += 2 * NW) {
+        if (kt + NW < stages) load(next, kt + NW);
+        multiply(now);
+        if (kt + 2 * NW < stages) load(now, kt + 2 * NW);
+        if (kt + NW < stages) multiply(next);
     }
-    // register e of lane l: column 4 (l / 16) + e, row l % 16
+    // 8 consecutive columns of a row: unit (tv, tt, p, lane) holds column 32 tv + 16 p + 8 (l / 32) of row 32 tt + l % 32
+    constexpr int kUnits = TV * TT * 2 * kWave;
+    floatx4* part = reinterpret_cast<floatx4*>(lds);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) part[wave][4 * (lane / 16) + e][lane % 16] = acc[e];
+    for (int i = 0; i < TV; ++i)
+#pragma unroll
+        for (int j = 0; j < TT; ++j)
+#pragma unroll
+            for (int p = 0; p < 2; ++p)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    floatx4 v;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[e] = acc[i][j][8 * p + 4 * h + e];
+                    part[((wave * 2 + h) * TV * TT * 2 + (i * TT + j) * 2 + p) * kWave + lane] = v;
+                }
     __syncthreads();
-    for (int i = threadIdx.x; i < kStreamCols * kStreamRows; i += NW * kWave) {
-        const int c = i % kStreamCols, r = i / kStreamCols;
-        float sum = 0.f;
+    for (int u = threadIdx.x; u < kUnits; u += NW * kWave) {
+        floatx4 lo = part[u], hi = part[kUnits + u];
 #pragma unroll
-        for (int w = 0; w < NW; ++w) sum += part[w][c][r];
-        if (v0 + c < a.cols && t0 + r < a.rows) static_cast<T*>(a.y)[(int64_t)(t0 + r) * a.y_stride + v0 + c] = (T)sum;
+        for (int w = 1; w < NW; ++w) {
+            lo += part[2 * w * kUnits + u];
+            hi += part[(2 * w + 1) * kUnits + u];
+        }
+        const int l = u % kWave, p = u / kWave % 2, ij = u / (2 * kWave);
+        const int row = t0 + 32 * (ij % TT) + l % 32, v = v0 + 32 * (ij / TT) + 16 * p + 8 * (l / 32);
+        if (row >= a.rows || v >= a.cols) continue;
+        T* dst = static_cast<T*>(a.y) + (int64_t)row * a.y_stride + v;
+        const float sums[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+        if (a.y_vec && v + 8 <= a.cols) {
+            *reinterpret_cast<u32x4*>(dst) = pack8<T>(sums);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (v + e < a.cols) dst[e] = (T)sums[e];
+        }
     }
 }
 
@@ -337,28 +701,48 @@ hipError_t allow_lds(K kernel, size_t bytes) {
     return hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
 }
 
+template <typename T, int TV, int TT, int NW>
+hipError_t split_launch(const Matmul8& a, hipStream_t s) {
+    constexpr size_t bytes = kSplitBytes<TV, TT, NW>;
+    const hipError_t allowed = allow_lds(&matmul8_split_kernel<T, TV, TT, NW>, bytes);
+    if (allowed != hipSuccess) return allowed;
+    matmul8_split_kernel<T, TV, TT, NW><<<xcd_grid(a.tiles_v * a.tiles_t), NW * kWave, bytes, s>>>(a);
+    return hipGetLastError();
+}
+
+template <typename T, int WV, int WT, int TV, int TT, int BUFFERS>
+hipError_t small_launch(const Matmul8& a, hipStream_t s) {
+    constexpr size_t bytes = SmallTile<WV, WT, TV, TT, BUFFERS>::kBytes;
+    const hipError_t allowed = allow_lds(&matmul8_small_kernel<T, WV, WT, TV, TT, BUFFERS>, bytes);
+    if (allowed != hipSuccess) return allowed;
+    matmul8_small_kernel<T, WV, WT, TV, TT, BUFFERS><<<xcd_grid(a.tiles_v * a.tiles_t * a.splits), 256, bytes, s>>>(a);
+    return hipGetLastError();
+}
+
 template <typename T>
 hipError_t typed(const Matmul8& a, int variant, hipStream_t s) {
-    if (variant == kMatmulStream) {
-        const dim3 grid((a.cols + kStreamCols - 1) / kStreamCols, (a.rows + kStreamRows - 1) / kStreamRows);
-        matmul8_stream_kernel<T, 4><<<grid, 4 * kWave, 0, s>>>(a);
-        return hipGetLastError();
-    }
     const int grid = xcd_grid(a.tiles_v * a.tiles_t);
-    if (variant == kMatmulMid) {
-        const hipError_t allowed = allow_lds(&matmul8_mid_kernel<T>, kMidBytes);
+    if (variant == kMatmulRows) matmul8_rows_kernel<T, 8><<<a.tiles_v, 8 * kWave, 0, s>>>(a);
+    else if (variant == kMatmulSplit) return split_launch<T, 1, 1, 8>(a, s);
+    else if (variant == kMatmulSmall) return small_launch<T, 2, 2, 1, 1, 4>(a, s);
+    else if (variant == kMatmulMid) return small_launch<T, 2, 2, 2, 2, 2>(a, s);
+    else {
+        const hipError_t allowed = allow_lds(&matmul8_kernel<T>, kRingBytes);
         if (allowed != hipSuccess) return allowed;
-        matmul8_mid_kernel<T><<<grid, 256, kMidBytes, s>>>(a);
-        return hipGetLastError();
+        matmul8_kernel<T><<<grid, 512, kRingBytes, s>>>(a);
     }
-    const hipError_t allowed = allow_lds(&matmul8_kernel<T>, kRingBytes);
-    if (allowed != hipSuccess) return allowed;
-    matmul8_kernel<T><<<grid, 512, kRingBytes, s>>>(a);
     return hipGetLastError();
 }
 
 }  // namespace
 
+hipError_t launch_matmul8_join(const Matmul8& a, int type, hipStream_t s) {
+    const int64_t items = (int64_t)a.rows * ((a.cols + 7) / 8);
+    const int grid = (int)std::min<int64_t>(8192, (items + 255) / 256);
+    if (type == kTypeBf16) matmul8_join_kernel<bf16><<<grid, 256, 0, s>>>(a);
+    else matmul8_join_kernel<f16><<<grid, 256, 0, s>>>(a);
+    return hipGetLastError();
+}
 hipError_t launch_matmul8(const Matmul8& a, int type, int variant, hipStream_t s) {
     return type == kTypeBf16 ? typed<bf16>(a, variant, s) : typed<f16>(a, variant, s);
 }

@@ -121,6 +121,10 @@ struct RowOperand {
     }
     // load J of the next stage to the slot at `dst` (with the wave's 1024 bytes in it)
     template <int J> __device__ inline void load(uint32_t dst) const { direct_load<J * WAVES * 1024>(next, off[J], dst); }
+    // the same `less` bytes before
+    template <int J> __device__ inline void load_before(uint32_t dst, uint32_t less) const {
+        direct_load<J * WAVES * 1024>(next, off[J] - less, dst);
+    }
     // the same where K ends `left` elements (a multiple of 8) on: zeros behind it
     template <int J> __device__ inline void load_tail(uint32_t dst, int left) const {
         direct_load_from<J * WAVES * 1024>(8 * chunk < left ? next + off[J] : kZeros, dst);
@@ -185,9 +189,9 @@ struct ColOperand {
     template <int J> __device__ inline void load_tail(uint32_t dst, int left) const {
         direct_load<J * WAVES * 1024>(next, (uint32_t)(min(row[J], left - 1) * (int64_t)pitch) + chunk[J], dst);
     }
-    // where rows beyond count as zero, whatever the last one holds
-    template <int J> __device__ inline void load_zeros(uint32_t dst, int left) const {
-        direct_load_from<J * WAVES * 1024>(row[J] < left ? next + off[J] : kZeros, dst);
+    // the same with a row's offset from 24 bits (pitch below 2^24)
+    template <int J> __device__ inline void load_clamped(uint32_t dst, int last) const {
+        direct_load<J * WAVES * 1024>(next, __umul24(min(row[J], last), pitch) + chunk[J], dst);
     }
     __device__ inline void advance() { next += step; }
     // fragment I (32 columns): lane l holds K 16 kc + 8 (l / 32) .. + 7 of its column
