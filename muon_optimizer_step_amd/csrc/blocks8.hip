@@ -124,16 +124,55 @@ template <typename T> __device__ inline void store8(T* p, const Raw<T>& r, int l
 }
 
 // ---------------------------------------------------------------- activation functions
-// gelu's F(u) = erfc(-u / sqrt 2) / 2 keeps its digits where F is small.
-constexpr float kHalfRoot = 0.70710678118654752440f, kInvRoot2Pi = 0.39894228040143267794f;
+// exp(x) for x <= 0 to a few ulp, subnormal results included (which the instruction itself flushes):
+// in base 2, with what the product with log2 e loses.
+constexpr float kLog2e = 1.44269504088896340736f, kLog2eLow = 1.92596299e-8f, kLn2 = 0.69314718055994530942f;
+__device__ inline float exp_of(float x) {
+#pragma clang fp contract(off)      // t is one rounded value in both places
+    const float t = x * kLog2e, rest = fmaf(x, kLog2eLow, fmaf(x, kLog2e, -t));
+    const bool low = t < -64.f;
+    return __builtin_amdgcn_exp2f(t + (low ? 64.f : 0.f)) * fmaf(rest, kLn2, 1.f) * (low ? 0x1p-64f : 1.f);
+}
+// silu's s = 1 / (1 + exp(-u)) and 1 - s, from exp(-|u|): no overflow, and digits where either is small.
+struct Sigmoid {
+    float s, rest;
+};
+__device__ inline Sigmoid sigmoid(float u) {
+    const float e = exp_of(-fabsf(u)), r = __builtin_amdgcn_rcpf(1.f + e);
+    return u < 0.f ? Sigmoid{e * r, r} : Sigmoid{r, e * r};
+}
+// gelu's F(u) = erfc(-u / sqrt 2) / 2 and exp(-u^2 / 2).  erfc(z) = exp(-z^2) t P(t), t = 1 / (1 + p z) for z >= 0 (the form
+// of Abramowitz and Stegun 7.1.26), p and the eight degrees of P fitted to exp(z^2) erfc(z) for z up to
+// 13.5 (minimax, 3.6e-8 of it; 3.4e-7 in float32): F keeps its digits where it is small, and shares the
+// exponential with the derivative.  Beyond |u| = 20 the exponential is zero.
+struct Gelu {
+    float f, e;
+};
+__device__ inline Gelu gelu_parts(float u) {
+    const float a = fminf(fabsf(u), 20.f), sq = a * a;
+    const float e = exp_of(-0.5f * sq) * fmaf(-0.5f, fmaf(a, a, -sq), 1.f);
+    const float t = __builtin_amdgcn_rcpf(fmaf(0.70710678118654752440f * 0.4965279f, a, 1.f));
+    float q = -0.058656517f;
+    q = fmaf(q, t, 0.28751397f);
+    q = fmaf(q, t, -0.50514156f);
+    q = fmaf(q, t, 0.30710346f);
+    q = fmaf(q, t, -0.040894862f);
+    q = fmaf(q, t, 0.20874296f);
+    q = fmaf(q, t, 0.24065824f);
+    q = fmaf(q, t, 0.28055322f);
+    q = fmaf(q, t, 0.28012112f);
+    const float tail = 0.5f * e * (q * t);
+    return {u < 0.f ? tail : 1.f - tail, e};
+}
+constexpr float kInvRoot2Pi = 0.39894228040143267794f;
 __device__ inline float positive(float u) { return u <= 0.f ? 0.f : u; }     // NaN stays
 template <int ACT> __device__ inline float act(float u) {
     if (ACT == kActRelu2) {
         const float t = positive(u);
         return t * t;
     }
-    if (ACT == kActSilu) return u / (1.f + expf(-u));
-    if (ACT == kActGelu) return u * (0.5f * erfcf(-kHalfRoot * u));
+    if (ACT == kActSilu) return u * sigmoid(u).s;
+    if (ACT == kActGelu) return u * gelu_parts(u).f;
     return u;
 }
 template <int ACT> __device__ inline float act_slope(float u) {
@@ -142,10 +181,11 @@ template <int ACT> __device__ inline float act_slope(float u) {
         return t + t;
     }
     if (ACT == kActSilu) {
-        const float s = 1.f / (1.f + expf(-u));
-        return s * fmaf(u, 1.f - s, 1.f);
+        const Sigmoid g = sigmoid(u);
+        return g.s * fmaf(u, g.rest, 1.f);
     }
-    return fmaf(u * kInvRoot2Pi, expf(-0.5f * u * u), 0.5f * erfcf(-kHalfRoot * u));
+    const Gelu g = gelu_parts(u);
+    return fmaf(u * kInvRoot2Pi, g.e, g.f);
 }
 
 // ---------------------------------------------------------------- rows

@@ -78,8 +78,10 @@ class _Coded:
         torch = _torch()
         if rows < 0 or dim < 1:
             raise ValueError(f"rows = {rows}, dim = {dim}: rows >= 0, dim >= 1")
+        # rows of whole cache lines, where that adds little: products read 128 bytes of a row at a time
+        width = _up(dim, 128) if dim > 512 else _up(dim, 16)
         with torch.cuda.stream(stream):
-            codes = torch.empty(rows, _up(dim, 16), dtype=torch.uint8, device=device).view(torch.float8_e4m3fn)
+            codes = torch.empty(rows, width, dtype=torch.uint8, device=device).view(torch.float8_e4m3fn)[:, :_up(dim, 16)]
             scale = torch.empty(-(-rows // cls._TALL), _up(_blocks(dim), 4), dtype=torch.uint8, device=device)
         return cls(codes, scale, dim)
 
@@ -93,7 +95,9 @@ class _Coded:
 
     def unpadded(self):
         """(codes [rows, dim], scales' bytes): views without the rows' padding."""
-        return self.codes[:, :self.dim], self.scale[:, :_blocks(self.dim)]
+        codes, scale, blocks = self.codes, self.scale, _blocks(self.dim)
+        return (codes if codes.shape[1] == self.dim else codes[:, :self.dim],
+                scale if scale.shape[1] == blocks else scale[:, :blocks])
 
     def decode(self, dtype=None, stream=None):
         """The values, rows x dim of dtype (bfloat16 by default, which holds them exactly)."""
@@ -132,7 +136,8 @@ class Activation8(_Coded):
 class Weight8(_Coded):
     """A weight matrix in 8 bits: as Activation8, with one scale for each 128 x 128 values.
 
-    T: the transpose in the same form, if there is one (what the gradient of a layer's input is multiplied with).
+    T: the transpose in the same form, if there is one (what the gradient of a layer's input is multiplied with); it has no
+    T of its own.
     """
 
     __slots__ = ("_turned",)
@@ -148,7 +153,7 @@ class Weight8(_Coded):
     def T(self) -> "Weight8":
         if self._turned is None:
             raise ValueError("this Weight8 has no transpose: encode it with transposed=True")
-        return Weight8(self._turned.codes, self._turned.scale, self._turned.dim, transposed=Weight8(self.codes, self.scale, self.dim))
+        return self._turned
 
     def _tensors(self):
         return super()._tensors() + (self._turned._tensors() if self._turned is not None else [])

@@ -181,7 +181,6 @@ def test_weight_encode(rows, dim, dtype):
     w8 = ms.weight8_encode(w.cuda())
     _same_codes(w8, want, "weight")
     _same_codes(w8.T, (want[0].T, want[1].T), "transposed")
-    _same_codes(w8.T.T, want, "twice")
     alone = ms.weight8_encode(w.cuda(), transposed=False)
     _same_codes(alone, want, "alone")
     with pytest.raises(ValueError, match="transpose"):
@@ -217,6 +216,36 @@ def test_backward(kind, rows, dim, dtype):
     assert only.grad is None
     for a, b in zip(only.grad8.unpadded(), r.grad8.unpadded()):
         assert np.array_equal(_codes(a), _codes(b))
+
+
+@pytest.mark.parametrize("kind", ["relu2", "silu", "gelu"])
+def test_activations_over_their_whole_range(kind):
+    """Every e4m3 value times 2^-12 .. 2^12, zero, NaN and the far ends among them, against the formulas."""
+    import torch
+    import muon_optimizer_step_amd as ms
+    table = np.concatenate([ol.code_values().astype(np.float64)[:127], -ol.code_values().astype(np.float64)[:127]])
+    x = np.zeros((25, 256), dtype=np.float32)
+    for i, p in enumerate(range(-12, 13)):
+        x[i, :127], x[i, 128:255] = np.ldexp(table[:127], p), np.ldexp(table[127:], p)
+        x[i, 127], x[i, 255] = np.ldexp(448.0, p), -np.ldexp(448.0, p)
+    u8 = ms.act8_encode(torch.from_numpy(x).cuda()).checkpoint
+    u = _f64(u8.decode(torch.float32))
+    assert np.array_equal(u, x.astype(np.float64))
+    with np.errstate(all="ignore"):
+        s, terms = ol.slope(u, kind)
+        y = ol.act(u, kind)
+    got = _f64(ms.act8_backward(u8, torch.ones(25, 256, device="cuda"), kind).grad)
+    assert (np.abs(got - s) <= 2.0 ** -20 * terms + 1e-37).all()
+    r = ms.act8_encode(torch.from_numpy(x).cuda(), activation=kind, checkpoint=False).out
+    codes, byte = (_codes(t) for t in r.unpadded())
+    scale = np.repeat(2.0 ** (byte.astype(np.float64) - 127), 128, axis=1)
+    assert (np.abs(byte.astype(int) - ol.scales(y)) <= 1).all()
+    assert (np.abs(ol.decode(codes, byte) - y) <= (2.0 ** -4 + 2.0 ** -18) * np.abs(y) + (2.0 ** -10 + 2.0 ** -18) * scale).all()
+    nan = torch.full((1, 128), float("nan"), device="cuda")
+    bad = ms.act8_encode(nan, activation=kind)
+    for q in bad:
+        assert ((_codes(q.codes) & 0x7F) == 0x7F).all()
+    assert torch.isnan(ms.act8_backward(bad.checkpoint, torch.ones(1, 128, device="cuda"), kind).grad).all()
 
 
 @pytest.mark.parametrize("kind", ["relu2", "silu", "gelu"])
