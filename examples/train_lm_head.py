@@ -4,13 +4,14 @@
 
 * the head's loss and its gradients: PreparedLinearCrossEntropy (the logits are never kept);
 * the body's gradients: torch autograd, started from the loss's grad_hidden;
-* W, a hidden matrix: PreparedMuonStep;
+* W, a hidden matrix: PreparedMuonStep; with --linear8 its layer runs in 8 bits (Linear8 below): the layer's input is kept as
+  its 8-bit codes alone, and W's gradient is computed from them;
 * the embedding, the head and the gain: one PreparedAdamW8 call, with 8-bit states for the two matrices and 32-bit
   ones for the gain; it also writes the bfloat16 copies that the next forward pass reads.
 
 The data is a synthetic Markov chain in which each token has four successors, so the loss can fall to log 4 = 1.39.
 
-    python examples/train_lm_head.py [--vocab 4096] [--dim 512] [--tokens 16384] [--steps 100]
+    python examples/train_lm_head.py [--vocab 4096] [--dim 512] [--tokens 16384] [--steps 100] [--linear8]
 """
 
 from __future__ import annotations
@@ -29,7 +30,28 @@ import muon_optimizer_step_amd as ms  # noqa: E402
 COEFFS = [(3.4445, -4.7750, 2.0315)] * 5
 
 
-def train(vocab=4096, dim=512, tokens=16384, steps=100, seed=0, masked=0.1, log=None):
+class Linear8(torch.autograd.Function):
+    """x W^T with both in 8 bits, and its backward pass.
+
+    What is kept of x is its 8-bit form.  The gradient of x is a product in 8 bits too, that of W one of the 16-bit
+    gradient with the 8-bit x, written in float32 where Muon reads it (so autograd gets none).
+    """
+
+    @staticmethod
+    def forward(ctx, x, w8, w_grad):
+        x8 = ms.act8_encode(x).checkpoint
+        ctx.saved = x8, w8, w_grad
+        return ms.matmul8(x8, w8)
+
+    @staticmethod
+    def backward(ctx, dy):
+        x8, w8, w_grad = ctx.saved
+        dy = dy.bfloat16().contiguous()
+        ms.act8_grad_weight(x8, dy, out=w_grad)
+        return ms.matmul8(ms.act8_encode(dy).checkpoint, w8.T), None, None
+
+
+def train(vocab=4096, dim=512, tokens=16384, steps=100, seed=0, masked=0.1, linear8=False, log=None):
     """Runs `steps` steps; returns the losses."""
     g = torch.Generator(device="cuda").manual_seed(seed)
     randn = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
@@ -51,6 +73,7 @@ def train(vocab=4096, dim=512, tokens=16384, steps=100, seed=0, masked=0.1, log=
     adamw = ms.PreparedAdamW8([emb, head, gain.detach()], grads, states, copies=[emb16.detach(), head16, None])
     w_grad, momentum = torch.empty_like(w), torch.zeros(dim, dim, device="cuda")
     muon = ms.PreparedMuonStep([w.detach()], [w_grad], [momentum])
+    encode_w = ms.PreparedWeight8Encode(w.detach()) if linear8 else None      # again after each update
 
     losses = []
     for step in range(1, steps + 1):
@@ -60,12 +83,12 @@ def train(vocab=4096, dim=512, tokens=16384, steps=100, seed=0, masked=0.1, log=
         targets[torch.rand(tokens, generator=g, device="cuda") < masked] = -100     # tokens that are not learned from
 
         h = torch.nn.functional.embedding(x, emb16).float()
-        h = h + torch.tanh(h @ w.T)
+        h = h + torch.tanh(Linear8.apply(h, encode_w(), w_grad).float() if linear8 else h @ w.T)
         out = (h * torch.rsqrt(h.square().mean(1, keepdim=True) + 1e-6) * gain).bfloat16()
         hidden.copy_(out.detach())
         r = loss()                                          # loss, grad_hidden, grad_weight of the head
-        d_emb, d_w, d_gain = torch.autograd.grad(out, (emb16, w, gain), r.grad_hidden)
-        for dst, src in ((grads[0], d_emb), (grads[2], d_gain), (w_grad, d_w)):
+        d_emb, d_gain, *d_w = torch.autograd.grad(out, (emb16, gain) if linear8 else (emb16, gain, w), r.grad_hidden)
+        for dst, src in zip((grads[0], grads[2], w_grad), (d_emb, d_gain, *d_w)):
             dst.copy_(src)
         muon(lr=0.02, momentum=min(0.95, 0.85 + 0.002 * step), weight_decay=0.0, coeffs=COEFFS)
         adamw(lr=0.01, betas=(0.9, 0.99), weight_decay=0.0, step=step, seed=seed)
@@ -79,9 +102,10 @@ def main():
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
     for name, value in (("vocab", 4096), ("dim", 512), ("tokens", 16384), ("steps", 100)):
         ap.add_argument("--" + name, type=int, default=value)
+    ap.add_argument("--linear8", action="store_true", help="the hidden matrix' layer in 8 bits")
     a = ap.parse_args()
     t = time.perf_counter()
-    losses = train(a.vocab, a.dim, a.tokens, a.steps, log=lambda s: print(s, flush=True))
+    losses = train(a.vocab, a.dim, a.tokens, a.steps, linear8=a.linear8, log=lambda s: print(s, flush=True))
     print(f"{a.steps} steps in {time.perf_counter() - t:.2f} s: loss {losses[0]:.3f} -> {losses[-1]:.3f}")
 
 
