@@ -112,24 +112,27 @@ struct CodeOperand {
 };
 
 // acc += x^T grad over `stages` stages of 64 rows, `left` rows in all; STEPS steps of 16 rows from
-// step0 on are this wave's.  LDS holds two stages of x and three of the gradient.  While
-// stage k is multiplied, x of k + 1 is decoded from registers (loaded at the end of k - 2), the
-// gradient of k + 2 is loaded straight to LDS and the codes of k + 3 to registers, a piece after every
-// second product.  The barrier sits before the products of a stage's last step, whose
-// fragments are in registers by then; the next stage's first ones are read behind it.
+// step0 on are this wave's.  LDS holds two stages of x and SLOTS of the gradient.  While stage k
+// is multiplied, x of k + 1 is decoded from registers, the gradient of k + SLOTS - 1 is loaded
+// straight to LDS and the codes of x of k + 1 + SETS to registers, a piece after every product or two.
+// The barrier sits before the products of a stage's last step, whose fragments are in
+// registers by then; the next stage's first ones are read behind it.
 // Near the end the last stage is loaded again, which nothing reads, so that the body has no branch;
 // rows behind the last are zero in the gradient's fragments of the last stage (x has the last
 // row again there).
-template <int STEPS, int TD, int TC, typename OX, typename OG>
+template <int STEPS, int SLOTS, int SETS, int TD, int TC, typename OX, typename OG>
 __device__ inline void k_loop_coded(floatx16 (&acc)[TD][TC], int stages, OX& X, OG& G, int left, int step0, uint32_t lds, int wave, int lane) {
     static_assert(OG::kLoads == 4 && TD * TC == 8 && (STEPS == 2 || STEPS == 4), "pieces of a stage");
-    constexpr int kUnderWay = 9 + OG::kLoads;      // loads of a stage of x and of the gradient
+    static_assert(SETS == 2 || SETS == 4, "codes in registers");
+    constexpr int kLoads = 9 + OG::kLoads;      // of a stage: x and the gradient
+    static_assert(kLoads * (SLOTS - 2) < 64, "the counter's range");
     using std::integral_constant;
     constexpr uint32_t kX = OX::kBytes, kG = OG::kBytes;
-    const uint32_t mine = wave * 1024;
-    uint32_t x0 = lds, x1 = lds + kX, g0 = lds + 2 * kX, g1 = g0 + kG, g2 = g1 + kG;
+    const uint32_t mine = wave * 1024, g_first = lds + 2 * kX, g_last = g_first + (SLOTS - 1) * kG;
+    uint32_t x0 = lds, x1 = lds + kX, now = g_first, put = g_first;      // slots of this stage, of the gradient's next load
+    auto after = [&](uint32_t slot) { return slot == g_last ? g_first : slot + kG; };
     u32x4 fa[2][TD], fb[2][TC];
-    typename OX::Codes c0, c1;
+    typename OX::Codes c[SETS];
     int left_x = left, left_g = left;      // rows from the stage that X and G load next
     auto next_x = [&] {
         const bool more = left_x > kHeadK;
@@ -140,26 +143,34 @@ __device__ inline void k_loop_coded(floatx16 (&acc)[TD][TC], int stages, OX& X, 
         X.template load<0, 8>(c, min(kHeadK, left_x) - 1);
         next_x();
     };
-    auto load_g = [&](auto j, uint32_t slot) { G.template load_clamped<decltype(j)::value>(slot + mine, min(kHeadK, left_g) - 1); };
+    auto load_g = [&](auto j) { G.template load_clamped<decltype(j)::value>(put + mine, min(kHeadK, left_g) - 1); };
     auto next_g = [&] {
         const bool more = left_g > kHeadK;
         G.next += more ? G.step : 0;
         left_g -= more ? kHeadK : 0;
+        put = after(put);
     };
-    auto whole_g = [&](uint32_t slot) {
-        load_g(integral_constant<int, 0>(), slot);
-        load_g(integral_constant<int, 1>(), slot);
-        load_g(integral_constant<int, 2>(), slot);
-        load_g(integral_constant<int, 3>(), slot);
+    auto whole_g = [&] {
+        load_g(integral_constant<int, 0>());
+        load_g(integral_constant<int, 1>());
+        load_g(integral_constant<int, 2>());
+        load_g(integral_constant<int, 3>());
         next_g();
     };
-    load_x(c1);
-    load_x(c0);
-    whole_g(g0);
-    X.decode_all(c1, x0);
-    whole_g(g1);
-    load_x(c1);
-    wait_loads<kUnderWay>(); // the gradient of stage 0
+    // Stage 0, and then, in the order in which the stages before the first would have issued
+    // them, the gradient of 1 .. SLOTS - 2 and x of 1 .. SETS: the counts of the loop's
+    // waits hold from its first stage on.
+    typename OX::Codes first;
+    load_x(first);
+    whole_g();
+    static_assert(SETS >= SLOTS - 2, "x is ahead at least as far");
+#pragma unroll
+    for (int i = 0; i < SETS; ++i) {
+        if (i >= SETS - (SLOTS - 2)) whole_g();
+        load_x(c[i]);
+    }
+    X.decode_all(first, x0);
+    wait_loads<9 * SETS + OG::kLoads * (SLOTS - 2)>();       // the gradient of stage 0
     wait_lds();
     bare_barrier();
     auto read = [&](int set, uint32_t x, uint32_t g, int step) { read_step(X, G, fa[set], fb[set], x, g, step); };
@@ -188,15 +199,15 @@ __device__ inline void k_loop_coded(floatx16 (&acc)[TD][TC], int stages, OX& X, 
         one(integral_constant<int, 6>());
         one(integral_constant<int, 7>());
     };
-    read(0, x0, g0, 0);
-    // a stage that another follows; c: x of the next stage, then of the third after
+    read(0, x0, now, 0);
+    // a stage that another follows; c: x of the next stage, then of the one SETS after that
     auto stage = [&](typename OX::Codes& c) {
         typename OX::Decoded v;
         auto piece_g = [&](auto n) {      // 0 .. 3
-            load_g(n, g2);
+            load_g(n);
             if (decltype(n)::value == 3) next_g();
         };
-        read(1, x0, g0, 1);
+        read(1, x0, now, 1);
         if constexpr (STEPS == 2) {
             multiply(0, [&](auto n) {
                 constexpr int N = decltype(n)::value;
@@ -211,41 +222,50 @@ __device__ inline void k_loop_coded(floatx16 (&acc)[TD][TC], int stages, OX& X, 
                 constexpr int N = decltype(n)::value;
                 if constexpr (N % 2 == 0) X.template decode<N / 2>(c, v);
             });
-            read(0, x0, g0, 2);
+            read(0, x0, now, 2);
             multiply(1, [&](auto n) {
                 constexpr int N = decltype(n)::value;
                 if constexpr (N % 2 == 0) X.template store<N / 2>(v, x1);
             });
-            read(1, x0, g0, 3);
+            read(1, x0, now, 3);
             multiply(0, [&](auto n) {
                 constexpr int N = decltype(n)::value;
                 if constexpr (N % 2 == 0) piece_g(integral_constant<int, N / 2>());
             });
         }
         wait_lds();          // this wave's last fragments of the stage, and its share of the next one's x
-        wait_loads<kUnderWay>();     // all but the newest of x and of the gradient
+        wait_loads<kLoads * (SLOTS - 2)>();      // the gradient of the next stage
         bare_barrier();
-        read(0, x1, g1, 0);
+        const uint32_t t = x0;
+        x0 = x1;
+        x1 = t;
+        now = after(now);
+        read(0, x0, now, 0);
         const int last = min(kHeadK, left_x) - 1;
         multiply(1, [&](auto n) {
             constexpr int N = decltype(n)::value;
             X.template load<N, N + 1>(c, last);
             if (N == 7) next_x();
         });
-        const uint32_t tx = x0, tg = g0;
-        x0 = x1; x1 = tx;
-        g0 = g1; g1 = g2; g2 = tg;
     };
     int kt = 0;
 #pragma unroll 1
-    for (; kt + 2 < stages; kt += 2) {
-        stage(c0);
-        stage(c1);
+    for (; kt + SETS < stages; kt += SETS) {
+        stage(c[0]);
+        stage(c[1]);
+        if constexpr (SETS == 4) {
+            stage(c[2]);
+            stage(c[3]);
+        }
     }
-    if (kt + 1 < stages) stage(c0);
+    if (kt + 1 < stages) stage(c[0]);
+    if constexpr (SETS == 4) {
+        if (kt + 2 < stages) stage(c[1]);
+        if (kt + 3 < stages) stage(c[2]);
+    }
 #pragma unroll
     for (int step = 0; step < STEPS; ++step) {
-        if (step + 1 < STEPS) read((step + 1) % 2, x0, g0, step + 1);
+        if (step + 1 < STEPS) read((step + 1) % 2, x0, now, step + 1);
         mask(fb[step % 2], step);
         multiply(step % 2, [](auto) {});
     }
@@ -293,18 +313,20 @@ __device__ inline void store_tile(const Grad8& a, floatx16 (&acc)[TD][TC], int s
     }
 }
 
-// EDGE x EDGE, waves of 128 x 64: 256 with 8 waves; 128 with 4 and two workgroups per compute
-// unit, two pairs of waves that take half of every stage's K each and meet in LDS (64 x 64 a
-// wave would read a third more fragments for its products).
-template <int EDGE> struct GradTile {
+// EDGE x EDGE, waves of 128 x 64: 256 with 8 waves; 128 with 4, two pairs of waves that take half
+// of every stage's K each and meet in LDS (64 x 64 a wave would read a third more fragments
+// for its products).  DEEP: one workgroup of 128 per compute unit, further ahead with its loads;
+// otherwise two.
+template <int EDGE, bool DEEP> struct GradTile {
     static constexpr int WD = EDGE / 128, WC = EDGE / 64, kParts = EDGE == 256 ? 1 : 2, NW = WD * WC * kParts, kThreads = NW * kWave;
-    static constexpr size_t kBytes = (size_t)5 * EDGE * kHeadK * 2;
+    static constexpr int kSlots = DEEP ? 6 : 3, kSets = DEEP ? 4 : 2;
+    static constexpr size_t kBytes = (size_t)(2 + kSlots) * EDGE * kHeadK * 2;
     static_assert(kParts == 1 || (size_t)NW * 16 * 1024 <= kBytes, "the pairs' meeting");
 };
 
-template <int EDGE>
-__global__ __launch_bounds__((GradTile<EDGE>::kThreads), 2) void grad8_kernel(const Grad8 a) {
-    typedef GradTile<EDGE> S;
+template <int EDGE, bool DEEP>
+__global__ __launch_bounds__((GradTile<EDGE, DEEP>::kThreads), DEEP ? 1 : 2) void grad8_kernel(const Grad8 a) {
+    typedef GradTile<EDGE, DEEP> S;
     constexpr int TD = 4, TC = 2, NW = S::NW, kSteps = kHeadK / 16 / S::kParts;
     extern __shared__ __align__(16) uint8_t lds[];
     const int item = xcd_item(a.tiles_c * a.tiles_d * a.splits);
@@ -322,7 +344,7 @@ __global__ __launch_bounds__((GradTile<EDGE>::kThreads), 2) void grad8_kernel(co
     for (int j = 0; j < TC; ++j) G.at[j] += part * kSteps * 16 * G.kRow;
     floatx16 acc[TD][TC];
     clear(acc);
-    k_loop_coded<kSteps, TD, TC>(acc, s1 - s0, X, G, min(a.rows - s0 * kHeadK, (s1 - s0) * kHeadK), part * kSteps, lds_address(lds),
+    k_loop_coded<kSteps, S::kSlots, S::kSets, TD, TC>(acc, s1 - s0, X, G, min(a.rows - s0 * kHeadK, (s1 - s0) * kHeadK), part * kSteps, lds_address(lds),
                                  wave, lane);
     if constexpr (S::kParts == 1) {
         store_tile<TD, TC>(a, acc, split, d0 + wd * TD * 32, c0 + wc * TC * 32, lane);
@@ -384,19 +406,26 @@ __global__ __launch_bounds__(256) void join8_kernel(const Join8 a) {
     }
 }
 
-template <int EDGE>
+template <int EDGE, bool DEEP>
 hipError_t launch(const Grad8& a, hipStream_t s) {
-    typedef GradTile<EDGE> S;
-    const hipError_t allowed = hipFuncSetAttribute(reinterpret_cast<const void*>(&grad8_kernel<EDGE>),
+    typedef GradTile<EDGE, DEEP> S;
+    const hipError_t allowed = hipFuncSetAttribute(reinterpret_cast<const void*>(&grad8_kernel<EDGE, DEEP>),
                                                    hipFuncAttributeMaxDynamicSharedMemorySize, (int)S::kBytes);
     if (allowed != hipSuccess) return allowed;
-    grad8_kernel<EDGE><<<xcd_grid(a.tiles_c * a.tiles_d * a.splits), S::kThreads, S::kBytes, s>>>(a);
+    grad8_kernel<EDGE, DEEP><<<xcd_grid(a.tiles_c * a.tiles_d * a.splits), S::kThreads, S::kBytes, s>>>(a);
     return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_grad8(const Grad8& a, int edge, hipStream_t s) { return edge == 128 ? launch<128>(a, s) : launch<256>(a, s); }
+hipError_t launch_grad8(const Grad8& a, int edge, hipStream_t s) {
+    if (edge == 256) return launch<256, false>(a, s);
+    // One workgroup per compute unit and many stages: the deep form (16384 x 2048 x 512, 64 stages, the data past the last
+    // cache / in it: 50.5 / 47.8 us against 59.4 / 46.9).  Few stages do not earn its longer start (22: 25.1 against
+    // 23.5), and two workgroups hide each other's loads (512 of 32 stages: 60.6 against 54.0).
+    const bool deep = a.tiles_c * a.tiles_d * a.splits <= 256 && a.stages_per_split >= 40;
+    return deep ? launch<128, true>(a, s) : launch<128, false>(a, s);
+}
 
 hipError_t launch_join8(const Join8& a, hipStream_t s) {
     const int64_t items = (int64_t)a.cols * ((a.dim + 3) / 4);
