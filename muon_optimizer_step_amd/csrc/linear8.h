@@ -24,7 +24,8 @@ struct Blocks8 {
 struct Rows8 {
     int64_t rows;
     int dim, dim16;          // dim rounded up to 16
-    int unit_log, col_groups, row_groups;      // at most 2^29 of both together
+    int unit_log, col_groups, row_groups;      // at most 2^30 of both together
+    int past;                // written past the caches
 };
 
 struct Encode8 {

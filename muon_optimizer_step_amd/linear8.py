@@ -2,6 +2,7 @@
 
 from __future__ import annotations
 
+import ctypes
 from typing import NamedTuple, Optional
 
 from . import _lib
@@ -177,7 +178,7 @@ class _Prepared:
         torch = _torch()
         lib = _lib.load()
         self._entry, self._keep, self.device, self.result = getattr(lib, entry), keep, device, result
-        self._args = (problem,)
+        self._args = (ctypes.byref(problem),)
         self.workspace = None
         if not has_workspace:
             return
@@ -190,7 +191,7 @@ class _Prepared:
         _check_workspace(workspace, device)
         self.workspace = workspace
         self._keep = [*keep, workspace]
-        self._args = (problem, workspace.data_ptr(), workspace.numel() * workspace.element_size())
+        self._args = (*self._args, workspace.data_ptr(), workspace.numel() * workspace.element_size())
 
     def __call__(self, stream=None):
         _run(self._entry, self._args, stream, self.device)
