@@ -114,11 +114,11 @@ template <typename T> __device__ inline Raw<T> load8(const T* p, int left, bool 
     for (int k = 0; k < 4 * ((int)sizeof(T) / 2); ++k) r.w[k / 4][k % 4] = word[k];
     return r;
 }
-template <typename T> __device__ inline void store8(T* p, const Raw<T>& r, int left, bool vec, bool past) {
+template <bool PAST, typename T> __device__ inline void store8(T* p, const Raw<T>& r, int left, bool vec) {
     if (vec && left >= 8) {
 #pragma unroll
         for (int k = 0; k < (int)sizeof(T) / 2; ++k) {
-            if (past) __builtin_nontemporal_store(r.w[k], reinterpret_cast<u32x4*>(p) + k);
+            if constexpr (PAST) __builtin_nontemporal_store(r.w[k], reinterpret_cast<u32x4*>(p) + k);
             else reinterpret_cast<u32x4*>(p)[k] = r.w[k];
         }
         return;
@@ -221,15 +221,16 @@ __device__ inline void for_units(const Rows8& r, F work) {
         work(u);
     }
 }
+template <bool PAST>
 __device__ inline void store_codes(const Rows8& r, const Blocks8& b, const Unit& u, int64_t row, const u32x2& w, int byte) {
     if (row >= r.rows || u.d >= r.dim16) return;
     u32x2* dst = reinterpret_cast<u32x2*>(b.codes + row * b.stride + u.d);
-    if (r.past) __builtin_nontemporal_store(w, dst);
+    if constexpr (PAST) __builtin_nontemporal_store(w, dst);
     else *dst = w;
     if (threadIdx.x % kLanes == 0) b.scale[row * b.scale_stride + u.block] = (uint8_t)byte;
 }
 
-template <typename T, int ACT, bool KEEP>
+template <typename T, int ACT, bool KEEP, bool PAST>
 __global__ __launch_bounds__(kThreads) void encode8_kernel(const Encode8 a) {
     for_units(a.r, [&](const Unit& u) {
         Raw<T> raw[kBatch];
@@ -247,19 +248,19 @@ __global__ __launch_bounds__(kThreads) void encode8_kernel(const Encode8 a) {
             to_float<T>(raw[k], v);
             if (KEEP) {
                 const u32x2 w = encode8(v, byte);
-                store_codes(a.r, a.codes, u, row, w, byte);
+                store_codes<PAST>(a.r, a.codes, u, row, w, byte);
             }
             if (ACT != kActNone) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) v[e] = act<ACT>(v[e]);
                 const u32x2 w = encode8(v, byte);
-                store_codes(a.r, a.out, u, row, w, byte);
+                store_codes<PAST>(a.r, a.out, u, row, w, byte);
             }
         }
     });
 }
 
-template <typename T, int ACT>
+template <typename T, int ACT, bool PAST>
 __global__ __launch_bounds__(kThreads) void backward8_kernel(const Backward8 a) {
     for_units(a.r, [&](const Unit& u) {
         Raw<T> grad[kBatch];
@@ -287,17 +288,17 @@ __global__ __launch_bounds__(kThreads) void backward8_kernel(const Backward8 a) 
 #pragma unroll
             for (int e = 0; e < 8; ++e) g[e] *= act_slope<ACT>(v[e]);
             if (a.out && row < a.r.rows)
-                store8(static_cast<T*>(a.out) + row * a.out_stride + u.d, from_float<T>(g), left, a.out_vec, a.r.past);
+                store8<PAST>(static_cast<T*>(a.out) + row * a.out_stride + u.d, from_float<T>(g), left, a.out_vec);
             if (a.out8.codes) {
                 int b;
                 const u32x2 w = encode8(g, b);
-                store_codes(a.r, a.out8, u, row, w, b);
+                store_codes<PAST>(a.r, a.out8, u, row, w, b);
             }
         }
     });
 }
 
-template <typename T>
+template <typename T, bool PAST>
 __global__ __launch_bounds__(kThreads) void decode8_kernel(const Decode8 a) {
     for_units(a.r, [&](const Unit& u) {
         const int left = a.r.dim - u.d;
@@ -308,7 +309,7 @@ __global__ __launch_bounds__(kThreads) void decode8_kernel(const Decode8 a) {
             const u32x2 w = *reinterpret_cast<const u32x2*>(a.x.codes + row * a.x.stride + u.d);
             float v[8];
             decode8(w, scale_value(a.x.scale[row / a.tall * a.x.scale_stride + u.block]), v);
-            store8(static_cast<T*>(a.out) + row * a.out_stride + u.d, from_float<T>(v), left, a.vec, a.r.past);
+            store8<PAST>(static_cast<T*>(a.out) + row * a.out_stride + u.d, from_float<T>(v), left, a.vec);
         }
     });
 }
@@ -417,12 +418,17 @@ __global__ __launch_bounds__(kThreads) void weight8_kernel(const Weight8 a) {
 // by the kernel's own loop.
 int rows_grid(const Rows8& r) { return (int)std::min<int64_t>((int64_t)r.row_groups * r.col_groups, 1 << 20); }
 
+template <typename T, int ACT, bool KEEP>
+hipError_t encode_kept(const Encode8& a, hipStream_t s) {
+    const int grid = rows_grid(a.r);
+    if (a.r.past) encode8_kernel<T, ACT, KEEP, true><<<grid, kThreads, 0, s>>>(a);
+    else encode8_kernel<T, ACT, KEEP, false><<<grid, kThreads, 0, s>>>(a);
+    return hipGetLastError();
+}
 template <typename T, int ACT>
 hipError_t encode_typed(const Encode8& a, hipStream_t s) {
-    const int grid = rows_grid(a.r);
-    if (ACT == kActNone || a.codes.codes) encode8_kernel<T, ACT, true><<<grid, kThreads, 0, s>>>(a);
-    else encode8_kernel<T, ACT, ACT == kActNone><<<grid, kThreads, 0, s>>>(a);
-    return hipGetLastError();
+    if (ACT == kActNone || a.codes.codes) return encode_kept<T, ACT, true>(a, s);
+    return encode_kept<T, ACT, ACT == kActNone>(a, s);
 }
 template <typename T>
 hipError_t encode_act(const Encode8& a, int act, hipStream_t s) {
@@ -431,19 +437,31 @@ hipError_t encode_act(const Encode8& a, int act, hipStream_t s) {
     if (act == kActGelu) return encode_typed<T, kActGelu>(a, s);
     return encode_typed<T, kActNone>(a, s);
 }
+template <typename T, int ACT>
+hipError_t backward_typed(const Backward8& a, hipStream_t s) {
+    const int grid = rows_grid(a.r);
+    if (a.r.past) backward8_kernel<T, ACT, true><<<grid, kThreads, 0, s>>>(a);
+    else backward8_kernel<T, ACT, false><<<grid, kThreads, 0, s>>>(a);
+    return hipGetLastError();
+}
 template <typename T>
 hipError_t backward_act(const Backward8& a, int act, hipStream_t s) {
+    if (act == kActRelu2) return backward_typed<T, kActRelu2>(a, s);
+    return act == kActSilu ? backward_typed<T, kActSilu>(a, s) : backward_typed<T, kActGelu>(a, s);
+}
+template <typename T>
+hipError_t decode_typed(const Decode8& a, hipStream_t s) {
     const int grid = rows_grid(a.r);
-    if (act == kActRelu2) backward8_kernel<T, kActRelu2><<<grid, kThreads, 0, s>>>(a);
-    else if (act == kActSilu) backward8_kernel<T, kActSilu><<<grid, kThreads, 0, s>>>(a);
-    else backward8_kernel<T, kActGelu><<<grid, kThreads, 0, s>>>(a);
+    if (a.r.past) decode8_kernel<T, true><<<grid, kThreads, 0, s>>>(a);
+    else decode8_kernel<T, false><<<grid, kThreads, 0, s>>>(a);
     return hipGetLastError();
 }
 
 // What a pass writes, from which on it is written past the caches: the last one keeps too little
 // of it for the next pass to find (the layer 16384 x 1024 x 4096, whose gradient's 201 MB are written so: the backward
-// pass with both products behind it 259 us either way, alone 62 against 73).  Below, what follows
-// finds it there (4096 x 1024 x 4096, encode and product: 42 us, 48 past the caches).
+// pass with both products behind it 257 us against 259, alone 62 against 73).  Below, what follows
+// finds it there (4096 x 1024 x 4096, encode and product: 42 us, 48 past the caches).  A template's
+// argument: as a branch, the two stores become one without the hint.
 constexpr int64_t kPastBytes = (int64_t)192 << 20;
 Rows8 plan(const Rows8& r, int64_t bytes_per_value) {
     Rows8 q = r;
@@ -475,11 +493,8 @@ hipError_t launch_backward8(const Backward8& a0, int type, int act, hipStream_t 
 hipError_t launch_decode8(const Decode8& a0, int type, hipStream_t s) {
     Decode8 a = a0;
     a.r = plan(a0.r, type == kTypeFp32 ? 4 : 2);
-    const int grid = rows_grid(a.r);
-    if (type == kTypeBf16) decode8_kernel<bf16><<<grid, kThreads, 0, s>>>(a);
-    else if (type == kTypeFp16) decode8_kernel<f16><<<grid, kThreads, 0, s>>>(a);
-    else decode8_kernel<float><<<grid, kThreads, 0, s>>>(a);
-    return hipGetLastError();
+    if (type == kTypeBf16) return decode_typed<bf16>(a, s);
+    return type == kTypeFp16 ? decode_typed<f16>(a, s) : decode_typed<float>(a, s);
 }
 hipError_t launch_weight8(const Weight8& a, int type, hipStream_t s) {
     const int64_t grid = (int64_t)((a.rows + kBlock8 - 1) / kBlock8) * ((a.dim + kBlock8 - 1) / kBlock8);
