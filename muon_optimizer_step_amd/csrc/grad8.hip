@@ -387,13 +387,21 @@ __global__ __launch_bounds__((GradTile<EDGE, DEEP>::kThreads), DEEP ? 1 : 2) voi
 }
 
 // The splits' sums in order, added to what is there.
-__global__ __launch_bounds__(256) void join8_kernel(const Join8 a) {
-    const int64_t quads = (a.dim + 3) / 4, items = quads * a.cols;
-    for (int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x; n < items; n += (int64_t)gridDim.x * 256) {
+__global__ __launch_bounds__(kJoinThreads) void join8_kernel(const Join8 a) {
+    const int64_t quads = (a.dim + 3) / 4, items = quads * a.cols, step = (int64_t)a.cols * a.partial_pitch;
+    for (int64_t n = (int64_t)blockIdx.x * kJoinThreads + threadIdx.x; n < items; n += (int64_t)gridDim.x * kJoinThreads) {
         const int64_t c = n / quads, d = (n - c * quads) * 4;
         floatx4 v = {0.f, 0.f, 0.f, 0.f};
         const float* src = a.partial + c * a.partial_pitch + d;
-        for (int s = 0; s < a.splits; ++s, src += (int64_t)a.cols * a.partial_pitch) v += *reinterpret_cast<const floatx4*>(src);
+        int s = 0;
+        for (; s + kJoinBatch <= a.splits; s += kJoinBatch) {
+            floatx4 part[kJoinBatch];
+#pragma unroll
+            for (int k = 0; k < kJoinBatch; ++k, src += step) part[k] = *reinterpret_cast<const floatx4*>(src);
+#pragma unroll
+            for (int k = 0; k < kJoinBatch; ++k) v += part[k];
+        }
+        for (; s < a.splits; ++s, src += step) v += *reinterpret_cast<const floatx4*>(src);
         float* dst = a.out + c * a.out_stride + d;
         if (a.out_vec) {
             if (a.accumulate) v += *reinterpret_cast<const floatx4*>(dst);
@@ -429,7 +437,7 @@ hipError_t launch_grad8(const Grad8& a, int edge, hipStream_t s) {
 
 hipError_t launch_join8(const Join8& a, hipStream_t s) {
     const int64_t items = (int64_t)a.cols * ((a.dim + 3) / 4);
-    join8_kernel<<<(int)std::min<int64_t>(8192, (items + 255) / 256), 256, 0, s>>>(a);
+    join8_kernel<<<(int)std::min<int64_t>(32768, (items + kJoinThreads - 1) / kJoinThreads), kJoinThreads, 0, s>>>(a);
     return hipGetLastError();
 }
 

@@ -63,6 +63,11 @@ hipError_t launch_backward8(const Backward8& a, int type, int act, hipStream_t s
 hipError_t launch_decode8(const Decode8& a, int type, hipStream_t s);
 hipError_t launch_weight8(const Weight8& a, int type, hipStream_t s);
 
+// The joins of parts: a wave a workgroup, kJoinBatch parts' loads under way together.  A gradient of 128 x 128 in 32
+// parts 14.6 us (16384 rows; one load at a time and workgroups of 256: 20.8, 8 at a time 13.7), y of 17 x 512
+// in 16 parts of K = 8192 7.9 us (10.8, 8 at a time 8.6).
+constexpr int kJoinThreads = 64, kJoinBatch = 4;
+
 // y = a b^T.
 // Kernels: up to 16 rows; 32 x 32 with K split over the waves; tiles of 64, 128 and 256.
 enum Matmul8Variant { kMatmulRows = 0, kMatmulSplit, kMatmulSmall, kMatmulMid, kMatmulTile };
@@ -71,7 +76,7 @@ struct Matmul8 {
     void* y;
     int64_t y_stride;
     int rows, cols, dim;
-    int y_vec;               // rows of y 16-byte aligned, cols a multiple of 8
+    int y_vec;               // rows of y 16-byte aligned
     int tiles_v, tiles_t;    // tiles along cols and rows
     int splits, stages_per_split;    // parts of K (kMatmulSmall, kMatmulMid; 1 otherwise), a multiple of 4 stages of 128 each
     float* partial;          // nullable: [split][rows][partial_pitch]

@@ -2,7 +2,6 @@
 // splits, and the launches behind muonstep_linear8.h.
 #include <algorithm>
 #include <cstring>
-#include <vector>
 
 #include "../../include/muonstep_linear8.h"
 #include "head.h"
@@ -34,7 +33,8 @@ bool whole_rows(const void* p, int64_t stride, int64_t size) {
 struct Checks {
     const char* entry;
     int rc = MUON_OK;
-    std::vector<Span> read, written;
+    Span read[8], written[8];        // no entry has more
+    int reads = 0, writes = 0;
 
     explicit Checks(const char* name) : entry(name) {}
     void sizes(int64_t rows, int64_t cols, int64_t dim) {
@@ -54,7 +54,7 @@ struct Checks {
         if (stride < dim) rc = fail(MUON_ERR_INVALID_ARG, "%s: stride of %s smaller than its rows' %lld", entry, what, (long long)dim);
         else if (stride > kFar) rc = fail(MUON_ERR_UNSUPPORTED, "%s: stride of %s beyond 2^22", entry, what);
     }
-    void buffer(const char* what, const void* p, int64_t bytes, int64_t align, bool writes) {
+    void buffer(const char* what, const void* p, int64_t bytes, int64_t align, bool writable) {
         if (rc || bytes <= 0) return;
         if (!p) {
             rc = fail(MUON_ERR_INVALID_ARG, "%s: %s must be non-NULL", entry, what);
@@ -65,14 +65,14 @@ struct Checks {
             rc = fail(MUON_ERR_INVALID_ARG, "%s: %s is not %lld-byte aligned", entry, what, (long long)align);
             return;
         }
-        (writes ? written : read).push_back({lo, lo + (uintptr_t)bytes, (int)(read.size() + written.size())});
+        (writable ? written[writes++] : read[reads++]) = {lo, lo + (uintptr_t)bytes, 0};
     }
-    void matrix(const char* what, const void* p, int64_t rows, int64_t dim, int64_t stride, int64_t size, bool writes) {
+    void matrix(const char* what, const void* p, int64_t rows, int64_t dim, int64_t stride, int64_t size, bool writable) {
         strides(what, stride, dim);
-        buffer(what, p, rows > 0 ? ((rows - 1) * stride + dim) * size : 0, size, writes);
+        buffer(what, p, rows > 0 ? ((rows - 1) * stride + dim) * size : 0, size, writable);
     }
     // tall: rows that share a scale
-    void coded(const char* what, const blocks8_t& b, int64_t rows, int64_t dim, int64_t tall, bool writes) {
+    void coded(const char* what, const blocks8_t& b, int64_t rows, int64_t dim, int64_t tall, bool writable) {
         if (rc) return;
         const int64_t wide = round_up(dim, 16), across = ceil_div(dim, MUON_BLOCK8), down = ceil_div(rows, tall);
         if (b.stride < wide || b.stride % 16 || b.scale_stride < across || b.scale_stride % 4) {
@@ -84,18 +84,18 @@ struct Checks {
             rc = fail(MUON_ERR_UNSUPPORTED, "%s: stride of %s beyond 2^22", entry, what);
             return;
         }
-        buffer(what, b.codes, rows > 0 ? (rows - 1) * b.stride + wide : 0, 16, writes);
+        buffer(what, b.codes, rows > 0 ? (rows - 1) * b.stride + wide : 0, 16, writable);
         // read in words of 4 scales
-        buffer(what, b.scale, down > 0 ? (down - 1) * b.scale_stride + (writes ? across : round_up(across, 4)) : 0, 4, writes);
+        buffer(what, b.scale, down > 0 ? (down - 1) * b.scale_stride + (writable ? across : round_up(across, 4)) : 0, 4, writable);
     }
     // what is written overlaps nothing else
     int done() {
         if (rc) return rc;
-        for (size_t i = 0; i < written.size(); ++i) {
+        for (int i = 0; i < writes; ++i) {
             auto meets = [&](const Span& x) { return written[i].lo < x.hi && x.lo < written[i].hi; };
-            for (const Span& x : read)
-                if (meets(x)) return fail(MUON_ERR_UNSUPPORTED, "%s: an output overlaps an input", entry);
-            for (size_t j = 0; j < i; ++j)
+            for (int j = 0; j < reads; ++j)
+                if (meets(read[j])) return fail(MUON_ERR_UNSUPPORTED, "%s: an output overlaps an input", entry);
+            for (int j = 0; j < i; ++j)
                 if (meets(written[j])) return fail(MUON_ERR_UNSUPPORTED, "%s: two outputs overlap", entry);
         }
         return MUON_OK;
@@ -172,7 +172,7 @@ GradPlan plan_grad(const act8_grad_weight_t& p) {
     q.cols8 = round_up(p.cols, 8);
     q.dim8 = round_up(p.dim, 8);
     const int64_t all = std::max<int64_t>(1, ceil_div(p.rows, kHeadK));
-    static const int tried[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32};
+    static const int tried[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64, 96, 128};
     double least = 1e300;
     auto consider = [&](int edge, double stage, double ends) {
         const int64_t tiles = ceil_div(p.cols, edge) * ceil_div(p.dim, edge);
@@ -180,7 +180,7 @@ GradPlan plan_grad(const act8_grad_weight_t& p) {
             if (splits > 1 && all / splits < kMinStages) break;
             const int64_t stages = ceil_div(all, splits), parts = ceil_div(all, stages);
             const double mb = (double)parts * p.cols * p.dim * 4e-6;         // a part's sums, written and read again
-            const double us = 4.5 + ceil_div(tiles * parts, kCus) * (stages * stage + ends) + (parts > 1 ? 2.0 + mb * 0.3 : 0.0);
+            const double us = 4.5 + ceil_div(tiles * parts, kCus) * (stages * stage + ends) + (parts > 1 ? 2.0 + parts * 0.06 + mb * 0.3 : 0.0);
             if (us >= least) continue;
             least = us;
             q.edge = edge;

@@ -514,14 +514,28 @@ __global__ __launch_bounds__(256, 2) void matmul8_small_kernel(const Matmul8 a) 
 
 // The sums of the parts of K in order, rounded once.
 template <typename T>
-__global__ __launch_bounds__(256) void matmul8_join_kernel(const Matmul8 a) {
-    const int64_t octs = (a.cols + 7) / 8, items = octs * a.rows;
-    for (int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x; n < items; n += (int64_t)gridDim.x * 256) {
+__global__ __launch_bounds__(kJoinThreads) void matmul8_join_kernel(const Matmul8 a) {
+    const int64_t octs = (a.cols + 7) / 8, items = octs * a.rows, step = (int64_t)a.rows * a.partial_pitch;
+    for (int64_t n = (int64_t)blockIdx.x * kJoinThreads + threadIdx.x; n < items; n += (int64_t)gridDim.x * kJoinThreads) {
         const int64_t row = n / octs;
         const int v = (int)(n - row * octs) * 8;
         floatx4 lo = {0.f, 0.f, 0.f, 0.f}, hi = lo;
         const float* src = a.partial + row * a.partial_pitch + v;
-        for (int s = 0; s < a.splits; ++s, src += (int64_t)a.rows * a.partial_pitch) {
+        int s = 0;
+        for (; s + kJoinBatch <= a.splits; s += kJoinBatch) {
+            floatx4 part[kJoinBatch][2];
+#pragma unroll
+            for (int k = 0; k < kJoinBatch; ++k, src += step) {
+                part[k][0] = reinterpret_cast<const floatx4*>(src)[0];
+                part[k][1] = reinterpret_cast<const floatx4*>(src)[1];
+            }
+#pragma unroll
+            for (int k = 0; k < kJoinBatch; ++k) {
+                lo += part[k][0];
+                hi += part[k][1];
+            }
+        }
+        for (; s < a.splits; ++s, src += step) {
             lo += reinterpret_cast<const floatx4*>(src)[0];
             hi += reinterpret_cast<const floatx4*>(src)[1];
         }
@@ -738,9 +752,9 @@ hipError_t typed(const Matmul8& a, int variant, hipStream_t s) {
 
 hipError_t launch_matmul8_join(const Matmul8& a, int type, hipStream_t s) {
     const int64_t items = (int64_t)a.rows * ((a.cols + 7) / 8);
-    const int grid = (int)std::min<int64_t>(8192, (items + 255) / 256);
-    if (type == kTypeBf16) matmul8_join_kernel<bf16><<<grid, 256, 0, s>>>(a);
-    else matmul8_join_kernel<f16><<<grid, 256, 0, s>>>(a);
+    const int grid = (int)std::min<int64_t>(32768, (items + kJoinThreads - 1) / kJoinThreads);
+    if (type == kTypeBf16) matmul8_join_kernel<bf16><<<grid, kJoinThreads, 0, s>>>(a);
+    else matmul8_join_kernel<f16><<<grid, kJoinThreads, 0, s>>>(a);
     return hipGetLastError();
 }
 hipError_t launch_matmul8(const Matmul8& a, int type, int variant, hipStream_t s) {
