@@ -133,7 +133,7 @@ MatmulPlan plan_matmul(const matmul8_t& p) {
             const int parts = (int)ceil_div(all, stages);
             if (splits > 1 && (parts < 2 || tiles * parts > kCus)) break;
             const double partial = (double)parts * p.rows * p.cols * 8;      // bytes, written and read
-            const double us = start + ceil_div(tiles * parts, kCus) * (stages * stage + ends) + (parts > 1 ? 2.5 + partial * 2e-7 : 0.0);
+            const double us = start + ceil_div(tiles * parts, kCus) * (stages * stage + ends) + (parts > 1 ? 2.5 + parts * 0.06 + partial * 2e-7 : 0.0);
             if (us < least) {
                 least = us;
                 best = {variant, tile, tile, parts, stages, 256};
@@ -141,7 +141,7 @@ MatmulPlan plan_matmul(const matmul8_t& p) {
         }
     };
     consider(kMatmulSplit, 32, 2.5, 0.20, 0.6, 1);
-    consider(kMatmulSmall, 64, 2.6, 0.24, 0.9, 16);
+    consider(kMatmulSmall, 64, 2.6, 0.24, 0.9, 64);
     consider(kMatmulMid, 128, 3.5, 0.56, 0.75, 8);
     consider(kMatmulTile, 256, 3.5, 1.55, 4.4, 1);
     if (best.splits > 1) best.bytes = round_up(4 * (int64_t)best.splits * p.rows * round_up(p.cols, 8), 256);

@@ -296,6 +296,13 @@ def test_matmul_no_rows_and_long_k(rows, cols, dim):
     _check_product(y, a, b, "bf16", "long")
 
 
+@pytest.mark.parametrize("rows,cols,dim", [(20, 70, 66000), (64, 64, 30001)])
+def test_matmul_of_many_parts(rows, cols, dim):
+    """K in tens of parts, the last one shorter, whose number is no multiple of what the join takes at a time."""
+    y, a, b = _product(rows, cols, dim, "fp16")
+    _check_product(y, a, b, "fp16", "parts")
+
+
 @pytest.mark.parametrize("rows,cols,dim", [(5, 64, 512), (64, 512, 2048), (300, 500, 1000), (2050, 2100, 700)])
 def test_matmul_error_in_norm(rows, cols, dim):
     """Against the bound of every value above, the errors of random products mostly cancel: in fp16 the output's rounding
@@ -369,7 +376,7 @@ def _check_grad(got, grad, x, before, label):
     assert (err <= tol).all(), f"{label}: worst {np.nanmax(err / tol):.3g} of the tolerance"
 
 
-@pytest.mark.parametrize("rows,cols,dim", GRADS)
+@pytest.mark.parametrize("rows,cols,dim", GRADS + [(33001, 40, 70), (20000, 136, 30)])
 def test_grad_weight(rows, cols, dim):
     import torch
     import muon_optimizer_step_amd as ms
