@@ -9,12 +9,13 @@
 // implementation.
 //
 // Bound: HBM; every value is read once and written once (a copy of 4 GiB: 4.7 TB/s, reads and
-// writes together).  Measured, inputs from memory: 16384 x 2048 bf16 to its codes and relu2's 26.9 us,
-// 5.0 TB/s; 16384 x 4096 bf16 to codes 34.8 us, 5.8; relu2's backward of 16384 x 4096, in 16 and in
-// 8 bits, 62 us, 6.5 TB/s; gelu's and silu's 89 and 85 us, for which the vector unit is the limit;
-// 8192 x 8192 float32 weights to codes and transposed codes 79 us, 5.1 TB/s; 16384 x 4096 codes to
+// writes together).  Measured, inputs from memory: 16384 x 2048 bf16 to its codes and relu2's 25.0 us,
+// 5.4 TB/s; 16384 x 4096 bf16 to codes 34.1 us, 5.9; relu2's backward of 16384 x 4096, in 16 and in
+// 8 bits, 62 us, 6.6 TB/s; gelu's and silu's 88 and 85 us, for which the vector unit is the limit;
+// 8192 x 8192 float32 weights to codes and transposed codes 77 us, 5.2 TB/s; 16384 x 4096 codes to
 // bf16 30 us, 6.6.  Small calls are a launch: 2048 values 2.9 us of kernel time.
 #include <algorithm>
+#include <type_traits>
 
 #include "linear8.h"
 #include "tiles.h"
@@ -36,9 +37,17 @@ __device__ inline uint32_t block_max(uint32_t x) {
     step((uint32_t)__builtin_amdgcn_mov_dpp((int)x, 0x121, 15, 15, true));
     return x;
 }
-__device__ inline uint32_t finite_bits(float x) {
-    const uint32_t b = __builtin_bit_cast(uint32_t, x) & 0x7FFFFFFFu;
-    return b < 0x7F800000u ? b : 0u;
+// The bits of the largest magnitude of N values; FINITE: of the finite ones.  Without it a NaN or an infinity is
+// larger than any value, so that a block where there is one is found and looked at again.
+constexpr uint32_t kInfBits = 0x7F800000u;
+template <bool FINITE, int N> __device__ inline uint32_t top_bits(const float* v) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        const uint32_t b = __builtin_bit_cast(uint32_t, v[k]) & 0x7FFFFFFFu, x = FINITE && b >= kInfBits ? 0u : b;
+        top = top > x ? top : x;
+    }
+    return top;
 }
 // The scale's byte from the bits of the block's largest magnitude.
 __device__ inline int scale_byte(uint32_t top) {
@@ -54,13 +63,9 @@ __device__ inline uint32_t codes4(const float* v, float inverse) {
 }
 // A lane's 8 values of a block to codes; every lane of the block takes part.
 __device__ inline u32x2 encode8(const float* v, int& byte) {
-    uint32_t top = 0;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        const uint32_t b = finite_bits(v[k]);
-        top = top > b ? top : b;
-    }
-    byte = scale_byte(block_max(top));
+    uint32_t top = block_max(top_bits<false, 8>(v));
+    if (top >= kInfBits) top = block_max(top_bits<true, 8>(v));      // all lanes of the block, or none
+    byte = scale_byte(top);
     const float inverse = scale_inverse(byte);
     return u32x2{codes4(v, inverse), codes4(v + 4, inverse)};
 }
@@ -318,8 +323,11 @@ __global__ __launch_bounds__(kThreads) void decode8_kernel(const Decode8 a) {
 // A workgroup for each 128 x 128 block.  A lane holds 4 x 4 values of each of 4 pieces:
 // 4 rows of 4 consecutive columns, so that both layouts are written from registers
 // in words: rows straight to memory (32 lanes cover a row's 128 bytes), columns
-// through LDS, whose word (column, 4 rows) sits in slot rows ^ column / 4 of its
-// column: the 32 lanes that write a row group meet 32 different banks.
+// through LDS, whose word (column, 4 rows) sits in slot rows ^ column / 4 ^ column % 4 of its
+// column: the 32 lanes that write a row group meet 32 different banks, and so do those that read four columns.
+// 8192 x 8192 float32 77 us, 64 where consecutive calls have one input (5.2 and 6.3 TB/s); bfloat16 56 and 44 us, with
+// loads that wait for one another 72; 512 x 512 3.9 us: 16 workgroups, a launch.
+template <typename T> using Quad = std::conditional_t<sizeof(T) == 4, u32x4, u32x2>;      // 4 values as they lie in memory
 template <typename T>
 __global__ __launch_bounds__(kThreads) void weight8_kernel(const Weight8 a) {
     __shared__ uint32_t tops[kThreads / kWave];
@@ -328,51 +336,67 @@ __global__ __launch_bounds__(kThreads) void weight8_kernel(const Weight8 a) {
     const int br = blockIdx.x / across, bd = blockIdx.x % across;
     const int col = 4 * (threadIdx.x % 32), group = threadIdx.x / 32;     // rows 4 (group + 8 q) + j
     const int d = bd * kBlock8 + col, row0 = br * kBlock8;
+    // All loads are issued before the first value is looked at.  Rows behind the last repeat it, and are zeros below.
+    Quad<T> raw[4][4];
+    auto at = [&](int q, int j) {
+        return static_cast<const T*>(a.w) + (int64_t)min(row0 + 4 * (group + 8 * q) + j, a.rows - 1) * a.w_stride + d;
+    };
+    if (a.vec && d + 4 <= a.dim) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) raw[q][j] = __builtin_nontemporal_load(reinterpret_cast<const Quad<T>*>(at(q, j)));
+    } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) raw[q][j] = Quad<T>{};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (d + e < a.dim) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        if constexpr (sizeof(T) == 4) raw[q][j][e] = __builtin_bit_cast(uint32_t, at(q, j)[e]);
+                        else raw[q][j][e / 2] |= (uint32_t)__builtin_bit_cast(uint16_t, at(q, j)[e]) << (16 * (e % 2));
+                    }
+            }
+    }
     float v[4][4][4];
 #pragma unroll
     for (int q = 0; q < 4; ++q)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const int row = row0 + 4 * (group + 8 * q) + j;
-            const T* p = static_cast<const T*>(a.w) + (int64_t)row * a.w_stride + d;
-            if (row < a.rows && a.vec && d + 4 <= a.dim) {
-                if constexpr (sizeof(T) == 4) {
-                    const u32x4 w = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
+            const bool there = row0 + 4 * (group + 8 * q) + j < a.rows;
+            float x[8];
+            if constexpr (sizeof(T) == 4) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) v[q][j][e] = as_float(w[e]);
-                } else {
-                    const u32x2 w = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(p));
-                    const u32x4 both = {w[0], w[1], 0u, 0u};
-                    float x[8];
-                    unpack8<T>(both, x);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) v[q][j][e] = x[e];
-                }
+                for (int e = 0; e < 4; ++e) x[e] = as_float(raw[q][j][e]);
             } else {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) v[q][j][e] = row < a.rows && d + e < a.dim ? (float)p[e] : 0.f;
+                unpack8<T>(u32x4{raw[q][j][0], raw[q][j][1], 0u, 0u}, x);
             }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[q][j][e] = there ? x[e] : 0.f;
         }
-    uint32_t top = 0;
+    auto block_top = [&](auto finite) {
+        uint32_t top = block_max(top_bits<decltype(finite)::value, 64>(&v[0][0][0]));
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
+        for (int off = 16; off < kWave; off <<= 1) {
+            const uint32_t y = (uint32_t)__shfl_xor((int)top, off, kWave);
+            top = top > y ? top : y;
+        }
+        if (threadIdx.x % kWave == 0) tops[threadIdx.x / kWave] = top;
+        __syncthreads();
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const uint32_t b = finite_bits(v[q][j][e]);
-                top = top > b ? top : b;
-            }
-    top = block_max(top);
-#pragma unroll
-    for (int off = 16; off < kWave; off <<= 1) {
-        const uint32_t y = (uint32_t)__shfl_xor((int)top, off, kWave);
-        top = top > y ? top : y;
+        for (int w = 0; w < kThreads / kWave; ++w) top = top > tops[w] ? top : tops[w];
+        return top;
+    };
+    uint32_t top = block_top(std::false_type());
+    if (top >= kInfBits) {       // the whole workgroup, or none of it
+        __syncthreads();
+        top = block_top(std::true_type());
     }
-    if (threadIdx.x % kWave == 0) tops[threadIdx.x / kWave] = top;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kThreads / kWave; ++w) top = top > tops[w] ? top : tops[w];
     const int byte = scale_byte(top);
     const float inverse = scale_inverse(byte);
     const int dim16 = (a.dim + 15) / 16 * 16, rows16 = (a.rows + 15) / 16 * 16;
@@ -395,9 +419,9 @@ __global__ __launch_bounds__(kThreads) void weight8_kernel(const Weight8 a) {
             const uint32_t lo23 = __builtin_amdgcn_perm(w[3], w[2], 0x05010400u), hi23 = __builtin_amdgcn_perm(w[3], w[2], 0x07030602u);
             const int slot = (group + 8 * q) ^ (col / 4);
             turned[col][slot] = __builtin_amdgcn_perm(lo23, lo01, 0x05040100u);
-            turned[col + 1][slot] = __builtin_amdgcn_perm(lo23, lo01, 0x07060302u);
-            turned[col + 2][slot] = __builtin_amdgcn_perm(hi23, hi01, 0x05040100u);
-            turned[col + 3][slot] = __builtin_amdgcn_perm(hi23, hi01, 0x07060302u);
+            turned[col + 1][slot ^ 1] = __builtin_amdgcn_perm(lo23, lo01, 0x07060302u);
+            turned[col + 2][slot ^ 2] = __builtin_amdgcn_perm(hi23, hi01, 0x05040100u);
+            turned[col + 3][slot ^ 3] = __builtin_amdgcn_perm(hi23, hi01, 0x07060302u);
         }
     }
     if (!a.transposed.codes) return;
@@ -408,7 +432,7 @@ __global__ __launch_bounds__(kThreads) void weight8_kernel(const Weight8 a) {
         const int out_row = bd * kBlock8 + c, out_col = row0 + 16 * chunk;
         u32x4 w;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) w[e] = turned[c][(4 * chunk + e) ^ (c / 4)];
+        for (int e = 0; e < 4; ++e) w[e] = turned[c][(4 * chunk + e) ^ (c / 4) ^ (c % 4)];
         if (out_row < a.dim && out_col < rows16)
             *reinterpret_cast<u32x4*>(a.transposed.codes + out_row * a.transposed.stride + out_col) = w;
     }

@@ -121,6 +121,15 @@ struct MatmulPlan {
     int variant, tile_v, tile_t, splits, stages;     // stages of a split
     int64_t bytes;
 };
+// Up to 16 rows one kernel; beyond, what a linear estimate of the time says is least: a start, for
+// each round of 256 workgroups the stages of K and the tile's ends, and for a split K the partial sums.  The constants are
+// fitted to measured times (us; rows x cols x dim, tiles of 32 / 64 / 128 / 256, K split where the estimate splits):
+//     17 x 512 x 512         4.1 /  4.5 /  4.9 /  8.4        2048 x 2048 x 512    29 /  9.6 /  6.6 / 10.3
+//     17 x 512 x 8192       14.9 /  7.9 / 11.1 / 67          2048 x 4096 x 1024   89 / 22   / 12.9 / 15.6
+//     64 x 8192 x 8192      35.6 / 20   / 21.9 / 70          4096 x 2048 x 2048  150 / 35   / 21   / 25
+//     128 x 1024 x 1024      4.5 /  5.5 /  7.6 / 13          16384 x 2048 x 512  213 / 59   / 27.4 / 23.6
+//     256 x 4096 x 4096     36   / 11.1 / 19.6 / 38.6        4096^3              562 / 121  / 70.5 / 56.5
+//     2048 x 512 x 512       8.8 /  4.7 /  5.8 /  9.6        8192^3                -        / 520  / 432
 MatmulPlan plan_matmul(const matmul8_t& p) {
     const int all = (int)ceil_div(p.dim, kBlock8);
     MatmulPlan best = {kMatmulRows, 16, 16, 1, all, 256};
@@ -166,6 +175,11 @@ struct GradPlan {
     int64_t cols8, dim8;
     int64_t grad, partial, bytes; // offsets, -1: not there
 };
+// As plan_matmul, for tiles of 128 and 256 and any of the splits below.  Measured (us; rows x cols x dim: tile / splits):
+//     16384 x 2048 x 512    128/4 50, 128/8 54, 256/12 51        8192 x 8192 x 4096    128/1 574, 256/1 437
+//     65536 x 128 x 128     128/32 28, 128/64 23                 16384 x 4096 x 1024   256/4 128
+//     16384 x 512 x 512     128/12 21                            512 x 512 x 512       128/1 9.8 (256 rows 7.5: a split saves nothing)
+// A part costs its sums' way through memory and 0.06 us of the join's latency.
 GradPlan plan_grad(const act8_grad_weight_t& p) {
     GradPlan q;
     q.pack = p.cols % 8 || !whole_rows(p.grad, p.grad_stride, 2);

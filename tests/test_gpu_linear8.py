@@ -187,6 +187,21 @@ def test_weight_encode(rows, dim, dtype):
         alone.T
 
 
+@pytest.mark.parametrize("dim", [1, 6, 127, 198, 255])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_weight_rows_that_end_inside_a_load(dim, dtype):
+    """Aligned rows of an odd length, between values that are none of the matrix: NaN would be seen in the codes."""
+    import torch
+    import muon_optimizer_step_amd as ms
+    w = torch.from_numpy(_values(131, dim, dim)).to(_type(dtype))
+    room = torch.full((131, 256), float("nan"), dtype=w.dtype, device="cuda")
+    room[:, :dim] = w.cuda()
+    want = ol.encode(_f64(w), 128)
+    w8 = ms.weight8_encode(room[:, :dim])
+    _same_codes(w8, want, "weight")
+    _same_codes(w8.T, (want[0].T, want[1].T), "transposed")
+
+
 @pytest.mark.parametrize("kind", ["relu2", "silu", "gelu"])
 @pytest.mark.parametrize("rows,dim,dtype", [(1, 1, "bf16"), (3, 130, "fp16"), (65, 1000, "bf16"), (129, 600, "fp32"), (64, 2048, "fp16")])
 def test_backward(kind, rows, dim, dtype):
