@@ -36,27 +36,28 @@ struct CodeOperand {
     struct Codes {
         uint32_t w[8], byte;
     };
-    const uint8_t* code;     // of the next stage to load
-    const uint8_t* scale;
+    uint8_t* code;           // of the next stage to load
+    uint8_t* scale;
     int64_t code_step, scale_step;
-    uint32_t code_stride, scale_stride, code_at, scale_at;
-    int row, scale_row;
+    int code_stride, scale_stride, code_gap, scale_gap;      // gap: from the end of a row's part in the tile to the next one
+    int code_at[8], scale_at;
     uint32_t put[2];         // LDS address of the lane's first and third column's chunk, less the slot's
     uint32_t at[4];          // of its chunk of fragment 0, by step ^ fragment
     // frag0: the wave's first column, step0 its first step (of 16 K) of a stage
     __device__ inline void init(const Blocks8& x, int d0, int dim, int64_t k0, int frag0, int step0, int thread, int lane) {
         const int col = 4 * (thread % kAcross), group = thread / kAcross;
         const int d = min(col, (dim + 15) / 16 * 16 - 4 - d0);
-        row = 8 * group;
-        scale_row = 8 * group + lane % 8;
-        code_stride = (uint32_t)x.stride;
-        scale_stride = (uint32_t)x.scale_stride;
+        code_stride = (int)x.stride;
+        scale_stride = (int)x.scale_stride;
         code_step = kHeadK * x.stride;
         scale_step = kHeadK * x.scale_stride;
         code = x.codes + k0 * x.stride + d0;
         scale = x.scale + k0 * x.scale_stride + d0 / kBlock8;
-        code_at = d;
-        scale_at = d / kBlock8;
+        code_gap = code_stride - ((dim + 15) / 16 * 16 - d0);
+        scale_gap = scale_stride - ((dim + kBlock8 - 1) / kBlock8 - d0 / kBlock8);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) code_at[j] = (8 * group + j) * code_stride + d;
+        scale_at = (8 * group + lane % 8) * scale_stride + d / kBlock8;
         auto f = [](int c) { return ((c >> 1) ^ (c >> 4)) & 7; };
 #pragma unroll
         for (int h = 0; h < 2; ++h) put[h] = (col + 2 * h) * 128 + ((group ^ f(col + 2 * h)) << 4);
@@ -64,16 +65,23 @@ struct CodeOperand {
 #pragma unroll
         for (int j = 0; j < 4; ++j) at[j] = r * 128 + (((2 * (j ^ step0) + lane / 32) ^ f(r)) << 4);
     }
-    // the next stage, whose last row is `last` (rows beyond repeat it)
-    template <int FIRST, int END> __device__ inline void load(Codes& c, int last) const {
+    // The next stage, from which on there are `left` rows (none, or some -64 SETS, behind the last stage).  Buffers that end
+    // behind the last row: the loads' own bounds check makes rows beyond zeros, and a lane's offsets are the same in
+    // every stage.  (Strides are no smaller than a row: any place in a row beyond is behind the buffer's end.)
+    template <int FIRST, int END> __device__ inline void load(Codes& c, int left) const {
+        constexpr int kRaw = 0x00027000;
+        const int rows = min(kHeadK, left);
+        const auto codes = __builtin_amdgcn_make_buffer_rsrc(code, 0, max(rows * code_stride - code_gap, 0), kRaw);
 #pragma unroll
-        for (int j = FIRST; j < END; ++j)
-            c.w[j] = *reinterpret_cast<const uint32_t*>(code + (__umul24(min(row + j, last), code_stride) + code_at));
-        if (END == 8) c.byte = scale[__umul24(min(scale_row, last), scale_stride) + scale_at];
+        for (int j = FIRST; j < END; ++j) c.w[j] = __builtin_amdgcn_raw_buffer_load_b32(codes, code_at[j], 0, 0);
+        if (END == 8) {
+            const auto scales = __builtin_amdgcn_make_buffer_rsrc(scale, 0, max(rows * scale_stride - scale_gap, 0), kRaw);
+            c.byte = __builtin_amdgcn_raw_buffer_load_b8(scales, scale_at, 0, 0);
+        }
     }
-    __device__ inline void advance(bool there) {
-        code += there ? code_step : 0;
-        scale += there ? scale_step : 0;
+    __device__ inline void advance() {
+        code += code_step;
+        scale += scale_step;
     }
     // rows 2 M and 2 M + 1: word M of each column's eight values
     struct Decoded {
@@ -81,8 +89,8 @@ struct CodeOperand {
     };
     template <int M> __device__ inline void decode(const Codes& c, Decoded& out) const {
         const int bits = (int)(c.byte << 23);       // row_newbcast: lane n of each 16
-        const float f0 = as_float((uint32_t)__builtin_amdgcn_update_dpp(0, bits, 0x150 + 2 * M, 15, 15, false));
-        const float f1 = as_float((uint32_t)__builtin_amdgcn_update_dpp(0, bits, 0x151 + 2 * M, 15, 15, false));
+        const float f0 = as_float((uint32_t)__builtin_amdgcn_mov_dpp(bits, 0x150 + 2 * M, 15, 15, true));
+        const float f1 = as_float((uint32_t)__builtin_amdgcn_mov_dpp(bits, 0x151 + 2 * M, 15, 15, true));
         auto half = [&](auto h) {
             constexpr bool H = decltype(h)::value;
             const uint32_t a = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)c.w[2 * M], f0, H));
@@ -120,9 +128,8 @@ struct CodeOperand {
 // straight to LDS and the codes of x of k + 1 + SETS to registers, a piece after every product or two.
 // The barrier sits before the products of a stage's last step, whose fragments are in
 // registers by then; the next stage's first ones are read behind it.
-// Near the end the last stage is loaded again, which nothing reads, so that the body has no branch;
-// rows behind the last are zero in the gradient's fragments of the last stage (x has the last
-// row again there).
+// Near the end the gradient's last stage is loaded again and no more of x, which nothing reads, so that the body has no
+// branch; rows behind the last are zero in the gradient's fragments of the last stage (and in x).
 template <int STEPS, int SLOTS, int SETS, int TD, int TC, typename OX, typename OG>
 __device__ inline void k_loop_coded(floatx16 (&acc)[TD][TC], int stages, OX& X, OG& G, int left, int step0, uint32_t lds, int wave, int lane) {
     static_assert(OG::kLoads == 4 && TD * TC == 8 && (STEPS == 2 || STEPS == 4), "pieces of a stage");
@@ -138,12 +145,11 @@ __device__ inline void k_loop_coded(floatx16 (&acc)[TD][TC], int stages, OX& X, 
     typename OX::Codes c[SETS];
     int left_x = left, left_g = left;      // rows from the stage that X and G load next
     auto next_x = [&] {
-        const bool more = left_x > kHeadK;
-        X.advance(more);
-        left_x -= more ? kHeadK : 0;
+        X.advance();
+        left_x -= kHeadK;
     };
     auto load_x = [&](typename OX::Codes& c) {
-        X.template load<0, 8>(c, min(kHeadK, left_x) - 1);
+        X.template load<0, 8>(c, left_x);
         next_x();
     };
     auto load_g = [&](auto j) { G.template load_clamped<decltype(j)::value>(put + mine, min(kHeadK, left_g) - 1); };
@@ -244,10 +250,9 @@ __device__ inline void k_loop_coded(floatx16 (&acc)[TD][TC], int stages, OX& X, 
         x1 = t;
         now = after(now);
         read(0, x0, now, 0);
-        const int last = min(kHeadK, left_x) - 1;
         multiply(1, [&](auto n) {
             constexpr int N = decltype(n)::value;
-            X.template load<N, N + 1>(c, last);
+            X.template load<N, N + 1>(c, left_x);
             if (N == 7) next_x();
         });
     };
