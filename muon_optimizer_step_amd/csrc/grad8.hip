@@ -221,10 +221,11 @@ __device__ inline void k_loop_coded(floatx16 (&acc)[TD][TC], int stages, OX& X, 
             multiply(0, [&](auto n) {
                 constexpr int N = decltype(n)::value;
                 if constexpr (N < 4) X.template decode<N>(c, v);
-                if constexpr (N >= 4) {
-                    X.template store<N - 4>(v, x1);
-                    piece_g(integral_constant<int, N - 4>());
+                if constexpr (N == 4 || N == 5) {        // early: the barrier waits for them
+                    X.template store<2 * (N - 4)>(v, x1);
+                    X.template store<2 * (N - 4) + 1>(v, x1);
                 }
+                if constexpr (N >= 4) piece_g(integral_constant<int, N - 4>());
             });
         } else {
             multiply(0, [&](auto n) {
