@@ -119,12 +119,15 @@ template <typename T> __device__ inline Raw<T> load8(const T* p, int left, bool 
     for (int k = 0; k < 4 * ((int)sizeof(T) / 2); ++k) r.w[k / 4][k % 4] = word[k];
     return r;
 }
-template <bool PAST, typename T> __device__ inline void store8(T* p, const Raw<T>& r, int left, bool vec) {
+// `whole` starts at p0, as p does `at` values on.
+template <bool PAST, typename T>
+__device__ inline void store8(const Through& whole, T* p0, int64_t at, const Raw<T>& r, int left, bool vec) {
+    T* p = p0 + at;
     if (vec && left >= 8) {
 #pragma unroll
         for (int k = 0; k < (int)sizeof(T) / 2; ++k) {
             if constexpr (PAST) __builtin_nontemporal_store(r.w[k], reinterpret_cast<u32x4*>(p) + k);
-            else reinterpret_cast<u32x4*>(p)[k] = r.w[k];
+            else whole.store((int)at * (int)sizeof(T) + 16 * k, r.w[k]);
         }
         return;
     }
@@ -209,7 +212,8 @@ constexpr int kBatch = 2;
 struct Unit {
     int d;               // the lane's first column
     int block;
-    int64_t row, step;   // first row, and from one row of the batch to the next
+    int64_t row0;        // the workgroup's first row
+    int row, step;       // the unit's first row from there on, and from one row of the batch to the next
 };
 template <typename F>
 __device__ inline void for_units(const Rows8& r, F work) {
@@ -222,17 +226,19 @@ __device__ inline void for_units(const Rows8& r, F work) {
         u.block = (int)(item - rg * r.col_groups) * across + (unit & (across - 1));
         u.d = u.block * kBlock8 + 8 * (threadIdx.x % kLanes);
         u.step = kUnits >> r.unit_log;
-        u.row = rg * per + (unit >> r.unit_log);
+        u.row0 = rg * per;
+        u.row = unit >> r.unit_log;
         work(u);
     }
 }
 template <bool PAST>
-__device__ inline void store_codes(const Rows8& r, const Blocks8& b, const Unit& u, int64_t row, const u32x2& w, int byte) {
-    if (row >= r.rows || u.d >= r.dim16) return;
-    u32x2* dst = reinterpret_cast<u32x2*>(b.codes + row * b.stride + u.d);
-    if constexpr (PAST) __builtin_nontemporal_store(w, dst);
-    else *dst = w;
-    if (threadIdx.x % kLanes == 0) b.scale[row * b.scale_stride + u.block] = (uint8_t)byte;
+__device__ inline void store_codes(const Rows8& r, const Blocks8& b, const Unit& u, int row, const u32x2& w, int byte) {
+    if (u.row0 + row >= r.rows || u.d >= r.dim16) return;
+    uint8_t* first = b.codes + u.row0 * b.stride;
+    const int at = row * (int)b.stride + u.d;
+    if constexpr (PAST) __builtin_nontemporal_store(w, reinterpret_cast<u32x2*>(first + at));
+    else Through(first).store(at, w);
+    if (threadIdx.x % kLanes == 0) b.scale[(u.row0 + row) * b.scale_stride + u.block] = (uint8_t)byte;
 }
 
 template <typename T, int ACT, bool KEEP, bool PAST>
@@ -242,12 +248,12 @@ __global__ __launch_bounds__(kThreads) void encode8_kernel(const Encode8 a) {
         const int left = a.r.dim - u.d;
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
-            const int64_t row = u.row + k * u.step;
+            const int64_t row = u.row0 + u.row + k * u.step;
             raw[k] = load8(static_cast<const T*>(a.x) + row * a.x_stride + u.d, row < a.r.rows ? left : 0, a.vec);
         }
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
-            const int64_t row = u.row + k * u.step;
+            const int row = u.row + k * u.step;
             float v[8];
             int byte;
             to_float<T>(raw[k], v);
@@ -274,7 +280,7 @@ __global__ __launch_bounds__(kThreads) void backward8_kernel(const Backward8 a) 
         const int left = a.r.dim - u.d;
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
-            const int64_t row = u.row + k * u.step;
+            const int64_t row = u.row0 + u.row + k * u.step;
             const bool there = row < a.r.rows && left > 0;
             grad[k] = load8(static_cast<const T*>(a.grad) + row * a.grad_stride + u.d, there ? left : 0, a.grad_vec);
             code[k] = u32x2{0u, 0u};
@@ -286,14 +292,16 @@ __global__ __launch_bounds__(kThreads) void backward8_kernel(const Backward8 a) 
         }
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
-            const int64_t row = u.row + k * u.step;
+            const int row = u.row + k * u.step;
             float v[8], g[8];
             decode8(code[k], scale_value(byte[k]), v);
             to_float<T>(grad[k], g);
 #pragma unroll
             for (int e = 0; e < 8; ++e) g[e] *= act_slope<ACT>(v[e]);
-            if (a.out && row < a.r.rows)
-                store8<PAST>(static_cast<T*>(a.out) + row * a.out_stride + u.d, from_float<T>(g), left, a.out_vec);
+            if (a.out && u.row0 + row < a.r.rows) {
+                T* first = static_cast<T*>(a.out) + u.row0 * a.out_stride;
+                store8<PAST>(Through(first), first, row * a.out_stride + u.d, from_float<T>(g), left, a.out_vec);
+            }
             if (a.out8.codes) {
                 int b;
                 const u32x2 w = encode8(g, b);
@@ -309,12 +317,13 @@ __global__ __launch_bounds__(kThreads) void decode8_kernel(const Decode8 a) {
         const int left = a.r.dim - u.d;
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
-            const int64_t row = u.row + k * u.step;
+            const int64_t row = u.row0 + u.row + k * u.step;
             if (row >= a.r.rows || left <= 0) continue;
             const u32x2 w = *reinterpret_cast<const u32x2*>(a.x.codes + row * a.x.stride + u.d);
             float v[8];
             decode8(w, scale_value(a.x.scale[row / a.tall * a.x.scale_stride + u.block]), v);
-            store8<PAST>(static_cast<T*>(a.out) + row * a.out_stride + u.d, from_float<T>(v), left, a.vec);
+            T* first = static_cast<T*>(a.out) + u.row0 * a.out_stride;
+            store8<PAST>(Through(first), first, (row - u.row0) * a.out_stride + u.d, from_float<T>(v), left, a.vec);
         }
     });
 }
@@ -404,6 +413,7 @@ __global__ __launch_bounds__(kThreads) void weight8_kernel(const Weight8 a) {
         a.codes.scale[br * a.codes.scale_stride + bd] = (uint8_t)byte;
         if (a.transposed.codes) a.transposed.scale[bd * a.transposed.scale_stride + br] = (uint8_t)byte;
     }
+    const Through rows_out(a.codes.codes + (int64_t)row0 * a.codes.stride);
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
         uint32_t w[4];
@@ -411,7 +421,7 @@ __global__ __launch_bounds__(kThreads) void weight8_kernel(const Weight8 a) {
         for (int j = 0; j < 4; ++j) {
             const int row = row0 + 4 * (group + 8 * q) + j;
             w[j] = codes4(v[q][j], inverse);
-            if (row < a.rows && d < dim16) *reinterpret_cast<uint32_t*>(a.codes.codes + row * a.codes.stride + d) = w[j];
+            if (row < a.rows && d < dim16) rows_out.store((row - row0) * (int)a.codes.stride + d, w[j]);
         }
         if (a.transposed.codes) {
             // 4 x 4 bytes turned: pairs of rows, then pairs of pairs
@@ -426,6 +436,7 @@ __global__ __launch_bounds__(kThreads) void weight8_kernel(const Weight8 a) {
     }
     if (!a.transposed.codes) return;
     __syncthreads();
+    const Through turned_out(a.transposed.codes + (int64_t)bd * kBlock8 * a.transposed.stride);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
         const int c = threadIdx.x / 8 + 32 * k, chunk = threadIdx.x % 8;
@@ -434,7 +445,7 @@ __global__ __launch_bounds__(kThreads) void weight8_kernel(const Weight8 a) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) w[e] = turned[c][(4 * chunk + e) ^ (c / 4) ^ (c % 4)];
         if (out_row < a.dim && out_col < rows16)
-            *reinterpret_cast<u32x4*>(a.transposed.codes + out_row * a.transposed.stride + out_col) = w;
+            turned_out.store(c * (int)a.transposed.stride + out_col, w);
     }
 }
 

@@ -398,7 +398,9 @@ template <int TV> constexpr int kStageBytes = 32 * 32 * TV * 2;
 template <typename T, int TV, int TT>
 __device__ inline void store_tile(const Matmul8& a, floatx16 (&acc)[TV][TT], int v0, int t0, int lane, uint8_t* stage) {
     constexpr int kChunks = 4 * TV;       // 16-byte chunks of a row; chunk c of row r in slot c ^ (r % kChunks)
-    const int half = lane / 32;
+    const int half = lane / 32, pitch = (int)a.y_stride * 2;
+    T* first = static_cast<T*>(a.y) + (int64_t)t0 * a.y_stride + v0;
+    const Through whole(first);
 #pragma unroll
     for (int tt = 0; tt < TT; ++tt) {
 #pragma unroll
@@ -418,10 +420,10 @@ __device__ inline void store_tile(const Matmul8& a, floatx16 (&acc)[TV][TT], int
             const u32x4 w = *reinterpret_cast<const u32x4*>(stage + (r * kChunks + (c ^ (r % kChunks))) * 16);
             const int row = t0 + 32 * tt + r, v = v0 + 8 * c;
             if (row >= a.rows || v >= a.cols) continue;
-            T* dst = static_cast<T*>(a.y) + (int64_t)row * a.y_stride + v;
             if (a.y_vec && v + 8 <= a.cols) {
-                *reinterpret_cast<u32x4*>(dst) = w;
+                whole.store((32 * tt + r) * pitch + 16 * c, w);
             } else {
+                T* dst = first + (int64_t)(32 * tt + r) * a.y_stride + 8 * c;
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
                     if (v + e < a.cols) dst[e] = __builtin_bit_cast(T, (uint16_t)(w[e / 2] >> (16 * (e % 2))));
