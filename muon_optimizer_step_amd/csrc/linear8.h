@@ -25,6 +25,13 @@ struct Through {
     __device__ inline void store(int offset, uint32_t w) const { __builtin_amdgcn_raw_buffer_store_b32(w, out, offset, 0, kDevice); }
 };
 
+// Between a wave's writes to LDS and what its other lanes read of them, and before it writes there again: LDS keeps a
+// wave's order, and this keeps the compiler from taking some lanes past the others.
+__device__ inline void wave_order() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
 // A matrix in 8 bits: codes and scales, strides in bytes.
 struct Blocks8 {
     uint8_t* codes;

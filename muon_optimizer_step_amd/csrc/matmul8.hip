@@ -398,7 +398,7 @@ template <int TV> constexpr int kStageBytes = 32 * 32 * TV * 2;
 template <typename T, int TV, int TT>
 __device__ inline void store_tile(const Matmul8& a, floatx16 (&acc)[TV][TT], int v0, int t0, int lane, uint8_t* stage) {
     constexpr int kChunks = 4 * TV;       // 16-byte chunks of a row; chunk c of row r in slot c ^ (r % kChunks)
-    const int half = lane / 32, pitch = (int)a.y_stride * 2;
+    const int half = lane / 32, pitch = (int)a.y_stride * 2, mine = lane % kChunks, left = a.cols - v0 - 8 * mine;
     T* first = static_cast<T*>(a.y) + (int64_t)t0 * a.y_stride + v0;
     const Through whole(first);
 #pragma unroll
@@ -413,22 +413,26 @@ __device__ inline void store_tile(const Matmul8& a, floatx16 (&acc)[TV][TT], int
                 const int r = lane % 32, c = 4 * tv + 2 * p + half;
                 *reinterpret_cast<u32x4*>(stage + (r * kChunks + (c ^ (r % kChunks))) * 16) = pack8<T>(v);
             }
-        // the same wave's data: LDS keeps its order
+        wave_order();
+        auto values = [&](int r) { return *reinterpret_cast<const u32x4*>(stage + (r * kChunks + (mine ^ (r % kChunks))) * 16); };
+        const int end = min(32, a.rows - t0 - 32 * tt);
+        if (a.y_vec && left >= 8) {
 #pragma unroll
-        for (int k = 0; k < kChunks / 2; ++k) {
-            const int r = k * (kWave / kChunks) + lane / kChunks, c = lane % kChunks;
-            const u32x4 w = *reinterpret_cast<const u32x4*>(stage + (r * kChunks + (c ^ (r % kChunks))) * 16);
-            const int row = t0 + 32 * tt + r, v = v0 + 8 * c;
-            if (row >= a.rows || v >= a.cols) continue;
-            if (a.y_vec && v + 8 <= a.cols) {
-                whole.store((32 * tt + r) * pitch + 16 * c, w);
-            } else {
-                T* dst = first + (int64_t)(32 * tt + r) * a.y_stride + 8 * c;
+            for (int k = 0; k < kChunks / 2; ++k) {
+                const int r = k * (kWave / kChunks) + lane / kChunks;
+                if (r < end) whole.store((32 * tt + r) * pitch + 16 * mine, values(r));
+            }
+        } else if (left > 0) {
+#pragma unroll 1
+            for (int r = lane / kChunks; r < end; r += kWave / kChunks) {
+                const u32x4 w = values(r);
+                T* dst = first + (int64_t)(32 * tt + r) * a.y_stride + 8 * mine;
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    if (v + e < a.cols) dst[e] = __builtin_bit_cast(T, (uint16_t)(w[e / 2] >> (16 * (e % 2))));
+                    if (e < left) dst[e] = __builtin_bit_cast(T, (uint16_t)(w[e / 2] >> (16 * (e % 2))));
             }
         }
+        wave_order();
     }
 }
 
