@@ -9,10 +9,10 @@
 // implementation.
 //
 // Bound: HBM; every value is read once and written once (a copy of 4 GiB: 4.7 TB/s, reads and
-// writes together).  Measured, inputs from memory: 16384 x 2048 bf16 to its codes and relu2's 25.0 us,
-// 5.4 TB/s; 16384 x 4096 bf16 to codes 34.1 us, 5.9; relu2's backward of 16384 x 4096, in 16 and in
-// 8 bits, 62 us, 6.6 TB/s; gelu's and silu's 88 and 85 us, for which the vector unit is the limit;
-// 8192 x 8192 float32 weights to codes and transposed codes 77 us, 5.2 TB/s; 16384 x 4096 codes to
+// writes together).  Measured, inputs from memory: 16384 x 2048 bf16 to its codes and relu2's 23.1 us,
+// 5.8 TB/s; 16384 x 4096 bf16 to codes 31.2 us, 6.5; relu2's backward of 16384 x 4096, in 16 and in
+// 8 bits, 69 us, 5.9 TB/s; gelu's and silu's 92 and 80 us, for which the vector unit is the limit;
+// 8192 x 8192 float32 weights to codes and transposed codes 74 us, 5.5 TB/s; 16384 x 4096 codes to
 // bf16 30 us, 6.6.  Small calls are a launch: 2048 values 2.9 us of kernel time.
 #include <algorithm>
 #include <type_traits>
@@ -231,17 +231,13 @@ __device__ inline void for_units(const Rows8& r, F work) {
         work(u);
     }
 }
-template <bool PAST>
 __device__ inline void store_codes(const Rows8& r, const Blocks8& b, const Unit& u, int row, const u32x2& w, int byte) {
     if (u.row0 + row >= r.rows || u.d >= r.dim16) return;
-    uint8_t* first = b.codes + u.row0 * b.stride;
-    const int at = row * (int)b.stride + u.d;
-    if constexpr (PAST) __builtin_nontemporal_store(w, reinterpret_cast<u32x2*>(first + at));
-    else Through(first).store(at, w);
+    Through(b.codes + u.row0 * b.stride).store(row * (int)b.stride + u.d, w);
     if (threadIdx.x % kLanes == 0) b.scale[(u.row0 + row) * b.scale_stride + u.block] = (uint8_t)byte;
 }
 
-template <typename T, int ACT, bool KEEP, bool PAST>
+template <typename T, int ACT, bool KEEP>
 __global__ __launch_bounds__(kThreads) void encode8_kernel(const Encode8 a) {
     for_units(a.r, [&](const Unit& u) {
         Raw<T> raw[kBatch];
@@ -259,13 +255,13 @@ __global__ __launch_bounds__(kThreads) void encode8_kernel(const Encode8 a) {
             to_float<T>(raw[k], v);
             if (KEEP) {
                 const u32x2 w = encode8(v, byte);
-                store_codes<PAST>(a.r, a.codes, u, row, w, byte);
+                store_codes(a.r, a.codes, u, row, w, byte);
             }
             if (ACT != kActNone) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) v[e] = act<ACT>(v[e]);
                 const u32x2 w = encode8(v, byte);
-                store_codes<PAST>(a.r, a.out, u, row, w, byte);
+                store_codes(a.r, a.out, u, row, w, byte);
             }
         }
     });
@@ -305,7 +301,7 @@ __global__ __launch_bounds__(kThreads) void backward8_kernel(const Backward8 a) 
             if (a.out8.codes) {
                 int b;
                 const u32x2 w = encode8(g, b);
-                store_codes<PAST>(a.r, a.out8, u, row, w, b);
+                store_codes(a.r, a.out8, u, row, w, b);
             }
         }
     });
@@ -334,8 +330,8 @@ __global__ __launch_bounds__(kThreads) void decode8_kernel(const Decode8 a) {
 // in words: rows straight to memory (32 lanes cover a row's 128 bytes), columns
 // through LDS, whose word (column, 4 rows) sits in slot rows ^ column / 4 ^ column % 4 of its
 // column: the 32 lanes that write a row group meet 32 different banks, and so do those that read four columns.
-// 8192 x 8192 float32 77 us, 64 where consecutive calls have one input (5.2 and 6.3 TB/s); bfloat16 56 and 44 us, with
-// loads that wait for one another 72; 512 x 512 3.9 us: 16 workgroups, a launch.
+// 8192 x 8192 float32 74 us, 62 where consecutive calls have one input (5.5 and 6.5 TB/s); bfloat16 54 and 43 us (56 and 44
+// with its results left in the L2, 72 with loads that wait for one another besides); 512 x 512 4.0 us: 16 workgroups, a launch.
 template <typename T> using Quad = std::conditional_t<sizeof(T) == 4, u32x4, u32x2>;      // 4 values as they lie in memory
 template <typename T>
 __global__ __launch_bounds__(kThreads) void weight8_kernel(const Weight8 a) {
@@ -455,9 +451,7 @@ int rows_grid(const Rows8& r) { return (int)std::min<int64_t>((int64_t)r.row_gro
 
 template <typename T, int ACT, bool KEEP>
 hipError_t encode_kept(const Encode8& a, hipStream_t s) {
-    const int grid = rows_grid(a.r);
-    if (a.r.past) encode8_kernel<T, ACT, KEEP, true><<<grid, kThreads, 0, s>>>(a);
-    else encode8_kernel<T, ACT, KEEP, false><<<grid, kThreads, 0, s>>>(a);
+    encode8_kernel<T, ACT, KEEP><<<rows_grid(a.r), kThreads, 0, s>>>(a);
     return hipGetLastError();
 }
 template <typename T, int ACT>
@@ -492,11 +486,12 @@ hipError_t decode_typed(const Decode8& a, hipStream_t s) {
     return hipGetLastError();
 }
 
-// What a pass writes, from which on it is written past the caches: the last one keeps too little
-// of it for the next pass to find (the layer 16384 x 1024 x 4096, whose gradient's 201 MB are written so: the backward
-// pass with both products behind it 257 us against 259, alone 62 against 73).  Below, what follows
-// finds it there (4096 x 1024 x 4096, encode and product: 42 us, 48 past the caches).  A template's
-// argument: as a branch, the two stores become one without the hint.
+// What a pass writes, from which on its 16 or 32-bit values are written past the caches: the last one keeps too
+// little of them for the next pass to find, and has room for the codes, which a product reads next.  The layer
+// 16384 x 1024 x 4096, whose gradient's 201 MB are written so: the backward pass with both products behind it 248 us;
+// nothing past the caches 254, the codes too 260 (alone 69, 69 and 62).  Below, what follows finds it there
+// (4096 x 1024 x 4096, encode and product: 42 us, 48 past the caches).  A template's argument: as a branch, the two
+// stores become one without the hint.
 constexpr int64_t kPastBytes = (int64_t)192 << 20;
 Rows8 plan(const Rows8& r, int64_t bytes_per_value) {
     Rows8 q = r;
@@ -515,7 +510,7 @@ Rows8 plan(const Rows8& r, int64_t bytes_per_value) {
 
 hipError_t launch_encode8(const Encode8& a0, int type, int act, hipStream_t s) {
     Encode8 a = a0;
-    a.r = plan(a0.r, (a.codes.codes != nullptr) + (a.out.codes != nullptr));
+    a.r = plan(a0.r, 0);
     if (type == kTypeBf16) return encode_act<bf16>(a, act, s);
     return type == kTypeFp16 ? encode_act<f16>(a, act, s) : encode_act<float>(a, act, s);
 }
