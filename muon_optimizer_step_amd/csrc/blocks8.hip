@@ -100,12 +100,12 @@ template <typename T> __device__ inline Raw<T> from_float(const float* v) {
     }
     return r;
 }
-// `left` values are there (zeros behind them); vec: p is 16-byte aligned.
-template <typename T> __device__ inline Raw<T> load8(const T* p, int left, bool vec) {
+// `left` values are there (zeros behind them).
+template <typename T> __device__ inline Raw<T> load8(const T* p, int left) {
     Raw<T> r;
-    if (vec && left >= 8) {
+    if (left >= 8) {
 #pragma unroll
-        for (int k = 0; k < (int)sizeof(T) / 2; ++k) r.w[k] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p) + k);
+        for (int k = 0; k < (int)sizeof(T) / 2; ++k) r.w[k] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_any*>(p) + k);
         return r;
     }
     uint32_t word[4 * (sizeof(T) / 2)] = {};
@@ -119,7 +119,7 @@ template <typename T> __device__ inline Raw<T> load8(const T* p, int left, bool 
     for (int k = 0; k < 4 * ((int)sizeof(T) / 2); ++k) r.w[k / 4][k % 4] = word[k];
     return r;
 }
-// `whole` starts at p0, as p does `at` values on.
+// To p0 + at, `whole` starts at p0; vec: p0 + at is 16-byte aligned.
 template <bool PAST, typename T>
 __device__ inline void store8(const Through& whole, T* p0, int64_t at, const Raw<T>& r, int left, bool vec) {
     T* p = p0 + at;
@@ -129,6 +129,11 @@ __device__ inline void store8(const Through& whole, T* p0, int64_t at, const Raw
             if constexpr (PAST) __builtin_nontemporal_store(r.w[k], reinterpret_cast<u32x4*>(p) + k);
             else whole.store((int)at * (int)sizeof(T) + 16 * k, r.w[k]);
         }
+        return;
+    }
+    if (left >= 8) {
+#pragma unroll
+        for (int k = 0; k < (int)sizeof(T) / 2; ++k) reinterpret_cast<u32x4_any*>(p)[k] = r.w[k];
         return;
     }
 #pragma unroll
@@ -245,7 +250,7 @@ __global__ __launch_bounds__(kThreads) void encode8_kernel(const Encode8 a) {
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
             const int64_t row = u.row0 + u.row + k * u.step;
-            raw[k] = load8(static_cast<const T*>(a.x) + row * a.x_stride + u.d, row < a.r.rows ? left : 0, a.vec);
+            raw[k] = load8(static_cast<const T*>(a.x) + row * a.x_stride + u.d, row < a.r.rows ? left : 0);
         }
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
@@ -278,7 +283,7 @@ __global__ __launch_bounds__(kThreads) void backward8_kernel(const Backward8 a) 
         for (int k = 0; k < kBatch; ++k) {
             const int64_t row = u.row0 + u.row + k * u.step;
             const bool there = row < a.r.rows && left > 0;
-            grad[k] = load8(static_cast<const T*>(a.grad) + row * a.grad_stride + u.d, there ? left : 0, a.grad_vec);
+            grad[k] = load8(static_cast<const T*>(a.grad) + row * a.grad_stride + u.d, there ? left : 0);
             code[k] = u32x2{0u, 0u};
             byte[k] = kScale8Low;
             if (there) {
@@ -333,6 +338,10 @@ __global__ __launch_bounds__(kThreads) void decode8_kernel(const Decode8 a) {
 // 8192 x 8192 float32 74 us, 62 where consecutive calls have one input (5.5 and 6.5 TB/s); bfloat16 54 and 43 us (56 and 44
 // with its results left in the L2, 72 with loads that wait for one another besides); 512 x 512 4.0 us: 16 workgroups, a launch.
 template <typename T> using Quad = std::conditional_t<sizeof(T) == 4, u32x4, u32x2>;      // 4 values as they lie in memory
+template <typename T> __device__ inline Quad<T> load_quad(const T* p) {
+    if constexpr (sizeof(T) == 4) return __builtin_nontemporal_load(reinterpret_cast<const u32x4_any*>(p));
+    else return __builtin_nontemporal_load(reinterpret_cast<const u32x2_any*>(p));
+}
 template <typename T>
 __global__ __launch_bounds__(kThreads) void weight8_kernel(const Weight8 a) {
     __shared__ uint32_t tops[kThreads / kWave];
@@ -346,11 +355,11 @@ __global__ __launch_bounds__(kThreads) void weight8_kernel(const Weight8 a) {
     auto at = [&](int q, int j) {
         return static_cast<const T*>(a.w) + (int64_t)min(row0 + 4 * (group + 8 * q) + j, a.rows - 1) * a.w_stride + d;
     };
-    if (a.vec && d + 4 <= a.dim) {
+    if (d + 4 <= a.dim) {
 #pragma unroll
         for (int q = 0; q < 4; ++q)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) raw[q][j] = __builtin_nontemporal_load(reinterpret_cast<const Quad<T>*>(at(q, j)));
+            for (int j = 0; j < 4; ++j) raw[q][j] = load_quad<T>(at(q, j));
     } else {
 #pragma unroll
         for (int q = 0; q < 4; ++q)

@@ -293,8 +293,8 @@ __device__ inline void store_tile(const Grad8& a, floatx16 (&acc)[TD][TC], int s
     const int64_t pitch = a.partial ? a.partial_pitch : a.out_stride;
     float* first = a.partial ? a.partial + ((int64_t)split * a.cols + c0) * pitch + d0 : a.out + c0 * pitch + d0;
     const Through whole(first);
-    const bool add = !a.partial && a.accumulate, vec = a.partial || a.out_vec;
     const int mine = lane % kChunks, d = d0 + 4 * mine;
+    const bool add = !a.partial && a.accumulate, vec = a.partial || (a.out_vec && d + 4 <= a.dim);
 #pragma unroll
     for (int j = 0; j < TC; ++j) {
 #pragma unroll
@@ -318,11 +318,16 @@ __device__ inline void store_tile(const Grad8& a, floatx16 (&acc)[TD][TC], int s
                 if (add) v += *reinterpret_cast<const floatx4*>(first + row * pitch + 4 * mine);
                 whole.store((row * (int)pitch + 4 * mine) * 4, __builtin_bit_cast(u32x4, v));
             }
-        } else {
-#pragma unroll 1
+        } else {       // rows that are not aligned, or that end in this chunk
+#pragma unroll 2
             for (int r = lane / kChunks; r < end; r += kWave / kChunks) {
-                const floatx4 v = sums(r);
+                floatx4 v = sums(r);
                 float* dst = first + (32 * j + r) * pitch + 4 * mine;
+                if (d + 4 <= a.dim) {
+                    if (add) v += *reinterpret_cast<const floatx4_any*>(dst);
+                    *reinterpret_cast<floatx4_any*>(dst) = v;
+                    continue;
+                }
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                     if (d + e < a.dim) dst[e] = v[e] + (add ? dst[e] : 0.f);
@@ -425,9 +430,9 @@ __global__ __launch_bounds__(kJoinThreads) void join8_kernel(const Join8 a) {
         }
         for (; s < a.splits; ++s, src += step) v += *reinterpret_cast<const floatx4*>(src);
         float* dst = a.out + c * a.out_stride + d;
-        if (a.out_vec) {
-            if (a.accumulate) v += *reinterpret_cast<const floatx4*>(dst);
-            *reinterpret_cast<floatx4*>(dst) = v;
+        if (d + 4 <= a.dim) {
+            if (a.accumulate) v += *reinterpret_cast<const floatx4_any*>(dst);
+            *reinterpret_cast<floatx4_any*>(dst) = v;
         } else {
 #pragma unroll
             for (int e = 0; e < 4; ++e)

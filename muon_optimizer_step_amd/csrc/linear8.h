@@ -25,6 +25,11 @@ struct Through {
     __device__ inline void store(int offset, uint32_t w) const { __builtin_amdgcn_raw_buffer_store_b32(w, out, offset, 0, kDevice); }
 };
 
+// 16 and 8 bytes at any multiple of 2: the same instructions as at their own alignment.
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
+typedef u32x2 u32x2_any __attribute__((aligned(2)));
+typedef floatx4 floatx4_any __attribute__((aligned(4)));
+
 // Between a wave's writes to LDS and what its other lanes read of them, and before it writes there again: LDS keeps a
 // wave's order, and this keeps the compiler from taking some lanes past the others.
 __device__ inline void wave_order() {
@@ -52,7 +57,6 @@ struct Encode8 {
     Rows8 r;
     const void* x;
     int64_t x_stride;        // elements
-    int vec;                 // rows of x 16-byte aligned
     Blocks8 codes, out;      // codes NULL: not wanted
 };
 struct Backward8 {
@@ -61,7 +65,7 @@ struct Backward8 {
     const void* grad;
     void* out;
     int64_t grad_stride, out_stride;
-    int grad_vec, out_vec;
+    int out_vec;             // rows of out 16-byte aligned
 };
 struct Decode8 {
     Rows8 r;
@@ -74,7 +78,7 @@ struct Decode8 {
 struct Weight8 {
     const void* w;
     int64_t w_stride;
-    int rows, dim, vec;
+    int rows, dim;
     Blocks8 codes, transposed;
 };
 

@@ -256,7 +256,7 @@ int act8_encode(const act8_encode_t* problem, void* stream) {
     if (const int rc = c.done()) return rc;
     if (p.rows == 0) return MUON_OK;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    const Encode8 a = {rows8(p.rows, p.dim), p.x, p.x_stride, whole_rows(p.x, p.x_stride, size_of(p.dtype)), blocks(p.codes), blocks(p.out)};
+    const Encode8 a = {rows8(p.rows, p.dim), p.x, p.x_stride, blocks(p.codes), blocks(p.out)};
     LINEAR8_TRY("act8_encode", launch_encode8(a, p.dtype, p.activation, s));
     return MUON_OK;
 }
@@ -299,7 +299,7 @@ int act8_backward(const act8_backward_t* problem, void* stream) {
     if (p.rows == 0) return MUON_OK;
     hipStream_t s = static_cast<hipStream_t>(stream);
     const Backward8 a = {rows8(p.rows, p.dim), blocks(p.u), blocks(p.out8), p.grad, p.out, p.grad_stride, p.out_stride,
-                         whole_rows(p.grad, p.grad_stride, size), whole_rows(p.out, p.out_stride, size)};
+                         whole_rows(p.out, p.out_stride, size)};
     LINEAR8_TRY("act8_backward", launch_backward8(a, p.dtype, p.activation, s));
     return MUON_OK;
 }
@@ -317,8 +317,7 @@ int weight8_encode(const weight8_encode_t* problem, void* stream) {
     if (p.transposed.codes) c.coded("transposed", p.transposed, p.dim, p.rows, MUON_BLOCK8, true);
     if (const int rc = c.done()) return rc;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    const Weight8 a = {p.weight, p.weight_stride, (int)p.rows, (int)p.dim, whole_rows(p.weight, p.weight_stride, size_of(p.dtype)),
-                       blocks(p.codes), blocks(p.transposed)};
+    const Weight8 a = {p.weight, p.weight_stride, (int)p.rows, (int)p.dim, blocks(p.codes), blocks(p.transposed)};
     LINEAR8_TRY("weight8_encode", launch_weight8(a, p.dtype, s));
     return MUON_OK;
 }

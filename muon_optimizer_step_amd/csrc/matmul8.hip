@@ -422,11 +422,15 @@ __device__ inline void store_tile(const Matmul8& a, floatx16 (&acc)[TV][TT], int
                 const int r = k * (kWave / kChunks) + lane / kChunks;
                 if (r < end) whole.store((32 * tt + r) * pitch + 16 * mine, values(r));
             }
-        } else if (left > 0) {
-#pragma unroll 1
+        } else if (left > 0) {       // rows that are not aligned, or that end in this chunk
+#pragma unroll 2
             for (int r = lane / kChunks; r < end; r += kWave / kChunks) {
                 const u32x4 w = values(r);
                 T* dst = first + (int64_t)(32 * tt + r) * a.y_stride + 8 * mine;
+                if (left >= 8) {
+                    *reinterpret_cast<u32x4_any*>(dst) = w;
+                    continue;
+                }
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
                     if (e < left) dst[e] = __builtin_bit_cast(T, (uint16_t)(w[e / 2] >> (16 * (e % 2))));
@@ -560,8 +564,8 @@ __global__ __launch_bounds__(kJoinThreads) void matmul8_join_kernel(const Matmul
         }
         const float sums[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
         T* dst = static_cast<T*>(a.y) + row * a.y_stride + v;
-        if (a.y_vec && v + 8 <= a.cols) {
-            *reinterpret_cast<u32x4*>(dst) = pack8<T>(sums);
+        if (v + 8 <= a.cols) {
+            *reinterpret_cast<u32x4_any*>(dst) = pack8<T>(sums);
         } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e)
@@ -722,8 +726,8 @@ __global__ __launch_bounds__(NW * kWave) void matmul8_split_kernel(const Matmul8
         if (row >= a.rows || v >= a.cols) continue;
         T* dst = static_cast<T*>(a.y) + (int64_t)row * a.y_stride + v;
         const float sums[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-        if (a.y_vec && v + 8 <= a.cols) {
-            *reinterpret_cast<u32x4*>(dst) = pack8<T>(sums);
+        if (v + 8 <= a.cols) {
+            *reinterpret_cast<u32x4_any*>(dst) = pack8<T>(sums);
         } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e)
