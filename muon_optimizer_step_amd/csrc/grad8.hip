@@ -318,18 +318,21 @@ __device__ inline void store_tile(const Grad8& a, floatx16 (&acc)[TD][TC], int s
                 if (add) v += *reinterpret_cast<const floatx4*>(first + row * pitch + 4 * mine);
                 whole.store((row * (int)pitch + 4 * mine) * 4, __builtin_bit_cast(u32x4, v));
             }
-        } else {       // rows that are not aligned, or that end in this chunk
-#pragma unroll 2
+        } else if (d + 4 <= a.dim) {       // rows that are not aligned
+#pragma unroll 8
             for (int r = lane / kChunks; r < end; r += kWave / kChunks) {
                 floatx4 v = sums(r);
+                floatx4_any* dst = reinterpret_cast<floatx4_any*>(first + (32 * j + r) * pitch + 4 * mine);
+                if (add) v += *dst;
+                *dst = v;
+            }
+        } else {                           // that end in this chunk
+#pragma unroll 4
+            for (int r = lane / kChunks; r < end; r += kWave / kChunks) {
+                const floatx4 v = sums(r);
                 float* dst = first + (32 * j + r) * pitch + 4 * mine;
-                if (d + 4 <= a.dim) {
-                    if (add) v += *reinterpret_cast<const floatx4_any*>(dst);
-                    *reinterpret_cast<floatx4_any*>(dst) = v;
-                    continue;
-                }
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
+                for (int e = 0; e < 3; ++e)
                     if (d + e < a.dim) dst[e] = v[e] + (add ? dst[e] : 0.f);
             }
         }
