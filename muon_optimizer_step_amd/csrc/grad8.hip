@@ -8,10 +8,11 @@
 // conversions and two 16-byte writes.  The products are 16-bit ones with the gradient as it is.
 //
 // Bound and measured: for large problems LDS (a stage of a 256 x 256 tile takes 2800 of its cycles, 2048 of the matrix
-// unit's) with MFMA close behind: 8192 x 8192 x 4096 (rows, cols, dim) 437 us, 1.26 PFLOP/s; 65 % of the cycles MFMA busy, no bank
-// conflicts.  For small matrices and many rows what a compute unit loads (24 KB a stage at 50 GB/s) and
-// the split of K, whose partial sums go through the caches: 16384 x 2048 x 512 50 us, of which start, partial sums and
-// join 17; the data in the last cache 48.  Few rows: a launch and some latencies, 64 x 512 x 512 5.8 us, 1024 x 512 x 512 11.5.
+// unit's) with MFMA close behind: 8192 x 8192 x 4096 (rows, cols, dim) 418 to 429 us, 1.28 to 1.31 PFLOP/s; 70 % of the cycles MFMA busy, no bank
+// conflicts.  For small matrices and many rows what a compute unit loads (24 KB a stage at 50 GB/s) and what its
+// waves issue (one for each SIMD: 150 instructions a stage, 4 cycles each), and the split of K, whose partial sums
+// go through memory: 16384 x 2048 x 512 47 to 48 us, of which start, partial sums and join some 15; the data in the last
+// cache 44.  Few rows: a launch and some latencies, 64 x 512 x 512 5.6 us, 1024 x 512 x 512 10.3.
 #include <algorithm>
 
 #include "linear8.h"
@@ -415,8 +416,8 @@ __global__ __launch_bounds__((GradTile<EDGE, DEEP>::kThreads), DEEP ? 1 : 2) voi
     }
 }
 
-// The splits' sums in order, added to what is there.  5.8 us for 4 parts of 2048 x 512.  Parts written past the caches, or read
-// so, cost 2 to 4 us more.
+// The splits' sums in order, added to what is there.  5.8 us for 4 parts of 2048 x 512.  Parts written past the last cache, or
+// read so, cost 2 to 4 us more.
 __global__ __launch_bounds__(kJoinThreads) void join8_kernel(const Join8 a) {
     const int64_t quads = (a.dim + 3) / 4, items = quads * a.cols, step = (int64_t)a.cols * a.partial_pitch;
     for (int64_t n = (int64_t)blockIdx.x * kJoinThreads + threadIdx.x; n < items; n += (int64_t)gridDim.x * kJoinThreads) {
@@ -459,8 +460,8 @@ hipError_t launch(const Grad8& a, hipStream_t s) {
 hipError_t launch_grad8(const Grad8& a, int edge, hipStream_t s) {
     if (edge == 256) return launch<256, false>(a, s);
     // One workgroup per compute unit and many stages: the deep form (16384 x 2048 x 512, 64 stages, the data past the last
-    // cache / in it: 50.5 / 47.8 us against 59.4 / 46.9).  Few stages do not earn its longer start (22: 25.1 against
-    // 23.5), and two workgroups hide each other's loads (512 of 32 stages: 60.6 against 54.0).
+    // cache / in it: 50.5 / 47.8 us against 59.4 / 46.9).  Few stages do not earn its longer start and code (22: 25.1
+    // against 23.5; 1 to 8: 1 us more), and two workgroups hide each other's loads (512 of 32 stages: 60.6 against 54.0).
     const bool deep = a.tiles_c * a.tiles_d * a.splits <= 256 && a.stages_per_split >= 40;
     return deep ? launch<128, true>(a, s) : launch<128, false>(a, s);
 }

@@ -50,7 +50,7 @@ struct Rows8 {
     int64_t rows;
     int dim, dim16;          // dim rounded up to 16
     int unit_log, col_groups, row_groups;      // at most 2^30 of both together
-    int past;                // written past the caches
+    int past;                // 16 and 32-bit results are written past the caches
 };
 
 struct Encode8 {

@@ -123,7 +123,8 @@ struct MatmulPlan {
 };
 // Up to 16 rows one kernel; beyond, what a linear estimate of the time says is least: a start, for
 // each round of 256 workgroups the stages of K and the tile's ends, and for a split K the partial sums.  The constants are
-// fitted to measured times (us; rows x cols x dim, tiles of 32 / 64 / 128 / 256, K split where the estimate splits):
+// fitted to these times (us, before results passed the L2, which takes 0 to 2 us off each; rows x cols x dim, tiles of
+// 32 / 64 / 128 / 256, K split where the estimate splits):
 //     17 x 512 x 512         4.1 /  4.5 /  4.9 /  8.4        2048 x 2048 x 512    29 /  9.6 /  6.6 / 10.3
 //     17 x 512 x 8192       14.9 /  7.9 / 11.1 / 67          2048 x 4096 x 1024   89 / 22   / 12.9 / 15.6
 //     64 x 8192 x 8192      35.6 / 20   / 21.9 / 70          4096 x 2048 x 2048  150 / 35   / 21   / 25
@@ -175,7 +176,7 @@ struct GradPlan {
     int64_t cols8, dim8;
     int64_t grad, partial, bytes; // offsets, -1: not there
 };
-// As plan_matmul, for tiles of 128 and 256 and any of the splits below.  Measured (us; rows x cols x dim: tile / splits):
+// As plan_matmul, for tiles of 128 and 256 and any of the splits below.  Fitted to (us; rows x cols x dim: tile / splits):
 //     16384 x 2048 x 512    128/4 50, 128/8 54, 256/12 51        8192 x 8192 x 4096    128/1 574, 256/1 437
 //     65536 x 128 x 128     128/32 28, 128/64 23                 16384 x 4096 x 1024   256/4 128
 //     16384 x 512 x 512     128/12 21                            512 x 512 x 512       128/1 9.8 (256 rows 7.5: a split saves nothing)

@@ -13,9 +13,9 @@
 // enter the float32 accumulators: 2.6e-5 of y in norm, where rounding y to 16 bits costs 1.7e-3
 // (bfloat16) or 2e-4 (float16).  A float32 y would show the difference, so there is none.
 //
-// Bound and measured: MFMA for large problems (8192^3: 432 us, 2.55 PFLOP/s; 400 us, 2.75, where consecutive calls
+// Bound and measured: MFMA for large problems (8192^3: 432 to 440 us, 2.5 PFLOP/s; 400 us, 2.75, where consecutive calls
 // have one input; a library's 8-bit product with one scale for each matrix reaches 2.64; MFMA busy two
-// thirds of the cycles); y's bytes where K is short (16384 x 2048 x 512: 24 to 29 us, 3.2 TB/s at best; MFMA 21 %); the weights' bytes where there are
+// thirds of the cycles); y's bytes where K is short (16384 x 2048 x 512: 25.6 us, 3.0 TB/s; MFMA 23 %); the weights' bytes where there are
 // few rows (1 x 8192 x 8192 13 us, 5.2 TB/s; 64 x 8192 x 8192 20 us); below, a launch (1 x 4096 x 1024 4.2 us, of which
 // 3.2 in the kernel).  Rows of codes off the 128-byte grid cost a quarter (3000 x 700 x 5000: 40 us, K = 4992 32),
 // so encoded matrices have whole lines where dim > 512.
@@ -243,7 +243,7 @@ template <int LOADS> __device__ inline void wait_stages(int stages) {
 }
 
 // The same for tiles of 128 x 128 by 4 waves, two buffers, two workgroups on a compute unit that fill
-// each other's waits: 4096 x 2048 x 2048 21 us (64: 35, 256: 25).
+// each other's waits: 4096 x 2048 x 2048 19 us (64: 35, 256: 25).
 template <int TA, int TB, typename OA, typename OB>
 __device__ inline void k_loop8_mid(floatx16 (&acc)[TA][TB], int stages, OA& A, OB& B, int left, uint32_t lds, int wave,
                                    Scales<TA, TB>& s) {
