@@ -85,7 +85,7 @@ def draw(rng):
         return {"op": op, "out": out, "dim": dim, "dtype": rng.choice(["fp32", "fp32", "bf16"])}
     case = {"op": op, "rows": _log_int(rng, 1, 16384), "out": out, "dim": dim}
     if op == "matmul":
-        case["dtype"] = rng.choice(["bf16", "bf16", "fp16"])
+        case["dtype"] = rng.choice(["bf16", "bf16", "fp16", "fp32"])
         most = 8192 ** 3
     else:
         case["add"] = rng.random() < 0.5
@@ -115,7 +115,7 @@ def work(case):
         return {"bytes": 2 * _size(case["dtype"]) * n * dim + _coded(n, dim) * (2 if case["codes"] else 1), "flops": 8.0 * n * dim}
     o = case["out"]
     if op == "matmul":
-        return {"bytes": _coded(n, dim) + _coded(o, dim, BLOCK) + 2.0 * n * o, "flops": 2.0 * n * o * dim}
+        return {"bytes": _coded(n, dim) + _coded(o, dim, BLOCK) + _size(case["dtype"]) * n * o, "flops": 2.0 * n * o * dim}
     return {"bytes": 2.0 * n * o + _coded(n, dim) + (8.0 if case["add"] else 4.0) * o * dim, "flops": 2.0 * n * o * dim}
 
 
