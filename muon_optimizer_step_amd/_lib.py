@@ -112,7 +112,7 @@ class Weight8Encode(ctypes.Structure):
 
 
 class Matmul8(ctypes.Structure):
-    _fields_ = _fields(blocks="a b", ptr="y", i64="rows cols dim y_stride", i32="dtype")
+    _fields_ = _fields(blocks="a b", ptr="y", i64="rows cols dim y_stride", i32="dtype exact")
 
 
 class Act8GradWeight(ctypes.Structure):

@@ -93,8 +93,9 @@ hipError_t launch_weight8(const Weight8& a, int type, hipStream_t s);
 constexpr int kJoinThreads = 64, kJoinBatch = 4;
 
 // y = a b^T.
-// Kernels: up to 16 rows; 32 x 32 with K split over the waves; tiles of 64, 128 and 256.
-enum Matmul8Variant { kMatmulRows = 0, kMatmulSplit, kMatmulSmall, kMatmulMid, kMatmulTile };
+// Kernels: up to 16 rows; 32 x 32 with K split over the waves; tiles of 64, 128 and 256; tiles of 64 and 128 with exact
+// products, whose result may be float32.
+enum Matmul8Variant { kMatmulRows = 0, kMatmulSplit, kMatmulSmall, kMatmulMid, kMatmulTile, kMatmulExactSmall, kMatmulExactMid };
 struct Matmul8 {
     Blocks8 a, b;
     void* y;
@@ -102,7 +103,7 @@ struct Matmul8 {
     int rows, cols, dim;
     int y_vec;               // rows of y 16-byte aligned
     int tiles_v, tiles_t;    // tiles along cols and rows
-    int splits, stages_per_split;    // parts of K (kMatmulSmall, kMatmulMid; 1 otherwise), a multiple of 4 stages of 128 each
+    int splits, stages_per_split;    // parts of K (tiles of 64 and 128; 1 otherwise), a multiple of 4 stages of 128 each
     float* partial;          // nullable: [split][rows][partial_pitch]
     int64_t partial_pitch;
 };

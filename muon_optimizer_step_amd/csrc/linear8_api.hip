@@ -131,29 +131,40 @@ struct MatmulPlan {
 //     128 x 1024 x 1024      4.5 /  5.5 /  7.6 / 13          16384 x 2048 x 512  213 / 59   / 27.4 / 23.6
 //     256 x 4096 x 4096     36   / 11.1 / 19.6 / 38.6        4096^3              562 / 121  / 70.5 / 56.5
 //     2048 x 512 x 512       8.8 /  4.7 /  5.8 /  9.6        8192^3                -        / 520  / 432
+// With exact products tiles of 64, two of which a compute unit takes in the time of one, and 128; float32 results, 64 / 128:
+//     1 x 8192 x 8192       22.8 / 25.4 (2 and 4 parts)      2048 x 4096 x 1024   27.8 / 26.8
+//     17 x 512 x 8192        8.4 / 14.6 (16 and 8)           4096 x 2048 x 2048   46.9 / 43.3
+//     256 x 4096 x 4096     21.7 / 26.9 (1 and 4)            16384 x 512 x 2048   46.5 / 41.0
+//     1021 x 2000 x 1000    11.0 / 14.6                      4096^3              164   / 142
+//     2048 x 2048 x 512     11.7 / 13.3                      8192^3                -   / 1020
 MatmulPlan plan_matmul(const matmul8_t& p) {
     const int all = (int)ceil_div(p.dim, kBlock8);
     MatmulPlan best = {kMatmulRows, 16, 16, 1, all, 256};
-    if (p.rows <= 16) return best;
+    if (p.rows <= 16 && !p.exact) return best;
     double least = 1e300;
-    auto consider = [&](int variant, int tile, double start, double stage, double ends, int most_splits) {
+    auto consider = [&](int variant, int tile, double start, double stage, double ends, int most_splits, int round = kCus) {
         const int64_t tiles = ceil_div(p.rows, tile) * ceil_div(p.cols, tile);
         for (int splits = 1; splits <= most_splits; splits *= 2) {
             const int stages = splits == 1 ? all : (int)round_up(ceil_div(all, splits), 4);
             const int parts = (int)ceil_div(all, stages);
             if (splits > 1 && (parts < 2 || tiles * parts > kCus)) break;
             const double partial = (double)parts * p.rows * p.cols * 8;      // bytes, written and read
-            const double us = start + ceil_div(tiles * parts, kCus) * (stages * stage + ends) + (parts > 1 ? 2.5 + parts * 0.06 + partial * 2e-7 : 0.0);
+            const double us = start + ceil_div(tiles * parts, round) * (stages * stage + ends) + (parts > 1 ? 2.5 + parts * 0.06 + partial * 2e-7 : 0.0);
             if (us < least) {
                 least = us;
                 best = {variant, tile, tile, parts, stages, 256};
             }
         }
     };
-    consider(kMatmulSplit, 32, 2.5, 0.20, 0.6, 1);
-    consider(kMatmulSmall, 64, 2.6, 0.24, 0.9, 64);
-    consider(kMatmulMid, 128, 3.5, 0.56, 0.75, 8);
-    consider(kMatmulTile, 256, 3.5, 1.55, 4.4, 1);
+    if (p.exact) {
+        consider(kMatmulExactSmall, 64, 3.0, 0.55, 2.0, 64, 2 * kCus);
+        consider(kMatmulExactMid, 128, 3.5, 1.08, 3.5, 8);
+    } else {
+        consider(kMatmulSplit, 32, 2.5, 0.20, 0.6, 1);
+        consider(kMatmulSmall, 64, 2.6, 0.24, 0.9, 64);
+        consider(kMatmulMid, 128, 3.5, 0.56, 0.75, 8);
+        consider(kMatmulTile, 256, 3.5, 1.55, 4.4, 1);
+    }
     if (best.splits > 1) best.bytes = round_up(4 * (int64_t)best.splits * p.rows * round_up(p.cols, 8), 256);
     return best;
 }
@@ -162,7 +173,8 @@ int check_matmul_sizes(const matmul8_t* p) {
     if (!p) return fail(MUON_ERR_INVALID_ARG, "matmul8: problem is NULL");
     Checks c("matmul8");
     c.sizes(p->rows, p->cols, p->dim);
-    c.one_of("dtype", p->dtype, MUON_T_FP16);
+    c.one_of("exact", p->exact, 1);
+    c.one_of("dtype", p->dtype, p->exact ? MUON_T_FP32 : MUON_T_FP16);
     if (!c.rc && ceil_div(p->rows, 128) * ceil_div(p->cols, 128) > (1 << 22))
         c.rc = fail(MUON_ERR_UNSUPPORTED, "matmul8: rows x cols beyond 2^36");
     return c.rc;
@@ -336,13 +348,13 @@ int matmul8(const matmul8_t* problem, void* workspace, size_t workspace_bytes, v
     Checks c("matmul8");
     c.coded("a", p.a, p.rows, p.dim, 1, false);
     c.coded("b", p.b, p.cols, p.dim, MUON_BLOCK8, false);
-    if (!c.rc) c.matrix("y", p.y, p.rows, p.cols, p.y_stride, 2, true);
+    if (!c.rc) c.matrix("y", p.y, p.rows, p.cols, p.y_stride, size_of(p.dtype), true);
     c.buffer("workspace", workspace, q.bytes, 256, true);
     if (const int rc = c.done()) return rc;
     if (p.rows == 0) return MUON_OK;
     hipStream_t s = static_cast<hipStream_t>(stream);
     const Matmul8 a = {blocks(p.a), blocks(p.b), p.y, p.y_stride, (int)p.rows, (int)p.cols, (int)p.dim,
-                       whole_rows(p.y, p.y_stride, 2), (int)ceil_div(p.cols, q.tile_v), (int)ceil_div(p.rows, q.tile_t),
+                       whole_rows(p.y, p.y_stride, size_of(p.dtype)), (int)ceil_div(p.cols, q.tile_v), (int)ceil_div(p.rows, q.tile_t),
                        q.splits, q.stages, q.splits > 1 ? static_cast<float*>(workspace) : nullptr, round_up(p.cols, 8)};
     LINEAR8_TRY("matmul8", launch_matmul8(a, p.dtype, q.variant, s));
     if (q.splits > 1) LINEAR8_TRY("matmul8_join", launch_matmul8_join(a, p.dtype, s));

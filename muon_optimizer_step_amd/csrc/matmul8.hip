@@ -11,9 +11,10 @@
 //
 // The matrix unit adds 8 products at a time, each cut to 2^-13 of the largest of them, and its sums of 8
 // enter the float32 accumulators: 2.6e-5 of y in norm, where rounding y to 16 bits costs 1.7e-3
-// (bfloat16) or 2e-4 (float16).  A float32 y would show the difference, so there is none.
+// (bfloat16) or 2e-4 (float16).  A float32 y would show the difference: it is computed from exact products (below), and so
+// are 16-bit ones where the caller asks for it.
 //
-// Bound and measured: MFMA for large problems (8192^3: 432 to 440 us, 2.5 PFLOP/s; 400 us, 2.75, where consecutive calls
+// Bound and measured, 8-bit products: MFMA for large problems (8192^3: 432 to 440 us, 2.5 PFLOP/s; 400 us, 2.75, where consecutive calls
 // have one input; a library's 8-bit product with one scale for each matrix reaches 2.64; MFMA busy two
 // thirds of the cycles); y's bytes where K is short (16384 x 2048 x 512: 25.6 us, 3.0 TB/s; MFMA 23 %); the weights' bytes where there are
 // few rows (1 x 8192 x 8192 13 us, 5.2 TB/s; 64 x 8192 x 8192 20 us); below, a launch (1 x 4096 x 1024 4.2 us, of which
@@ -242,9 +243,57 @@ template <int LOADS> __device__ inline void wait_stages(int stages) {
     }
 }
 
+// The products of half a stage, on top of acc.
+template <int TA, int TB>
+__device__ inline void multiply8(floatx16 (&acc)[TA][TB], const v8i (&fa)[TA], const v8i (&fb)[TB], const Scales<TA, TB>& s) {
+#pragma unroll
+    for (int i = 0; i < TA; ++i)
+#pragma unroll
+        for (int j = 0; j < TB; ++j) acc[i][j] = mfma8(fa[i], fb[j], acc[i][j], s.b.w[0], s.a[j].w[0]);
+}
+
+// The same without the scales, with every digit: a code is a bfloat16 value, the 16-bit instruction's products are
+// exact and its sums float32.  A step's 32 codes of a lane go to four products of 16 K; which K a lane's codes are
+// does not matter, as both operands have the same.  The scales come to a stage's sums, so that any power of two will do.
+// Half of the 8-bit rate at best: 8192^3 1020 us, 1.08 PFLOP/s of the 1.36 that a 16-bit library product reaches;
+// 16384 x 2048 x 512 54 us, y's 134 MB 29 of them at a copy's rate; 1021 x 2000 x 1000 11 us.
+__device__ inline void widen8(const v8i& codes, u32x4 (&w)[4]) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        w[k / 2][2 * (k % 2)] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes[k], 1.f, false));
+        w[k / 2][2 * (k % 2) + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes[k], 1.f, true));
+    }
+}
+template <int TA, int TB>
+__device__ inline void multiply_exact(floatx16 (&sums)[TA][TB], const v8i (&fa)[TA], const v8i (&fb)[TB]) {
+    u32x4 wa[TA][4], wb[TB][4];
+#pragma unroll
+    for (int i = 0; i < TA; ++i) widen8(fa[i], wa[i]);
+#pragma unroll
+    for (int j = 0; j < TB; ++j) widen8(fb[j], wb[j]);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int i = 0; i < TA; ++i)
+#pragma unroll
+            for (int j = 0; j < TB; ++j) sums[i][j] = mfma<bf16>(wa[i][k], wb[j][k], sums[i][j]);
+}
+// acc += a stage's sums times both scales, whatever powers of two these are.
+template <int TA, int TB>
+__device__ inline void add_scaled(floatx16 (&acc)[TA][TB], const floatx16 (&sums)[TA][TB], const Scales<TA, TB>& s) {
+#pragma unroll
+    for (int j = 0; j < TB; ++j) {
+        const int power = (int)(s.b.w[0] & 0xFFu) + (int)(s.a[j].w[0] & 0xFFu) - 254;
+#pragma unroll
+        for (int i = 0; i < TA; ++i)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) acc[i][j][e] += ldexpf(sums[i][j][e], power);
+    }
+}
+
 // The same for tiles of 128 x 128 by 4 waves, two buffers, two workgroups on a compute unit that fill
-// each other's waits: 4096 x 2048 x 2048 19 us (64: 35, 256: 25).
-template <int TA, int TB, typename OA, typename OB>
+// each other's waits: 4096 x 2048 x 2048 19 us (64: 35, 256: 25).  EXACT: sums in float32 (above).
+template <bool EXACT, int TA, int TB, typename OA, typename OB>
 __device__ inline void k_loop8_mid(floatx16 (&acc)[TA][TB], int stages, OA& A, OB& B, int left, uint32_t lds, int wave,
                                    Scales<TA, TB>& s) {
     constexpr uint32_t kStage = OA::kBytes + OB::kBytes;
@@ -263,15 +312,24 @@ __device__ inline void k_loop8_mid(floatx16 (&acc)[TA][TB], int stages, OA& A, O
                 load_stage(A, other + mine, left - (kt + 1) * kHeadK);
                 load_stage(B, other + OA::kBytes + mine, left - (kt + 1) * kHeadK);
             }
+            v8i fa[TA], fb[TB];
+            if constexpr (EXACT) {
+                floatx16 sums[TA][TB];
+                clear(sums);
 #pragma unroll
-            for (int step = 0; step < 2; ++step) {
-                v8i fa[TA], fb[TB];
-                read8(A, fa, now, step);
-                read8(B, fb, now + OA::kBytes, step);
+                for (int step = 0; step < 2; ++step) {
+                    read8(A, fa, now, step);
+                    read8(B, fb, now + OA::kBytes, step);
+                    multiply_exact(sums, fa, fb);
+                }
+                add_scaled(acc, sums, s);
+            } else {
 #pragma unroll
-                for (int i = 0; i < TA; ++i)
-#pragma unroll
-                    for (int j = 0; j < TB; ++j) acc[i][j] = mfma8(fa[i], fb[j], acc[i][j], s.b.w[0], s.a[j].w[0]);
+                for (int step = 0; step < 2; ++step) {
+                    read8(A, fa, now, step);
+                    read8(B, fb, now + OA::kBytes, step);
+                    multiply8(acc, fa, fb, s);
+                }
             }
             s.advance();
             const uint32_t t = now;
@@ -440,26 +498,32 @@ __device__ inline void store_tile(const Matmul8& a, floatx16 (&acc)[TV][TT], int
     }
 }
 
-// The same as float32 sums of a part of K, straight from the registers: they stay in the caches.
+// The same as float32 values, straight from the registers: sums of a part of K, which stay in the caches, or y.  Row r of
+// `out` at out + r pitch, `cols` columns.
 template <int TV, int TT>
-__device__ inline void store_partial(const Matmul8& a, floatx16 (&acc)[TV][TT], int split, int v0, int t0, int lane) {
+__device__ inline void store_sums(float* out, int64_t pitch, int rows, int cols, floatx16 (&acc)[TV][TT], int v0, int t0, int lane) {
 #pragma unroll
     for (int tt = 0; tt < TT; ++tt) {
         const int row = t0 + 32 * tt + lane % 32;
-        if (row >= a.rows) continue;
+        if (row >= rows) continue;
 #pragma unroll
         for (int tv = 0; tv < TV; ++tv)
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
                 const int v = v0 + 32 * tv + 16 * p + 8 * (lane / 32);
-                if (v >= a.cols) continue;
-                floatx4* dst = reinterpret_cast<floatx4*>(a.partial + ((int64_t)split * a.rows + row) * a.partial_pitch + v);
+                float* dst = out + row * pitch + v;
+                if (v + 8 <= cols) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    floatx4 x;
+                    for (int h = 0; h < 2; ++h) {
+                        floatx4 x;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) x[e] = acc[tv][tt][8 * p + 4 * h + e];
-                    dst[h] = x;
+                        for (int e = 0; e < 4; ++e) x[e] = acc[tv][tt][8 * p + 4 * h + e];
+                        reinterpret_cast<floatx4_any*>(dst)[h] = x;
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if (v + e < cols) dst[e] = acc[tv][tt][8 * p + e];
                 }
             }
     }
@@ -499,13 +563,15 @@ __global__ __launch_bounds__(512, 2) void matmul8_kernel(const Matmul8 a) {
 
 // 32 WV TV columns x 32 WT TT rows by 4 waves, BUFFERS stages, two workgroups per compute
 // unit; K in a.splits parts, whose sums matmul8_join adds.
+// EXACT: sums in float32 of products that lose nothing, the only form with float32 results.
 template <int WV, int WT, int TV, int TT, int BUFFERS> struct SmallTile {
     static constexpr int kCols = 32 * WV * TV, kRows = 32 * WT * TT;
     static constexpr size_t kBytes = (size_t)BUFFERS * (kCols + kRows) * kBlock8;
     static_assert(WV * WT == 4 && kBlock8 % (32 * TV) == 0 && kStageBytes<TV> * 4 <= (int)kBytes, "tile");
 };
-template <typename T, int WV, int WT, int TV, int TT, int BUFFERS>
+template <typename T, bool EXACT, int WV, int WT, int TV, int TT, int BUFFERS>
 __global__ __launch_bounds__(256, 2) void matmul8_small_kernel(const Matmul8 a) {
+    static_assert(EXACT ? BUFFERS == 2 : sizeof(T) == 2, "forms");
     typedef SmallTile<WV, WT, TV, TT, BUFFERS> S;
     extern __shared__ __align__(16) uint8_t lds[];
     const int tiles = a.tiles_v * a.tiles_t, item = xcd_item(tiles * a.splits);
@@ -525,14 +591,18 @@ __global__ __launch_bounds__(256, 2) void matmul8_small_kernel(const Matmul8 a) 
     floatx16 acc[TV][TT];
     clear(acc);
     const int left = min((a.dim + 15) / 16 * 8 - s0 * kHeadK, stages * kHeadK);
-    if constexpr (BUFFERS == 2) k_loop8_mid(acc, stages, B, A, left, lds_address(lds), wave, s);
+    if constexpr (BUFFERS == 2) k_loop8_mid<EXACT>(acc, stages, B, A, left, lds_address(lds), wave, s);
     else k_loop8_small<BUFFERS>(acc, stages, B, A, left, lds_address(lds), wave, lane, s);
     if (a.partial) {
-        store_partial<TV, TT>(a, acc, split, v0, t0, lane);
+        store_sums(a.partial + (int64_t)split * a.rows * a.partial_pitch, a.partial_pitch, a.rows, (int)a.partial_pitch, acc, v0, t0, lane);
         return;
     }
-    bare_barrier();
-    store_tile<T, TV, TT>(a, acc, v0, t0, lane, lds + wave * kStageBytes<TV>);
+    if constexpr (sizeof(T) == 4) {
+        store_sums(static_cast<float*>(a.y), a.y_stride, a.rows, a.cols, acc, v0, t0, lane);
+    } else {
+        bare_barrier();
+        store_tile<T, TV, TT>(a, acc, v0, t0, lane, lds + wave * kStageBytes<TV>);
+    }
 }
 
 // The sums of the parts of K in order, rounded once.
@@ -565,7 +635,12 @@ __global__ __launch_bounds__(kJoinThreads) void matmul8_join_kernel(const Matmul
         const float sums[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
         T* dst = static_cast<T*>(a.y) + row * a.y_stride + v;
         if (v + 8 <= a.cols) {
-            *reinterpret_cast<u32x4_any*>(dst) = pack8<T>(sums);
+            if constexpr (sizeof(T) == 4) {
+                reinterpret_cast<floatx4_any*>(dst)[0] = lo;
+                reinterpret_cast<floatx4_any*>(dst)[1] = hi;
+            } else {
+                *reinterpret_cast<u32x4_any*>(dst) = pack8<T>(sums);
+            }
         } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e)
@@ -750,12 +825,12 @@ hipError_t split_launch(const Matmul8& a, hipStream_t s) {
     return hipGetLastError();
 }
 
-template <typename T, int WV, int WT, int TV, int TT, int BUFFERS>
+template <typename T, bool EXACT, int WV, int WT, int TV, int TT, int BUFFERS>
 hipError_t small_launch(const Matmul8& a, hipStream_t s) {
     constexpr size_t bytes = SmallTile<WV, WT, TV, TT, BUFFERS>::kBytes;
-    const hipError_t allowed = allow_lds(&matmul8_small_kernel<T, WV, WT, TV, TT, BUFFERS>, bytes);
+    const hipError_t allowed = allow_lds(&matmul8_small_kernel<T, EXACT, WV, WT, TV, TT, BUFFERS>, bytes);
     if (allowed != hipSuccess) return allowed;
-    matmul8_small_kernel<T, WV, WT, TV, TT, BUFFERS><<<xcd_grid(a.tiles_v * a.tiles_t * a.splits), 256, bytes, s>>>(a);
+    matmul8_small_kernel<T, EXACT, WV, WT, TV, TT, BUFFERS><<<xcd_grid(a.tiles_v * a.tiles_t * a.splits), 256, bytes, s>>>(a);
     return hipGetLastError();
 }
 
@@ -764,8 +839,8 @@ hipError_t typed(const Matmul8& a, int variant, hipStream_t s) {
     const int grid = xcd_grid(a.tiles_v * a.tiles_t);
     if (variant == kMatmulRows) matmul8_rows_kernel<T, 8><<<a.tiles_v, 8 * kWave, 0, s>>>(a);
     else if (variant == kMatmulSplit) return split_launch<T, 1, 1, 8>(a, s);
-    else if (variant == kMatmulSmall) return small_launch<T, 2, 2, 1, 1, 4>(a, s);
-    else if (variant == kMatmulMid) return small_launch<T, 2, 2, 2, 2, 2>(a, s);
+    else if (variant == kMatmulSmall) return small_launch<T, false, 2, 2, 1, 1, 4>(a, s);
+    else if (variant == kMatmulMid) return small_launch<T, false, 2, 2, 2, 2, 2>(a, s);
     else {
         const hipError_t allowed = allow_lds(&matmul8_kernel<T>, kRingBytes);
         if (allowed != hipSuccess) return allowed;
@@ -774,16 +849,27 @@ hipError_t typed(const Matmul8& a, int variant, hipStream_t s) {
     return hipGetLastError();
 }
 
+template <typename T>
+hipError_t exact_typed(const Matmul8& a, int variant, hipStream_t s) {
+    if (variant == kMatmulExactSmall) return small_launch<T, true, 2, 2, 1, 1, 2>(a, s);
+    return small_launch<T, true, 2, 2, 2, 2, 2>(a, s);
+}
+
 }  // namespace
 
 hipError_t launch_matmul8_join(const Matmul8& a, int type, hipStream_t s) {
     const int64_t items = (int64_t)a.rows * ((a.cols + 7) / 8);
     const int grid = (int)std::min<int64_t>(32768, (items + kJoinThreads - 1) / kJoinThreads);
     if (type == kTypeBf16) matmul8_join_kernel<bf16><<<grid, kJoinThreads, 0, s>>>(a);
-    else matmul8_join_kernel<f16><<<grid, kJoinThreads, 0, s>>>(a);
+    else if (type == kTypeFp16) matmul8_join_kernel<f16><<<grid, kJoinThreads, 0, s>>>(a);
+    else matmul8_join_kernel<float><<<grid, kJoinThreads, 0, s>>>(a);
     return hipGetLastError();
 }
 hipError_t launch_matmul8(const Matmul8& a, int type, int variant, hipStream_t s) {
+    if (variant == kMatmulExactSmall || variant == kMatmulExactMid) {
+        if (type == kTypeBf16) return exact_typed<bf16>(a, variant, s);
+        return type == kTypeFp16 ? exact_typed<f16>(a, variant, s) : exact_typed<float>(a, variant, s);
+    }
     return type == kTypeBf16 ? typed<bf16>(a, variant, s) : typed<f16>(a, variant, s);
 }
 

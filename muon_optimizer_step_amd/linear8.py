@@ -318,31 +318,35 @@ def weight8_encode(weight, *, transposed: bool = True, stream=None) -> Weight8:
 class PreparedMatmul8(_Prepared):
     """a8 @ b8.T: activations [rows, dim] times a weight [cols, dim], both in 8 bits, rounded once to dtype.
 
-    dtype: bfloat16 (the default) or float16; the matrix unit's sums of 8-bit products do not have float32's digits.
-    out: a tensor [rows, cols] for the result (rows may be strided).
+    dtype: bfloat16 (the default), float16, or float32.  out: a tensor [rows, cols] for the result (rows may be strided).
+    exact: sums in float32 of products that lose nothing, at the rate of 16-bit ones; None (the default) has them for
+    float32 results only, and False refuses these: the matrix unit's sums of 8-bit products do not have float32's digits.
     """
 
-    def __init__(self, a8, b8, *, dtype=None, out=None, workspace=None, stream=None):
+    def __init__(self, a8, b8, *, dtype=None, out=None, exact: Optional[bool] = None, workspace=None, stream=None):
         torch = _torch()
         _check_coded(a8, Activation8, "a8")
         _check_coded(b8, Weight8, "b8")
         (rows, dim), cols = a8.shape, b8.shape[0]
         if b8.dim != dim:
             raise ValueError(f"b8 has {b8.dim} columns, a8 {dim}")
-        short = (torch.bfloat16, torch.float16)
-        if dtype is not None and dtype not in short:
-            raise TypeError(f"dtype must be torch.bfloat16 or torch.float16, got {dtype}")
+        kinds = (torch.bfloat16, torch.float16) + ((torch.float32,) if exact or exact is None else ())
+        if dtype is not None and dtype not in kinds:
+            raise TypeError(f"dtype must be {' or '.join(str(d) for d in kinds)}{' (float32 with exact=True)' if exact is False else ''}, got {dtype}")
         if out is None:
             out = _room(rows, cols, torch.bfloat16 if dtype is None else dtype, a8.device, stream)
-        ptr, stride = _check_matrix(out, "out", short if dtype is None else (dtype,), (rows, cols))
+        ptr, stride = _check_matrix(out, "out", kinds if dtype is None else (dtype,), (rows, cols))
+        if exact is None:
+            exact = out.dtype == torch.float32
         device = _same_device((a8.codes, b8.codes, out), "matmul8")
-        problem = _lib.Matmul8(a8._abi(), b8._abi(), ptr, rows, cols, dim, stride, _types()[out.dtype])
+        problem = _lib.Matmul8(a8._abi(), b8._abi(), ptr, rows, cols, dim, stride, _types()[out.dtype], int(bool(exact)))
         self._prepare("matmul8", problem, [*a8._tensors(), *b8._tensors(), out], device, out, stream, workspace, True)
 
 
-def matmul8(a8, b8, *, dtype=None, out=None, workspace=None, stream=None):
-    """a8 @ b8.T (see PreparedMatmul8).  workspace: None takes one for this call from the stream's memory."""
-    return _once(PreparedMatmul8(a8, b8, dtype=dtype, out=out, workspace=workspace, stream=stream), stream)
+def matmul8(a8, b8, *, dtype=None, out=None, exact: bool = False, workspace=None, stream=None):
+    """a8 @ b8.T (see PreparedMatmul8).  float32 results are for exact=True.  workspace: None takes one for this call from
+    the stream's memory."""
+    return _once(PreparedMatmul8(a8, b8, dtype=dtype, out=out, exact=bool(exact), workspace=workspace, stream=stream), stream)
 
 
 class PreparedAct8GradWeight(_Prepared):
