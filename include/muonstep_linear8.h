@@ -54,7 +54,8 @@ extern "C" {
  * are powers of two cost no rounding of their own, the matrix unit applies
  * them itself, and what a block stands for is exact in bfloat16 (from
  * MUON_SCALE8_LOW on no value is below its normal range).  A block that is zero
- * has s = MUON_SCALE8_LOW.  The entries below take any s from 1 to 254. */
+ * has s = MUON_SCALE8_LOW.  The nearest code of a magnitude above 248 2^120 stands for 2^128, which float32 and bfloat16
+ * have as infinity.  The entries below take any s from 1 to 254. */
 #define MUON_BLOCK8 128
 #define MUON_SCALE8_LOW 10
 #define MUON_LINEAR8_MAX_ROWS (1 << 24)

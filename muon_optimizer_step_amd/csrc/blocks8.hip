@@ -145,8 +145,8 @@ __device__ inline void store8(const Through& whole, T* p0, int64_t at, const Raw
 }
 
 // ---------------------------------------------------------------- activation functions
-// exp(x) for x <= 0 to a few ulp, subnormal results included (which the instruction itself flushes):
-// in base 2, with what the product with log2 e loses.
+// exp(x) for -2^127 <= x <= 0 to a few ulp, subnormal results included (which the instruction itself flushes):
+// in base 2, with what the product with log2 e loses (and which would be infinite below).
 constexpr float kLog2e = 1.44269504088896340736f, kLog2eLow = 1.92596299e-8f, kLn2 = 0.69314718055994530942f;
 __device__ inline float exp_of(float x) {
 #pragma clang fp contract(off)      // t is one rounded value in both places
@@ -154,7 +154,7 @@ __device__ inline float exp_of(float x) {
     const bool low = t < -64.f;
     return __builtin_amdgcn_exp2f(t + (low ? 64.f : 0.f)) * fmaf(rest, kLn2, 1.f) * (low ? 0x1p-64f : 1.f);
 }
-// silu's s = 1 / (1 + exp(-u)) and 1 - s, from exp(-|u|): no overflow, and digits where either is small.
+// silu's s = 1 / (1 + exp(-u)) and 1 - s, from exp(-|u|), |u| <= 2^127: no overflow, and digits where either is small.
 struct Sigmoid {
     float s, rest;
 };
@@ -192,10 +192,11 @@ template <int ACT> __device__ inline float act(float u) {
         const float t = positive(u);
         return t * t;
     }
-    if (ACT == kActSilu) return u * sigmoid(u).s;
+    if (ACT == kActSilu) return u * sigmoid(__builtin_amdgcn_fmed3f(u, -200.f, 200.f)).s;      // beyond, s is 0 or 1; a NaN stays one
     if (ACT == kActGelu) return u * gelu_parts(u).f;
     return u;
 }
+// u: finite or NaN, but for relu2.
 template <int ACT> __device__ inline float act_slope(float u) {
     if (ACT == kActRelu2) {
         const float t = positive(u);
@@ -272,6 +273,10 @@ __global__ __launch_bounds__(kThreads) void encode8_kernel(const Encode8 a) {
     });
 }
 
+// silu's and gelu's derivatives are 1 or 0 from |u| = 200 on, which with scales from this byte on (2^113) is every code but zero and NaN:
+// larger ones count as this one, so that u is finite.
+constexpr int kFarScale = 240;
+
 template <typename T, int ACT, bool PAST>
 __global__ __launch_bounds__(kThreads) void backward8_kernel(const Backward8 a) {
     for_units(a.r, [&](const Unit& u) {
@@ -295,7 +300,7 @@ __global__ __launch_bounds__(kThreads) void backward8_kernel(const Backward8 a) 
         for (int k = 0; k < kBatch; ++k) {
             const int row = u.row + k * u.step;
             float v[8], g[8];
-            decode8(code[k], scale_value(byte[k]), v);
+            decode8(code[k], scale_value(ACT == kActRelu2 ? byte[k] : min(byte[k], kFarScale)), v);
             to_float<T>(grad[k], g);
 #pragma unroll
             for (int e = 0; e < 8; ++e) g[e] *= act_slope<ACT>(v[e]);
