@@ -119,19 +119,15 @@ template <typename T> __device__ inline Raw<T> load8(const T* p, int left) {
     for (int k = 0; k < 4 * ((int)sizeof(T) / 2); ++k) r.w[k / 4][k % 4] = word[k];
     return r;
 }
-// To p0 + at, `whole` starts at p0; vec: p0 + at is 16-byte aligned.
-template <bool PAST, typename T>
-__device__ inline void store8(const Through& whole, T* p0, int64_t at, const Raw<T>& r, int left, bool vec) {
+// To p0 + at, `whole` starts at p0; through: the rows are 16-byte aligned, and 16-bit values pass the L2.
+template <typename T>
+__device__ inline void store8(const Through& whole, T* p0, int64_t at, const Raw<T>& r, int left, bool through) {
     T* p = p0 + at;
-    if (vec && left >= 8) {
-#pragma unroll
-        for (int k = 0; k < (int)sizeof(T) / 2; ++k) {
-            if constexpr (PAST) __builtin_nontemporal_store(r.w[k], reinterpret_cast<u32x4*>(p) + k);
-            else whole.store((int)at * (int)sizeof(T) + 16 * k, r.w[k]);
-        }
-        return;
-    }
     if (left >= 8) {
+        if (sizeof(T) == 2 && through) {
+            whole.store((int)at * 2, r.w[0]);
+            return;
+        }
 #pragma unroll
         for (int k = 0; k < (int)sizeof(T) / 2; ++k) reinterpret_cast<u32x4_any*>(p)[k] = r.w[k];
         return;
@@ -277,7 +273,7 @@ __global__ __launch_bounds__(kThreads) void encode8_kernel(const Encode8 a) {
 // larger ones count as this one, so that u is finite.
 constexpr int kFarScale = 240;
 
-template <typename T, int ACT, bool PAST>
+template <typename T, int ACT>
 __global__ __launch_bounds__(kThreads) void backward8_kernel(const Backward8 a) {
     for_units(a.r, [&](const Unit& u) {
         Raw<T> grad[kBatch];
@@ -306,7 +302,7 @@ __global__ __launch_bounds__(kThreads) void backward8_kernel(const Backward8 a) 
             for (int e = 0; e < 8; ++e) g[e] *= act_slope<ACT>(v[e]);
             if (a.out && u.row0 + row < a.r.rows) {
                 T* first = static_cast<T*>(a.out) + u.row0 * a.out_stride;
-                store8<PAST>(Through(first), first, row * a.out_stride + u.d, from_float<T>(g), left, a.out_vec);
+                store8(Through(first), first, row * a.out_stride + u.d, from_float<T>(g), left, a.out_through);
             }
             if (a.out8.codes) {
                 int b;
@@ -317,7 +313,7 @@ __global__ __launch_bounds__(kThreads) void backward8_kernel(const Backward8 a) 
     });
 }
 
-template <typename T, bool PAST>
+template <typename T>
 __global__ __launch_bounds__(kThreads) void decode8_kernel(const Decode8 a) {
     for_units(a.r, [&](const Unit& u) {
         const int left = a.r.dim - u.d;
@@ -329,7 +325,7 @@ __global__ __launch_bounds__(kThreads) void decode8_kernel(const Decode8 a) {
             float v[8];
             decode8(w, scale_value(a.x.scale[row / a.tall * a.x.scale_stride + u.block]), v);
             T* first = static_cast<T*>(a.out) + u.row0 * a.out_stride;
-            store8<PAST>(Through(first), first, (row - u.row0) * a.out_stride + u.d, from_float<T>(v), left, a.vec);
+            store8(Through(first), first, (row - u.row0) * a.out_stride + u.d, from_float<T>(v), left, a.out_through);
         }
     });
 }
@@ -482,9 +478,7 @@ hipError_t encode_act(const Encode8& a, int act, hipStream_t s) {
 }
 template <typename T, int ACT>
 hipError_t backward_typed(const Backward8& a, hipStream_t s) {
-    const int grid = rows_grid(a.r);
-    if (a.r.past) backward8_kernel<T, ACT, true><<<grid, kThreads, 0, s>>>(a);
-    else backward8_kernel<T, ACT, false><<<grid, kThreads, 0, s>>>(a);
+    backward8_kernel<T, ACT><<<rows_grid(a.r), kThreads, 0, s>>>(a);
     return hipGetLastError();
 }
 template <typename T>
@@ -494,22 +488,12 @@ hipError_t backward_act(const Backward8& a, int act, hipStream_t s) {
 }
 template <typename T>
 hipError_t decode_typed(const Decode8& a, hipStream_t s) {
-    const int grid = rows_grid(a.r);
-    if (a.r.past) decode8_kernel<T, true><<<grid, kThreads, 0, s>>>(a);
-    else decode8_kernel<T, false><<<grid, kThreads, 0, s>>>(a);
+    decode8_kernel<T><<<rows_grid(a.r), kThreads, 0, s>>>(a);
     return hipGetLastError();
 }
 
-// What a pass writes, from which on its 16 or 32-bit values are written past the caches: the last one keeps too
-// little of them for the next pass to find, and has room for the codes, which a product reads next.  The layer
-// 16384 x 1024 x 4096, whose gradient's 201 MB are written so: the backward pass with both products behind it 248 us;
-// nothing past the caches 254, the codes too 260 (alone 69, 69 and 62).  Below, what follows finds it there
-// (4096 x 1024 x 4096, encode and product: 42 us, 48 past the caches).  A template's argument: as a branch, the two
-// stores become one without the hint.
-constexpr int64_t kPastBytes = (int64_t)192 << 20;
-Rows8 plan(const Rows8& r, int64_t bytes_per_value) {
+Rows8 plan(const Rows8& r) {
     Rows8 q = r;
-    q.past = r.rows * r.dim * bytes_per_value >= kPastBytes;
     const int blocks = (q.dim + kBlock8 - 1) / kBlock8;
     q.dim16 = (q.dim + 15) / 16 * 16;
     q.unit_log = 0;
@@ -524,19 +508,19 @@ Rows8 plan(const Rows8& r, int64_t bytes_per_value) {
 
 hipError_t launch_encode8(const Encode8& a0, int type, int act, hipStream_t s) {
     Encode8 a = a0;
-    a.r = plan(a0.r, 0);
+    a.r = plan(a0.r);
     if (type == kTypeBf16) return encode_act<bf16>(a, act, s);
     return type == kTypeFp16 ? encode_act<f16>(a, act, s) : encode_act<float>(a, act, s);
 }
 hipError_t launch_backward8(const Backward8& a0, int type, int act, hipStream_t s) {
     Backward8 a = a0;
-    a.r = plan(a0.r, (a.out ? (type == kTypeFp32 ? 4 : 2) : 0) + (a.out8.codes != nullptr));
+    a.r = plan(a0.r);
     if (type == kTypeBf16) return backward_act<bf16>(a, act, s);
     return type == kTypeFp16 ? backward_act<f16>(a, act, s) : backward_act<float>(a, act, s);
 }
 hipError_t launch_decode8(const Decode8& a0, int type, hipStream_t s) {
     Decode8 a = a0;
-    a.r = plan(a0.r, type == kTypeFp32 ? 4 : 2);
+    a.r = plan(a0.r);
     if (type == kTypeBf16) return decode_typed<bf16>(a, s);
     return type == kTypeFp16 ? decode_typed<f16>(a, s) : decode_typed<float>(a, s);
 }

@@ -14,8 +14,11 @@ constexpr int kScale8Low = 10;    // the smallest scale's byte
 
 // Part of a result from `base` (the same for the whole wave) on, written with the device's scope: through the XCD's
 // L2.  What a kernel leaves there is written back when it ends, and the next one waits for that: y of
-// 2048 x 2048 x 512 6.0 us against 6.7, of 16384 x 2048 x 512 25.1 against 27.2 (with an encoding of y behind it
-// 49.2 against 51.5).  For whole 128-byte lines; offsets in bytes, below 2^31.
+// 2048 x 2048 x 512 6.2 us against 6.9, of 16384 x 2048 x 512 26.3 against 28.5 (with an encoding of y behind it
+// 42 against 46 to 49).  Meant for whole 128-byte lines: 16 lanes of 8 codes, 32 of 4, 8 of 16 bytes.  Rows that begin or end inside a
+// line break two of them, which is no loss in codes (65536 x 200: 9.7 against 10.6) and little in y and the weight's gradient (16384 x 1000 x
+// 512: 15.0 against 15.4, with a reader 28.2 against 26.6; gradient of 1000 x 4000 x 2004 25.7 and 25.7, 40 and 37).  Offsets in
+// bytes, below 2^31.
 struct Through {
     static constexpr int kDevice = 16;      // the instruction's sc1
     __amdgpu_buffer_rsrc_t out;
@@ -50,7 +53,6 @@ struct Rows8 {
     int64_t rows;
     int dim, dim16;          // dim rounded up to 16
     int unit_log, col_groups, row_groups;      // at most 2^30 of both together
-    int past;                // 16 and 32-bit results are written past the caches
 };
 
 struct Encode8 {
@@ -65,7 +67,7 @@ struct Backward8 {
     const void* grad;
     void* out;
     int64_t grad_stride, out_stride;
-    int out_vec;             // rows of out 16-byte aligned
+    int out_through;         // 16-bit results pass the L2
 };
 struct Decode8 {
     Rows8 r;
@@ -73,7 +75,7 @@ struct Decode8 {
     int tall;                // rows of a block: 1 or kBlock8
     void* out;
     int64_t out_stride;
-    int vec;
+    int out_through;         // as above
 };
 struct Weight8 {
     const void* w;

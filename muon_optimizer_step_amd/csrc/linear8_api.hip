@@ -28,6 +28,19 @@ Blocks8 blocks(const blocks8_t& b) {
 bool whole_rows(const void* p, int64_t stride, int64_t size) {
     return reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride * size % 16 == 0;
 }
+// Whether the row-wise passes write a 16 or 32-bit result through the L2 (Through in linear8.h).  Not where an instruction's
+// pieces leave no whole lines: float32, of which it holds 16 of every 32 bytes (relu2's backward of 8192 x 4096 105 us, by
+// ordinary stores 59, with an encoding of the result behind it 128 and 81), and not large results whose rows lie off the 128-byte grid
+// (in 16 bits, 25152 x 1000: 30 us and 30, fp16 22.6 and 24; 50304 x 1000: 64 and 60, fp16 50 and 47; 134208 x 1000: 170 and
+// 153).  On the grid the two are within a per cent, small results up to 1 us quicker through the L2.  Past the last cache too is no better where a
+// reader follows: 16384 x 4096 decoded to bfloat16 and encoded 69 us (63), the backward pass of 16384 x 4096 with both
+// products behind it 247 to 254 us either way.
+constexpr int64_t kRaggedBytes = (int64_t)64 << 20;
+bool through(const void* p, int64_t rows, int64_t dim, int64_t stride, int dtype) {
+    if (dtype == MUON_T_FP32 || !whole_rows(p, stride, 2)) return false;
+    const bool lines = reinterpret_cast<uintptr_t>(p) % 128 == 0 && stride * 2 % 128 == 0;
+    return lines || rows * dim * 2 < kRaggedBytes;
+}
 
 // Checks of one call: each returns its first failure's code, and the next ones return it too.
 struct Checks {
@@ -286,7 +299,8 @@ int act8_decode(const blocks8_t* x, int32_t tall, int64_t rows, int64_t dim, voi
     if (const int rc = c.done()) return rc;
     if (rows == 0) return MUON_OK;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    const Decode8 a = {rows8(rows, dim), blocks(*x), tall ? kBlock8 : 1, out, out_stride, whole_rows(out, out_stride, size_of(dtype))};
+    const Decode8 a = {rows8(rows, dim), blocks(*x), tall ? kBlock8 : 1, out, out_stride,
+                       through(out, rows, dim, out_stride, dtype)};
     LINEAR8_TRY("act8_decode", launch_decode8(a, dtype, s));
     return MUON_OK;
 }
@@ -312,7 +326,7 @@ int act8_backward(const act8_backward_t* problem, void* stream) {
     if (p.rows == 0) return MUON_OK;
     hipStream_t s = static_cast<hipStream_t>(stream);
     const Backward8 a = {rows8(p.rows, p.dim), blocks(p.u), blocks(p.out8), p.grad, p.out, p.grad_stride, p.out_stride,
-                         whole_rows(p.out, p.out_stride, size)};
+                         through(p.out, p.rows, p.dim, p.out_stride, p.dtype)};
     LINEAR8_TRY("act8_backward", launch_backward8(a, p.dtype, p.activation, s));
     return MUON_OK;
 }
