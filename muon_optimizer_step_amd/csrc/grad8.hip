@@ -457,12 +457,8 @@ hipError_t launch(const Grad8& a, hipStream_t s) {
 
 }  // namespace
 
-hipError_t launch_grad8(const Grad8& a, int edge, hipStream_t s) {
+hipError_t launch_grad8(const Grad8& a, int edge, bool deep, hipStream_t s) {
     if (edge == 256) return launch<256, false>(a, s);
-    // One workgroup per compute unit and many stages: the deep form (16384 x 2048 x 512, 64 stages, the data past the last
-    // cache / in it: 50.5 / 47.8 us against 59.4 / 46.9).  Few stages do not earn its longer start and code (22: 25.1
-    // against 23.5; 1 to 8: 1 us more), and two workgroups hide each other's loads (512 of 32 stages: 60.6 against 54.0).
-    const bool deep = a.tiles_c * a.tiles_d * a.splits <= 256 && a.stages_per_split >= 40;
     return deep ? launch<128, true>(a, s) : launch<128, false>(a, s);
 }
 

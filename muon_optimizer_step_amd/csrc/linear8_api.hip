@@ -130,6 +130,9 @@ Rows8 rows8(int64_t rows, int64_t dim) {
 }
 
 // ---------------------------------------------------------------- the product
+// Launches' names in messages and in the profiling hook, by Matmul8Variant.
+const char* const kMatmulNames[] = {"matmul8_rows", "matmul8_32", "matmul8_64", "matmul8_128", "matmul8_256", "matmul8_exact_64",
+                                    "matmul8_exact_128"};
 struct MatmulPlan {
     int variant, tile_v, tile_t, splits, stages;     // stages of a split
     int64_t bytes;
@@ -196,7 +199,7 @@ int check_matmul_sizes(const matmul8_t* p) {
 // ---------------------------------------------------------------- the weight's gradient
 constexpr int kMinStages = 4;     // of a split
 struct GradPlan {
-    bool pack;
+    bool pack, deep;
     int edge, splits, stages;     // stages of a split
     int64_t cols8, dim8;
     int64_t grad, partial, bytes; // offsets, -1: not there
@@ -230,6 +233,10 @@ GradPlan plan_grad(const act8_grad_weight_t& p) {
     };
     consider(128, 0.48, 2.5);
     consider(256, 1.5, 5.0);
+    // Tiles of 128, one workgroup per compute unit and many stages: the deep form (16384 x 2048 x 512, 64 stages, the data past the
+    // last cache / in it: 50.5 / 47.8 us against 59.4 / 46.9).  Few stages do not earn its longer start and code (22: 25.1
+    // against 23.5; 1 to 8: 1 us more), and two workgroups hide each other's loads (512 of 32 stages: 60.6 against 54.0).
+    q.deep = q.edge == 128 && ceil_div(p.cols, 128) * ceil_div(p.dim, 128) * q.splits <= kCus && q.stages >= 40;
     int64_t off = 0;
     auto take = [&](bool there, int64_t bytes) {
         const int64_t at = there ? off : -1;
@@ -370,7 +377,7 @@ int matmul8(const matmul8_t* problem, void* workspace, size_t workspace_bytes, v
     const Matmul8 a = {blocks(p.a), blocks(p.b), p.y, p.y_stride, (int)p.rows, (int)p.cols, (int)p.dim,
                        whole_rows(p.y, p.y_stride, size_of(p.dtype)), (int)ceil_div(p.cols, q.tile_v), (int)ceil_div(p.rows, q.tile_t),
                        q.splits, q.stages, q.splits > 1 ? static_cast<float*>(workspace) : nullptr, round_up(p.cols, 8)};
-    LINEAR8_TRY("matmul8", launch_matmul8(a, p.dtype, q.variant, s));
+    LINEAR8_TRY(kMatmulNames[q.variant], launch_matmul8(a, p.dtype, q.variant, s));
     if (q.splits > 1) LINEAR8_TRY("matmul8_join", launch_matmul8_join(a, p.dtype, s));
     return MUON_OK;
 }
@@ -427,7 +434,7 @@ int act8_grad_weight(const act8_grad_weight_t* problem, void* workspace, size_t 
     a.accumulate = p.accumulate != 0;
     a.partial = q.partial >= 0 ? reinterpret_cast<float*>(ws + q.partial) : nullptr;
     a.partial_pitch = q.dim8;
-    LINEAR8_TRY("act8_grad_weight", launch_grad8(a, q.edge, s));
+    LINEAR8_TRY(q.edge == 256 ? "act8_grad_256" : q.deep ? "act8_grad_128_deep" : "act8_grad_128", launch_grad8(a, q.edge, q.deep, s));
     if (a.partial) {
         j.partial = a.partial;
         LINEAR8_TRY("act8_grad_join", launch_join8(j, s));
