@@ -498,9 +498,9 @@ __device__ inline void store_tile(const Matmul8& a, floatx16 (&acc)[TV][TT], int
     }
 }
 
-// The same as float32 values, straight from the registers: sums of a part of K, which stay in the caches, or y.  Row r of
-// `out` at out + r pitch, `cols` columns.
-template <int TV, int TT>
+// The same as float32 values, straight from the registers: sums of a part of K (PARTIAL: rows of whole 8 values), which stay in the
+// caches, or y.  Row r of `out` at out + r pitch, `cols` columns.
+template <bool PARTIAL, int TV, int TT>
 __device__ inline void store_sums(float* out, int64_t pitch, int rows, int cols, floatx16 (&acc)[TV][TT], int v0, int t0, int lane) {
 #pragma unroll
     for (int tt = 0; tt < TT; ++tt) {
@@ -511,8 +511,9 @@ __device__ inline void store_sums(float* out, int64_t pitch, int rows, int cols,
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
                 const int v = v0 + 32 * tv + 16 * p + 8 * (lane / 32);
+                if (PARTIAL && v >= cols) continue;
                 float* dst = out + row * pitch + v;
-                if (v + 8 <= cols) {
+                if (PARTIAL || v + 8 <= cols) {
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         floatx4 x;
@@ -594,11 +595,11 @@ __global__ __launch_bounds__(256, 2) void matmul8_small_kernel(const Matmul8 a) 
     if constexpr (BUFFERS == 2) k_loop8_mid<EXACT>(acc, stages, B, A, left, lds_address(lds), wave, s);
     else k_loop8_small<BUFFERS>(acc, stages, B, A, left, lds_address(lds), wave, lane, s);
     if (a.partial) {
-        store_sums(a.partial + (int64_t)split * a.rows * a.partial_pitch, a.partial_pitch, a.rows, (int)a.partial_pitch, acc, v0, t0, lane);
+        store_sums<true>(a.partial + (int64_t)split * a.rows * a.partial_pitch, a.partial_pitch, a.rows, a.cols, acc, v0, t0, lane);
         return;
     }
     if constexpr (sizeof(T) == 4) {
-        store_sums(static_cast<float*>(a.y), a.y_stride, a.rows, a.cols, acc, v0, t0, lane);
+        store_sums<false>(static_cast<float*>(a.y), a.y_stride, a.rows, a.cols, acc, v0, t0, lane);
     } else {
         bare_barrier();
         store_tile<T, TV, TT>(a, acc, v0, t0, lane, lds + wave * kStageBytes<TV>);
