@@ -98,6 +98,7 @@ constexpr int kJoinThreads = 64, kJoinBatch = 4;
 // Kernels: up to 16 rows; 32 x 32 with K split over the waves; tiles of 64, 128 and 256; tiles of 64 and 128 with exact
 // products, whose result may be float32.
 enum Matmul8Variant { kMatmulRows = 0, kMatmulSplit, kMatmulSmall, kMatmulMid, kMatmulTile, kMatmulExactSmall, kMatmulExactMid };
+constexpr int kRingStages = 3;      // of 128 K, that kMatmulTile has at least
 struct Matmul8 {
     Blocks8 a, b;
     void* y;

@@ -179,7 +179,7 @@ MatmulPlan plan_matmul(const matmul8_t& p) {
         consider(kMatmulSplit, 32, 2.5, 0.20, 0.6, 1);
         consider(kMatmulSmall, 64, 2.6, 0.24, 0.9, 64);
         consider(kMatmulMid, 128, 3.5, 0.56, 0.75, 8);
-        consider(kMatmulTile, 256, 3.5, 1.55, 4.4, 1);
+        if (all >= kRingStages) consider(kMatmulTile, 256, 3.5, 1.55, 4.4, 1);      // of fewer, 128 is the estimate's choice anyway
     }
     if (best.splits > 1) best.bytes = round_up(4 * (int64_t)best.splits * p.rows * round_up(p.cols, 8), 256);
     return best;

@@ -99,7 +99,7 @@ template <typename Op, int N> __device__ inline void read8(const Op& op, v8i (&f
     static_assert(N == 1 || N == 2 || N == 4, "fragments of a wave");
 }
 
-// acc += A B^T over `stages` stages of 128 K, which ends after `left` pairs of bytes.  Tile
+// acc += A B^T over `stages` stages (kRingStages or more) of 128 K, which ends after `left` pairs of bytes.  Tile
 // 256 x 256, 8 waves of 128 x 64, LDS a ring of five operand slots: A of stage k in
 // slot 2 k mod 5, B in 2 k + 1 mod 5.  The barrier is in the middle of a stage, when
 // every wave has the fragments of its second half in registers: it frees the stage's two
@@ -144,24 +144,15 @@ __device__ inline void k_loop8(floatx16 (&acc)[TA][TB], int stages, OA& A, OB& B
         return join(w[0], w[1]);
     };
     s.load(0, stages);
-    load_all(A, s0 + mine, stages == 1 ? behind : 0);
-    load_all(B, s1 + mine, stages == 1 ? behind : 0);
-    if (stages > 1) {
-        load_all(A, s2 + mine, stages == 2 ? behind : 0);
-        load_all(B, s3 + mine, stages == 2 ? behind : 0);
-        wait_loads<8>();
-    } else {
-        wait_loads<0>();
-    }
+    load_all(A, s0 + mine, 0);
+    load_all(B, s1 + mine, 0);
+    load_all(A, s2 + mine, 0);
+    load_all(B, s3 + mine, 0);
+    wait_loads<8>();
     bare_barrier();
     read8(A, fa, s0, 0);
-    if (stages > 1) {
-        fb = frag8<0>(B, s1, 0);
-        fc[0] = frag8<1>(B, s1, 0);
-    } else {
-        fb = frag_last(integral_constant<int, 0>(), s1, 0);
-        fc[0] = frag_last(integral_constant<int, 1>(), s1, 0);
-    }
+    fb = frag8<0>(B, s1, 0);
+    fc[0] = frag8<1>(B, s1, 0);
     // a stage that loads another one; the last but one, the last
     enum { kLoads, kBeforeLast, kLast };
     auto stage = [&](auto kind, uint32_t less) {
@@ -222,10 +213,8 @@ __device__ inline void k_loop8(floatx16 (&acc)[TA][TB], int stages, OA& A, OB& B
         for (; kt < end; ++kt) stage(integral_constant<int, kLoads>(), kt + 3 == stages ? behind : 0);
         if (kt % kScaleStages == 0) s.load(kt, stages);
     }
-    if (stages > 1) {
-        stage(integral_constant<int, kBeforeLast>(), 0);
-        if (++kt % kScaleStages == 0) s.load(kt, stages);
-    }
+    stage(integral_constant<int, kBeforeLast>(), 0);
+    if (++kt % kScaleStages == 0) s.load(kt, stages);
     stage(integral_constant<int, kLast>(), 0);
 }
 
