@@ -135,7 +135,7 @@ struct Join8 {
     int splits, cols, dim;   // splits == 0: zeros
     float* out;
     int64_t out_stride;
-    int out_vec, accumulate;
+    int accumulate;
 };
 hipError_t launch_grad8(const Grad8& a, int edge, bool deep, hipStream_t s);     // tiles of 128 or 256; deep: further ahead, 128 only
 hipError_t launch_join8(const Join8& a, hipStream_t s);

@@ -400,8 +400,7 @@ int act8_grad_weight(const act8_grad_weight_t* problem, void* workspace, size_t 
     if (const int rc = c.done()) return rc;
     hipStream_t s = static_cast<hipStream_t>(stream);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
-    const int out_vec = whole_rows(p.out, p.out_stride, 4) && p.dim % 4 == 0;
-    Join8 j = {nullptr, q.dim8, q.splits, (int)p.cols, (int)p.dim, p.out, p.out_stride, out_vec, p.accumulate != 0};
+    Join8 j = {nullptr, q.dim8, q.splits, (int)p.cols, (int)p.dim, p.out, p.out_stride, p.accumulate != 0};
     if (p.rows == 0) {
         j.splits = 0;
         if (!p.accumulate) LINEAR8_TRY("act8_grad_join", launch_join8(j, s));
@@ -430,7 +429,7 @@ int act8_grad_weight(const act8_grad_weight_t* problem, void* workspace, size_t 
     a.tiles_d = (int)ceil_div(p.dim, q.edge);
     a.out = p.out;
     a.out_stride = p.out_stride;
-    a.out_vec = out_vec;
+    a.out_vec = whole_rows(p.out, p.out_stride, 4) && p.dim % 4 == 0;
     a.accumulate = p.accumulate != 0;
     a.partial = q.partial >= 0 ? reinterpret_cast<float*>(ws + q.partial) : nullptr;
     a.partial_pitch = q.dim8;

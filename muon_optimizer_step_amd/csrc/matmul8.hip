@@ -701,10 +701,10 @@ __global__ __launch_bounds__(NW * kWave) void matmul8_rows_kernel(const Matmul8 
     }
 }
 
-// Otherwise 32 TV columns x 32 TT rows a workgroup, where that alone fills the chip and K is short: 128 x 1024 x 1024
+// Otherwise 32 columns x 32 rows a workgroup, where that alone fills the chip and K is short: 128 x 1024 x 1024
 // 4.5 us (64: 5.5, 128: 7.6).
-template <int TV, int TT, int NW> constexpr size_t kSplitBytes = (size_t)NW * TV * TT * 16 * kWave * 4;
-template <typename T, int TV, int TT, int NW>
+template <int NW> constexpr size_t kSplitBytes = (size_t)NW * 16 * kWave * 4;
+template <typename T, int NW>
 __global__ __launch_bounds__(NW * kWave) void matmul8_split_kernel(const Matmul8 a) {
     extern __shared__ __align__(16) uint8_t lds[];
     const int item = xcd_item(a.tiles_v * a.tiles_t);
@@ -712,47 +712,36 @@ __global__ __launch_bounds__(NW * kWave) void matmul8_split_kernel(const Matmul8
     int tile_v, tile_t;
     tile_of(a, item, tile_v, tile_t);
     const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), half = lane / 32;
-    const int v0 = tile_v * 32 * TV, t0 = tile_t * 32 * TT;
+    const int v0 = tile_v * 32, t0 = tile_t * 32;
     const int stages = (a.dim + kBlock8 - 1) / kBlock8, end = (a.dim + 15) / 16 * 16 - 16 * half;
-    const uint8_t* code[TV + TT];
-    const uint8_t* scale[1 + TT];        // the columns of a tile share a block
-    static_assert(kBlock8 % (32 * TV) == 0, "one block of weights");
-#pragma unroll
-    for (int i = 0; i < TV; ++i) code[i] = a.b.codes + (int64_t)min(v0 + 32 * i + swap23(lane % 32), a.cols - 1) * a.b.stride + 16 * half;
-    scale[0] = a.b.scale + (int64_t)(v0 / kBlock8) * a.b.scale_stride;
-#pragma unroll
-    for (int j = 0; j < TT; ++j) {
-        const int64_t t = min(t0 + 32 * j + lane % 32, a.rows - 1);
-        code[TV + j] = a.a.codes + t * a.a.stride + 16 * half;
-        scale[1 + j] = a.a.scale + t * a.a.scale_stride;
-    }
+    const int64_t v = min(v0 + swap23(lane % 32), a.cols - 1), t = min(t0 + lane % 32, a.rows - 1);
+    const uint8_t* const b = a.b.codes + v * a.b.stride + 16 * half;
+    const uint8_t* const x = a.a.codes + t * a.a.stride + 16 * half;
+    const uint8_t* const sb = a.b.scale + (int64_t)(v0 / kBlock8) * a.b.scale_stride;      // a tile's columns share a block
+    const uint8_t* const sa = a.a.scale + t * a.a.scale_stride;
     struct Stage {
-        u32x4 w[TV + TT][4];
-        int s[1 + TT];
+        u32x4 b[4], x[4];
+        int sb, sa;
     };
-    floatx16 acc[TV][TT];
-    clear(acc);
+    floatx16 acc(0.f);
     auto load = [&](Stage& s, int kt) {
-#pragma unroll
-        for (int i = 0; i < TV + TT; ++i)
+        auto row = [&](u32x4 (&w)[4], const uint8_t* from) {
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 const int k = kt * kBlock8 + 32 * c;
-                s.w[i][c] = u32x4{0u, 0u, 0u, 0u};
-                if (k < end) s.w[i][c] = *reinterpret_cast<const u32x4*>(code[i] + k);
+                w[c] = u32x4{0u, 0u, 0u, 0u};
+                if (k < end) w[c] = *reinterpret_cast<const u32x4*>(from + k);
             }
-#pragma unroll
-        for (int i = 0; i < 1 + TT; ++i) s.s[i] = scale[i][kt];
+        };
+        row(s.b, b);
+        row(s.x, x);
+        s.sb = sb[kt];
+        s.sa = sa[kt];
     };
     auto multiply = [&](const Stage& s) {
 #pragma unroll
         for (int step = 0; step < 2; ++step)
-#pragma unroll
-            for (int i = 0; i < TV; ++i)
-#pragma unroll
-                for (int j = 0; j < TT; ++j)
-                    acc[i][j] = mfma8(join(s.w[i][2 * step], s.w[i][2 * step + 1]), join(s.w[TV + j][2 * step], s.w[TV + j][2 * step + 1]),
-                                      acc[i][j], s.s[0], s.s[1 + j]);
+            acc = mfma8(join(s.b[2 * step], s.b[2 * step + 1]), join(s.x[2 * step], s.x[2 * step + 1]), acc, s.sb, s.sa);
     };
     Stage now, next;
     if (wave < stages) load(now, wave);
@@ -762,22 +751,18 @@ __global__ __launch_bounds__(NW * kWave) void matmul8_split_kernel(const Matmul8
         if (kt + 2 * NW < stages) load(now, kt + 2 * NW);
         if (kt + NW < stages) multiply(next);
     }
-    // 8 consecutive columns of a row: unit (tv, tt, p, lane) holds column 32 tv + 16 p + 8 (l / 32) of row 32 tt + l % 32
-    constexpr int kUnits = TV * TT * 2 * kWave;
+    // 8 consecutive columns of a row: unit (p, lane) holds column 16 p + 8 (l / 32) of row l % 32
+    constexpr int kUnits = 2 * kWave;
     floatx4* part = reinterpret_cast<floatx4*>(lds);
 #pragma unroll
-    for (int i = 0; i < TV; ++i)
+    for (int p = 0; p < 2; ++p)
 #pragma unroll
-        for (int j = 0; j < TT; ++j)
+        for (int h = 0; h < 2; ++h) {
+            floatx4 w;
 #pragma unroll
-            for (int p = 0; p < 2; ++p)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    floatx4 v;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) v[e] = acc[i][j][8 * p + 4 * h + e];
-                    part[((wave * 2 + h) * TV * TT * 2 + (i * TT + j) * 2 + p) * kWave + lane] = v;
-                }
+            for (int e = 0; e < 4; ++e) w[e] = acc[8 * p + 4 * h + e];
+            part[((wave * 2 + h) * 2 + p) * kWave + lane] = w;
+        }
     __syncthreads();
     for (int u = threadIdx.x; u < kUnits; u += NW * kWave) {
         floatx4 lo = part[u], hi = part[kUnits + u];
@@ -786,17 +771,16 @@ __global__ __launch_bounds__(NW * kWave) void matmul8_split_kernel(const Matmul8
             lo += part[2 * w * kUnits + u];
             hi += part[(2 * w + 1) * kUnits + u];
         }
-        const int l = u % kWave, p = u / kWave % 2, ij = u / (2 * kWave);
-        const int row = t0 + 32 * (ij % TT) + l % 32, v = v0 + 32 * (ij / TT) + 16 * p + 8 * (l / 32);
-        if (row >= a.rows || v >= a.cols) continue;
-        T* dst = static_cast<T*>(a.y) + (int64_t)row * a.y_stride + v;
+        const int l = u % kWave, row = t0 + l % 32, col = v0 + 16 * (u / kWave) + 8 * (l / 32);
+        if (row >= a.rows || col >= a.cols) continue;
+        T* dst = static_cast<T*>(a.y) + (int64_t)row * a.y_stride + col;
         const float sums[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-        if (v + 8 <= a.cols) {
+        if (col + 8 <= a.cols) {
             *reinterpret_cast<u32x4_any*>(dst) = pack8<T>(sums);
         } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                if (v + e < a.cols) dst[e] = (T)sums[e];
+                if (col + e < a.cols) dst[e] = (T)sums[e];
         }
     }
 }
@@ -806,12 +790,11 @@ hipError_t allow_lds(K kernel, size_t bytes) {
     return hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
 }
 
-template <typename T, int TV, int TT, int NW>
+template <typename T, int NW>
 hipError_t split_launch(const Matmul8& a, hipStream_t s) {
-    constexpr size_t bytes = kSplitBytes<TV, TT, NW>;
-    const hipError_t allowed = allow_lds(&matmul8_split_kernel<T, TV, TT, NW>, bytes);
+    const hipError_t allowed = allow_lds(&matmul8_split_kernel<T, NW>, kSplitBytes<NW>);
     if (allowed != hipSuccess) return allowed;
-    matmul8_split_kernel<T, TV, TT, NW><<<xcd_grid(a.tiles_v * a.tiles_t), NW * kWave, bytes, s>>>(a);
+    matmul8_split_kernel<T, NW><<<xcd_grid(a.tiles_v * a.tiles_t), NW * kWave, kSplitBytes<NW>, s>>>(a);
     return hipGetLastError();
 }
 
@@ -828,7 +811,7 @@ template <typename T>
 hipError_t typed(const Matmul8& a, int variant, hipStream_t s) {
     const int grid = xcd_grid(a.tiles_v * a.tiles_t);
     if (variant == kMatmulRows) matmul8_rows_kernel<T, 8><<<a.tiles_v, 8 * kWave, 0, s>>>(a);
-    else if (variant == kMatmulSplit) return split_launch<T, 1, 1, 8>(a, s);
+    else if (variant == kMatmulSplit) return split_launch<T, 8>(a, s);
     else if (variant == kMatmulSmall) return small_launch<T, false, 2, 2, 1, 1, 4>(a, s);
     else if (variant == kMatmulMid) return small_launch<T, false, 2, 2, 2, 2, 2>(a, s);
     else {
