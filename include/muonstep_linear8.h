@@ -46,7 +46,7 @@ extern "C" {
  *                 are zero.  stride: a multiple of 16, >= dim rounded up to 16.
  *   scale         s of row (weights: row of blocks) i and block b at
  *                 scale[i * scale_stride + b], 4-byte aligned.  scale_stride: a
- *                 multiple of 4, >= ceil(dim / MUON_BLOCK8).
+ *                 multiple of 4, >= ceil(dim / MUON_BLOCK8); rows are read in words of 4.
  * Encoding: s - 127 is the smallest power with top / 2^(s - 127) <= 448, top the
  * block's largest finite magnitude, but s >= MUON_SCALE8_LOW; a code is
  * value / 2^(s - 127) rounded to the nearest e4m3 value, halves to even.  A NaN or

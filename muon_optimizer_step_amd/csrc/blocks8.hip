@@ -161,7 +161,8 @@ __device__ inline Sigmoid sigmoid(float u) {
 // gelu's F(u) = erfc(-u / sqrt 2) / 2 and exp(-u^2 / 2).  erfc(z) = exp(-z^2) t P(t), t = 1 / (1 + p z) for z >= 0 (the form
 // of Abramowitz and Stegun 7.1.26), p and the eight degrees of P fitted to exp(z^2) erfc(z) for z up to
 // 13.5 (minimax, 3.6e-8 of it; 1e-7 with coefficients of float32's digits, 3.4e-7 in float32; the fit is in
-// tests/test_linear8_gelu_host.py): F keeps its digits where it is small, and shares the exponential with the derivative.  Beyond |u| = 20 the exponential is zero.
+// tests/test_linear8_gelu_host.py): F keeps its digits where it is small, and shares the
+// exponential with the derivative.  Beyond |u| = 20 the exponential is zero.
 struct Gelu {
     float f, e;
 };
@@ -269,8 +270,8 @@ __global__ __launch_bounds__(kThreads) void encode8_kernel(const Encode8 a) {
     });
 }
 
-// silu's and gelu's derivatives are 1 or 0 from |u| = 200 on, which with scales from this byte on (2^113) is every code but zero and NaN:
-// larger ones count as this one, so that u is finite.
+// silu's and gelu's derivatives are 1 or 0 from |u| = 200 on, which with scales from this byte on (2^113) is every code but
+// zero and NaN: larger ones count as this one, so that u is finite.
 constexpr int kFarScale = 240;
 
 template <typename T, int ACT>

@@ -13,12 +13,14 @@ constexpr int kBlock8 = 128;      // values of a row that share a scale
 constexpr int kScale8Low = 10;    // the smallest scale's byte
 
 // Part of a result from `base` (the same for the whole wave) on, written with the device's scope: through the XCD's
-// L2.  What a kernel leaves there is written back when it ends, and the next one waits for that: y of
-// 2048 x 2048 x 512 6.2 us against 6.9, of 16384 x 2048 x 512 26.3 against 28.5 (with an encoding of y behind it
-// 42 against 46 to 49).  Meant for whole 128-byte lines: 16 lanes of 8 codes, 32 of 4, 8 of 16 bytes.  Rows that begin or end inside a
-// line break two of them, which is no loss in codes (65536 x 200: 9.7 against 10.6) and little in y and the weight's gradient (16384 x 1000 x
-// 512: 15.0 against 15.4, with a reader 28.2 against 26.6; gradient of 1000 x 4000 x 2004 25.7 and 25.7, 40 and 37).  Offsets in
-// bytes, below 2^31.
+// L2.  What a kernel leaves there is written back when it ends, and the next one waits for that.  Meant for whole
+// 128-byte lines: 16 lanes of 8 codes, 32 of 4, 8 of 16 bytes.  Rows that begin or end inside a line break two of them,
+// which is no loss in codes and little in y and the weight's gradient.  Through the L2 / by ordinary stores, us, in a
+// graph, three sets of inputs in turn; in brackets with a reader behind it:
+//     y 2048 x 2048 x 512      6.2 / 6.9  (11.0 / 11.6)      codes of 16384 x 4096    32.0 / 35.0 (59.9 / 62.6)
+//     y 16384 x 2048 x 512    26.3 / 28.4 (42 / 46 to 49)    codes of 65536 x 200      9.7 / 10.6 (22.5 / 23.6)
+//     y 16384 x 1000 x 512    15.0 / 15.4 (28.2 / 26.6)      gradient 1000 x 4000 x 2004   25.7 / 25.7 (40 / 37)
+// Offsets in bytes, below 2^31.
 struct Through {
     static constexpr int kDevice = 16;      // the instruction's sc1
     __amdgpu_buffer_rsrc_t out;

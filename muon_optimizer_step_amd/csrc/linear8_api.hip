@@ -28,13 +28,15 @@ Blocks8 blocks(const blocks8_t& b) {
 bool whole_rows(const void* p, int64_t stride, int64_t size) {
     return reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride * size % 16 == 0;
 }
-// Whether the row-wise passes write a 16 or 32-bit result through the L2 (Through in linear8.h).  Not where an instruction's
-// pieces leave no whole lines: float32, of which it holds 16 of every 32 bytes (relu2's backward of 8192 x 4096 105 us, by
-// ordinary stores 59, with an encoding of the result behind it 128 and 81), and not large results whose rows lie off the 128-byte grid
-// (in 16 bits, 25152 x 1000: 30 us and 30, fp16 22.6 and 24; 50304 x 1000: 64 and 60, fp16 50 and 47; 134208 x 1000: 170 and
-// 153).  On the grid the two are within a per cent, small results up to 1 us quicker through the L2.  Past the last cache too is no better where a
-// reader follows: 16384 x 4096 decoded to bfloat16 and encoded 69 us (63), the backward pass of 16384 x 4096 with both
-// products behind it 247 to 254 us either way.
+// Whether the row-wise passes write a 16 or 32-bit result through the L2 (Through in linear8.h).  Not where an
+// instruction's pieces leave no whole lines: float32, of which it holds 16 of every 32 bytes (relu2's backward of
+// 8192 x 4096 105 us, by ordinary stores 59, with an encoding of the result behind it 128 and 81), and not large
+// results whose rows lie off the 128-byte grid (bfloat16 / float16, us through the L2 and by ordinary stores):
+//     25152 x 1000    29.8, 29.7 / 22.6, 24.0       50304 x 1000    64.4, 60.4 / 49.8, 46.9
+//     134208 x 1000    170,  153 /  129,  114
+// On the grid the two are within a per cent, and small results up to 1 us quicker through the L2.  Past the last cache
+// too is no better where a reader follows: 16384 x 4096 decoded to bfloat16 and encoded 69 us (63), the backward pass of
+// 16384 x 4096 with both products behind it 247 to 254 us either way.
 constexpr int64_t kRaggedBytes = (int64_t)64 << 20;
 bool through(const void* p, int64_t rows, int64_t dim, int64_t stride, int dtype) {
     if (dtype == MUON_T_FP32 || !whole_rows(p, stride, 2)) return false;
