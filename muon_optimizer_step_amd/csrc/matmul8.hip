@@ -14,9 +14,9 @@
 // (bfloat16) or 2e-4 (float16).  A float32 y would show the difference: it is computed from exact products (below), and so
 // are 16-bit ones where the caller asks for it.
 //
-// Bound and measured, 8-bit products: MFMA for large problems (8192^3: 432 to 440 us, 2.5 PFLOP/s; 400 us, 2.75, where consecutive calls
+// Bound and measured, 8-bit products: MFMA for large problems (8192^3: 431 to 440 us, 2.5 PFLOP/s; 400 us, 2.75, where consecutive calls
 // have one input; a library's 8-bit product with one scale for each matrix reaches 2.64; MFMA busy two
-// thirds of the cycles); y's bytes where K is short (16384 x 2048 x 512: 25.6 us, 3.0 TB/s; MFMA 23 %); the weights' bytes where there are
+// thirds of the cycles); y's bytes where K is short (16384 x 2048 x 512: 23.4 to 25.6 us, 3.2 TB/s; MFMA 23 %); the weights' bytes where there are
 // few rows (1 x 8192 x 8192 13 us, 5.2 TB/s; 64 x 8192 x 8192 20 us); below, a launch (1 x 4096 x 1024 4.2 us, of which
 // 3.2 in the kernel).  Rows of codes off the 128-byte grid cost a quarter (3000 x 700 x 5000: 40 us, K = 4992 32),
 // so encoded matrices have whole lines where dim > 512.
