@@ -193,12 +193,9 @@ template <int ACT> __device__ inline float act(float u) {
     if (ACT == kActGelu) return u * gelu_parts(u).f;
     return u;
 }
-// u: finite or NaN, but for relu2.
+// The derivative, relu2's less its factor of 2; u: |u| <= 2^127 or NaN.
 template <int ACT> __device__ inline float act_slope(float u) {
-    if (ACT == kActRelu2) {
-        const float t = positive(u);
-        return t + t;
-    }
+    if (ACT == kActRelu2) return positive(u);
     if (ACT == kActSilu) {
         const Sigmoid g = sigmoid(u);
         return g.s * fmaf(u, g.rest, 1.f);
@@ -270,8 +267,9 @@ __global__ __launch_bounds__(kThreads) void encode8_kernel(const Encode8 a) {
     });
 }
 
-// silu's and gelu's derivatives are 1 or 0 from |u| = 200 on, which with scales from this byte on (2^113) is every code but
-// zero and NaN: larger ones count as this one, so that u is finite.
+// Larger scales count as this one (2^113), so that u is finite.  silu's and gelu's derivatives are 1 or 0 from |u| = 200 on, which
+// with such scales is every code but zero and NaN; relu2's gets the rest of the scale and its factor of 2 behind the product
+// with the gradient, so that nothing is infinite where the result is not.
 constexpr int kFarScale = 240;
 
 template <typename T, int ACT>
@@ -297,10 +295,15 @@ __global__ __launch_bounds__(kThreads) void backward8_kernel(const Backward8 a) 
         for (int k = 0; k < kBatch; ++k) {
             const int row = u.row + k * u.step;
             float v[8], g[8];
-            decode8(code[k], scale_value(ACT == kActRelu2 ? byte[k] : min(byte[k], kFarScale)), v);
+            const int near = min(byte[k], kFarScale);
+            const float rest = scale_value(128 + byte[k] - near);
+            decode8(code[k], scale_value(near), v);
             to_float<T>(grad[k], g);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) g[e] *= act_slope<ACT>(v[e]);
+            for (int e = 0; e < 8; ++e) {
+                if (ACT == kActRelu2) g[e] = g[e] * act_slope<ACT>(v[e]) * rest;
+                else g[e] *= act_slope<ACT>(v[e]);
+            }
             if (a.out && u.row0 + row < a.r.rows) {
                 T* first = static_cast<T*>(a.out) + u.row0 * a.out_stride;
                 store8(Through(first), first, row * a.out_stride + u.d, from_float<T>(g), left, a.out_through);

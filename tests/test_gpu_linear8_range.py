@@ -94,3 +94,56 @@ def test_values_that_are_not_finite(kind):
     r = ms.act8_encode(x.cuda(), activation=kind)
     nan = (base._codes(r.out.codes) & 0x7F) == 0x7F
     assert nan[0, 5] and nan[1, 5] and nan[:2].sum() == 2 and (nan[2].sum() == nan[2, 5])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_relu2_backward_of_far_values(dtype):
+    """2 u is beyond float32 from 1.7e38 on, and u is where its code stands for 2^128; their products with a small gradient, and with
+    zero, are not."""
+    import torch
+    import muon_optimizer_step_amd as ms
+    x = _rows(dtype)
+    gu.say(f"[far] backward relu2 {dtype}")
+    u8 = ms.act8_encode(x.cuda()).checkpoint
+    u, _ = _meant(u8)
+    assert u.max() == 2.0 ** 128
+    for value in (0.0, 2.0 ** -20, -2.0 ** -100):
+        grad = torch.full(x.shape, value, dtype=base._type(dtype), device="cuda")
+        r = ms.act8_backward(u8, grad, "relu2", codes=True)
+        want = value * 2 * np.maximum(u, 0)
+        got = base._f64(r.grad)
+        assert np.isfinite(got).all(), f"{value}: {np.argwhere(~np.isfinite(got)).tolist()}"
+        assert (np.abs(got - want) <= (base.U[dtype] + 2.0 ** -20) * np.abs(want) + base.TINY[dtype]).all(), value
+        values, scale = _meant(r.grad8)
+        assert (np.abs(values - want) <= (2.0 ** -4 + 2.0 ** -18) * np.abs(want) + (2.0 ** -10 + 2.0 ** -18) * scale).all(), value
+    nan = torch.full((1, 128), float("nan"), device="cuda")
+    bad = ms.act8_backward(ms.act8_encode(nan).checkpoint, torch.zeros(1, 128, device="cuda"), "relu2", codes=True)
+    assert torch.isnan(bad.grad).all() and ((base._codes(bad.grad8.codes) & 0x7F) == 0x7F).all()
+
+
+def test_relu2_backward_with_any_scale():
+    """448 2^(scale - 127) and 2^-9 of it, times 2 and a gradient that brings the product back: exact."""
+    import torch
+    import muon_optimizer_step_amd as ms
+    x = torch.zeros(2, 130)
+    x[:, 0], x[:, 1], x[:, 3], x[:, 4] = 448.0, -448.0, float("nan"), 2.0 ** -9
+    q = ms.act8_encode(x.cuda()).checkpoint
+    for scale in (1, 10, 127, 239, 240, 241, 247, 254):
+        u8 = ms.Activation8(q.codes, torch.full_like(q.scale, scale), 130)
+        power = max(-126, 127 - scale - 9)
+        got = ms.act8_backward(u8, torch.full((2, 130), 2.0 ** power, device="cuda"), "relu2").grad.cpu().double()
+        unit = 2.0 ** (scale - 127 + power + 1)
+        assert (got[:, 0] == 448.0 * unit).all() and (got[:, 1] == 0).all() and torch.isnan(got[:, 3]).all(), scale
+        assert (got[:, 4] == 2.0 ** -9 * unit).all() and (got[:, 5:] == 0).all(), scale
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_relu2_backward_of_far_gradients(dtype):
+    """The largest finite gradient times a small u: exact where both are powers of two but for the gradient's own digits."""
+    import torch
+    import muon_optimizer_step_amd as ms
+    top = torch.finfo(base._type(dtype)).max
+    for power in (-2, -30, -100):
+        u8 = ms.act8_encode(torch.full((3, 40), 2.0 ** power, device="cuda")).checkpoint
+        got = ms.act8_backward(u8, torch.full((3, 40), top, dtype=base._type(dtype), device="cuda"), "relu2").grad
+        assert (got.double() == top * 2.0 ** (power + 1)).all(), power
