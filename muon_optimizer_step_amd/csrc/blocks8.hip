@@ -11,7 +11,7 @@
 // Bound: HBM; every value is read once and written once (a copy of 4 GiB: 4.7 TB/s, reads and
 // writes together).  Measured, inputs from memory: 16384 x 2048 bf16 to its codes and relu2's 23.1 us,
 // 5.8 TB/s; 16384 x 4096 bf16 to codes 31.2 us, 6.5; relu2's backward of 16384 x 4096, in 16 and in
-// 8 bits, 69 us, 5.9 TB/s; gelu's and silu's 92 and 80 us, for which the vector unit is the limit;
+// 8 bits, 68 us, 6.0 TB/s; gelu's and silu's 90 and 78 us, for which the vector unit is the limit;
 // 8192 x 8192 float32 weights to codes and transposed codes 74 us, 5.5 TB/s; 16384 x 4096 codes to
 // bf16 30 us, 6.6.  Small calls are a launch: 2048 values 2.9 us of kernel time.
 #include <algorithm>
